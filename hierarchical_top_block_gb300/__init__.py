@@ -85,6 +85,16 @@ def lib() -> ct.CDLL:
         L.pisa_decode_step_ws.restype = ct.c_int
         L.pisa_decode_step_ws.argtypes = [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, ct.c_size_t, pisa_shape,
                                           pisa_params, _P]
+        L.pisa_cache_write.restype = ct.c_int
+        L.pisa_cache_write.argtypes = [_P] * 10 + [pisa_shape, _P]
+        L.pisa_cache_read.restype = ct.c_int
+        L.pisa_cache_read.argtypes = [_P] * 8 + [pisa_shape, _P]
+        L.pisa_sparse_attn_cache.restype = ct.c_int
+        L.pisa_sparse_attn_cache.argtypes = [_P] * 10 + [pisa_shape, pisa_params, _P]
+        L.pisa_prefix_attn_workspace_bytes.restype = ct.c_size_t
+        L.pisa_prefix_attn_workspace_bytes.argtypes = [pisa_shape, pisa_params]
+        L.pisa_prefix_attn.restype = ct.c_int
+        L.pisa_prefix_attn.argtypes = [_P] * 12 + [ct.c_size_t, pisa_shape, pisa_params, _P]
         L.pisa_status_string.restype = ct.c_char_p
         L.pisa_status_string.argtypes = [ct.c_int]
         L.pisa_get_last_device_error.restype = ct.c_int
@@ -471,3 +481,185 @@ def pisa_decode_step(q, k, v, Kc, Vc, Pc, seq_len, K_sel: int, scale: float = 0.
                                      _stream(q)),
            "pisa_decode_step_ws")
     return o
+
+
+# ---- 8-bit cache ------------------------------------------------------------------------
+def _fits(t, name, shape, dtype, device):
+    """_expect, with the checks in the order that costs a valid call least."""
+    if t is not None and not (t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous()):
+        _expect(t, name, shape, dtype, device)
+
+
+def _cuda(t, name):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def _call(fn, what, device, *args):
+    """Calls a library function on the device's current stream, with that device current."""
+    if device.index == torch.cuda.current_device():
+        rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    if rc != PISA_OK:
+        raise PisaError(rc, what)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _cache_shape(Kq, name):
+    if Kq.dim() != 4:
+        raise ValueError(f"{name} must be [B, H_kv, N_cap, d]")
+    return Kq.shape
+
+
+def _check_cache(Kq, Vq, k_scale, v_scale, device):
+    shape = _cache_shape(Kq, "Kq")
+    if k_scale is None or v_scale is None:
+        raise ValueError("k_scale and v_scale must be given")
+    _fits(Kq, "Kq", shape, torch.int8, device)
+    _fits(Vq, "Vq", shape, torch.int8, device)
+    _fits(k_scale, "k_scale", shape[:3], torch.float32, device)
+    _fits(v_scale, "v_scale", shape[:3], torch.float32, device)
+    return shape
+
+
+def pisa_cache_write(k, v, Kq, Vq, k_scale, v_scale, seq_len, new_len=None, k_out=None, v_out=None) -> None:
+    """Quantise T new rows of every sequence into the 8-bit cache at rows seq_len[b] + t.
+
+    k, v [B, H_kv, T, d] (or [B, H_kv, d] for one) bf16; Kq, Vq [B, H_kv, N_cap, d] int8; k_scale, v_scale
+    [B, H_kv, N_cap] fp32; seq_len [B] int32, not changed; new_len [B] int32: rows in use of each sequence
+    (None: T).  k_out, v_out (None: not wanted) receive the values the cache then holds, as bf16; they may be
+    k and v."""
+    dev = _cuda(k, "k")
+    B, H_kv, N_cap, d = _check_cache(Kq, Vq, k_scale, v_scale, dev)
+    T = 1 if k.dim() == 3 else k.shape[2] if k.dim() == 4 else -1
+    want = (B, H_kv, d) if k.dim() == 3 else (B, H_kv, T, d)
+    _fits(k, "k", want, torch.bfloat16, dev)
+    _fits(v, "v", want, torch.bfloat16, dev)
+    _fits(k_out, "k_out", want, torch.bfloat16, dev)
+    _fits(v_out, "v_out", want, torch.bfloat16, dev)
+    if seq_len is None:
+        raise ValueError("seq_len must be given")
+    _fits(seq_len, "seq_len", (B,), torch.int32, dev)
+    _fits(new_len, "new_len", (B,), torch.int32, dev)
+    _call(lib().pisa_cache_write, "pisa_cache_write", dev, k.data_ptr(), v.data_ptr(), Kq.data_ptr(), Vq.data_ptr(),
+          k_scale.data_ptr(), v_scale.data_ptr(), seq_len.data_ptr(), _addr(new_len), _addr(k_out), _addr(v_out),
+          pisa_shape(B, T, H_kv, H_kv, d, N_cap))
+
+
+def pisa_cache_read(Kq, Vq, k_scale, v_scale, T: int, start=None, length=None, k_out=None, v_out=None):
+    """Read rows start[b] .. start[b] + length[b] - 1 (None: 0 and T) of the 8-bit cache back as bf16.
+
+    Returns k_out, v_out [B, H_kv, T, d]; rows past a sequence's length are left as they are (zero where the
+    output is allocated here).  Kq with k_scale, or Vq with v_scale, may be None: that side is not read."""
+    if Kq is None and Vq is None:
+        raise ValueError("Kq or Vq must be given")
+    ref = Kq if Kq is not None else Vq
+    dev = _cuda(ref, "the cache")
+    shape = _cache_shape(ref, "the cache")
+    B, H_kv, N_cap, d = shape
+    out = []
+    for q, s, o, n in ((Kq, k_scale, k_out, "k"), (Vq, v_scale, v_out, "v")):
+        if q is None:
+            if o is not None or s is not None:
+                raise ValueError(f"{n}_scale and {n}_out go with a cache")
+            out.append(None)
+            continue
+        if s is None:
+            raise ValueError(f"{n}_scale must be given")
+        _fits(q, n.upper() + "q", shape, torch.int8, dev)
+        _fits(s, n + "_scale", shape[:3], torch.float32, dev)
+        if o is None:
+            o = torch.zeros((B, H_kv, T, d), dtype=torch.bfloat16, device=dev)
+        _fits(o, n + "_out", (B, H_kv, T, d), torch.bfloat16, dev)
+        out.append(o)
+    _fits(start, "start", (B,), torch.int32, dev)
+    _fits(length, "length", (B,), torch.int32, dev)
+    _call(lib().pisa_cache_read, "pisa_cache_read", dev, _addr(Kq), _addr(Vq), _addr(k_scale), _addr(v_scale),
+          _addr(start), _addr(length), _addr(out[0]), _addr(out[1]), pisa_shape(B, T, H_kv, H_kv, d, N_cap))
+    return out[0], out[1]
+
+
+def pisa_sparse_attn_cache(q, Kq, Vq, k_scale, v_scale, idx, seq_len, new_len=None, scale: float = 0.0, O=None,
+                           LSE=None, want_lse: bool = True):
+    """Attention of T new tokens a sequence, token t at position seq_len[b] + t, over the blocks idx
+    [B, H_kv, T, K] of the 8-bit cache (which holds the new tokens' rows already).  q [B, T, H_q, d] (or
+    [B, H_q, d] with idx [B, H_kv, K] for one).  Returns O like q and LSE [B, T, H_q] (or [B, H_q]); rows
+    t >= new_len[b], and sequences whose lengths do not fit, are left as they are (zero where allocated here)."""
+    dev = _cuda(q, "q")
+    B, H_kv, N_cap, d = _check_cache(Kq, Vq, k_scale, v_scale, dev)
+    one = q.dim() == 3
+    if q.dim() not in (3, 4) or idx.dim() != q.dim():
+        raise ValueError("q must be [B, T, H_q, d] with idx [B, H_kv, T, K], or [B, H_q, d] with idx [B, H_kv, K]")
+    T, H_q, K_sel = 1 if one else q.shape[1], q.shape[-2], idx.shape[-1]
+    want = (B, H_q, d) if one else (B, T, H_q, d)
+    _fits(q, "q", want, torch.bfloat16, dev)
+    _fits(idx, "idx", (B, H_kv, K_sel) if one else (B, H_kv, T, K_sel), torch.int32, dev)
+    if seq_len is None:
+        raise ValueError("seq_len must be given")
+    _fits(seq_len, "seq_len", (B,), torch.int32, dev)
+    _fits(new_len, "new_len", (B,), torch.int32, dev)
+    if O is None:
+        O = torch.zeros(want, dtype=torch.bfloat16, device=dev)
+    _fits(O, "O", want, torch.bfloat16, dev)
+    if want_lse and LSE is None:
+        LSE = torch.zeros(want[:-1], dtype=torch.float32, device=dev)
+    _fits(LSE, "LSE", want[:-1], torch.float32, dev)
+    _call(lib().pisa_sparse_attn_cache, "pisa_sparse_attn_cache", dev, q.data_ptr(), Kq.data_ptr(), Vq.data_ptr(),
+          k_scale.data_ptr(), v_scale.data_ptr(), idx.data_ptr(), seq_len.data_ptr(), _addr(new_len), O.data_ptr(),
+          _addr(LSE if want_lse else None), pisa_shape(B, T, H_q, H_kv, d, N_cap),
+          pisa_params(64, 2, K_sel, 1, float(scale), 0))
+    return O, (LSE if want_lse else None)
+
+
+# ---- attention over a shared prefix -------------------------------------------------------
+def pisa_prefix_attn_workspace_bytes(shape: pisa_shape, params: pisa_params) -> int:
+    return int(lib().pisa_prefix_attn_workspace_bytes(shape, params))
+
+
+def pisa_prefix_attn(q, Kp, Vp, prefix_len, row_start=None, k_scale=None, v_scale=None, o_own=None, lse_own=None,
+                     scale: float = 0.0, o=None, lse=None, want_lse: bool = True, ws=None):
+    """Attention of R query rows q [R, H_q, d] in n groups over the prefixes Kp, Vp [n, H_kv, N_cap, d] (bf16, or
+    int8 with k_scale, v_scale [n, H_kv, N_cap]) of prefix_len [n] keys: rows row_start[p] .. row_start[p + 1] - 1
+    (row_start [n + 1] int32; None: one group of all rows) are group p's.  o_own [R, H_q, d] bf16 and lse_own
+    [R, H_q]: what the rows attended on their own, joined by log-sum-exp.  Returns o and lse [R, H_q] of the joined
+    result; rows of no group are left as they are (zero where allocated here)."""
+    dev = _cuda(q, "q")
+    n, H_kv, N_cap, d = _cache_shape(Kp, "Kp")
+    if q.dim() != 3:
+        raise ValueError("q must be [R, H_q, d]")
+    R, H_q = q.shape[:2]
+    want = (R, H_q, d)
+    _fits(q, "q", want, torch.bfloat16, dev)
+    dtype = torch.bfloat16 if k_scale is None else torch.int8
+    _fits(Kp, "Kp", Kp.shape, dtype, dev)
+    _fits(Vp, "Vp", Kp.shape, dtype, dev)
+    _fits(k_scale, "k_scale", Kp.shape[:3], torch.float32, dev)
+    _fits(v_scale, "v_scale", Kp.shape[:3], torch.float32, dev)
+    if prefix_len is None:
+        raise ValueError("prefix_len must be given")
+    _fits(prefix_len, "prefix_len", (n,), torch.int32, dev)
+    _fits(row_start, "row_start", (n + 1,), torch.int32, dev)
+    _fits(o_own, "o_own", want, torch.bfloat16, dev)
+    _fits(lse_own, "lse_own", want[:2], torch.float32, dev)
+    new = torch.empty if row_start is None and n == 1 else torch.zeros
+    if o is None:
+        o = new(want, dtype=torch.bfloat16, device=dev)
+    _fits(o, "o", want, torch.bfloat16, dev)
+    if want_lse and lse is None:
+        lse = new(want[:2], dtype=torch.float32, device=dev)
+    _fits(lse, "lse", want[:2], torch.float32, dev)
+    shape, params = pisa_shape(n, R, H_q, H_kv, d, N_cap), pisa_params(64, 2, 1, 0, float(scale), 0)
+    need = lib().pisa_prefix_attn_workspace_bytes(shape, params)
+    if need == 0 and R > 0:
+        raise PisaError(2, "pisa_prefix_attn: unsupported shape or parameters")
+    ws = _workspace(ws, need, dev)
+    _call(lib().pisa_prefix_attn, "pisa_prefix_attn", dev, q.data_ptr(), Kp.data_ptr(), Vp.data_ptr(), _addr(k_scale),
+          _addr(v_scale), prefix_len.data_ptr(), _addr(row_start), _addr(o_own), _addr(lse_own), o.data_ptr(),
+          _addr(lse if want_lse else None), ws.data_ptr(), ws.numel(), shape, params)
+    return o, (lse if want_lse else None)

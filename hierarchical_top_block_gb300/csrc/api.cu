@@ -77,9 +77,11 @@ DeviceState g_dev[MAX_DEVICES];
 // ---- per-phase device time (profiling aid) ------------------------------------------------
 // While enabled, each entry point records a CUDA event on its stream at the start of its work
 // and after each kernel phase; pisa_phase_times() resolves the events and sums the phases.
-enum Phase { PH_PYRAMID, PH_STAGE1, PH_CLUSTER, PH_LEAF_LSE, PH_TOPK, PH_ATTN, PH_BSA, PH_DECODE, PH_BACKWARD, NPHASE };
+enum Phase { PH_PYRAMID, PH_STAGE1, PH_CLUSTER, PH_LEAF_LSE, PH_TOPK, PH_ATTN, PH_BSA, PH_DECODE, PH_BACKWARD,
+             PH_CACHE_WRITE, PH_CACHE_READ, PH_ATTN_CACHE, PH_PREFIX, NPHASE };
 const char* const PHASE_NAMES[NPHASE] = {"pyramid", "stage1", "cluster", "leaf_lse", "topk",
-                                         "sparse_attn", "bsa_select", "decode", "attn_backward"};
+                                         "sparse_attn", "bsa_select", "decode", "attn_backward",
+                                         "cache_write", "cache_read", "sparse_attn_cache", "prefix_attn"};
 
 std::atomic<bool> g_timing{false};
 
@@ -786,6 +788,130 @@ pisa_status pisa_decode_step_ws(const uint16_t* q, const uint16_t* k, const uint
       launch_decode(q, k, v, Kc, Vc, Pc, seq_len, o, lse, idx_out, static_cast<float*>(ws), p, geo_cap, st->err,
                     static_cast<cudaStream_t>(stream));
   tm.mark(PH_DECODE);
+  return cuda_status(e);
+}
+
+namespace {
+
+// The 8-bit cache's entry points take no method parameters: those that check_params wants are set
+// to values every call accepts.
+pisa_status check_cache(const pisa_shape& shape, Problem* p) {
+  pisa_shape s = shape;
+  s.H_q = s.H_kv;
+  const pisa_params pr{64, 2, 1, 1, 0.f, 0};
+  return check_params(s, pr, p);
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+}  // namespace
+
+pisa_status pisa_cache_write(const uint16_t* k, const uint16_t* v, int8_t* Kq, int8_t* Vq, float* k_scale,
+                             float* v_scale, const int32_t* seq_len, const int32_t* new_len, uint16_t* k_out,
+                             uint16_t* v_out, pisa_shape shape, pisa_stream stream) {
+  Problem p;
+  pisa_status rc = check_cache(shape, &p);
+  if (rc != PISA_OK) return rc;
+  if (p.B == 0 || p.N == 0) return PISA_OK;
+  if (!k || !v || !Kq || !Vq || !k_scale || !v_scale || !seq_len) return PISA_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(Kq) || !aligned16(Vq) || !aligned16(k_scale) ||
+      !aligned16(v_scale) || !aligned4(seq_len) || !aligned4(new_len) || !aligned16(k_out) || !aligned16(v_out))
+    return PISA_ERR_INVALID_ARG;
+  DeviceState* st;
+  if ((rc = device_state(&st)) != PISA_OK) return rc;
+  PhaseTimer tm(static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_cache_write(k, v, Kq, Vq, k_scale, v_scale, seq_len, new_len, k_out, v_out, p,
+                                           st->num_sms, st->err, static_cast<cudaStream_t>(stream));
+  tm.mark(PH_CACHE_WRITE);
+  return cuda_status(e);
+}
+
+pisa_status pisa_cache_read(const int8_t* Kq, const int8_t* Vq, const float* k_scale, const float* v_scale,
+                            const int32_t* start, const int32_t* len, uint16_t* k_out, uint16_t* v_out,
+                            pisa_shape shape, pisa_stream stream) {
+  Problem p;
+  pisa_status rc = check_cache(shape, &p);
+  if (rc != PISA_OK) return rc;
+  if (p.B == 0 || p.N == 0) return PISA_OK;
+  if ((!k_out && !v_out) || (k_out && (!Kq || !k_scale)) || (v_out && (!Vq || !v_scale))) return PISA_ERR_INVALID_ARG;
+  if (!aligned16(Kq) || !aligned16(Vq) || !aligned16(k_scale) || !aligned16(v_scale) || !aligned4(start) ||
+      !aligned4(len) || !aligned16(k_out) || !aligned16(v_out))
+    return PISA_ERR_INVALID_ARG;
+  DeviceState* st;
+  if ((rc = device_state(&st)) != PISA_OK) return rc;
+  PhaseTimer tm(static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_cache_read(Kq, Vq, k_scale, v_scale, start, len, k_out, v_out, p, st->num_sms, st->err,
+                                          static_cast<cudaStream_t>(stream));
+  tm.mark(PH_CACHE_READ);
+  return cuda_status(e);
+}
+
+pisa_status pisa_sparse_attn_cache(const uint16_t* q, const int8_t* Kq, const int8_t* Vq, const float* k_scale,
+                                   const float* v_scale, const int32_t* idx, const int32_t* seq_len,
+                                   const int32_t* new_len, uint16_t* O, float* LSE, pisa_shape shape,
+                                   pisa_params params, pisa_stream stream) {
+  Problem p;
+  pisa_status rc = check_params(shape, params, &p);
+  if (rc != PISA_OK) return rc;
+  if (p.causal != 1) return PISA_ERR_UNSUPPORTED;
+  if (p.B == 0 || p.N == 0) return PISA_OK;
+  if (!q || !Kq || !Vq || !k_scale || !v_scale || !idx || !seq_len || !O) return PISA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(Kq) || !aligned16(Vq) || !aligned16(k_scale) || !aligned16(v_scale) ||
+      !aligned4(idx) || !aligned4(seq_len) || !aligned4(new_len) || !aligned16(O) || !aligned4(LSE))
+    return PISA_ERR_INVALID_ARG;
+  DeviceState* st;
+  if ((rc = device_state(&st)) != PISA_OK) return rc;
+  PhaseTimer tm(static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_sparse_cache(q, Kq, Vq, k_scale, v_scale, idx, seq_len, new_len, O, LSE, p,
+                                            st->num_sms, st->err, static_cast<cudaStream_t>(stream));
+  tm.mark(PH_ATTN_CACHE);
+  return cuda_status(e);
+}
+
+namespace {
+
+// The prefix attention's shape: B prefixes, N query rows (all groups together), N_cap rows a prefix.
+pisa_status check_prefix(const pisa_shape& shape, const pisa_params& params, Problem* p) {
+  if (shape.N_cap <= 0 || shape.N < 0) return PISA_ERR_INVALID_ARG;
+  pisa_shape s = shape;
+  s.N = 0;
+  const pisa_status rc = check_params(s, params, p);
+  if (rc != PISA_OK) return rc;
+  if (p->causal != 0) return PISA_ERR_UNSUPPORTED;  // every row sees the whole prefix
+  if ((long long)shape.N * shape.H_q >= (1LL << 31)) return PISA_ERR_UNSUPPORTED;
+  p->N = p->t_hi = shape.N;
+  return PISA_OK;
+}
+
+}  // namespace
+
+size_t pisa_prefix_attn_workspace_bytes(pisa_shape shape, pisa_params params) {
+  Problem p;
+  return check_prefix(shape, params, &p) == PISA_OK ? prefix_workspace_bytes(p) : 0;
+}
+
+pisa_status pisa_prefix_attn(const uint16_t* q, const void* Kp, const void* Vp, const float* k_scale,
+                             const float* v_scale, const int32_t* prefix_len, const int32_t* row_start,
+                             const uint16_t* o_own, const float* lse_own, uint16_t* o, float* lse, void* ws,
+                             size_t ws_bytes, pisa_shape shape, pisa_params params, pisa_stream stream) {
+  Problem p;
+  pisa_status rc = check_prefix(shape, params, &p);
+  if (rc != PISA_OK) return rc;
+  if (p.B == 0 || p.N == 0) return PISA_OK;
+  if (!q || !Kp || !Vp || !prefix_len || !o || !ws) return PISA_ERR_INVALID_ARG;
+  if ((k_scale == nullptr) != (v_scale == nullptr) || (o_own == nullptr) != (lse_own == nullptr)) return PISA_ERR_INVALID_ARG;
+  if (!row_start && p.B != 1) return PISA_ERR_INVALID_ARG;  // one group is all rows; more need their bounds
+  if (!aligned16(q) || !aligned16(Kp) || !aligned16(Vp) || !aligned16(k_scale) || !aligned16(v_scale) ||
+      !aligned4(prefix_len) || !aligned4(row_start) || !aligned16(o_own) || !aligned4(lse_own) || !aligned16(o) ||
+      !aligned4(lse) || (reinterpret_cast<uintptr_t>(ws) & 255u))
+    return PISA_ERR_INVALID_ARG;
+  if (ws_bytes < prefix_workspace_bytes(p)) return PISA_ERR_WORKSPACE;
+  DeviceState* st;
+  if ((rc = device_state(&st)) != PISA_OK) return rc;
+  PhaseTimer tm(static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_prefix_attn(q, Kp, Vp, k_scale, v_scale, prefix_len, row_start, o_own, lse_own, o, lse,
+                                           ws, p, st->num_sms, st->err, static_cast<cudaStream_t>(stream));
+  tm.mark(PH_PREFIX);
   return cuda_status(e);
 }
 

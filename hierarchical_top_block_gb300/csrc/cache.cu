@@ -1,0 +1,213 @@
+// The 8-bit key/value cache: rows are quantised as they are written, and read back as bf16.
+//
+// A row x (d values of one key or value head) is stored as int8 codes and one fp32 scale:
+//   a = max_i |x_i|,  scale = a / 127,  code_i = sign(x_i) floor(127 |x_i| / a + 1/2)
+// (a = 0: codes and scale 0; a row with an infinity or a NaN: codes 0, scale NaN, so that the row
+// reads back as NaN).  The scale is per (token, head): a row never changes after it was written,
+// so tokens can be appended one at a time and the attention can keep the codes as whole numbers
+// (they are exact in bf16) and apply the scale to the fp32 logit or weight.
+//
+// Rounding half away from zero makes the codes exact with one fp32 reciprocal a row: with
+// X, M < 2^8 the integer significands of x and a and e the difference of their exponents,
+// 127 |x| / a = 127 X / (M 2^e), so a value that is not half-way between two codes is at least
+// 2^-(e+8) from half-way, while its size is below 2^(8-e).  Multiplying by (127 / a)(1 + 2^-20)
+// moves it by less than 2^(8.3-e-20) (the two roundings included), too little to cross, and
+// moves an exact half-way value up, never down.
+//
+// Both kernels move bytes: 16 lanes (d = 128) or 8 lanes (d = 64) take a row, 8 values a lane, so
+// every access of a warp is whole 128-byte lines; a thread has RPT rows in flight.
+#include "kernels.cuh"
+
+namespace pisa {
+namespace {
+
+constexpr int THREADS = 256;
+constexpr int RPT = 4;  // rows a thread has in flight
+
+struct CacheParams {
+  const uint16_t* x[2];  // write: K and V rows in
+  uint16_t* y[2];        // values out (read: the rows; write: nullable)
+  int8_t* q[2];
+  float* s[2];
+  const int32_t* start;  // first cache row of each sequence (nullable: 0)
+  const int32_t* count;  // rows of each sequence in use (nullable: T)
+  uint32_t rows;         // B * H * T
+  int H, T, N_cap;
+  uint32_t* err;
+};
+
+// The place of row `row` of [B][H][T]: its cache row, or -1 where there is none (behind the
+// sequence's count, or a sequence whose rows do not fit: nothing of it is read or written).
+__device__ __forceinline__ long long cache_row(const CacheParams& p, uint32_t row) {
+  const uint32_t bh = row / (uint32_t)p.T, t = row - bh * (uint32_t)p.T, b = bh / (uint32_t)p.H;
+  const int first = p.start ? __ldg(p.start + b) : 0, n = p.count ? __ldg(p.count + b) : p.T;
+  if (first < 0 || n < 0 || n > p.T || first > p.N_cap - n) {
+    report_error(p.err, ERR_BAD_INDEX);
+    return -1;
+  }
+  return t < (uint32_t)n ? (long long)bh * p.N_cap + first + t : -1;
+}
+
+template <int D, bool VALUES>
+__global__ void __launch_bounds__(THREADS) cache_write_kernel(CacheParams p) {
+  constexpr int LANES = D / 8, RPB = THREADS / LANES;  // lanes a row, rows a block and step
+  const int part = threadIdx.x % LANES, kv = blockIdx.y;
+  int8_t* q = kv ? p.q[1] : p.q[0];
+  float* s = kv ? p.s[1] : p.s[0];
+  uint16_t* y = kv ? p.y[1] : p.y[0];
+  const uint16_t* x = kv ? p.x[1] : p.x[0];  // may be the values out as well: each lane reads its part before it writes it
+  for (uint64_t r0 = (uint64_t)blockIdx.x * RPB * RPT; r0 < p.rows; r0 += (uint64_t)gridDim.x * RPB * RPT) {
+    const uint64_t first = r0 + threadIdx.x / LANES;
+    uint4 w[RPT];
+    long long at[RPT];
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+      const uint64_t row = first + (uint64_t)i * RPB;
+      at[i] = row < p.rows ? cache_row(p, (uint32_t)row) : -1;
+      w[i] = at[i] >= 0 ? *reinterpret_cast<const uint4*>(x + row * D + 8 * part) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+      const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+      // the largest |x| by its bits (bf16 magnitudes order as integers; NaN above infinity)
+      uint32_t a = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) a = max(a, max(u[j] & 0x7fffu, (u[j] >> 16) & 0x7fffu));
+#pragma unroll
+      for (int o = LANES / 2; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
+      const float amax = __uint_as_float(a << 16);
+      const bool finite = a < 0x7f80u;
+      const float scale = finite ? __fdiv_rn(amax, 127.f) : __uint_as_float(0x7fc00000u);
+      // 127 / a overflows below 2^-121: both sides times 2^64 there (exact)
+      const float up = amax < 5.421010862427522e-20f ? 1.8446744073709552e19f : 1.f;
+      const float inv = (a == 0 || !finite) ? 0.f : __fdiv_rn(127.f, amax * up) * (1.f + 9.5367431640625e-07f);
+      float t[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float lo = bf16_lo(u[j]), hi = bf16_hi(u[j]);
+        t[2 * j] = inv > 0.f ? truncf(fmaf(lo * up, inv, copysignf(0.5f, lo))) : 0.f;
+        t[2 * j + 1] = inv > 0.f ? truncf(fmaf(hi * up, inv, copysignf(0.5f, hi))) : 0.f;
+      }
+      if (at[i] < 0) continue;
+      uint32_t code[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t b01 = __byte_perm((uint32_t)(int)t[4 * h], (uint32_t)(int)t[4 * h + 1], 0x0040);
+        const uint32_t b23 = __byte_perm((uint32_t)(int)t[4 * h + 2], (uint32_t)(int)t[4 * h + 3], 0x0040);
+        code[h] = __byte_perm(b01, b23, 0x5410);
+      }
+      *reinterpret_cast<uint2*>(q + at[i] * D + 8 * part) = make_uint2(code[0], code[1]);
+      if (part == 0) s[at[i]] = scale;
+      if (VALUES) {
+        uint4 v;
+        v.x = pack_bf16x2(t[0] * scale, t[1] * scale);
+        v.y = pack_bf16x2(t[2] * scale, t[3] * scale);
+        v.z = pack_bf16x2(t[4] * scale, t[5] * scale);
+        v.w = pack_bf16x2(t[6] * scale, t[7] * scale);
+        if (y) *reinterpret_cast<uint4*>(y + (first + (uint64_t)i * RPB) * D + 8 * part) = v;
+      }
+    }
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(THREADS) cache_read_kernel(CacheParams p) {
+  constexpr int LANES = D / 8, RPB = THREADS / LANES;
+  const int part = threadIdx.x % LANES;
+  const int kv = p.y[0] == nullptr ? 1 : blockIdx.y;  // K, V or both
+  const int8_t* __restrict__ q = kv ? p.q[1] : p.q[0];
+  const float* __restrict__ s = kv ? p.s[1] : p.s[0];
+  uint16_t* y = kv ? p.y[1] : p.y[0];
+  for (uint64_t r0 = (uint64_t)blockIdx.x * RPB * RPT; r0 < p.rows; r0 += (uint64_t)gridDim.x * RPB * RPT) {
+    const uint64_t first = r0 + threadIdx.x / LANES;
+    uint2 w[RPT];
+    float sc[RPT];
+    long long at[RPT];
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+      const uint64_t row = first + (uint64_t)i * RPB;
+      at[i] = row < p.rows ? cache_row(p, (uint32_t)row) : -1;
+      w[i] = at[i] >= 0 ? __ldg(reinterpret_cast<const uint2*>(q + at[i] * D + 8 * part)) : make_uint2(0, 0);
+      sc[i] = at[i] >= 0 ? __ldg(s + at[i]) : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+      if (at[i] < 0) continue;
+      float f[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        f[j] = (float)(int8_t)(w[i].x >> (8 * j)) * sc[i];
+        f[4 + j] = (float)(int8_t)(w[i].y >> (8 * j)) * sc[i];
+      }
+      uint4 v;
+      v.x = pack_bf16x2(f[0], f[1]);
+      v.y = pack_bf16x2(f[2], f[3]);
+      v.z = pack_bf16x2(f[4], f[5]);
+      v.w = pack_bf16x2(f[6], f[7]);
+      *reinterpret_cast<uint4*>(y + (first + (uint64_t)i * RPB) * D + 8 * part) = v;
+    }
+  }
+}
+
+unsigned blocks_for(uint32_t rows, int rows_per_step, int num_sms) {
+  const uint64_t need = (rows + (uint64_t)rows_per_step - 1) / rows_per_step;
+  const uint64_t most = (uint64_t)num_sms * 8;
+  return (unsigned)(need < most ? need : most);
+}
+
+CacheParams params_of(const Problem& p, uint32_t* err) {
+  CacheParams c{};
+  c.rows = (uint32_t)p.B * (uint32_t)p.H_kv * (uint32_t)p.N;
+  c.H = p.H_kv;
+  c.T = p.N;
+  c.N_cap = p.N_cap;
+  c.err = err;
+  return c;
+}
+
+}  // namespace
+
+cudaError_t launch_cache_write(const uint16_t* k, const uint16_t* v, int8_t* Kq, int8_t* Vq, float* k_scale,
+                               float* v_scale, const int32_t* seq_len, const int32_t* new_len, uint16_t* k_out,
+                               uint16_t* v_out, const Problem& p, int num_sms, uint32_t* err, cudaStream_t s) {
+  CacheParams c = params_of(p, err);
+  c.x[0] = k;
+  c.x[1] = v;
+  c.y[0] = k_out;
+  c.y[1] = v_out;
+  c.q[0] = Kq;
+  c.q[1] = Vq;
+  c.s[0] = k_scale;
+  c.s[1] = v_scale;
+  c.start = seq_len;
+  c.count = new_len;
+  const dim3 grid(blocks_for(c.rows, THREADS / (p.d / 8) * RPT, num_sms), 2);
+  const bool values = k_out || v_out;
+  if (p.d == 128)
+    (values ? cache_write_kernel<128, true> : cache_write_kernel<128, false>)<<<grid, THREADS, 0, s>>>(c);
+  else
+    (values ? cache_write_kernel<64, true> : cache_write_kernel<64, false>)<<<grid, THREADS, 0, s>>>(c);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_cache_read(const int8_t* Kq, const int8_t* Vq, const float* k_scale, const float* v_scale,
+                              const int32_t* start, const int32_t* len, uint16_t* k_out, uint16_t* v_out,
+                              const Problem& p, int num_sms, uint32_t* err, cudaStream_t s) {
+  CacheParams c = params_of(p, err);
+  c.y[0] = k_out;
+  c.y[1] = v_out;
+  c.q[0] = const_cast<int8_t*>(Kq);
+  c.q[1] = const_cast<int8_t*>(Vq);
+  c.s[0] = const_cast<float*>(k_scale);
+  c.s[1] = const_cast<float*>(v_scale);
+  c.start = start;
+  c.count = len;
+  const dim3 grid(blocks_for(c.rows, THREADS / (p.d / 8) * RPT, num_sms), k_out && v_out ? 2 : 1);
+  if (p.d == 128)
+    cache_read_kernel<128><<<grid, THREADS, 0, s>>>(c);
+  else
+    cache_read_kernel<64><<<grid, THREADS, 0, s>>>(c);
+  return cudaGetLastError();
+}
+
+}  // namespace pisa

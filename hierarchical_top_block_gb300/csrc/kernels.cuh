@@ -83,6 +83,29 @@ cudaError_t launch_decode(const uint16_t* q, const uint16_t* k, const uint16_t* 
                           uint16_t* Pc, int32_t* seq_len, uint16_t* o, float* lse, int32_t* idx_out, float* logits,
                           const Problem& p, const Geometry& geo_cap, uint32_t* err, cudaStream_t s);
 
+// 8-bit cache: quantise T rows a sequence as they are written (k_out / v_out, nullable: the values
+// the cache then holds), and read rows back as bf16 (either output nullable).  p.N = T.
+cudaError_t launch_cache_write(const uint16_t* k, const uint16_t* v, int8_t* Kq, int8_t* Vq, float* k_scale,
+                               float* v_scale, const int32_t* seq_len, const int32_t* new_len, uint16_t* k_out,
+                               uint16_t* v_out, const Problem& p, int num_sms, uint32_t* err, cudaStream_t s);
+cudaError_t launch_cache_read(const int8_t* Kq, const int8_t* Vq, const float* k_scale, const float* v_scale,
+                              const int32_t* start, const int32_t* len, uint16_t* k_out, uint16_t* v_out,
+                              const Problem& p, int num_sms, uint32_t* err, cudaStream_t s);
+
+// Attention of T = p.N new tokens a sequence over selected blocks of the 8-bit cache.
+cudaError_t launch_sparse_cache(const uint16_t* q, const int8_t* Kq, const int8_t* Vq, const float* k_scale,
+                                const float* v_scale, const int32_t* idx, const int32_t* seq_len,
+                                const int32_t* new_len, uint16_t* o, float* lse, const Problem& p, int num_sms,
+                                uint32_t* err, cudaStream_t s);
+
+// Attention of p.N query rows in p.B groups over their groups' prefixes (k_scale null: bf16 caches),
+// joined with the rows' own partial results where given.
+size_t prefix_workspace_bytes(const Problem& p);
+cudaError_t launch_prefix_attn(const uint16_t* q, const void* Kp, const void* Vp, const float* k_scale,
+                               const float* v_scale, const int32_t* prefix_len, const int32_t* row_start,
+                               const uint16_t* o_own, const float* lse_own, uint16_t* o, float* lse, void* ws,
+                               const Problem& p, int num_sms, uint32_t* err, cudaStream_t s);
+
 // One CTA whose bounded waits run out after limit_ns (checks the timeout path).
 cudaError_t launch_wait_check(uint64_t limit_ns, uint32_t* err, cudaStream_t s);
 

@@ -1,0 +1,231 @@
+// Attention of a batch over prefixes that its sequences share: R query rows in P groups, the
+// rows of group p over all keys of prefix p (a bf16 or an 8-bit cache), joined with what each
+// row attended on its own.
+//
+// Reading the prefix once for the whole group is the point: G_Q n_p query rows share each key, so
+// with few rows the reads bound the work, and with many the products do (4 d operations a row
+// and key).  This kernel: 16 rows a tile on mma.sync with the cache read straight into registers.
+#include <algorithm>
+
+#include "cache_attn.cuh"
+#include "kernels.cuh"
+#include "pdl.cuh"
+#include "prefix_plan.cuh"
+
+namespace pisa {
+namespace {
+
+constexpr int THREADS = 128;
+constexpr int FEW_ROWS = 16;
+
+// Joins a finished row's prefix part with its own part (log-sum-exp `own`) and writes one element.
+__device__ __forceinline__ void write_out(const PrefixParams& p, size_t at, size_t row, bool write_lse, float acc,
+                                          float m, float l, float own) {
+  float fa, fo, lse;
+  join_own(m, l, own, fa, fo, lse);
+  float v = fa == 0.f ? 0.f : acc * fa;
+  if (p.o_own && fo != 0.f) v += bf16_to_f32(p.o_own[at]) * fo;
+  p.o[at] = f32_to_bf16_rne(v);
+  if (write_lse && p.lse) p.lse[row] = lse;
+}
+
+template <int D, int BITS, bool HI>
+__global__ void __launch_bounds__(THREADS) prefix_few_kernel(PrefixParams p) {
+  pdl_trigger();
+  using Tile = CacheTile<D, BITS>;
+  __shared__ float po[4 * 16 * D];
+  __shared__ float pm[4][16], pl[4][16], bm[16], bl[16], bo[16];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, q = lane & 3;
+  PrefixWalk w;
+  w.init(p, blockIdx.x, blockIdx.x == 0 && warp == 0);
+  while (w.next(p, blockIdx.x)) {
+    const int m0 = w.tile * FEW_ROWS;                       // first query row of the tile
+    const int rows = min(FEW_ROWS, w.g.n * p.GQ - m0);      // query row m: token m / G, head m % G
+    uint32_t qa[Tile::QW], qb[Tile::QW];
+    auto q_row = [&](int i) {
+      const int m = m0 + i, tok = m / p.GQ;
+      return ((size_t)(w.g.first + tok) * p.H_q + (size_t)w.head * p.GQ + (m - tok * p.GQ));
+    };
+    Tile::load_q(p.q + q_row(r < rows ? r : 0) * D, r < rows, q, qa);
+    Tile::load_q(p.q + q_row(r + 8 < rows ? r + 8 : 0) * D, HI && r + 8 < rows, q, qb);
+    const size_t ph = (size_t)w.p * p.H_kv + w.head;
+    const uint8_t* K = p.K + ph * p.N_cap * Tile::ROWB;
+    const uint8_t* V = p.V + ph * p.N_cap * Tile::ROWB;
+    const float* ks = BITS == 8 ? p.ks + ph * p.N_cap : nullptr;
+    const float* vs = BITS == 8 ? p.vs + ph * p.N_cap : nullptr;
+    typename Tile::State st;
+    Tile::clear(st);
+    const int key_end = min(w.g.len, w.k1 * PREFIX_KT);
+    for (int key0 = w.k0 * PREFIX_KT + warp * Tile::KEYS; key0 < key_end; key0 += 4 * Tile::KEYS) {
+      const int n = min(Tile::KEYS, key_end - key0);
+      typename Tile::Regs regs;
+      Tile::load(regs, K, V, ks, vs, key0, n, r, q);
+      Tile::template add<HI>(st, regs, qa, qb, n, p.sl2, q);
+    }
+    // read before any row is written: lse may be lse_own
+    if (threadIdx.x < rows) bo[threadIdx.x] = p.lse_own ? p.lse_own[q_row(threadIdx.x)] : NEG_INF;
+    join_warps<D, BITS, HI>(st, po, pm, pl, bm, bl, rows);
+    __syncthreads();
+    if (w.slot < 0) {
+      for (int i = threadIdx.x; i < rows * D; i += THREADS) {
+        const int row = i / D, c = i - row * D;
+        const size_t orow = q_row(row);
+        write_out(p, orow * D + c, orow, c == 0, po[i], bm[row], bl[row], bo[row]);
+      }
+    } else {
+      float* dst = p.part_o + (size_t)w.slot * FEW_ROWS * D;
+      for (int i = threadIdx.x; i < rows * D; i += THREADS) dst[i] = po[i];
+      if (threadIdx.x < rows) p.part_ml[(size_t)w.slot * FEW_ROWS + threadIdx.x] = make_float2(bm[threadIdx.x], bl[threadIdx.x]);
+    }
+    __syncthreads();  // the next segment writes the shared arrays again
+  }
+}
+
+// Joins the parts of every job that spans blocks: one warp a (row, query head).
+template <int D>
+__global__ void __launch_bounds__(THREADS) prefix_join_kernel(PrefixParams p) {
+  pdl_wait();
+  constexpr int V = D / 32;  // columns a lane
+  const int lane = threadIdx.x & 31;
+  const long long S = p.base[p.P];
+  for (long long i = (long long)blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5); i < (long long)p.R * p.H_q;
+       i += (long long)gridDim.x * (THREADS / 32)) {
+    const int row = (int)(i / p.H_q), hq = (int)(i - (long long)row * p.H_q);
+    int gp = 0;
+    if (p.row_start) {
+      int lo = 0, hi = p.P;  // first group with row_start[g + 1] > row
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(p.row_start + mid + 1) > row)
+          hi = mid;
+        else
+          lo = mid + 1;
+      }
+      gp = lo;
+      if (gp >= p.P) continue;
+    }
+    const PrefixGroup g = prefix_group(p, gp);
+    if (row < g.first || row >= g.first + g.n) continue;
+    const int head = hq / p.GQ;
+    const int m = (row - g.first) * p.GQ + (hq - head * p.GQ);
+    const int tile = m / p.rows, local = m - tile * p.rows;
+    const long long s0 = p.base[gp] + ((long long)head * g.tiles + tile) * g.steps, s1 = s0 + g.steps;
+    const int blocks = line_blocks(S, p.blocks);
+    const int c0 = block_of(S, blocks, s0), c1 = block_of(S, blocks, s1 - 1);
+    if (c0 == c1) continue;  // finished by its block
+    const int slot0 = 2 * c0 + (range_start(S, blocks, c0) == s0 ? 0 : 1);
+    float M = NEG_INF;
+    for (int c = c0; c <= c1; ++c)
+      M = fmaxf(M, p.part_ml[(size_t)(c == c0 ? slot0 : 2 * c) * p.rows + local].x);
+    float l = 0.f, acc[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) acc[j] = 0.f;
+    for (int c = c0; c <= c1; ++c) {
+      const size_t at = (size_t)(c == c0 ? slot0 : 2 * c) * p.rows + local;
+      const float2 ml = p.part_ml[at];
+      if (ml.x == NEG_INF) {
+        l += ml.y;  // 0, or NaN where every logit was
+        continue;
+      }
+      const float f = fast_exp2(ml.x - M);
+      l += ml.y * f;
+      const float* src = p.part_o + at * D + lane * V;
+      if constexpr (V == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(src);
+        acc[0] += x.x * f;
+        acc[1] += x.y * f;
+        acc[2] += x.z * f;
+        acc[3] += x.w * f;
+      } else {
+        const float2 x = *reinterpret_cast<const float2*>(src);
+        acc[0] += x.x * f;
+        acc[1] += x.y * f;
+      }
+    }
+    const float own = p.lse_own ? p.lse_own[i] : NEG_INF;
+    float fa, fo, lse;
+    join_own(M, l, own, fa, fo, lse);
+    const size_t at = (size_t)i * D + lane * V;
+    float v[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      v[j] = fa == 0.f ? 0.f : acc[j] * fa;
+      if (p.o_own && fo != 0.f) v[j] += bf16_to_f32(p.o_own[at + j]) * fo;
+    }
+    if constexpr (V == 4)
+      *reinterpret_cast<uint2*>(p.o + at) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    else
+      *reinterpret_cast<uint32_t*>(p.o + at) = pack_bf16x2(v[0], v[1]);
+    __syncwarp();  // lse may be lse_own: every lane has read it
+    if (p.lse && lane == 0) p.lse[i] = lse;
+  }
+}
+
+constexpr int MAX_BLOCKS = 304;  // two a SM of this GPU: the scratch does not depend on the device at hand
+int prefix_rows(const Problem&) { return FEW_ROWS; }
+
+template <int D, int BITS>
+cudaError_t launch_few(const PrefixParams& p, cudaStream_t s) {
+  // a tile has rows above 8 unless all groups together are shorter
+  if ((long long)p.R * p.GQ > 8)
+    prefix_few_kernel<D, BITS, true><<<p.blocks, THREADS, 0, s>>>(p);
+  else
+    prefix_few_kernel<D, BITS, false><<<p.blocks, THREADS, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+}  // namespace
+
+size_t prefix_workspace_bytes(const Problem& p) {
+  const size_t parts = (size_t)2 * MAX_BLOCKS * prefix_rows(p);
+  return up256(parts * p.d * 4) + up256(parts * 8) + up256((size_t)(p.B + 1) * 8);
+}
+
+cudaError_t launch_prefix_attn(const uint16_t* q, const void* Kp, const void* Vp, const float* k_scale,
+                               const float* v_scale, const int32_t* prefix_len, const int32_t* row_start,
+                               const uint16_t* o_own, const float* lse_own, uint16_t* o, float* lse, void* ws,
+                               const Problem& pr, int num_sms, uint32_t* err, cudaStream_t s) {
+  PrefixParams p;
+  p.q = q;
+  p.K = static_cast<const uint8_t*>(Kp);
+  p.V = static_cast<const uint8_t*>(Vp);
+  p.ks = k_scale;
+  p.vs = v_scale;
+  p.prefix_len = prefix_len;
+  p.row_start = row_start;
+  p.o_own = o_own;
+  p.lse_own = lse_own;
+  p.o = o;
+  p.lse = lse;
+  p.P = pr.B;
+  p.R = pr.N;
+  p.H_q = pr.H_q;
+  p.H_kv = pr.H_kv;
+  p.GQ = pr.GQ;
+  p.N_cap = pr.N_cap;
+  p.sl2 = pr.scale * LOG2E;
+  p.err = err;
+  p.rows = prefix_rows(pr);
+  p.blocks = std::min(MAX_BLOCKS, 2 * num_sms);
+  const size_t parts = (size_t)2 * p.blocks * p.rows;
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  p.part_o = reinterpret_cast<float*>(w);
+  w += up256(parts * pr.d * 4);
+  p.part_ml = reinterpret_cast<float2*>(w);
+  w += up256(parts * 8);
+  p.base = reinterpret_cast<long long*>(w);
+  cudaError_t e;
+  if (pr.d == 128)
+    e = k_scale ? launch_few<128, 8>(p, s) : launch_few<128, 16>(p, s);
+  else
+    e = k_scale ? launch_few<64, 8>(p, s) : launch_few<64, 16>(p, s);
+  if (e != cudaSuccess) return e;
+  const long long warps = (long long)p.R * p.H_q;
+  const unsigned grid = (unsigned)std::min<long long>((warps + 3) / 4, (long long)num_sms * 16);
+  return pr.d == 128 ? launch_pdl(prefix_join_kernel<128>, dim3(grid), dim3(THREADS), 0, s, p)
+                     : launch_pdl(prefix_join_kernel<64>, dim3(grid), dim3(THREADS), 0, s, p);
+}
+
+}  // namespace pisa

@@ -1,0 +1,175 @@
+// How the attention over shared prefixes is divided over thread blocks.
+//
+// A job is (group p, KV head, tile of ROWS query rows); it takes the group's prefix in steps of
+// PREFIX_KT keys.  The jobs' steps, one job after the other, form one line of S steps, cut into
+// equal ranges, one a block: whatever the number of groups, rows and keys, every block gets the
+// same number of steps (to within one).  A job that lies in one block is finished there; of a job
+// that spans blocks, each block stores its part (row maxima, sums and output sums), and a second
+// kernel joins them.  A block has at most two such parts: the first job of its range and the last.
+// The cut depends on the sizes alone, so results are the same in every run.
+#pragma once
+
+#include "common.cuh"
+
+namespace pisa {
+
+struct PrefixParams {
+  const uint16_t* q;
+  const uint8_t* K;
+  const uint8_t* V;
+  const float* ks;           // null: a bf16 cache
+  const float* vs;
+  const int32_t* prefix_len; // [P]
+  const int32_t* row_start;  // [P + 1], nullable: one group of all R rows
+  const uint16_t* o_own;     // nullable (both)
+  const float* lse_own;
+  uint16_t* o;
+  float* lse;                // nullable
+  float* part_o;             // [2 blocks][ROWS][d] output sums relative to the row maximum
+  float2* part_ml;           // [2 blocks][ROWS] row maximum (log2 units) and sum
+  long long* base;           // [P + 1] first step of each group; the last entry is S
+  int P, R, H_q, H_kv, GQ, N_cap;
+  int rows;                  // ROWS
+  int blocks;                // thread blocks the steps are divided over
+  float sl2;
+  uint32_t* err;
+};
+
+constexpr int PREFIX_KT = 128;  // keys a step
+
+struct PrefixGroup {
+  int first, n, len;      // first row, rows, prefix keys
+  int tiles, steps;       // tiles a head; steps a job (an empty prefix has one, with no key)
+};
+
+__device__ __forceinline__ PrefixGroup prefix_group(const PrefixParams& p, int i) {
+  PrefixGroup g;
+  int lo = p.row_start ? __ldg(p.row_start + i) : 0, hi = p.row_start ? __ldg(p.row_start + i + 1) : p.R;
+  lo = min(max(lo, 0), p.R);
+  hi = min(max(hi, lo), p.R);
+  g.first = lo;
+  g.n = hi - lo;
+  g.len = min(max(__ldg(p.prefix_len + i), 0), p.N_cap);
+  g.tiles = (int)(((long long)g.n * p.GQ + p.rows - 1) / p.rows);
+  g.steps = max(1, (g.len + PREFIX_KT - 1) / PREFIX_KT);
+  return g;
+}
+__device__ __forceinline__ long long group_steps(const PrefixParams& p, const PrefixGroup& g) {
+  return (long long)p.H_kv * g.tiles * g.steps;
+}
+
+// Blocks the line of S steps is divided over: every one of them gets a step at least, so a job's
+// parts are in consecutive blocks.
+__device__ __forceinline__ int line_blocks(long long S, int blocks) { return (int)min((long long)blocks, S); }
+// Block c's range of the line.
+__device__ __forceinline__ long long range_start(long long S, int blocks, int c) { return S * c / blocks; }
+// The block that holds step s.
+__device__ __forceinline__ int block_of(long long S, int blocks, long long s) { return (int)(((s + 1) * blocks - 1) / S); }
+
+// Walks a block's range job by job.  Every thread of a warp holds the same state.
+struct PrefixWalk {
+  long long S, at, end;   // line length; next step and end of the range
+  long long lo;           // start of the range
+  int p;                  // current group
+  long long gbase;        // its first step
+  PrefixGroup g;
+  // current segment
+  int head, tile, k0, k1; // KV head, tile, steps [k0, k1) of the job
+  int slot;               // -1: the whole job; else the part's slot (2 block + 0 or 1)
+
+  // Warp-wide.  `record`: this warp writes the groups' first steps and reports bad inputs.
+  __device__ void init(const PrefixParams& prm, int block, bool record) {
+    const int lane = threadIdx.x & 31;
+    long long total = 0;
+    for (int i0 = 0; i0 < prm.P; i0 += 32) {
+      const int i = i0 + lane;
+      long long s = 0;
+      if (i < prm.P) {
+        s = group_steps(prm, prefix_group(prm, i));
+        if (record) {
+          const int n = __ldg(prm.prefix_len + i);
+          bool bad = n < 0 || n > prm.N_cap;
+          if (prm.row_start) {
+            const int a = __ldg(prm.row_start + i), b = __ldg(prm.row_start + i + 1);
+            bad = bad || a < 0 || b < a || b > prm.R;
+          }
+          if (bad) report_error(prm.err, ERR_BAD_INDEX);
+        }
+      }
+      long long x = s;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (record && i < prm.P) prm.base[i] = total + x - s;
+      total += __shfl_sync(0xffffffffu, x, 31);
+    }
+    if (record && lane == 0) prm.base[prm.P] = total;
+    S = total;
+    const int blocks = line_blocks(S, prm.blocks);
+    p = 0;
+    lo = at = end = gbase = 0;
+    if (block >= blocks) return;
+    lo = at = range_start(S, blocks, block);
+    end = range_start(S, blocks, block + 1);
+    // the group that holds step `at`
+    long long before = 0;
+    for (int i0 = 0; i0 < prm.P; i0 += 32) {
+      const int i = i0 + lane;
+      const long long s = i < prm.P ? group_steps(prm, prefix_group(prm, i)) : 0;
+      long long x = s;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, before + x > at);
+      if (past) {
+        const int l = __ffs(past) - 1;
+        p = i0 + l;
+        gbase = before + __shfl_sync(0xffffffffu, x - s, l);
+        break;
+      }
+      before += __shfl_sync(0xffffffffu, x, 31);
+    }
+    g = prefix_group(prm, p);
+  }
+
+  // Moves to the next segment; false at the end of the range.
+  __device__ bool next(const PrefixParams& prm, int block) {
+    if (at >= end) return false;
+    while (at >= gbase + group_steps(prm, g)) {
+      gbase += group_steps(prm, g);
+      g = prefix_group(prm, ++p);  // at < end <= S: a later group holds it
+    }
+    const long long off = at - gbase;
+    const int job = (int)(off / g.steps);
+    head = job / g.tiles;
+    tile = job - head * g.tiles;
+    k0 = (int)(off - (long long)job * g.steps);
+    k1 = (int)min((long long)g.steps, k0 + (end - at));
+    const bool first = at == lo;
+    slot = (k0 == 0 && k1 == g.steps) ? -1 : 2 * block + (first ? 0 : 1);
+    at += k1 - k0;
+    return true;
+  }
+};
+
+// One (row, head): joins its prefix part (maximum m and sum l, log2 units; acc relative to m) with
+// what the row attended on its own.  Returns the factors of acc and of the own output, and the
+// joined log-sum-exp (natural).  Rows that nothing was attended for: both 0, -inf.  Without an
+// own part (own = -inf) its factor is 0 whatever the prefix part holds, NaN included.
+__device__ __forceinline__ void join_own(float m, float l, float own, float& f_acc, float& f_own, float& lse) {
+  // prefix part: weight l at scale 2^m; own part: weight 1 at scale 2^(own log2 e)
+  const float mo = own * LOG2E;
+  float M = fmaxf(m, mo);
+  if (M == NEG_INF) M = 0.f;
+  const float a = fast_exp2(m - M), b = own == NEG_INF ? 0.f : fast_exp2(mo - M);
+  const float t = l * a + b;
+  f_acc = t == 0.f ? 0.f : a / t;
+  f_own = b == 0.f ? 0.f : b / t;
+  lse = t == 0.f ? NEG_INF : (M + log2f(t)) * LN2;
+}
+
+}  // namespace pisa

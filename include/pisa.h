@@ -256,6 +256,91 @@ PISA_API pisa_status pisa_decode_step_ws(const uint16_t* q, const uint16_t* k, c
                                          int32_t* idx_out, void* ws, size_t ws_bytes, pisa_shape shape,
                                          pisa_params params, pisa_stream stream);
 
+/* ---- 8-bit key/value cache ------------------------------------------------------------ */
+
+/* A decode cache in half the bytes of bf16 (the paper has no counterpart; it reads raw bf16
+ * keys).  A row x of d values (one token of one KV head) is held as int8 codes and one fp32
+ * scale:  a = max |x_i|,  scale = a / 127 (rounded to nearest),  code_i = sign(x_i)
+ * floor(127 |x_i| / a + 1/2), computed exactly (halves away from zero).  A row of zeros has scale
+ * and codes 0; a row that holds an infinity or a NaN has codes 0 and scale NaN, so that it
+ * reads back as NaN.  What a row reads back as is bf16(code * scale), both roundings to nearest.
+ *   Kq, Vq            [B][H_kv][N_cap][d] int8;   k_scale, v_scale [B][H_kv][N_cap] fp32.
+ * Bases are 16-byte aligned, as everywhere (int32 arrays and LSE: 4-byte aligned).  No argument
+ * may overlap another unless this says so. */
+
+/* Writes shape.N = T new rows of every sequence into the caches at rows seq_len[b] + t.
+ *   k, v     [B][H_kv][T][d] bf16 (the decode step's [B][H_kv][d] for T = 1).
+ *   seq_len  [B] int32 (device): rows already in the cache; not changed by the call.
+ *   new_len  [B] int32 (device), nullable: rows of sequence b in use, 0 .. T (NULL: T).  Rows
+ *            t >= new_len[b] are neither read nor written anywhere.
+ *   k_out, v_out  [B][H_kv][T][d] bf16, each nullable: the values the cache now holds for the rows
+ *            (what pisa_cache_read gives), for attending over them or building the pyramid from
+ *            them before they are read back.  k_out = k and v_out = v are allowed.
+ * A sequence whose seq_len or new_len is negative, whose new_len exceeds T or whose rows do not
+ * fit below N_cap is left as it is, and PISA_ERR_BAD_INDEX is flagged.  shape.H_q is ignored. */
+PISA_API pisa_status pisa_cache_write(const uint16_t* k, const uint16_t* v, int8_t* Kq, int8_t* Vq, float* k_scale,
+                                      float* v_scale, const int32_t* seq_len, const int32_t* new_len, uint16_t* k_out,
+                                      uint16_t* v_out, pisa_shape shape, pisa_stream stream);
+
+/* Reads rows start[b] .. start[b] + len[b] - 1 of every sequence back as bf16, into rows
+ * 0 .. len[b] - 1 of k_out, v_out [B][H_kv][T][d], T = shape.N; later rows are left as they are.
+ * start and len are [B] int32 on the device, each nullable (0 and T).  k_out or v_out may be NULL
+ * (not both): that side is not read, and its cache and scales may be NULL too.  A sequence whose
+ * range is negative, longer than T or not inside N_cap is skipped and flags PISA_ERR_BAD_INDEX. */
+PISA_API pisa_status pisa_cache_read(const int8_t* Kq, const int8_t* Vq, const float* k_scale, const float* v_scale,
+                                     const int32_t* start, const int32_t* len, uint16_t* k_out, uint16_t* v_out,
+                                     pisa_shape shape, pisa_stream stream);
+
+/* Attention of shape.N = T new tokens of every sequence over selected blocks of the 8-bit cache
+ * (step 4 over idx, reading codes): query t of sequence b stands at position seq_len[b] + t and
+ * sees the keys at or before it of the blocks in its list,
+ *   z_c = scale k_scale_c (q . Kq_c),  o = sum_c softmax(z)_c v_scale_c Vq_c,  LSE = log sum_c exp z_c.
+ * The new tokens' own rows are in the cache already (pisa_cache_write with the same seq_len), so
+ * T > 1 tokens (drafted ones, a chunk of a prompt) see each other as far as their lists name
+ * their blocks.  The lists may come from the step that attended last, another layer or a rule of the
+ * caller's own; a block listed twice counts twice.
+ *   q, O [B][T][H_q][d] bf16;  idx [B][H_kv][T][K] int32, entries < 0 skipped, entries >=
+ *   ceil(N_cap/C) skipped and flagged (PISA_ERR_BAD_INDEX);  LSE [B][T][H_q] fp32, nullable.
+ *   new_len as for pisa_cache_write: rows t >= new_len[b] of O and LSE are left as they are.
+ * A row with no visible key gives O = 0 and LSE = -inf; a sequence whose lengths do not fit is
+ * skipped and flagged.  Causal only; params.K, scale and causal are used.  No scratch memory. */
+PISA_API pisa_status pisa_sparse_attn_cache(const uint16_t* q, const int8_t* Kq, const int8_t* Vq, const float* k_scale,
+                                            const float* v_scale, const int32_t* idx, const int32_t* seq_len,
+                                            const int32_t* new_len, uint16_t* O, float* LSE, pisa_shape shape,
+                                            pisa_params params, pisa_stream stream);
+
+/* ---- attention over a shared prefix ------------------------------------------------------ */
+
+/* Attention of R query rows in n groups, the rows of group p over every key of prefix p: a batch
+ * whose sequences begin alike reads the common part once (the paper has no counterpart).  Dense:
+ * with many rows to a key the products are cheap beside a selection of each row's own.  What a row
+ * attended elsewhere (its own tokens: pisa_decode_step, pisa_sparse_attn_cache) is joined by
+ * log-sum-exp, so the result is that of one softmax over both:
+ *   lse = log(e^lse_prefix + e^lse_own),  o = e^(lse_prefix - lse) o_prefix + e^(lse_own - lse) o_own.
+ * shape.B = n prefixes, shape.N = R rows, shape.N_cap = rows of each prefix cache; params.scale is
+ * used, params.causal must be 0 (every row sees the whole prefix).
+ *   q, o        [R][H_q][d] bf16: one row a token; several tokens of a sequence are several rows.
+ *   Kp, Vp      [n][H_kv][N_cap][d]: bf16 with k_scale = v_scale = NULL, or int8 codes with
+ *               k_scale, v_scale [n][H_kv][N_cap] fp32 (the 8-bit cache above).
+ *   prefix_len  [n] int32 (device), 0 .. N_cap: keys past it are not used, whatever they hold.
+ *   row_start   [n + 1] int32 (device), not decreasing, within 0 .. R: rows row_start[p] ..
+ *               row_start[p+1] - 1 are group p's; rows before the first and behind the last
+ *               are left as they are.  NULL with n = 1: all rows.
+ *   o_own [R][H_q][d] bf16, lse_own [R][H_q] fp32: both or neither.  o = o_own and lse = lse_own
+ *               are allowed.  A row with lse_own = -inf takes nothing of o_own.
+ *   lse         [R][H_q] fp32 out, nullable (natural log, of the joined result).
+ *   ws          device scratch, 256-B aligned, ws_bytes >= pisa_prefix_attn_workspace_bytes();
+ *               not to be used by other work until the call has run (two captured graphs that
+ *               may run at once need one each).
+ * A row that sees nothing gives o = 0 and lse = -inf.  Lengths or bounds out of range are brought
+ * into range and flagged (PISA_ERR_BAD_INDEX).  Results are the same in every run. */
+/* 0 for arguments pisa_prefix_attn refuses. */
+PISA_API size_t pisa_prefix_attn_workspace_bytes(pisa_shape shape, pisa_params params);
+PISA_API pisa_status pisa_prefix_attn(const uint16_t* q, const void* Kp, const void* Vp, const float* k_scale,
+                                      const float* v_scale, const int32_t* prefix_len, const int32_t* row_start,
+                                      const uint16_t* o_own, const float* lse_own, uint16_t* o, float* lse, void* ws,
+                                      size_t ws_bytes, pisa_shape shape, pisa_params params, pisa_stream stream);
+
 /* ---- status ---------------------------------------------------------------------------- */
 
 PISA_API const char* pisa_status_string(pisa_status status);
@@ -270,7 +355,7 @@ PISA_API pisa_status pisa_get_last_device_error(pisa_stream stream);
 /* While enabled, every compute entry point records a CUDA event on its stream when its work
  * starts and after each of its kernel phases: pyramid, Stage 1 (with the clustering histogram),
  * clustering, Stage 2 leaf LSE, top-K, sparse attention, BSA selection, decode step, attention
- * backward.  The records cost a few microseconds per call and add no ordering beyond the
+ * backward, 8-bit cache write, read and sparse attention, prefix attention.  The records cost a few microseconds per call and add no ordering beyond the
  * stream's own.  Events are recorded on the device current at the call.
  * pisa_phase_timing(1) enables recording and clears the current device's totals; (0) disables
  * it (the totals are kept).  Returns PISA_ERR_CUDA if resolving earlier records failed.
