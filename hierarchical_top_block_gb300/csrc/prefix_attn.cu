@@ -4,7 +4,8 @@
 //
 // Reading the prefix once for the whole group is the point: G_Q n_p query rows share each key, so
 // with few rows the reads bound the work, and with many the products do (4 d operations a row
-// and key).  This kernel: 16 rows a tile on mma.sync with the cache read straight into registers.
+// and key).  Few rows: the kernel here, 16 rows a tile on mma.sync with the cache read straight into
+// registers.  Many: prefix_tc.cu.
 #include <algorithm>
 
 #include "cache_attn.cuh"
@@ -161,8 +162,22 @@ __global__ void __launch_bounds__(THREADS) prefix_join_kernel(PrefixParams p) {
   }
 }
 
-constexpr int MAX_BLOCKS = 304;  // two a SM of this GPU: the scratch does not depend on the device at hand
-int prefix_rows(const Problem&) { return FEW_ROWS; }
+constexpr int MAX_SMS = 152;  // this GPU's: the scratch does not depend on the device at hand
+
+// Which kernel, by the query rows a group has on average (the groups' own sizes are on the device;
+// either kernel takes any).
+struct Plan {
+  bool tc;
+  int rows, blocks_per_sm;
+};
+Plan prefix_plan(const Problem& p) {
+#ifdef PISA_FORCE
+  const bool tc = PISA_FORCE;
+#else
+  const bool tc = (long long)p.N * p.GQ > 16LL * p.B;
+#endif
+  return tc ? Plan{true, TC_ROWS, 1} : Plan{false, FEW_ROWS, 2};
+}
 
 template <int D, int BITS>
 cudaError_t launch_few(const PrefixParams& p, cudaStream_t s) {
@@ -179,7 +194,8 @@ size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 }  // namespace
 
 size_t prefix_workspace_bytes(const Problem& p) {
-  const size_t parts = (size_t)2 * MAX_BLOCKS * prefix_rows(p);
+  const Plan plan = prefix_plan(p);
+  const size_t parts = (size_t)2 * plan.blocks_per_sm * MAX_SMS * plan.rows;
   return up256(parts * p.d * 4) + up256(parts * 8) + up256((size_t)(p.B + 1) * 8);
 }
 
@@ -207,8 +223,9 @@ cudaError_t launch_prefix_attn(const uint16_t* q, const void* Kp, const void* Vp
   p.N_cap = pr.N_cap;
   p.sl2 = pr.scale * LOG2E;
   p.err = err;
-  p.rows = prefix_rows(pr);
-  p.blocks = std::min(MAX_BLOCKS, 2 * num_sms);
+  const Plan plan = prefix_plan(pr);
+  p.rows = plan.rows;
+  p.blocks = plan.blocks_per_sm * std::min(MAX_SMS, num_sms);
   const size_t parts = (size_t)2 * p.blocks * p.rows;
   uint8_t* w = static_cast<uint8_t*>(ws);
   p.part_o = reinterpret_cast<float*>(w);
@@ -217,7 +234,9 @@ cudaError_t launch_prefix_attn(const uint16_t* q, const void* Kp, const void* Vp
   w += up256(parts * 8);
   p.base = reinterpret_cast<long long*>(w);
   cudaError_t e;
-  if (pr.d == 128)
+  if (plan.tc)
+    e = launch_prefix_tc(p, pr.d, s);
+  else if (pr.d == 128)
     e = k_scale ? launch_few<128, 8>(p, s) : launch_few<128, 16>(p, s);
   else
     e = k_scale ? launch_few<64, 8>(p, s) : launch_few<64, 16>(p, s);

@@ -172,4 +172,8 @@ __device__ __forceinline__ void join_own(float m, float l, float own, float& f_a
   lse = t == 0.f ? NEG_INF : (M + log2f(t)) * LN2;
 }
 
+// The tensor-core kernel (prefix_tc.cu): tiles of TC_ROWS rows, one block a SM.
+constexpr int TC_ROWS = 256;
+cudaError_t launch_prefix_tc(const PrefixParams& p, int d, cudaStream_t s);
+
 }  // namespace pisa
