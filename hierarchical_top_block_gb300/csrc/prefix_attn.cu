@@ -82,15 +82,18 @@ __global__ void __launch_bounds__(THREADS) prefix_few_kernel(PrefixParams p) {
   }
 }
 
-// Joins the parts of every job that spans blocks: one warp a (row, query head).
+// Joins the parts of every job that spans blocks: a block a (row, query head).  A part is D floats,
+// one 16-byte (8-byte) piece a lane; the block's four warps take the parts in turn, BATCH of them
+// in flight, each warp with its own running maximum, and meet in shared memory.
 template <int D>
 __global__ void __launch_bounds__(THREADS) prefix_join_kernel(PrefixParams p) {
   pdl_wait();
-  constexpr int V = D / 32;  // columns a lane
-  const int lane = threadIdx.x & 31;
-  const long long S = p.base[p.P];
-  for (long long i = (long long)blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5); i < (long long)p.R * p.H_q;
-       i += (long long)gridDim.x * (THREADS / 32)) {
+  constexpr int V = D / 32, BATCH = 8, WARPS = THREADS / 32;
+  __shared__ float so[WARPS][D];
+  __shared__ float2 sml[WARPS];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long len = range_len(p.base[p.P], p.blocks);
+  for (long long i = blockIdx.x; i < (long long)p.R * p.H_q; i += gridDim.x) {
     const int row = (int)(i / p.H_q), hq = (int)(i - (long long)row * p.H_q);
     int gp = 0;
     if (p.row_start) {
@@ -108,57 +111,90 @@ __global__ void __launch_bounds__(THREADS) prefix_join_kernel(PrefixParams p) {
     const PrefixGroup g = prefix_group(p, gp);
     if (row < g.first || row >= g.first + g.n) continue;
     const int head = hq / p.GQ;
-    const int m = (row - g.first) * p.GQ + (hq - head * p.GQ);
-    const int tile = m / p.rows, local = m - tile * p.rows;
+    const int mrow = (row - g.first) * p.GQ + (hq - head * p.GQ);
+    const int tile = mrow / p.rows, local = mrow - tile * p.rows;
     const long long s0 = p.base[gp] + ((long long)head * g.tiles + tile) * g.steps, s1 = s0 + g.steps;
-    const int blocks = line_blocks(S, p.blocks);
-    const int c0 = block_of(S, blocks, s0), c1 = block_of(S, blocks, s1 - 1);
+    const int c0 = block_of(s0, len), c1 = block_of(s1 - 1, len);
     if (c0 == c1) continue;  // finished by its block
-    const int slot0 = 2 * c0 + (range_start(S, blocks, c0) == s0 ? 0 : 1);
-    float M = NEG_INF;
-    for (int c = c0; c <= c1; ++c)
-      M = fmaxf(M, p.part_ml[(size_t)(c == c0 ? slot0 : 2 * c) * p.rows + local].x);
-    float l = 0.f, acc[V];
+    const int slot0 = 2 * c0 + (len * c0 == s0 ? 0 : 1);
+    const float own = p.lse_own ? p.lse_own[i] : NEG_INF;
+    float m = NEG_INF, l = 0.f, acc[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) acc[j] = 0.f;
-    for (int c = c0; c <= c1; ++c) {
-      const size_t at = (size_t)(c == c0 ? slot0 : 2 * c) * p.rows + local;
-      const float2 ml = p.part_ml[at];
-      if (ml.x == NEG_INF) {
-        l += ml.y;  // 0, or NaN where every logit was
-        continue;
-      }
-      const float f = fast_exp2(ml.x - M);
-      l += ml.y * f;
-      const float* src = p.part_o + at * D + lane * V;
-      if constexpr (V == 4) {
-        const float4 x = *reinterpret_cast<const float4*>(src);
-        acc[0] += x.x * f;
-        acc[1] += x.y * f;
-        acc[2] += x.z * f;
-        acc[3] += x.w * f;
-      } else {
-        const float2 x = *reinterpret_cast<const float2*>(src);
-        acc[0] += x.x * f;
-        acc[1] += x.y * f;
-      }
-    }
-    const float own = p.lse_own ? p.lse_own[i] : NEG_INF;
-    float fa, fo, lse;
-    join_own(M, l, own, fa, fo, lse);
-    const size_t at = (size_t)i * D + lane * V;
-    float v[V];
+    for (int c = c0 + warp; c <= c1; c += WARPS * BATCH) {
+      float2 ml[BATCH];
+      float x[BATCH][V];
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      v[j] = fa == 0.f ? 0.f : acc[j] * fa;
-      if (p.o_own && fo != 0.f) v[j] += bf16_to_f32(p.o_own[at + j]) * fo;
+      for (int u = 0; u < BATCH; ++u) {
+        const int cc = c + u * WARPS;
+        const bool in = cc <= c1;
+        const size_t at = (size_t)(cc == c0 || !in ? slot0 : 2 * cc) * p.rows + local;
+        ml[u] = in ? p.part_ml[at] : make_float2(NEG_INF, 0.f);
+        const float* src = p.part_o + at * D + lane * V;
+        if constexpr (V == 4)
+          *reinterpret_cast<float4*>(x[u]) = *reinterpret_cast<const float4*>(src);
+        else
+          *reinterpret_cast<float2*>(x[u]) = *reinterpret_cast<const float2*>(src);
+      }
+      float top = m;
+#pragma unroll
+      for (int u = 0; u < BATCH; ++u) top = fmaxf(top, ml[u].x);
+      const float f0 = m == NEG_INF ? 0.f : fast_exp2(m - top);
+      if (m != NEG_INF) l *= f0;
+      m = top;
+#pragma unroll
+      for (int j = 0; j < V; ++j) acc[j] *= f0;
+#pragma unroll
+      for (int u = 0; u < BATCH; ++u) {
+        if (ml[u].x == NEG_INF) {
+          l += ml[u].y;  // 0, or NaN where every logit was
+          continue;
+        }
+        const float f = fast_exp2(ml[u].x - m);
+        l += ml[u].y * f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) acc[j] += x[u][j] * f;
+      }
     }
-    if constexpr (V == 4)
-      *reinterpret_cast<uint2*>(p.o + at) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-    else
-      *reinterpret_cast<uint32_t*>(p.o + at) = pack_bf16x2(v[0], v[1]);
-    __syncwarp();  // lse may be lse_own: every lane has read it
-    if (p.lse && lane == 0) p.lse[i] = lse;
+#pragma unroll
+    for (int j = 0; j < V; ++j) so[warp][lane * V + j] = acc[j];
+    if (lane == 0) sml[warp] = make_float2(m, l);
+    __syncthreads();
+    if (warp == 0) {
+      m = NEG_INF;
+#pragma unroll
+      for (int u = 0; u < WARPS; ++u) m = fmaxf(m, sml[u].x);
+      l = 0.f;
+#pragma unroll
+      for (int j = 0; j < V; ++j) acc[j] = 0.f;
+#pragma unroll
+      for (int u = 0; u < WARPS; ++u) {
+        const float2 ml = sml[u];
+        if (ml.x == NEG_INF) {
+          l += ml.y;
+          continue;
+        }
+        const float f = fast_exp2(ml.x - m);
+        l += ml.y * f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) acc[j] += so[u][lane * V + j] * f;
+      }
+      float fa, fo, lse;
+      join_own(m, l, own, fa, fo, lse);
+      const size_t at = (size_t)i * D + lane * V;
+      float v[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        v[j] = fa == 0.f ? 0.f : acc[j] * fa;
+        if (p.o_own && fo != 0.f) v[j] += bf16_to_f32(p.o_own[at + j]) * fo;
+      }
+      if constexpr (V == 4)
+        *reinterpret_cast<uint2*>(p.o + at) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+      else
+        *reinterpret_cast<uint32_t*>(p.o + at) = pack_bf16x2(v[0], v[1]);
+      if (p.lse && lane == 0) p.lse[i] = lse;  // lse may be lse_own: read above, before the block met
+    }
+    __syncthreads();
   }
 }
 
@@ -168,7 +204,7 @@ constexpr int MAX_SMS = 152;  // this GPU's: the scratch does not depend on the 
 // either kernel takes any).
 struct Plan {
   bool tc;
-  int rows, blocks_per_sm;
+  int rows, blocks;
 };
 Plan prefix_plan(const Problem& p) {
 #ifdef PISA_FORCE
@@ -176,7 +212,7 @@ Plan prefix_plan(const Problem& p) {
 #else
   const bool tc = (long long)p.N * p.GQ > 16LL * p.B;
 #endif
-  return tc ? Plan{true, TC_ROWS, 1} : Plan{false, FEW_ROWS, 2};
+  return tc ? Plan{true, TC_ROWS, MAX_SMS / 2} : Plan{false, FEW_ROWS, 2 * MAX_SMS};
 }
 
 template <int D, int BITS>
@@ -195,7 +231,7 @@ size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 size_t prefix_workspace_bytes(const Problem& p) {
   const Plan plan = prefix_plan(p);
-  const size_t parts = (size_t)2 * plan.blocks_per_sm * MAX_SMS * plan.rows;
+  const size_t parts = (size_t)2 * plan.blocks * plan.rows;
   return up256(parts * p.d * 4) + up256(parts * 8) + up256((size_t)(p.B + 1) * 8);
 }
 
@@ -225,7 +261,7 @@ cudaError_t launch_prefix_attn(const uint16_t* q, const void* Kp, const void* Vp
   p.err = err;
   const Plan plan = prefix_plan(pr);
   p.rows = plan.rows;
-  p.blocks = plan.blocks_per_sm * std::min(MAX_SMS, num_sms);
+  p.blocks = plan.blocks;
   const size_t parts = (size_t)2 * p.blocks * p.rows;
   uint8_t* w = static_cast<uint8_t*>(ws);
   p.part_o = reinterpret_cast<float*>(w);
@@ -241,8 +277,7 @@ cudaError_t launch_prefix_attn(const uint16_t* q, const void* Kp, const void* Vp
   else
     e = k_scale ? launch_few<64, 8>(p, s) : launch_few<64, 16>(p, s);
   if (e != cudaSuccess) return e;
-  const long long warps = (long long)p.R * p.H_q;
-  const unsigned grid = (unsigned)std::min<long long>((warps + 3) / 4, (long long)num_sms * 16);
+  const unsigned grid = (unsigned)std::min<long long>((long long)p.R * p.H_q, (long long)num_sms * 16);
   return pr.d == 128 ? launch_pdl(prefix_join_kernel<128>, dim3(grid), dim3(THREADS), 0, s, p)
                      : launch_pdl(prefix_join_kernel<64>, dim3(grid), dim3(THREADS), 0, s, p);
 }

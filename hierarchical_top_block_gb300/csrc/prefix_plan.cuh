@@ -58,13 +58,15 @@ __device__ __forceinline__ long long group_steps(const PrefixParams& p, const Pr
   return (long long)p.H_kv * g.tiles * g.steps;
 }
 
-// Blocks the line of S steps is divided over: every one of them gets a step at least, so a job's
-// parts are in consecutive blocks.
-__device__ __forceinline__ int line_blocks(long long S, int blocks) { return (int)min((long long)blocks, S); }
-// Block c's range of the line.
-__device__ __forceinline__ long long range_start(long long S, int blocks, int c) { return S * c / blocks; }
+// Block c's range of the line of S steps: [c len, (c + 1) len).  Every block up to the last in use
+// has a step, so a job's parts are in consecutive blocks.
+__device__ __forceinline__ long long range_len(long long S, int blocks) {
+  return (S >> 31) ? (S + blocks - 1) / blocks : (long long)(((uint32_t)S + (uint32_t)blocks - 1) / (uint32_t)blocks);
+}
 // The block that holds step s.
-__device__ __forceinline__ int block_of(long long S, int blocks, long long s) { return (int)(((s + 1) * blocks - 1) / S); }
+__device__ __forceinline__ int block_of(long long s, long long len) {
+  return (s >> 32) || (len >> 32) ? (int)(s / len) : (int)((uint32_t)s / (uint32_t)len);
+}
 
 // Walks a block's range job by job.  Every thread of a warp holds the same state.
 struct PrefixWalk {
@@ -107,12 +109,12 @@ struct PrefixWalk {
     }
     if (record && lane == 0) prm.base[prm.P] = total;
     S = total;
-    const int blocks = line_blocks(S, prm.blocks);
+    const long long len = range_len(S, prm.blocks);
     p = 0;
-    lo = at = end = gbase = 0;
-    if (block >= blocks) return;
-    lo = at = range_start(S, blocks, block);
-    end = range_start(S, blocks, block + 1);
+    gbase = 0;
+    lo = at = min(S, len * block);
+    end = min(S, len * (block + 1));
+    if (at >= end) return;
     // the group that holds step `at`
     long long before = 0;
     for (int i0 = 0; i0 < prm.P; i0 += 32) {
@@ -172,8 +174,9 @@ __device__ __forceinline__ void join_own(float m, float l, float own, float& f_a
   lse = t == 0.f ? NEG_INF : (M + log2f(t)) * LN2;
 }
 
-// The tensor-core kernel (prefix_tc.cu): tiles of TC_ROWS rows, one block a SM.
-constexpr int TC_ROWS = 256;
+// The tensor-core kernel (prefix_tc.cu): tiles of TC_ROWS rows, a block here is a pair of CTAs on
+// two SMs.
+constexpr int TC_ROWS = 512;
 cudaError_t launch_prefix_tc(const PrefixParams& p, int d, cudaStream_t s);
 
 }  // namespace pisa

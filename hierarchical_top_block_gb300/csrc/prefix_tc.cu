@@ -1,24 +1,33 @@
-// Attention over shared prefixes on the tensor cores of the 5th generation: 256 query rows of one
-// (group, KV head) a tile, 128 keys a step.
+// Attention over shared prefixes on the tensor cores of the 5th generation: up to 512 query rows of
+// one (group, KV head) a tile, 128 keys a step, by a pair of CTAs (a cluster on two SMs).
 //
 //   S = Q K^T (fp32 in tensor memory), P = 2^(S scale log2 e - m) as bf16 back into tensor memory
 //   over S, O += P V in tensor memory, l = sum of the unrounded P
 //
 // m is a row's reference, not its running maximum: it is raised, and O multiplied by 2^(old - new),
 // only when the maximum has grown by more than 2^8 past it (P stays below 2^8, far from the end of
-// bf16's and of fp32's range, and the final division by l is exact whatever m is).  With the usual logits that
-// happens in a job's first steps alone, so O is left where the MMA accumulates it.  P is rounded
-// to bf16 (half a step, 2^-8 of each weight, the size of the output's own rounding).
+// bf16's and of fp32's range, and the division by l at the end is exact whatever m is).  With the
+// usual logits that happens in a job's first steps alone, so O is left where the MMA accumulates it.
+// P is rounded to bf16 (half a step, 2^-8 of each weight, the size of the output's own rounding).
+//
+// Why pairs: an MMA of 128 x 128 x 16 reads 8 KB of shared memory in 64 cycles, all that an SM's
+// shared memory gives, beside the copies that write the next tiles.  Over a pair (256 x 128 x 16)
+// each SM reads its own 128 rows of A and half of B: 6 KB for the first product, 2 KB for the second
+// (A from tensor memory), and holds, copies and widens half of every K and V tile.
+//
+// Two streams keep the tensor pipe busy while the softmax of the other one runs, a warpgroup a CTA
+// for each.  With more than 256 rows a stream is a half of the rows, and both use the same tiles;
+// with fewer, both streams have all rows, one the even steps and one the odd ones, each with
+// its own m, l and O, which are joined when a job's segment ends.
 //
 // The 8-bit cache: four warps widen the codes to bf16 (exact) into the swizzled tiles that the MMA
 // reads; the key's scale multiplies the logit and the value's scale the weight, both in fp32.
 //
-// Roles: two softmax warpgroups, one for each 128 rows of the tile (a row a thread), so that one
-// tile's softmax runs while the tensor pipe works for the other; a producer warp (TMA); a warp that
-// issues the MMAs; with the 8-bit cache the widening warpgroup.  TMEM: S of half i at 128 i (its first 64
-// columns hold P afterwards), O of half i at 256 + 128 i.  MMAs of one thread run in order, so S(j + 1)
-// of a half is issued right behind its O += P V of step j, which reads P from the same columns.
-// Every wait is bounded.
+// Roles in each CTA: two softmax warpgroups (a row a thread); a producer warp (TMA); a warp that issues
+// the pair's MMAs in the CTA of rank 0 and tells it of the arrived tiles in that of rank 1; with
+// the 8-bit cache the widening warpgroup.  TMEM: S of stream i at 128 i (its first 64 columns hold P
+// afterwards), O of stream i at 256 + 128 i.  The MMAs of one thread run in order, so a stream's next S
+// is issued right behind its O += P V, which reads P from the same columns.  Every wait is bounded.
 #include <algorithm>
 
 #include "cache_attn.cuh"
@@ -29,27 +38,31 @@
 namespace pisa {
 namespace {
 
-constexpr int ROWS = TC_ROWS, HALF = 128, KT = PREFIX_KT;
+constexpr int ROWS = TC_ROWS, KT = PREFIX_KT;
 constexpr float MAX_GROWTH = 8.f;  // log2 units the maximum may pass a row's reference
 
 template <int D, int BITS>
 struct Cfg {
   static constexpr int THREADS = BITS == 8 ? 512 : 384;
   static constexpr int PRODUCER = BITS == 8 ? 12 : 8, ISSUER = PRODUCER + 1;  // warps
-  static constexpr uint32_t QH_BYTES = HALF * D * 2;    // 128 query rows
-  static constexpr uint32_t TILE = KT * D * 2;          // a K or V tile in bf16
-  static constexpr uint32_t RAW = KT * D;               // in codes
-  static constexpr int SLOTS = BITS == 8 ? 3 : 5;       // bf16 tiles: K, V, K, ...
-  static constexpr int RSLOTS = BITS == 8 ? 3 : 0;       // tiles of codes
-  static constexpr size_t SMEM = 1024 + 2 * QH_BYTES + SLOTS * TILE + RSLOTS * RAW;
+  static constexpr uint32_t QT_BYTES = 128 * D * 2;     // a CTA's 128 query rows of a stream
+  static constexpr uint32_t TILE = 64 * D * 2;          // its half of a tile in bf16: 64 keys of K, D / 2 columns of V
+  static constexpr uint32_t RAW = 64 * D;               // in codes
+  static constexpr int SLOTS = BITS == 8 ? 6 : 9;
+  static constexpr int RSLOTS = 6;
+  static constexpr size_t SMEM = 1024 + 2 * QT_BYTES + SLOTS * TILE + (BITS == 8 ? RSLOTS * RAW : 0);
 };
 
+constexpr int SC_SLOTS = 8;
+
 struct Bars {
-  uint64_t q_full, q_empty;
-  uint64_t full[5], empty[5];          // bf16 tiles
-  uint64_t raw_full[4], raw_empty[4];  // tiles of codes
-  uint64_t sc_full[4];                 // a step's scales
+  uint64_t q_full, q_empty, q_peer;
+  uint64_t full[9], empty[9];          // bf16 tiles
+  uint64_t peer[9];                    // the other CTA's half has arrived (rank 0)
+  uint64_t raw_full[6], raw_empty[6];  // tiles of codes
+  uint64_t sc_full[SC_SLOTS];          // a step's scales
   uint64_t s_full[2], p_full[2], o_done[2];
+  uint64_t x_full, x_done;             // the streams' meeting at the end of a segment
   uint64_t drain;
 };
 
@@ -62,130 +75,175 @@ __device__ __forceinline__ void set_regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
 
-// One query row's finished part: to the output (the whole job) or to the block's partial slot.
-template <int D>
-__device__ __forceinline__ void finish_row(const PrefixParams& p, const PrefixWalk& w, int local, uint32_t o_tmem,
-                                           float m, float l, bool live) {
-  size_t orow = 0;
-  float fa = 0.f, fo = 0.f, lse = 0.f;
-  if (live && w.slot < 0) {
-    const int mrow = w.tile * ROWS + local, tok = mrow / p.GQ;
-    orow = (size_t)(w.g.first + tok) * p.H_q + (size_t)w.head * p.GQ + (mrow - tok * p.GQ);
-    join_own(m, l, p.lse_own ? p.lse_own[orow] : NEG_INF, fa, fo, lse);
-    if (p.lse) p.lse[orow] = lse;
+// A segment's streams: by rows (`lag` 1: both use every tile) or by steps (`lag` 2: stream = step
+// mod 2).  The tiles' order is that of their use: K 0 .. lag - 1, then V j and K j + lag.
+struct Segment {
+  int rows, nk, lag;
+  __device__ __forceinline__ Segment(const PrefixParams& p, const PrefixWalk& w) {
+    rows = min(ROWS, w.g.n * p.GQ - w.tile * ROWS);
+    nk = w.k1 - w.k0;
+    lag = rows > ROWS / 2 ? 1 : 2;
   }
-  float* dst = p.part_o + ((size_t)(w.slot < 0 ? 0 : w.slot) * ROWS + local) * D;
-  if (live && w.slot >= 0) p.part_ml[(size_t)w.slot * ROWS + local] = make_float2(m, l);
-#pragma unroll 1
-  for (int c = 0; c < D; c += 32) {
-    uint32_t r[32];
-    tmem_ld32(o_tmem + c, r);
-    tmem_wait_ld();
-    if (!live) continue;
-    if (w.slot < 0) {
-#pragma unroll
-      for (int j = 0; j < 32; j += 8) {
-        uint4 own = make_uint4(0, 0, 0, 0);
-        if (p.o_own && fo != 0.f) own = *reinterpret_cast<const uint4*>(p.o_own + orow * D + c + j);
-        const uint32_t ow[4] = {own.x, own.y, own.z, own.w};
-        uint32_t v[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float a = fa == 0.f ? 0.f : __uint_as_float(r[j + 2 * e]) * fa;
-          float b = fa == 0.f ? 0.f : __uint_as_float(r[j + 2 * e + 1]) * fa;
-          if (p.o_own && fo != 0.f) {
-            a += bf16_lo(ow[e]) * fo;
-            b += bf16_hi(ow[e]) * fo;
-          }
-          v[e] = pack_bf16x2(a, b);
-        }
-        *reinterpret_cast<uint4*>(p.o + orow * D + c + j) = make_uint4(v[0], v[1], v[2], v[3]);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 32; j += 4)
-        *reinterpret_cast<uint4*>(dst + c + j) = make_uint4(r[j], r[j + 1], r[j + 2], r[j + 3]);
+  __device__ __forceinline__ int tiles() const { return 2 * nk; }
+  // Tile i of the order: returns its step, and whether it is a V.
+  __device__ __forceinline__ int tile(int i, bool& is_v) const {
+    const int head = min(lag, nk), both = 2 * (nk - head);
+    if (i < head) {
+      is_v = false;
+      return i;
     }
+    i -= head;
+    if (i < both) {
+      is_v = (i & 1) == 0;
+      return is_v ? i >> 1 : head + (i >> 1);
+    }
+    is_v = true;
+    return nk - head + (i - both);
+  }
+};
+
+// Where a finished query row goes: the output (the whole job was this segment) or a part's slot.
+struct RowOut {
+  bool live;
+  int slot;
+  size_t orow;
+  float own;         // the row's own log-sum-exp
+  float fa, fo;
+  float* part;
+};
+template <int D>
+__device__ __forceinline__ RowOut row_out(const PrefixParams& p, const PrefixWalk& w, int local, bool live) {
+  RowOut r;
+  r.live = live;
+  r.slot = w.slot;
+  const int mrow = w.tile * ROWS + local, tok = mrow / p.GQ;
+  r.orow = (size_t)(w.g.first + tok) * p.H_q + (size_t)w.head * p.GQ + (mrow - tok * p.GQ);
+  r.own = live && w.slot < 0 && p.lse_own ? p.lse_own[r.orow] : NEG_INF;
+  r.part = p.part_o + ((size_t)(w.slot < 0 ? 0 : w.slot) * ROWS + local) * D;
+  r.fa = r.fo = 0.f;
+  return r;
+}
+// The row's factors, and (stats) its log-sum-exp or maximum and sum.
+__device__ __forceinline__ void put_stats(const PrefixParams& p, RowOut& r, int local, float m, float l, bool stats) {
+  if (!r.live) return;
+  if (r.slot < 0) {
+    float lse;
+    join_own(m, l, r.own, r.fa, r.fo, lse);
+    if (stats && p.lse) p.lse[r.orow] = lse;
+  } else if (stats) {
+    p.part_ml[(size_t)r.slot * ROWS + local] = make_float2(m, l);
+  }
+}
+// 32 columns from c on of the row's output sums, relative to its maximum.
+template <int D>
+__device__ __forceinline__ void put_columns(const PrefixParams& p, const RowOut& r, int c, const uint32_t (&x)[32]) {
+  if (!r.live) return;
+  if (r.slot < 0) {
+#pragma unroll
+    for (int j = 0; j < 32; j += 8) {
+      uint4 own = make_uint4(0, 0, 0, 0);
+      const bool with = p.o_own && r.fo != 0.f;
+      if (with) own = *reinterpret_cast<const uint4*>(p.o_own + r.orow * D + c + j);
+      const uint32_t ow[4] = {own.x, own.y, own.z, own.w};
+      uint32_t v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float a = r.fa == 0.f ? 0.f : __uint_as_float(x[j + 2 * e]) * r.fa;
+        float b = r.fa == 0.f ? 0.f : __uint_as_float(x[j + 2 * e + 1]) * r.fa;
+        if (with) {
+          a += bf16_lo(ow[e]) * r.fo;
+          b += bf16_hi(ow[e]) * r.fo;
+        }
+        v[e] = pack_bf16x2(a, b);
+      }
+      *reinterpret_cast<uint4*>(p.o + r.orow * D + c + j) = make_uint4(v[0], v[1], v[2], v[3]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 32; j += 4)
+      *reinterpret_cast<uint4*>(r.part + c + j) = make_uint4(x[j], x[j + 1], x[j + 2], x[j + 3]);
   }
 }
 
 template <int D, int BITS>
-__global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
     prefix_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
                      const __grid_constant__ CUtensorMap mapV, PrefixParams p) {
   pdl_trigger();
   using C = Cfg<D, BITS>;
-  constexpr int DH = D / 64;  // 64-column halves of a row
+  constexpr int DH = D / 64;  // 64-column pieces of a Q or K row
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t* sQ = smem;
-  uint8_t* sT = sQ + 2 * C::QH_BYTES;
+  uint8_t* sT = sQ + 2 * C::QT_BYTES;
   uint8_t* sR = sT + C::SLOTS * C::TILE;
   __shared__ Bars bar;
-  __shared__ __align__(16) float sc[BITS == 8 ? 4 : 1][2][KT];  // scales of the step: keys', values'
+  __shared__ __align__(16) float sc[BITS == 8 ? SC_SLOTS : 1][2][KT];  // scales of a step: keys', values'
+  __shared__ float2 s_ml[2][128];
   __shared__ uint32_t tmem_base_s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int block = blockIdx.x >> 1;  // the pair
   uint32_t* err = p.err;
 
   if (threadIdx.x == 0) {
     mbar_init(&bar.q_full, 1);
     mbar_init(&bar.q_empty, 1);
+    mbar_init(&bar.q_peer, 1);
     for (int i = 0; i < C::SLOTS; ++i) {
-      mbar_init(&bar.full[i], BITS == 8 ? 4 : 1);
+      mbar_init(&bar.full[i], BITS == 8 ? 8 : 1);  // widened by the warps of both CTAs; or the copy
       mbar_init(&bar.empty[i], 1);
+      mbar_init(&bar.peer[i], 1);
     }
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < C::RSLOTS; ++i) {
       mbar_init(&bar.raw_full[i], 1);
       mbar_init(&bar.raw_empty[i], 4);
-      mbar_init(&bar.sc_full[i], 4);
     }
+    for (int i = 0; i < SC_SLOTS; ++i) mbar_init(&bar.sc_full[i], 4);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.s_full[i], 1);
-      mbar_init(&bar.p_full[i], 4);
+      mbar_init(&bar.p_full[i], 8);  // the warps of both CTAs
       mbar_init(&bar.o_done[i], 1);
     }
+    mbar_init(&bar.x_full, 8);
+    mbar_init(&bar.x_done, 8);
     mbar_init(&bar.drain, 1);
     mbar_fence_init();
   }
-  if (warp == C::ISSUER) {
-    tmem_alloc(&tmem_base_s, 512);
-    tmem_relinquish();
-  }
+  if (warp == C::ISSUER) tmem_alloc_pair(&tmem_base_s, 512);
   __syncthreads();
+  cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem = tmem_base_s;
 
   PrefixWalk w;
-  w.init(p, blockIdx.x, blockIdx.x == 0 && warp == 0);
+  w.init(p, block, blockIdx.x == 0 && warp == 0);
 
   if (warp < 8) {
     // ------------------------------ softmax ------------------------------
     if constexpr (BITS == 8) set_regs_up<184>();
-    const int half = warp >> 2;
-    const int local = half * HALF + (warp & 3) * 32 + lane;  // row in the tile
+    const int h = warp >> 2;                                 // stream
+    const int trow = (warp & 3) * 32 + lane;                 // TMEM lane
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t s_tmem = tmem + lanes + 128 * half, o_tmem = tmem + lanes + 256 + 128 * half;
-    uint32_t it = 0, step0 = 0;  // this half's steps; the block's steps
+    const uint32_t s_tmem = tmem + lanes + 128 * h, o_tmem = tmem + lanes + 256 + 128 * h;
+    uint32_t it[2] = {0, 0}, step0 = 0, meets = 0;           // the streams' steps; all steps
     bool failed = false;
-    while (!failed && w.next(p, blockIdx.x)) {
-      const int rows = min(ROWS, w.g.n * p.GQ - w.tile * ROWS);
-      const int nk = w.k1 - w.k0;
-      if (half * HALF >= rows) {  // the tile has no second half
-        step0 += nk;
-        continue;
-      }
-      const bool live = local < rows, any = half * HALF + (warp & 3) * 32 < rows;
+    while (!failed && w.next(p, block)) {
+      const Segment sg(p, w);
+      const int local = (sg.lag == 1 ? 256 * h : 0) + 128 * (int)rank + trow;  // row in the tile
+      const bool live = local < sg.rows, any = local - lane < sg.rows;
       float m = NEG_INF, top = NEG_INF;  // reference and maximum, log2 units
       unsigned long long l2 = pack_f32x2(0.f, 0.f);
-      for (int j = 0; j < nk; ++j, ++it) {
+      uint32_t n = it[h];
+      for (int j = sg.lag == 1 ? 0 : h; j < sg.nk; j += sg.lag, ++n) {
         const int valid = min(KT, w.g.len - (w.k0 + j) * KT);
         const uint32_t gs = step0 + j;
-        if (!mbar_wait_warp(&bar.s_full[half], it & 1, err)) {
+        if (!mbar_wait_warp(&bar.s_full[h], n & 1, err)) {
           failed = true;
           break;
         }
         if constexpr (BITS == 8) {  // done already (S was formed from the same tile): makes the scales visible
-          if (!mbar_wait_warp(&bar.sc_full[gs & 3], (gs >> 2) & 1, err)) {
+          if (!mbar_wait_warp(&bar.sc_full[gs % SC_SLOTS], (gs / SC_SLOTS) & 1, err)) {
             failed = true;
             break;
           }
@@ -197,7 +255,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
           for (int c = 0; c < KT; c += 32) tmem_ld32(s_tmem + c, *reinterpret_cast<uint32_t(*)[32]>(s + c));
           tmem_wait_ld();
           if constexpr (BITS == 8) {
-            const float4* ks = reinterpret_cast<const float4*>(sc[gs & 3][0]);
+            const float4* ks = reinterpret_cast<const float4*>(sc[gs % SC_SLOTS][0]);
 #pragma unroll
             for (int c = 0; c < KT; c += 4) {
               const float4 f = ks[c / 4];
@@ -228,8 +286,8 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
             float a, b;
             unpack_f32x2(l2, a, b);
             l2 = pack_f32x2(a * f, b * f);
-            if (j > 0) {
-              if (!mbar_wait_warp(&bar.o_done[half], (it - 1) & 1, err)) {
+            if (n != it[h]) {
+              if (!mbar_wait_warp(&bar.o_done[h], (n - 1) & 1, err)) {
                 failed = true;
                 break;
               }
@@ -260,7 +318,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
               unsigned long long xy = pack_f32x2(x, y);
               l2 = add_f32x2(l2, xy);
               if constexpr (BITS == 8) {
-                const float2 f = *reinterpret_cast<const float2*>(&sc[gs & 3][1][c + e]);
+                const float2 f = *reinterpret_cast<const float2*>(&sc[gs % SC_SLOTS][1][c + e]);
                 unpack_f32x2(mul_f32x2(xy, pack_f32x2(f.x, f.y)), x, y);
               }
               pk[e / 2] = pack_bf16x2(x, y);
@@ -271,64 +329,126 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.p_full[half]);
+        if (lane == 0) mbar_arrive_at(&bar.p_full[h], 0);
       }
-      step0 += nk;
+      // the streams' steps of this segment
+      const uint32_t n0 = sg.lag == 1 ? sg.nk : (sg.nk + 1) / 2, n1 = sg.lag == 1 ? sg.nk : sg.nk / 2;
+      it[0] += n0;
+      it[1] += n1;
+      step0 += sg.nk;
       if (failed) break;
-      if (!mbar_wait_warp(&bar.o_done[half], (it - 1) & 1, err)) {
-        failed = true;
-        break;
+      float la, lb;
+      unpack_f32x2(l2, la, lb);
+      float l = la + lb;
+      RowOut out = row_out<D>(p, w, local, live);
+      if (sg.lag == 1) {
+        if (!mbar_wait_warp(&bar.o_done[h], (it[h] - 1) & 1, err)) {
+          failed = true;
+          break;
+        }
+        tc_fence_after();
+        if (any) {
+          put_stats(p, out, local, m, l, true);
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t r[32];
+            tmem_ld32(o_tmem + c, r);
+            tmem_wait_ld();
+            put_columns<D>(p, out, c, r);
+          }
+        }
+        tc_fence_before();
+      } else {
+        // both streams have parts of every row: joined here, half of the columns by each warpgroup
+        if (!mbar_wait_warp(&bar.o_done[0], (it[0] - 1) & 1, err) ||
+            (n1 > 0 && !mbar_wait_warp(&bar.o_done[1], (it[1] - 1) & 1, err))) {
+          failed = true;
+          break;
+        }
+        s_ml[h][trow] = make_float2(m, l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.x_full);
+        if (!mbar_wait_warp(&bar.x_full, meets & 1, err)) {  // (the row's own log-sum-exp has been read by both)
+          failed = true;
+          break;
+        }
+        tc_fence_after();
+        if (any) {
+          const float2 a = s_ml[0][trow], b = s_ml[1][trow];
+          m = fmaxf(a.x, b.x);
+          const float f0 = a.x == NEG_INF ? 0.f : fast_exp2(a.x - m), f1 = b.x == NEG_INF ? 0.f : fast_exp2(b.x - m);
+          l = (a.x == NEG_INF ? a.y : a.y * f0) + (b.x == NEG_INF ? b.y : b.y * f1);
+          put_stats(p, out, local, m, l, h == 0);
+          const uint32_t o0 = tmem + lanes + 256;
+#pragma unroll 1
+          for (int c = h * (D / 2); c < (h + 1) * (D / 2); c += 32) {
+            uint32_t r[32], r1[32];
+            tmem_ld32(o0 + c, r);
+            if (n1 > 0) tmem_ld32(o0 + 128 + c, r1);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              float x = __uint_as_float(r[e]) * f0;
+              if (n1 > 0) x = fmaf(__uint_as_float(r1[e]), f1, x);
+              r[e] = __float_as_uint(x);
+            }
+            put_columns<D>(p, out, c, r);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.x_done);
+        if (!mbar_wait_warp(&bar.x_done, meets & 1, err)) {  // both O have been read: the next segment may write them
+          failed = true;
+          break;
+        }
+        ++meets;
       }
-      tc_fence_after();
-      float a, b;
-      unpack_f32x2(l2, a, b);
-      if (any) finish_row<D>(p, w, local, o_tmem, m, a + b, live);
-      tc_fence_before();
     }
   } else if (warp == C::PRODUCER) {
     // ------------------------------ producer ------------------------------
     if constexpr (BITS == 8) set_regs_down<64>();
-    uint32_t nt = 0, seg = 0;  // tiles (K, V, K, ...) and segments so far
+    constexpr uint32_t N = BITS == 8 ? C::RSLOTS : C::SLOTS;
+    uint32_t nt = 0, seg = 0;  // tiles and segments so far
     bool failed = false;
-    while (!failed && w.next(p, blockIdx.x)) {
-      const int rows = min(ROWS, w.g.n * p.GQ - w.tile * ROWS), halves = rows > HALF ? 2 : 1;
+    while (!failed && w.next(p, block)) {
+      const Segment sg(p, w);
       if (!mbar_wait_warp(&bar.q_empty, (seg & 1) ^ 1, err)) break;
       if (lane == 0) {
-        mbar_arrive_expect_tx(&bar.q_full, halves * C::QH_BYTES);
-        for (int h = 0; h < halves; ++h)
+        const int streams = sg.lag == 1 ? 2 : 1;
+        mbar_arrive_expect_tx(&bar.q_full, streams * C::QT_BYTES);
+        for (int h = 0; h < streams; ++h)
           for (int c = 0; c < DH; ++c)
-            tma_load_4d(sQ + h * C::QH_BYTES + c * (HALF * 128), &mapQ, &bar.q_full, 64 * c, 0, w.head,
-                        w.g.first + (w.tile * ROWS + h * HALF) / p.GQ);
+            tma_load_4d(sQ + h * C::QT_BYTES + c * (128 * 128), &mapQ, &bar.q_full, 64 * c, 0, w.head,
+                        w.g.first + (w.tile * ROWS + h * 256 + (int)rank * 128) / p.GQ);
       }
       ++seg;
       const int ph = w.p * p.H_kv + w.head;
-      for (int j = 0; j < w.k1 - w.k0 && !failed; ++j) {
-        const int key0 = (w.k0 + j) * KT;
-#pragma unroll 1
-        for (int kv = 0; kv < 2; ++kv, ++nt) {
+      for (int i = 0; i < sg.tiles(); ++i, ++nt) {
+        bool is_v;
+        const int key0 = (w.k0 + sg.tile(i, is_v)) * KT;
+        const int st = nt % N;
+        uint64_t* full = BITS == 8 ? &bar.raw_full[st] : &bar.full[st];
+        if (!mbar_wait_warp(BITS == 8 ? &bar.raw_empty[st] : &bar.empty[st], ((nt / N) & 1) ^ 1, err)) {
+          failed = true;
+          break;
+        }
+        if (lane == 0) {
           if constexpr (BITS == 8) {
-            const int st = nt % C::RSLOTS;
-            if (!mbar_wait_warp(&bar.raw_empty[st], ((nt / C::RSLOTS) & 1) ^ 1, err)) {
-              failed = true;
-              break;
-            }
-            if (lane == 0) {
-              // rows past the cache's end are not copied; what the slot holds there is finite, and masked
-              const uint32_t bytes = (uint32_t)min(KT, p.N_cap - key0) * D;
-              mbar_arrive_expect_tx(&bar.raw_full[st], bytes);
-              bulk_load(sR + st * C::RAW, (kv ? p.V : p.K) + ((size_t)ph * p.N_cap + key0) * D, bytes, &bar.raw_full[st]);
-            }
+            mbar_arrive_expect_tx(full, C::RAW);
+            uint8_t* dst = sR + st * C::RAW;
+            if (is_v)  // columns of this CTA, all keys
+              tma_load_3d(dst, &mapV, full, (int)rank * (D / 2), key0, ph);
+            else       // keys of this CTA, all columns
+              tma_load_3d(dst, &mapK, full, 0, key0 + (int)rank * 64, ph);
           } else {
-            const int st = nt % C::SLOTS;
-            if (!mbar_wait_warp(&bar.empty[st], ((nt / C::SLOTS) & 1) ^ 1, err)) {
-              failed = true;
-              break;
-            }
-            if (lane == 0) {
-              mbar_arrive_expect_tx(&bar.full[st], C::TILE);
+            mbar_arrive_expect_tx(full, C::TILE);
+            uint8_t* dst = sT + st * C::TILE;
+            if (is_v)
+              tma_load_3d(dst, &mapV, full, (int)rank * (D / 2), key0, ph);
+            else
               for (int c = 0; c < DH; ++c)
-                tma_load_3d(sT + st * C::TILE + c * (KT * 128), kv ? &mapV : &mapK, &bar.full[st], 64 * c, key0, ph);
-            }
+                tma_load_3d(dst + c * (64 * 128), &mapK, full, 64 * c, key0 + (int)rank * 64, ph);
           }
         }
       }
@@ -336,162 +456,231 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
     // copies still in flight land before shared memory goes away (bounded; at once unless a wait failed)
     if (lane == 0) {
       if (seg > 0) mbar_wait(&bar.q_full, (seg - 1) & 1, err, 100000000ull);
-      constexpr uint32_t N = BITS == 8 ? C::RSLOTS : C::SLOTS;
       for (uint32_t u = nt > N ? nt - N : 0; u < nt; ++u)
         mbar_wait(BITS == 8 ? &bar.raw_full[u % N] : &bar.full[u % N], (u / N) & 1, err, 100000000ull);
     }
     __syncwarp();
   } else if (warp == C::ISSUER) {
-    // ------------------------------ MMAs ------------------------------
     if constexpr (BITS == 8) set_regs_down<64>();
-    constexpr uint32_t id_qk = idesc_bf16_f32(HALF, KT);
-    constexpr uint32_t id_pv = idesc_bf16_f32(HALF, D) | (1u << 16);  // V: d contiguous, N-major
-    uint32_t gs = 0, seg = 0, it[2] = {0, 0};
-    bool failed = false;
-    auto tile_full = [&](uint32_t n) { return mbar_wait_warp(&bar.full[n % C::SLOTS], (n / C::SLOTS) & 1, err); };
-    auto qk = [&](int h, uint32_t n) {
-      const uint32_t a = smem_u32(sQ) + h * C::QH_BYTES, b = smem_u32(sT) + (n % C::SLOTS) * C::TILE;
-#pragma unroll
-      for (int s = 0; s < D / 16; ++s)
-        umma_bf16(tmem + 128 * h, smem_desc_sw128(a + (s >> 2) * (HALF * 128) + (s & 3) * 32, 16, 1024),
-                  smem_desc_sw128(b + (s >> 2) * (KT * 128) + (s & 3) * 32, 16, 1024), id_qk, s > 0 ? 1u : 0u);
-      umma_commit(&bar.s_full[h]);
-    };
-    while (!failed && w.next(p, blockIdx.x)) {
-      const int rows = min(ROWS, w.g.n * p.GQ - w.tile * ROWS), halves = rows > HALF ? 2 : 1;
-      const int nk = w.k1 - w.k0;
-      if (!mbar_wait_warp(&bar.q_full, seg & 1, err) || !tile_full(2 * gs)) break;
-      ++seg;
-      tc_fence_after();
-      if (lane == 0) {
-        for (int h = 0; h < halves; ++h) qk(h, 2 * gs);
-        umma_commit(&bar.empty[(2 * gs) % C::SLOTS]);
-        if (nk == 1) umma_commit(&bar.q_empty);
-      }
+    // values past the prefix's end are multiplied by weights of 0: they have to be finite
+    auto clear_tail = [&](uint32_t n, int valid) {
+      uint8_t* t = sT + (n % C::SLOTS) * C::TILE;
+      for (int i = max(0, valid) * (D / 16) + lane; i < KT * (D / 16); i += 32)
+        *reinterpret_cast<uint4*>(t + i * 16) = make_uint4(0, 0, 0, 0);
+      fence_proxy_async();
       __syncwarp();
-      for (int j = 0; j < nk && !failed; ++j, ++gs) {
-        const uint32_t nv = 2 * gs + 1, nn = 2 * gs + 2;
-        if (!tile_full(nv)) {
-          failed = true;
-          break;
-        }
+    };
+    if (rank != 0) {
+      // ------------- what has arrived here, told to the CTA that issues -------------
+      uint32_t nt = 0, seg = 0;
+      bool failed = false;
+      while (!failed && w.next(p, block)) {
+        const Segment sg(p, w);
+        if (!mbar_wait_warp(&bar.q_full, seg & 1, err)) break;
+        ++seg;
+        if (lane == 0) mbar_arrive_at(&bar.q_peer, 0);
         if constexpr (BITS == 16) {
-          // values past the prefix's end are multiplied by weights of 0: they have to be finite
-          const int valid = max(0, min(KT, w.g.len - (w.k0 + j) * KT));
-          if (valid < KT) {
-            uint8_t* t = sT + (nv % C::SLOTS) * C::TILE;
-            for (int c = 0; c < DH; ++c)
-              for (int i = valid * 8 + lane; i < KT * 8; i += 32)
-                *reinterpret_cast<uint4*>(t + c * (KT * 128) + i * 16) = make_uint4(0, 0, 0, 0);
-            fence_proxy_async();
-            __syncwarp();
-          }
-        }
-        for (int h = 0; h < halves; ++h) {
-          if (!mbar_wait_warp(&bar.p_full[h], it[h] & 1, err)) {
-            failed = true;
-            break;
-          }
-          ++it[h];
-          tc_fence_after();
-          if (lane == 0) {
-            const uint32_t b = smem_u32(sT) + (nv % C::SLOTS) * C::TILE;
-#pragma unroll
-            for (int s = 0; s < KT / 16; ++s)
-              umma_bf16_ts(tmem + 256 + 128 * h, tmem + 128 * h + 8 * s, smem_desc_sw128(b + s * 2048, KT * 128, 1024),
-                           id_pv, (j > 0 || s > 0) ? 1u : 0u);
-            umma_commit(&bar.o_done[h]);
-            if (h == halves - 1) umma_commit(&bar.empty[nv % C::SLOTS]);
-          }
-          __syncwarp();
-          if (j + 1 < nk) {
-            if (h == 0 && !tile_full(nn)) {
+          for (int i = 0; i < sg.tiles(); ++i, ++nt) {
+            bool is_v;
+            const int valid = w.g.len - (w.k0 + sg.tile(i, is_v)) * KT;
+            if (!mbar_wait_warp(&bar.full[nt % C::SLOTS], (nt / C::SLOTS) & 1, err)) {
               failed = true;
               break;
             }
-            tc_fence_after();
-            if (lane == 0) {
-              qk(h, nn);
-              if (h == halves - 1) {
-                umma_commit(&bar.empty[nn % C::SLOTS]);
-                if (j + 2 == nk) umma_commit(&bar.q_empty);
-              }
-            }
-            __syncwarp();
+            if (is_v && valid < KT) clear_tail(nt, valid);
+            if (lane == 0) mbar_arrive_at(&bar.peer[nt % C::SLOTS], 0);
           }
         }
       }
+    } else {
+      // ------------------------------ MMAs ------------------------------
+      constexpr uint32_t id_qk = idesc_bf16_f32(256, KT);
+      constexpr uint32_t id_pv = idesc_bf16_f32(256, D) | (1u << 16);  // V: d contiguous, N-major
+      uint32_t nt = 0, seg = 0, it[2] = {0, 0};
+      bool failed = false;
+      // tile n is here, in both CTAs (v_valid: a V tile's keys in use)
+      auto tile_here = [&](uint32_t n, int v_valid) {
+        const uint32_t st = n % C::SLOTS, ph = (n / C::SLOTS) & 1;
+        if constexpr (BITS == 8) {
+          return mbar_wait_warp_cluster(&bar.full[st], ph, err);
+        } else {
+          if (!mbar_wait_warp(&bar.full[st], ph, err)) return false;
+          if (v_valid < KT) clear_tail(n, v_valid);
+          return mbar_wait_warp_cluster(&bar.peer[st], ph, err);
+        }
+      };
+      auto qk = [&](int h, int qs, uint32_t n) {  // S of stream h = Q (slot qs) K^T
+        const uint32_t a = smem_u32(sQ) + qs * C::QT_BYTES, b = smem_u32(sT) + (n % C::SLOTS) * C::TILE;
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s)
+          umma_bf16_pair(tmem + 128 * h, smem_desc_sw128(a + (s >> 2) * (128 * 128) + (s & 3) * 32, 16, 1024),
+                         smem_desc_sw128(b + (s >> 2) * (64 * 128) + (s & 3) * 32, 16, 1024), id_qk, s > 0 ? 1u : 0u);
+        umma_commit_pair(&bar.s_full[h]);
+      };
+      auto pv = [&](int h, uint32_t n, bool first) {  // O of stream h (+)= P V
+        const uint32_t b = smem_u32(sT) + (n % C::SLOTS) * C::TILE;
+#pragma unroll
+        for (int s = 0; s < KT / 16; ++s) {
+          const uint64_t bd = D == 128 ? smem_desc_sw128(b + s * 2048, 16, 1024) : smem_desc_sw64(b + s * 1024, 16, 512);
+          umma_bf16_pair_ts(tmem + 256 + 128 * h, tmem + 128 * h + 8 * s, bd, id_pv, (first && s == 0) ? 0u : 1u);
+        }
+        umma_commit_pair(&bar.o_done[h]);
+      };
+      while (!failed && w.next(p, block)) {
+        const Segment sg(p, w);
+        if (!mbar_wait_warp(&bar.q_full, seg & 1, err) || !mbar_wait_warp_cluster(&bar.q_peer, seg & 1, err)) break;
+        ++seg;
+        const int head = min(sg.lag, sg.nk);
+        for (int j = 0; j < head && !failed; ++j, ++nt) {
+          if (!tile_here(nt, KT)) {
+            failed = true;
+            break;
+          }
+          tc_fence_after();
+          if (lane == 0) {
+            if (sg.lag == 1) {
+              qk(0, 0, nt);
+              qk(1, 1, nt);
+            } else {
+              qk(j, 0, nt);
+            }
+            umma_commit_pair(&bar.empty[nt % C::SLOTS]);
+            if (j == sg.nk - 1) umma_commit_pair(&bar.q_empty);
+          }
+          __syncwarp();
+        }
+        for (int j = 0; j < sg.nk && !failed; ++j) {
+          const uint32_t nv = nt++;
+          const bool more = j + sg.lag < sg.nk;
+          const uint32_t nn = more ? nt++ : 0;
+          if (!tile_here(nv, w.g.len - (w.k0 + j) * KT)) {
+            failed = true;
+            break;
+          }
+          const int h0 = sg.lag == 1 ? 0 : j & 1, h1 = sg.lag == 1 ? 1 : h0;
+          for (int h = h0; h <= h1; ++h) {
+            if (!mbar_wait_warp_cluster(&bar.p_full[h], it[h] & 1, err)) {
+              failed = true;
+              break;
+            }
+            ++it[h];
+            tc_fence_after();
+            if (lane == 0) {
+              pv(h, nv, j < sg.lag);
+              if (h == h1) umma_commit_pair(&bar.empty[nv % C::SLOTS]);
+            }
+            __syncwarp();
+            if (more) {
+              if (h == h0 && !tile_here(nn, KT)) {
+                failed = true;
+                break;
+              }
+              tc_fence_after();
+              if (lane == 0) {
+                qk(h, sg.lag == 1 ? h : 0, nn);
+                if (h == h1) {
+                  umma_commit_pair(&bar.empty[nn % C::SLOTS]);
+                  if (j + sg.lag == sg.nk - 1) umma_commit_pair(&bar.q_empty);
+                }
+              }
+              __syncwarp();
+            }
+          }
+        }
+      }
+      if (lane == 0) {  // every MMA issued has completed before the tensor memory is released (bounded)
+        umma_commit_pair(&bar.drain);
+        mbar_wait(&bar.drain, 0, err);
+      }
+      __syncwarp();
     }
-    if (lane == 0) {  // every MMA issued has completed before the tensor memory is released (bounded)
-      umma_commit(&bar.drain);
-      mbar_wait(&bar.drain, 0, err);
-    }
-    __syncwarp();
   } else if (BITS == 8 && warp < 12) {
     // ------------------------------ codes to bf16 ------------------------------
     if constexpr (BITS == 8) {
       set_regs_down<80>();
       const int t = threadIdx.x - 256;
-      constexpr int CH = D / 16;  // 16-code chunks a row
-      uint32_t nt = 0, gs = 0;
+      uint32_t nt = 0, step0 = 0;
       bool failed = false;
-      while (!failed && w.next(p, blockIdx.x)) {
+      while (!failed && w.next(p, block)) {
+        const Segment sg(p, w);
         const size_t row0 = ((size_t)w.p * p.H_kv + w.head) * p.N_cap;
-        for (int j = 0; j < w.k1 - w.k0 && !failed; ++j, ++gs) {
+        for (int i = 0; i < sg.tiles(); ++i, ++nt) {
+          bool is_v;
+          const int j = sg.tile(i, is_v);
           const int key = (w.k0 + j) * KT + t;
-          const float ks = key < w.g.len ? __ldg(p.ks + row0 + key) : 0.f;
-          const float vs = key < w.g.len ? __ldg(p.vs + row0 + key) : 0.f;
-#pragma unroll 1
-          for (int kv = 0; kv < 2; ++kv, ++nt) {
-            const int rs = nt % C::RSLOTS, cs = nt % C::SLOTS;
-            if (!mbar_wait_warp(&bar.raw_full[rs], (nt / C::RSLOTS) & 1, err) ||
-                !mbar_wait_warp(&bar.empty[cs], ((nt / C::SLOTS) & 1) ^ 1, err)) {
-              failed = true;
-              break;
-            }
-            if (kv == 0) {
-              // the slots of the scales and of the tiles turn together: the tile slot that was just
-              // found free was last used after the softmax of the step four before had read these
-              sc[gs & 3][0][t] = ks;
-              sc[gs & 3][1][t] = vs;
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&bar.sc_full[gs & 3]);
-            }
-            const uint8_t* src = sR + rs * C::RAW;
-            uint8_t* dst = sT + cs * C::TILE;
-#pragma unroll 4
-            for (int i = t; i < KT * CH; i += 128) {
-              const int row = i / CH, c = i % CH;
-              const uint4 x = *reinterpret_cast<const uint4*>(src + i * 16);
-              const uint32_t wd[4] = {x.x, x.y, x.z, x.w};
-              uint32_t o[8];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                o[2 * e] = widen_codes(__byte_perm(wd[e], 0, 0x4140));
-                o[2 * e + 1] = widen_codes(__byte_perm(wd[e], 0, 0x4342));
-              }
-              uint8_t* r = dst + (c >> 2) * (KT * 128) + row * 128;
-              const int ch = 2 * (c & 3);
-              *reinterpret_cast<uint4*>(r + ((ch ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-              *reinterpret_cast<uint4*>(r + (((ch + 1) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
-            }
-            fence_proxy_async();
+          float ks = 0.f, vs = 0.f;
+          if (!is_v && key < w.g.len) {
+            ks = __ldg(p.ks + row0 + key);
+            vs = __ldg(p.vs + row0 + key);
+          }
+          const int rs = nt % C::RSLOTS, cs = nt % C::SLOTS;
+          if (!mbar_wait_warp(&bar.raw_full[rs], (nt / C::RSLOTS) & 1, err) ||
+              !mbar_wait_warp(&bar.empty[cs], ((nt / C::SLOTS) & 1) ^ 1, err)) {
+            failed = true;
+            break;
+          }
+          if (!is_v) {
+            // these scales' places were last used eight steps before; the tile slot just found free held
+            // the K of three steps before, whose S was issued after the softmax of two steps before that
+            const uint32_t gs = step0 + j;
+            sc[gs % SC_SLOTS][0][t] = ks;
+            sc[gs % SC_SLOTS][1][t] = vs;
             __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(&bar.full[cs]);
-              mbar_arrive(&bar.raw_empty[rs]);
+            if (lane == 0) mbar_arrive(&bar.sc_full[gs % SC_SLOTS]);
+          }
+          const uint8_t* src = sR + rs * C::RAW;
+          uint8_t* dst = sT + cs * C::TILE;
+          // 16 codes a piece; K: 64 rows of D codes, V: 128 rows of D / 2
+          auto widen = [&](int row, int c, int per_row, uint8_t* piece, int swizzle) {
+            const uint4 x = *reinterpret_cast<const uint4*>(src + (row * per_row + c) * 16);
+            const uint32_t wd[4] = {x.x, x.y, x.z, x.w};
+            uint32_t o[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              o[2 * e] = widen_codes(__byte_perm(wd[e], 0, 0x4140));
+              o[2 * e + 1] = widen_codes(__byte_perm(wd[e], 0, 0x4342));
+            }
+            const int ch = 2 * (c & 3);
+            *reinterpret_cast<uint4*>(piece + ((ch ^ swizzle) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4*>(piece + (((ch + 1) ^ swizzle) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+          };
+          if (!is_v) {
+#pragma unroll
+            for (int u = 0; u < D / 32; ++u) {  // two rows of four pieces to eight lanes: stores of all banks
+              const int row = (t >> 2) + 32 * (u & 1), c = (t & 3) + 4 * (u >> 1);
+              widen(row, c, D / 16, dst + (u >> 1) * (64 * 128) + row * 128, row & 7);
+            }
+          } else if (D == 128) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const int row = (t >> 2) + 32 * u;
+              widen(row, t & 3, 4, dst + row * 128, row & 7);
+            }
+          } else {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {  // rows of 64 bytes, 64-byte swizzle
+              const int row = (t >> 1) + 64 * u;
+              widen(row, t & 1, 2, dst + row * 64, (row >> 1) & 3);
             }
           }
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive_at(&bar.full[cs], 0);
+            mbar_arrive(&bar.raw_empty[rs]);
+          }
         }
+        step0 += sg.nk;
       }
     }
   } else {
     if constexpr (BITS == 8) set_regs_down<64>();
   }
   __syncthreads();
+  cluster_sync_all();  // nothing of this CTA is read, written or arrived on from the other any more
   if (warp == C::ISSUER) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc_pair(tmem, 512);
   }
 }
 
@@ -503,21 +692,27 @@ cudaError_t launch_t(const PrefixParams& p, cudaStream_t s) {
     // 128 rows of one KV head's group: (64 columns, G_Q heads, 1 KV head, 128 / G_Q tokens)
     const uint64_t dims[4] = {(uint64_t)D, (uint64_t)p.GQ, (uint64_t)p.H_kv, (uint64_t)p.R};
     const uint64_t strides[3] = {(uint64_t)D * 2, (uint64_t)p.GQ * D * 2, (uint64_t)p.H_q * D * 2};
-    const uint32_t box[4] = {64, (uint32_t)p.GQ, 1, (uint32_t)(HALF / p.GQ)};
+    const uint32_t box[4] = {64, (uint32_t)p.GQ, 1, (uint32_t)(128 / p.GQ)};
     if (!encode_tensor_map(&mapQ, p.q, 4, dims, strides, box)) return cudaErrorInvalidValue;
   }
-  mapK = mapV = mapQ;  // not used by the 8-bit cache, whose tiles are plain bulk copies
-  if (BITS == 16) {
-    const uint64_t dims[3] = {(uint64_t)D, (uint64_t)p.N_cap, (uint64_t)p.P * p.H_kv};
-    const uint64_t strides[2] = {(uint64_t)D * 2, (uint64_t)p.N_cap * D * 2};
-    const uint32_t box[3] = {64, (uint32_t)KT, 1};
-    if (!encode_tensor_map(&mapK, p.K, 3, dims, strides, box)) return cudaErrorInvalidValue;
-    if (!encode_tensor_map(&mapV, p.V, 3, dims, strides, box)) return cudaErrorInvalidValue;
+  // K: 64 keys of all columns; V: all 128 keys of D / 2 columns
+  const uint64_t rowb = (uint64_t)D * BITS / 8;
+  const uint64_t dims[3] = {(uint64_t)D, (uint64_t)p.N_cap, (uint64_t)p.P * p.H_kv};
+  const uint64_t strides[2] = {rowb, (uint64_t)p.N_cap * rowb};
+  const uint32_t boxK[3] = {BITS == 8 ? (uint32_t)D : 64u, 64, 1}, boxV[3] = {(uint32_t)D / 2, (uint32_t)KT, 1};
+  if (BITS == 8) {
+    if (!encode_tensor_map_kind(&mapK, p.K, 3, dims, strides, boxK, TileKind::BYTES)) return cudaErrorInvalidValue;
+    if (!encode_tensor_map_kind(&mapV, p.V, 3, dims, strides, boxV, TileKind::BYTES)) return cudaErrorInvalidValue;
+  } else {
+    if (!encode_tensor_map(&mapK, p.K, 3, dims, strides, boxK)) return cudaErrorInvalidValue;
+    if (!(D == 128 ? encode_tensor_map(&mapV, p.V, 3, dims, strides, boxV)
+                   : encode_tensor_map_kind(&mapV, p.V, 3, dims, strides, boxV, TileKind::BF16_SW64)))
+      return cudaErrorInvalidValue;
   }
   auto kern = prefix_tc_kernel<D, BITS>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
   if (e != cudaSuccess) return e;
-  kern<<<p.blocks, C::THREADS, C::SMEM, s>>>(mapQ, mapK, mapV, p);
+  kern<<<2 * p.blocks, C::THREADS, C::SMEM, s>>>(mapQ, mapK, mapV, p);
   return cudaGetLastError();
 }
 
