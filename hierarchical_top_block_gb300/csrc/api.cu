@@ -410,12 +410,9 @@ bool encode_tensor_map(CUtensorMap* map, const void* base, int rank, const uint6
                 CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-bool encode_tensor_map_kind(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
-                            const uint64_t* strides_bytes, const uint32_t* box, TileKind kind) {
-  const bool bytes = kind == TileKind::BYTES;
-  return encode(map, base, rank, dims, strides_bytes, box,
-                bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                bytes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_64B);
+bool encode_byte_tensor_map(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
+                            const uint64_t* strides_bytes, const uint32_t* box) {
+  return encode(map, base, rank, dims, strides_bytes, box, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 }  // namespace pisa

@@ -112,9 +112,8 @@ cudaError_t launch_wait_check(uint64_t limit_ns, uint32_t* err, cudaStream_t s);
 // Tensor-map encoding through the driver entry point (no link-time libcuda dependency).
 bool encode_tensor_map(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
                        const uint64_t* strides_bytes, const uint32_t* box);
-// The same for bytes (unswizzled) or for bf16 boxes of 64-byte rows (64-byte swizzle).
-enum class TileKind { BYTES, BF16_SW64 };
-bool encode_tensor_map_kind(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
-                            const uint64_t* strides_bytes, const uint32_t* box, TileKind kind);
+// The same for bytes, unswizzled.
+bool encode_byte_tensor_map(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
+                            const uint64_t* strides_bytes, const uint32_t* box);
 
 }  // namespace pisa

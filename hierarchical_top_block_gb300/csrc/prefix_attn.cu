@@ -212,7 +212,7 @@ Plan prefix_plan(const Problem& p) {
 #else
   const bool tc = (long long)p.N * p.GQ > 16LL * p.B;
 #endif
-  return tc ? Plan{true, TC_ROWS, MAX_SMS / 2} : Plan{false, FEW_ROWS, 2 * MAX_SMS};
+  return tc ? Plan{true, TC_ROWS, MAX_SMS} : Plan{false, FEW_ROWS, 2 * MAX_SMS};
 }
 
 template <int D, int BITS>

@@ -70,17 +70,17 @@ __device__ __forceinline__ int block_of(long long s, long long len) {
 
 // Walks a block's range job by job.  Every thread of a warp holds the same state.
 struct PrefixWalk {
-  long long S, at, end;   // line length; next step and end of the range
-  long long lo;           // start of the range
+  long long at, end;      // next step and end of the range
+  long long gbase;        // first step of the current group
   int p;                  // current group
-  long long gbase;        // its first step
+  bool begun;             // a segment of the range is behind
   PrefixGroup g;
   // current segment
   int head, tile, k0, k1; // KV head, tile, steps [k0, k1) of the job
   int slot;               // -1: the whole job; else the part's slot (2 block + 0 or 1)
 
   // Warp-wide.  `record`: this warp writes the groups' first steps and reports bad inputs.
-  __device__ void init(const PrefixParams& prm, int block, bool record) {
+  __device__ __forceinline__ void init(const PrefixParams& prm, int block, bool record) {
     const int lane = threadIdx.x & 31;
     long long total = 0;
     for (int i0 = 0; i0 < prm.P; i0 += 32) {
@@ -108,11 +108,11 @@ struct PrefixWalk {
       total += __shfl_sync(0xffffffffu, x, 31);
     }
     if (record && lane == 0) prm.base[prm.P] = total;
-    S = total;
-    const long long len = range_len(S, prm.blocks);
+    const long long S = total, len = range_len(S, prm.blocks);
+    begun = false;
     p = 0;
     gbase = 0;
-    lo = at = min(S, len * block);
+    at = min(S, len * block);
     end = min(S, len * (block + 1));
     if (at >= end) return;
     // the group that holds step `at`
@@ -139,7 +139,7 @@ struct PrefixWalk {
   }
 
   // Moves to the next segment; false at the end of the range.
-  __device__ bool next(const PrefixParams& prm, int block) {
+  __device__ __forceinline__ bool next(const PrefixParams& prm, int block) {
     if (at >= end) return false;
     while (at >= gbase + group_steps(prm, g)) {
       gbase += group_steps(prm, g);
@@ -151,8 +151,8 @@ struct PrefixWalk {
     tile = job - head * g.tiles;
     k0 = (int)(off - (long long)job * g.steps);
     k1 = (int)min((long long)g.steps, k0 + (end - at));
-    const bool first = at == lo;
-    slot = (k0 == 0 && k1 == g.steps) ? -1 : 2 * block + (first ? 0 : 1);
+    slot = (k0 == 0 && k1 == g.steps) ? -1 : 2 * block + (begun ? 1 : 0);
+    begun = true;
     at += k1 - k0;
     return true;
   }
@@ -174,9 +174,8 @@ __device__ __forceinline__ void join_own(float m, float l, float own, float& f_a
   lse = t == 0.f ? NEG_INF : (M + log2f(t)) * LN2;
 }
 
-// The tensor-core kernel (prefix_tc.cu): tiles of TC_ROWS rows, a block here is a pair of CTAs on
-// two SMs.
-constexpr int TC_ROWS = 512;
+// The tensor-core kernel (prefix_tc.cu): tiles of TC_ROWS rows, one block a SM.
+constexpr int TC_ROWS = 256;
 cudaError_t launch_prefix_tc(const PrefixParams& p, int d, cudaStream_t s);
 
 }  // namespace pisa

@@ -1,5 +1,5 @@
-// Attention over shared prefixes on the tensor cores of the 5th generation: up to 512 query rows of
-// one (group, KV head) a tile, 128 keys a step, by a pair of CTAs (a cluster on two SMs).
+// Attention over shared prefixes on the tensor cores of the 5th generation: up to 256 query rows of
+// one (group, KV head) a tile, 128 keys a step, one block a SM.
 //
 //   S = Q K^T (fp32 in tensor memory), P = 2^(S scale log2 e - m) as bf16 back into tensor memory
 //   over S, O += P V in tensor memory, l = sum of the unrounded P
@@ -10,24 +10,19 @@
 // usual logits that happens in a job's first steps alone, so O is left where the MMA accumulates it.
 // P is rounded to bf16 (half a step, 2^-8 of each weight, the size of the output's own rounding).
 //
-// Why pairs: an MMA of 128 x 128 x 16 reads 8 KB of shared memory in 64 cycles, all that an SM's
-// shared memory gives, beside the copies that write the next tiles.  Over a pair (256 x 128 x 16)
-// each SM reads its own 128 rows of A and half of B: 6 KB for the first product, 2 KB for the second
-// (A from tensor memory), and holds, copies and widens half of every K and V tile.
-//
-// Two streams keep the tensor pipe busy while the softmax of the other one runs, a warpgroup a CTA
-// for each.  With more than 256 rows a stream is a half of the rows, and both use the same tiles;
-// with fewer, both streams have all rows, one the even steps and one the odd ones, each with
-// its own m, l and O, which are joined when a job's segment ends.
+// Two streams keep the tensor pipe busy while the softmax of the other one runs, a warpgroup for
+// each.  With more than 128 rows a stream is a half of the rows, and both use the same tiles; with
+// fewer, both streams have all rows, one the even steps and one the odd ones, each with its own
+// m, l and O, which are joined when a job's segment ends.
 //
 // The 8-bit cache: four warps widen the codes to bf16 (exact) into the swizzled tiles that the MMA
 // reads; the key's scale multiplies the logit and the value's scale the weight, both in fp32.
 //
-// Roles in each CTA: two softmax warpgroups (a row a thread); a producer warp (TMA); a warp that issues
-// the pair's MMAs in the CTA of rank 0 and tells it of the arrived tiles in that of rank 1; with
-// the 8-bit cache the widening warpgroup.  TMEM: S of stream i at 128 i (its first 64 columns hold P
-// afterwards), O of stream i at 256 + 128 i.  The MMAs of one thread run in order, so a stream's next S
-// is issued right behind its O += P V, which reads P from the same columns.  Every wait is bounded.
+// Roles: two softmax warpgroups (a row a thread); a producer warp (TMA); a warp that issues the MMAs;
+// with the 8-bit cache the widening warpgroup.  TMEM: S of stream i at 128 i (its first 64 columns
+// hold P afterwards), O of stream i at 256 + 128 i.  The MMAs of one thread run in order, so a stream's
+// next S is issued right behind its O += P V, which reads P from the same columns.  Every wait is
+// bounded.
 #include <algorithm>
 
 #include "cache_attn.cuh"
@@ -44,26 +39,37 @@ constexpr float MAX_GROWTH = 8.f;  // log2 units the maximum may pass a row's re
 template <int D, int BITS>
 struct Cfg {
   static constexpr int THREADS = BITS == 8 ? 512 : 384;
-  static constexpr int PRODUCER = BITS == 8 ? 12 : 8, ISSUER = PRODUCER + 1;  // warps
-  static constexpr uint32_t QT_BYTES = 128 * D * 2;     // a CTA's 128 query rows of a stream
-  static constexpr uint32_t TILE = 64 * D * 2;          // its half of a tile in bf16: 64 keys of K, D / 2 columns of V
-  static constexpr uint32_t RAW = 64 * D;               // in codes
-  static constexpr int SLOTS = BITS == 8 ? 6 : 9;
-  static constexpr int RSLOTS = 6;
-  static constexpr size_t SMEM = 1024 + 2 * QT_BYTES + SLOTS * TILE + (BITS == 8 ? RSLOTS * RAW : 0);
+  static constexpr int PRODUCER = BITS == 8 ? 12 : 8, ISSUER = PRODUCER + 1, WORKERS = ISSUER + 1;  // warps
+  static constexpr uint32_t QT_BYTES = 128 * D * 2;     // 128 query rows
+  static constexpr uint32_t TILE = KT * D * 2;          // a K or V tile in bf16
+  static constexpr uint32_t RAW = KT * D;               // in codes
+  static constexpr int SLOTS = BITS == 8 ? 3 : 5;
+  static constexpr int RSLOTS = 3;
+  static constexpr size_t TILES = 2 * QT_BYTES + SLOTS * TILE + (BITS == 8 ? RSLOTS * RAW : 0);
 };
 
-constexpr int SC_SLOTS = 8;
+constexpr int SC_SLOTS = 4;
 
 struct Bars {
-  uint64_t q_full, q_empty, q_peer;
-  uint64_t full[9], empty[9];          // bf16 tiles
-  uint64_t peer[9];                    // the other CTA's half has arrived (rank 0)
-  uint64_t raw_full[6], raw_empty[6];  // tiles of codes
+  uint64_t q_full, q_empty;
+  uint64_t full[5], empty[5];          // bf16 tiles
+  uint64_t raw_full[3], raw_empty[3];  // tiles of codes
   uint64_t sc_full[SC_SLOTS];          // a step's scales
   uint64_t s_full[2], p_full[2], o_done[2];
   uint64_t x_full, x_done;             // the streams' meeting at the end of a segment
   uint64_t drain;
+};
+
+// What follows the tiles in shared memory (all of it dynamic: with five bf16 tiles there is room for
+// 3 KB beside them, and none for an alignment gap).
+template <int BITS>
+struct Shared {
+  Bars bar;
+  float2 ml[2][128];                               // the streams' maxima and sums, when they meet
+  PrefixWalk walks[BITS == 8 ? 14 : 10];           // each working warp's walk over the segments: the
+                                                   // softmax needs the registers
+  uint32_t tmem;
+  __align__(16) float sc[BITS == 8 ? SC_SLOTS : 1][2][BITS == 8 ? KT : 4];  // scales of a step: keys', values'
 };
 
 template <int R>
@@ -166,34 +172,28 @@ __device__ __forceinline__ void put_columns(const PrefixParams& p, const RowOut&
 }
 
 template <int D, int BITS>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
+__global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
     prefix_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
                      const __grid_constant__ CUtensorMap mapV, PrefixParams p) {
   pdl_trigger();
   using C = Cfg<D, BITS>;
   constexpr int DH = D / 64;  // 64-column pieces of a Q or K row
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sQ = smem;
   uint8_t* sT = sQ + 2 * C::QT_BYTES;
   uint8_t* sR = sT + C::SLOTS * C::TILE;
-  __shared__ Bars bar;
-  __shared__ __align__(16) float sc[BITS == 8 ? SC_SLOTS : 1][2][KT];  // scales of a step: keys', values'
-  __shared__ float2 s_ml[2][128];
-  __shared__ uint32_t tmem_base_s;
+  Shared<BITS>& sh = *reinterpret_cast<Shared<BITS>*>(smem + C::TILES);
+  Bars& bar = sh.bar;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_rank();
-  const int block = blockIdx.x >> 1;  // the pair
+  const int block = blockIdx.x;
   uint32_t* err = p.err;
 
   if (threadIdx.x == 0) {
     mbar_init(&bar.q_full, 1);
     mbar_init(&bar.q_empty, 1);
-    mbar_init(&bar.q_peer, 1);
     for (int i = 0; i < C::SLOTS; ++i) {
-      mbar_init(&bar.full[i], BITS == 8 ? 8 : 1);  // widened by the warps of both CTAs; or the copy
+      mbar_init(&bar.full[i], BITS == 8 ? 4 : 1);  // the widening warps; or the copy
       mbar_init(&bar.empty[i], 1);
-      mbar_init(&bar.peer[i], 1);
     }
     for (int i = 0; i < C::RSLOTS; ++i) {
       mbar_init(&bar.raw_full[i], 1);
@@ -202,7 +202,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<D, BITS>::THREAD
     for (int i = 0; i < SC_SLOTS; ++i) mbar_init(&bar.sc_full[i], 4);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.s_full[i], 1);
-      mbar_init(&bar.p_full[i], 8);  // the warps of both CTAs
+      mbar_init(&bar.p_full[i], 4);
       mbar_init(&bar.o_done[i], 1);
     }
     mbar_init(&bar.x_full, 8);
@@ -210,27 +210,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<D, BITS>::THREAD
     mbar_init(&bar.drain, 1);
     mbar_fence_init();
   }
-  if (warp == C::ISSUER) tmem_alloc_pair(&tmem_base_s, 512);
+  if (warp == C::ISSUER) {
+    tmem_alloc(&sh.tmem, 512);
+    tmem_relinquish();
+  }
   __syncthreads();
-  cluster_sync_all();
   tc_fence_after();
-  const uint32_t tmem = tmem_base_s;
+  const uint32_t tmem = sh.tmem;
 
-  PrefixWalk w;
-  w.init(p, block, blockIdx.x == 0 && warp == 0);
+  const PrefixWalk& w = sh.walks[warp < C::WORKERS ? warp : 0];
+  if (warp < C::WORKERS) {
+    PrefixWalk first;
+    first.init(p, block, block == 0 && warp == 0);
+    if (lane == 0) sh.walks[warp] = first;
+    __syncwarp();
+  }
+  auto next_segment = [&]() {
+    PrefixWalk at = sh.walks[warp];
+    __syncwarp();
+    const bool more = at.next(p, block);
+    if (lane == 0) sh.walks[warp] = at;
+    __syncwarp();
+    return more;
+  };
 
   if (warp < 8) {
     // ------------------------------ softmax ------------------------------
-    if constexpr (BITS == 8) set_regs_up<184>();
+    set_regs_up<BITS == 8 ? 192 : 216>();
     const int h = warp >> 2;                                 // stream
     const int trow = (warp & 3) * 32 + lane;                 // TMEM lane
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_tmem = tmem + lanes + 128 * h, o_tmem = tmem + lanes + 256 + 128 * h;
     uint32_t it[2] = {0, 0}, step0 = 0, meets = 0;           // the streams' steps; all steps
     bool failed = false;
-    while (!failed && w.next(p, block)) {
+    while (!failed && next_segment()) {
       const Segment sg(p, w);
-      const int local = (sg.lag == 1 ? 256 * h : 0) + 128 * (int)rank + trow;  // row in the tile
+      const int local = (sg.lag == 1 ? 128 * h : 0) + trow;  // row in the tile
       const bool live = local < sg.rows, any = local - lane < sg.rows;
       float m = NEG_INF, top = NEG_INF;  // reference and maximum, log2 units
       unsigned long long l2 = pack_f32x2(0.f, 0.f);
@@ -255,7 +270,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<D, BITS>::THREAD
           for (int c = 0; c < KT; c += 32) tmem_ld32(s_tmem + c, *reinterpret_cast<uint32_t(*)[32]>(s + c));
           tmem_wait_ld();
           if constexpr (BITS == 8) {
-            const float4* ks = reinterpret_cast<const float4*>(sc[gs % SC_SLOTS][0]);
+            const float4* ks = reinterpret_cast<const float4*>(sh.sc[gs % SC_SLOTS][0]);
 #pragma unroll
             for (int c = 0; c < KT; c += 4) {
               const float4 f = ks[c / 4];
@@ -318,7 +333,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<D, BITS>::THREAD
               unsigned long long xy = pack_f32x2(x, y);
               l2 = add_f32x2(l2, xy);
               if constexpr (BITS == 8) {
-                const float2 f = *reinterpret_cast<const float2*>(&sc[gs % SC_SLOTS][1][c + e]);
+                const float2 f = *reinterpret_cast<const float2*>(&sh.sc[gs % SC_SLOTS][1][c + e]);
                 unpack_f32x2(mul_f32x2(xy, pack_f32x2(f.x, f.y)), x, y);
               }
               pk[e / 2] = pack_bf16x2(x, y);
@@ -329,7 +344,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<D, BITS>::THREAD
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_at(&bar.p_full[h], 0);
+        if (lane == 0) mbar_arrive(&bar.p_full[h]);
       }
       // the streams' steps of this segment
       const uint32_t n0 = sg.lag == 1 ? sg.nk : (sg.nk + 1) / 2, n1 = sg.lag == 1 ? sg.nk : sg.nk / 2;
@@ -365,7 +380,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<D, BITS>::THREAD
           failed = true;
           break;
         }
-        s_ml[h][trow] = make_float2(m, l);
+        sh.ml[h][trow] = make_float2(m, l);
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.x_full);
         if (!mbar_wait_warp(&bar.x_full, meets & 1, err)) {  // (the row's own log-sum-exp has been read by both)
@@ -374,7 +389,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<D, BITS>::THREAD
         }
         tc_fence_after();
         if (any) {
-          const float2 a = s_ml[0][trow], b = s_ml[1][trow];
+          const float2 a = sh.ml[0][trow], b = sh.ml[1][trow];
           m = fmaxf(a.x, b.x);
           const float f0 = a.x == NEG_INF ? 0.f : fast_exp2(a.x - m), f1 = b.x == NEG_INF ? 0.f : fast_exp2(b.x - m);
           l = (a.x == NEG_INF ? a.y : a.y * f0) + (b.x == NEG_INF ? b.y : b.y * f1);
@@ -407,11 +422,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<D, BITS>::THREAD
     }
   } else if (warp == C::PRODUCER) {
     // ------------------------------ producer ------------------------------
-    if constexpr (BITS == 8) set_regs_down<64>();
+    set_regs_down<BITS == 8 ? 56 : 72>();
     constexpr uint32_t N = BITS == 8 ? C::RSLOTS : C::SLOTS;
     uint32_t nt = 0, seg = 0;  // tiles and segments so far
     bool failed = false;
-    while (!failed && w.next(p, block)) {
+    while (!failed && next_segment()) {
       const Segment sg(p, w);
       if (!mbar_wait_warp(&bar.q_empty, (seg & 1) ^ 1, err)) break;
       if (lane == 0) {
@@ -420,7 +435,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<D, BITS>::THREAD
         for (int h = 0; h < streams; ++h)
           for (int c = 0; c < DH; ++c)
             tma_load_4d(sQ + h * C::QT_BYTES + c * (128 * 128), &mapQ, &bar.q_full, 64 * c, 0, w.head,
-                        w.g.first + (w.tile * ROWS + h * 256 + (int)rank * 128) / p.GQ);
+                        w.g.first + (w.tile * ROWS + h * 128) / p.GQ);
       }
       ++seg;
       const int ph = w.p * p.H_kv + w.head;
@@ -437,18 +452,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<D, BITS>::THREAD
           if constexpr (BITS == 8) {
             mbar_arrive_expect_tx(full, C::RAW);
             uint8_t* dst = sR + st * C::RAW;
-            if (is_v)  // columns of this CTA, all keys
-              tma_load_3d(dst, &mapV, full, (int)rank * (D / 2), key0, ph);
-            else       // keys of this CTA, all columns
-              tma_load_3d(dst, &mapK, full, 0, key0 + (int)rank * 64, ph);
+            tma_load_3d(dst, is_v ? &mapV : &mapK, full, 0, key0, ph);
           } else {
             mbar_arrive_expect_tx(full, C::TILE);
             uint8_t* dst = sT + st * C::TILE;
-            if (is_v)
-              tma_load_3d(dst, &mapV, full, (int)rank * (D / 2), key0, ph);
-            else
-              for (int c = 0; c < DH; ++c)
-                tma_load_3d(dst + c * (64 * 128), &mapK, full, 64 * c, key0 + (int)rank * 64, ph);
+            for (int c = 0; c < DH; ++c) tma_load_3d(dst + c * (KT * 128), is_v ? &mapV : &mapK, full, 64 * c, key0, ph);
           }
         }
       }
@@ -461,147 +469,121 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<D, BITS>::THREAD
     }
     __syncwarp();
   } else if (warp == C::ISSUER) {
-    if constexpr (BITS == 8) set_regs_down<64>();
-    // values past the prefix's end are multiplied by weights of 0: they have to be finite
-    auto clear_tail = [&](uint32_t n, int valid) {
-      uint8_t* t = sT + (n % C::SLOTS) * C::TILE;
-      for (int i = max(0, valid) * (D / 16) + lane; i < KT * (D / 16); i += 32)
-        *reinterpret_cast<uint4*>(t + i * 16) = make_uint4(0, 0, 0, 0);
-      fence_proxy_async();
-      __syncwarp();
-    };
-    if (rank != 0) {
-      // ------------- what has arrived here, told to the CTA that issues -------------
-      uint32_t nt = 0, seg = 0;
-      bool failed = false;
-      while (!failed && w.next(p, block)) {
-        const Segment sg(p, w);
-        if (!mbar_wait_warp(&bar.q_full, seg & 1, err)) break;
-        ++seg;
-        if (lane == 0) mbar_arrive_at(&bar.q_peer, 0);
-        if constexpr (BITS == 16) {
-          for (int i = 0; i < sg.tiles(); ++i, ++nt) {
-            bool is_v;
-            const int valid = w.g.len - (w.k0 + sg.tile(i, is_v)) * KT;
-            if (!mbar_wait_warp(&bar.full[nt % C::SLOTS], (nt / C::SLOTS) & 1, err)) {
-              failed = true;
-              break;
-            }
-            if (is_v && valid < KT) clear_tail(nt, valid);
-            if (lane == 0) mbar_arrive_at(&bar.peer[nt % C::SLOTS], 0);
-          }
-        }
+    // ------------------------------ MMAs ------------------------------
+    set_regs_down<BITS == 8 ? 56 : 72>();
+    constexpr uint32_t id_qk = idesc_bf16_f32(128, KT);
+    constexpr uint32_t id_pv = idesc_bf16_f32(128, D) | (1u << 16);  // V: d contiguous, N-major
+    uint32_t nt = 0, seg = 0, it[2] = {0, 0};
+    bool failed = false;
+    // tile n is here (v_valid: a V tile's keys in use)
+    auto tile_here = [&](uint32_t n, int v_valid) {
+      if (!mbar_wait_warp(&bar.full[n % C::SLOTS], (n / C::SLOTS) & 1, err)) return false;
+      if (BITS == 16 && v_valid < KT) {
+        // values past the prefix's end are multiplied by weights of 0: they have to be finite
+        uint8_t* t = sT + (n % C::SLOTS) * C::TILE;
+        for (int c = 0; c < DH; ++c)
+          for (int i = max(0, v_valid) * 8 + lane; i < KT * 8; i += 32)
+            *reinterpret_cast<uint4*>(t + c * (KT * 128) + i * 16) = make_uint4(0, 0, 0, 0);
+        fence_proxy_async();
+        __syncwarp();
       }
-    } else {
-      // ------------------------------ MMAs ------------------------------
-      constexpr uint32_t id_qk = idesc_bf16_f32(256, KT);
-      constexpr uint32_t id_pv = idesc_bf16_f32(256, D) | (1u << 16);  // V: d contiguous, N-major
-      uint32_t nt = 0, seg = 0, it[2] = {0, 0};
-      bool failed = false;
-      // tile n is here, in both CTAs (v_valid: a V tile's keys in use)
-      auto tile_here = [&](uint32_t n, int v_valid) {
-        const uint32_t st = n % C::SLOTS, ph = (n / C::SLOTS) & 1;
-        if constexpr (BITS == 8) {
-          return mbar_wait_warp_cluster(&bar.full[st], ph, err);
-        } else {
-          if (!mbar_wait_warp(&bar.full[st], ph, err)) return false;
-          if (v_valid < KT) clear_tail(n, v_valid);
-          return mbar_wait_warp_cluster(&bar.peer[st], ph, err);
-        }
-      };
-      auto qk = [&](int h, int qs, uint32_t n) {  // S of stream h = Q (slot qs) K^T
-        const uint32_t a = smem_u32(sQ) + qs * C::QT_BYTES, b = smem_u32(sT) + (n % C::SLOTS) * C::TILE;
+      return true;
+    };
+    // descriptors of the first tile and Q slot: the others differ in the address field alone (16-byte units)
+    const uint64_t q_desc = smem_desc_sw128(smem_u32(sQ), 16, 1024), k_desc = smem_desc_sw128(smem_u32(sT), 16, 1024);
+    const uint64_t v_desc = smem_desc_sw128(smem_u32(sT), KT * 128, 1024);
+    auto qk = [&](int h, int qs, uint32_t n) {  // S of stream h = Q (slot qs) K^T
+      const uint64_t a = q_desc + qs * (C::QT_BYTES >> 4), b = k_desc + (n % C::SLOTS) * (C::TILE >> 4);
+      const uint32_t d = tmem + 128 * h;
 #pragma unroll
-        for (int s = 0; s < D / 16; ++s)
-          umma_bf16_pair(tmem + 128 * h, smem_desc_sw128(a + (s >> 2) * (128 * 128) + (s & 3) * 32, 16, 1024),
-                         smem_desc_sw128(b + (s >> 2) * (64 * 128) + (s & 3) * 32, 16, 1024), id_qk, s > 0 ? 1u : 0u);
-        umma_commit_pair(&bar.s_full[h]);
-      };
-      auto pv = [&](int h, uint32_t n, bool first) {  // O of stream h (+)= P V
-        const uint32_t b = smem_u32(sT) + (n % C::SLOTS) * C::TILE;
+      for (int s = 0; s < D / 16; ++s)
+        umma_bf16(d, a + (((s >> 2) * (128 * 128) + (s & 3) * 32) >> 4), b + (((s >> 2) * (KT * 128) + (s & 3) * 32) >> 4),
+                       id_qk, s > 0 ? 1u : 0u);
+      umma_commit(&bar.s_full[h]);
+    };
+    auto pv = [&](int h, uint32_t n, bool first) {  // O of stream h (+)= P V
+      const uint64_t b = v_desc + (n % C::SLOTS) * (C::TILE >> 4);
+      const uint32_t d = tmem + 256 + 128 * h, a = tmem + 128 * h;
 #pragma unroll
-        for (int s = 0; s < KT / 16; ++s) {
-          const uint64_t bd = D == 128 ? smem_desc_sw128(b + s * 2048, 16, 1024) : smem_desc_sw64(b + s * 1024, 16, 512);
-          umma_bf16_pair_ts(tmem + 256 + 128 * h, tmem + 128 * h + 8 * s, bd, id_pv, (first && s == 0) ? 0u : 1u);
+      for (int s = 0; s < KT / 16; ++s)
+        umma_bf16_ts(d, a + 8 * s, b + ((s * 16 * 128) >> 4), id_pv, s > 0 ? 1u : first ? 0u : 1u);
+      umma_commit(&bar.o_done[h]);
+    };
+    while (!failed && next_segment()) {
+      const Segment sg(p, w);
+      if (!mbar_wait_warp(&bar.q_full, seg & 1, err)) break;
+      ++seg;
+      const int head = min(sg.lag, sg.nk);
+      for (int j = 0; j < head && !failed; ++j, ++nt) {
+        if (!tile_here(nt, KT)) {
+          failed = true;
+          break;
         }
-        umma_commit_pair(&bar.o_done[h]);
-      };
-      while (!failed && w.next(p, block)) {
-        const Segment sg(p, w);
-        if (!mbar_wait_warp(&bar.q_full, seg & 1, err) || !mbar_wait_warp_cluster(&bar.q_peer, seg & 1, err)) break;
-        ++seg;
-        const int head = min(sg.lag, sg.nk);
-        for (int j = 0; j < head && !failed; ++j, ++nt) {
-          if (!tile_here(nt, KT)) {
+        tc_fence_after();
+        if (elect_one()) {
+          if (sg.lag == 1) {
+            qk(0, 0, nt);
+            qk(1, 1, nt);
+          } else {
+            qk(j, 0, nt);
+          }
+          umma_commit(&bar.empty[nt % C::SLOTS]);
+          if (j == sg.nk - 1) umma_commit(&bar.q_empty);
+        }
+        __syncwarp();
+      }
+      for (int j = 0; j < sg.nk && !failed; ++j) {
+        const uint32_t nv = nt++;
+        const bool more = j + sg.lag < sg.nk;
+        const uint32_t nn = more ? nt++ : 0;
+        if (!tile_here(nv, w.g.len - (w.k0 + j) * KT)) {
+          failed = true;
+          break;
+        }
+        const int h0 = sg.lag == 1 ? 0 : j & 1, h1 = sg.lag == 1 ? 1 : h0;
+        for (int h = h0; h <= h1; ++h) {
+          if (!mbar_wait_warp(&bar.p_full[h], it[h] & 1, err)) {
             failed = true;
             break;
           }
+          ++it[h];
           tc_fence_after();
-          if (lane == 0) {
-            if (sg.lag == 1) {
-              qk(0, 0, nt);
-              qk(1, 1, nt);
-            } else {
-              qk(j, 0, nt);
-            }
-            umma_commit_pair(&bar.empty[nt % C::SLOTS]);
-            if (j == sg.nk - 1) umma_commit_pair(&bar.q_empty);
+          if (elect_one()) {
+            pv(h, nv, j < sg.lag);
+            if (h == h1) umma_commit(&bar.empty[nv % C::SLOTS]);
           }
           __syncwarp();
-        }
-        for (int j = 0; j < sg.nk && !failed; ++j) {
-          const uint32_t nv = nt++;
-          const bool more = j + sg.lag < sg.nk;
-          const uint32_t nn = more ? nt++ : 0;
-          if (!tile_here(nv, w.g.len - (w.k0 + j) * KT)) {
-            failed = true;
-            break;
-          }
-          const int h0 = sg.lag == 1 ? 0 : j & 1, h1 = sg.lag == 1 ? 1 : h0;
-          for (int h = h0; h <= h1; ++h) {
-            if (!mbar_wait_warp_cluster(&bar.p_full[h], it[h] & 1, err)) {
+          if (more) {
+            if (h == h0 && !tile_here(nn, KT)) {
               failed = true;
               break;
             }
-            ++it[h];
             tc_fence_after();
-            if (lane == 0) {
-              pv(h, nv, j < sg.lag);
-              if (h == h1) umma_commit_pair(&bar.empty[nv % C::SLOTS]);
+            if (elect_one()) {
+              qk(h, sg.lag == 1 ? h : 0, nn);
+              if (h == h1) {
+                umma_commit(&bar.empty[nn % C::SLOTS]);
+                if (j + sg.lag == sg.nk - 1) umma_commit(&bar.q_empty);
+              }
             }
             __syncwarp();
-            if (more) {
-              if (h == h0 && !tile_here(nn, KT)) {
-                failed = true;
-                break;
-              }
-              tc_fence_after();
-              if (lane == 0) {
-                qk(h, sg.lag == 1 ? h : 0, nn);
-                if (h == h1) {
-                  umma_commit_pair(&bar.empty[nn % C::SLOTS]);
-                  if (j + sg.lag == sg.nk - 1) umma_commit_pair(&bar.q_empty);
-                }
-              }
-              __syncwarp();
-            }
           }
         }
       }
-      if (lane == 0) {  // every MMA issued has completed before the tensor memory is released (bounded)
-        umma_commit_pair(&bar.drain);
-        mbar_wait(&bar.drain, 0, err);
-      }
-      __syncwarp();
     }
+    if (elect_one()) {  // every MMA issued has completed before the tensor memory is released (bounded)
+      umma_commit(&bar.drain);
+      mbar_wait(&bar.drain, 0, err);
+    }
+    __syncwarp();
   } else if (BITS == 8 && warp < 12) {
     // ------------------------------ codes to bf16 ------------------------------
     if constexpr (BITS == 8) {
-      set_regs_down<80>();
+      set_regs_down<72>();
       const int t = threadIdx.x - 256;
       uint32_t nt = 0, step0 = 0;
       bool failed = false;
-      while (!failed && w.next(p, block)) {
+      while (!failed && next_segment()) {
         const Segment sg(p, w);
         const size_t row0 = ((size_t)w.p * p.H_kv + w.head) * p.N_cap;
         for (int i = 0; i < sg.tiles(); ++i, ++nt) {
@@ -620,19 +602,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<D, BITS>::THREAD
             break;
           }
           if (!is_v) {
-            // these scales' places were last used eight steps before; the tile slot just found free held
-            // the K of three steps before, whose S was issued after the softmax of two steps before that
+            // these scales' places were last used four steps before, whose softmax is done: the slot just
+            // found free held a tile that was used after it
             const uint32_t gs = step0 + j;
-            sc[gs % SC_SLOTS][0][t] = ks;
-            sc[gs % SC_SLOTS][1][t] = vs;
+            sh.sc[gs % SC_SLOTS][0][t] = ks;
+            sh.sc[gs % SC_SLOTS][1][t] = vs;
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.sc_full[gs % SC_SLOTS]);
           }
           const uint8_t* src = sR + rs * C::RAW;
           uint8_t* dst = sT + cs * C::TILE;
-          // 16 codes a piece; K: 64 rows of D codes, V: 128 rows of D / 2
-          auto widen = [&](int row, int c, int per_row, uint8_t* piece, int swizzle) {
-            const uint4 x = *reinterpret_cast<const uint4*>(src + (row * per_row + c) * 16);
+          // 16 codes a piece; eight lanes take two rows of four pieces, so that their stores meet all banks
+#pragma unroll
+          for (int u = 0; u < D / 16; ++u) {
+            const int row = (t >> 2) + 32 * (u & 3), c = (t & 3) + 4 * (u >> 2);
+            const uint4 x = *reinterpret_cast<const uint4*>(src + row * D + c * 16);
             const uint32_t wd[4] = {x.x, x.y, x.z, x.w};
             uint32_t o[8];
 #pragma unroll
@@ -640,33 +624,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<D, BITS>::THREAD
               o[2 * e] = widen_codes(__byte_perm(wd[e], 0, 0x4140));
               o[2 * e + 1] = widen_codes(__byte_perm(wd[e], 0, 0x4342));
             }
+            uint8_t* piece = dst + (u >> 2) * (KT * 128) + row * 128;
             const int ch = 2 * (c & 3);
-            *reinterpret_cast<uint4*>(piece + ((ch ^ swizzle) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-            *reinterpret_cast<uint4*>(piece + (((ch + 1) ^ swizzle) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
-          };
-          if (!is_v) {
-#pragma unroll
-            for (int u = 0; u < D / 32; ++u) {  // two rows of four pieces to eight lanes: stores of all banks
-              const int row = (t >> 2) + 32 * (u & 1), c = (t & 3) + 4 * (u >> 1);
-              widen(row, c, D / 16, dst + (u >> 1) * (64 * 128) + row * 128, row & 7);
-            }
-          } else if (D == 128) {
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const int row = (t >> 2) + 32 * u;
-              widen(row, t & 3, 4, dst + row * 128, row & 7);
-            }
-          } else {
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {  // rows of 64 bytes, 64-byte swizzle
-              const int row = (t >> 1) + 64 * u;
-              widen(row, t & 1, 2, dst + row * 64, (row >> 1) & 3);
-            }
+            *reinterpret_cast<uint4*>(piece + ((ch ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4*>(piece + (((ch + 1) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
           }
           fence_proxy_async();
           __syncwarp();
           if (lane == 0) {
-            mbar_arrive_at(&bar.full[cs], 0);
+            mbar_arrive(&bar.full[cs]);
             mbar_arrive(&bar.raw_empty[rs]);
           }
         }
@@ -674,13 +640,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<D, BITS>::THREAD
       }
     }
   } else {
-    if constexpr (BITS == 8) set_regs_down<64>();
+    set_regs_down<BITS == 8 ? 56 : 72>();
   }
   __syncthreads();
-  cluster_sync_all();  // nothing of this CTA is read, written or arrived on from the other any more
   if (warp == C::ISSUER) {
     tc_fence_after();
-    tmem_dealloc_pair(tmem, 512);
+    tmem_dealloc(tmem, 512);
   }
 }
 
@@ -695,24 +660,18 @@ cudaError_t launch_t(const PrefixParams& p, cudaStream_t s) {
     const uint32_t box[4] = {64, (uint32_t)p.GQ, 1, (uint32_t)(128 / p.GQ)};
     if (!encode_tensor_map(&mapQ, p.q, 4, dims, strides, box)) return cudaErrorInvalidValue;
   }
-  // K: 64 keys of all columns; V: all 128 keys of D / 2 columns
   const uint64_t rowb = (uint64_t)D * BITS / 8;
   const uint64_t dims[3] = {(uint64_t)D, (uint64_t)p.N_cap, (uint64_t)p.P * p.H_kv};
   const uint64_t strides[2] = {rowb, (uint64_t)p.N_cap * rowb};
-  const uint32_t boxK[3] = {BITS == 8 ? (uint32_t)D : 64u, 64, 1}, boxV[3] = {(uint32_t)D / 2, (uint32_t)KT, 1};
-  if (BITS == 8) {
-    if (!encode_tensor_map_kind(&mapK, p.K, 3, dims, strides, boxK, TileKind::BYTES)) return cudaErrorInvalidValue;
-    if (!encode_tensor_map_kind(&mapV, p.V, 3, dims, strides, boxV, TileKind::BYTES)) return cudaErrorInvalidValue;
-  } else {
-    if (!encode_tensor_map(&mapK, p.K, 3, dims, strides, boxK)) return cudaErrorInvalidValue;
-    if (!(D == 128 ? encode_tensor_map(&mapV, p.V, 3, dims, strides, boxV)
-                   : encode_tensor_map_kind(&mapV, p.V, 3, dims, strides, boxV, TileKind::BF16_SW64)))
-      return cudaErrorInvalidValue;
-  }
+  const uint32_t box[3] = {BITS == 8 ? (uint32_t)D : 64u, (uint32_t)KT, 1};  // 128 keys
+  auto encode = BITS == 8 ? encode_byte_tensor_map : encode_tensor_map;
+  if (!encode(&mapK, p.K, 3, dims, strides, box) || !encode(&mapV, p.V, 3, dims, strides, box)) return cudaErrorInvalidValue;
+  constexpr size_t smem = C::TILES + sizeof(Shared<BITS>);
+  static_assert(smem <= 227 * 1024, "a block's shared memory");
   auto kern = prefix_tc_kernel<D, BITS>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  kern<<<2 * p.blocks, C::THREADS, C::SMEM, s>>>(mapQ, mapK, mapV, p);
+  kern<<<p.blocks, C::THREADS, smem, s>>>(mapQ, mapK, mapV, p);
   return cudaGetLastError();
 }
 
