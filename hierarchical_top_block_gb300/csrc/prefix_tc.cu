@@ -239,6 +239,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
     set_regs_up<BITS == 8 ? 192 : 216>();
     const int h = warp >> 2;                                 // stream
     const int trow = (warp & 3) * 32 + lane;                 // TMEM lane
+    const int q = lane & 3;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_tmem = tmem + lanes + 128 * h, o_tmem = tmem + lanes + 256 + 128 * h;
     uint32_t it[2] = {0, 0}, step0 = 0, meets = 0;           // the streams' steps; all steps
@@ -247,60 +248,87 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
       const Segment sg(p, w);
       const int local = (sg.lag == 1 ? 128 * h : 0) + trow;  // row in the tile
       const bool live = local < sg.rows, any = local - lane < sg.rows;
-      float m = NEG_INF, top = NEG_INF;  // reference and maximum, log2 units
-      unsigned long long l2 = pack_f32x2(0.f, 0.f);
+      // rows r, r + 8, r + 16, r + 24 of the warp's 32: a lane holds a quarter of the columns of each, so a key's
+      // scales are wanted by eight lanes only and fit in registers
+      float m[4], top[4];              // reference and maximum, log2 units
+      unsigned long long l2[4];        // a lane's share of the sum, even and odd columns
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        m[i] = top[i] = NEG_INF;
+        l2[i] = pack_f32x2(0.f, 0.f);
+      }
       uint32_t n = it[h];
       for (int j = sg.lag == 1 ? 0 : h; j < sg.nk; j += sg.lag, ++n) {
         const int valid = min(KT, w.g.len - (w.k0 + j) * KT);
         const uint32_t gs = step0 + j;
-        if (!mbar_wait_warp(&bar.s_full[h], n & 1, err)) {
-          failed = true;
-          break;
-        }
-        if constexpr (BITS == 8) {  // done already (S was formed from the same tile): makes the scales visible
+        float2 kf[BITS == 8 ? 16 : 1];
+        if constexpr (BITS == 8) {
           if (!mbar_wait_warp(&bar.sc_full[gs % SC_SLOTS], (gs / SC_SLOTS) & 1, err)) {
             failed = true;
             break;
           }
+#pragma unroll
+          for (int g = 0; g < 16; ++g) kf[g] = *reinterpret_cast<const float2*>(&sh.sc[gs % SC_SLOTS][0][8 * g + 2 * q]);
+        }
+        if (!mbar_wait_warp(&bar.s_full[h], n & 1, err)) {
+          failed = true;
+          break;
         }
         tc_fence_after();
         if (any) {
-          uint32_t s[KT];
+          uint32_t s[2][64];  // [rows below / from 16][four a group of 8 columns]
 #pragma unroll
-          for (int c = 0; c < KT; c += 32) tmem_ld32(s_tmem + c, *reinterpret_cast<uint32_t(*)[32]>(s + c));
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) tmem_ld_16x64(s_tmem + ((uint32_t)(16 * i) << 16) + 64 * c, &s[i][32 * c]);
           tmem_wait_ld();
           if constexpr (BITS == 8) {
-            const float4* ks = reinterpret_cast<const float4*>(sh.sc[gs % SC_SLOTS][0]);
 #pragma unroll
-            for (int c = 0; c < KT; c += 4) {
-              const float4 f = ks[c / 4];
-              float x[4];
-              unpack_f32x2(mul_f32x2(pack_u32x2(s[c], s[c + 1]), pack_f32x2(f.x, f.y)), x[0], x[1]);
-              unpack_f32x2(mul_f32x2(pack_u32x2(s[c + 2], s[c + 3]), pack_f32x2(f.z, f.w)), x[2], x[3]);
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) s[c + e] = __float_as_uint(x[e]);
-            }
+              for (int g = 0; g < 16; ++g)
+#pragma unroll
+                for (int e = 0; e < 4; e += 2) {
+                  float x, y;
+                  unpack_f32x2(mul_f32x2(pack_u32x2(s[i][4 * g + e], s[i][4 * g + e + 1]), pack_f32x2(kf[g].x, kf[g].y)), x, y);
+                  s[i][4 * g + e] = __float_as_uint(x);
+                  s[i][4 * g + e + 1] = __float_as_uint(y);
+                }
           }
           if (valid < KT) {
 #pragma unroll
-            for (int c = 0; c < KT; ++c)
-              if (c >= valid) s[c] = __float_as_uint(NEG_INF);
-          }
-          float mx[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
+            for (int g = 0; g < 16; ++g)
 #pragma unroll
-          for (int c = 0; c < KT; c += 8) {
+              for (int c = 0; c < 2; ++c)
+                if (8 * g + 2 * q + c >= valid)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              mx[e] = fmaxf(fmaxf(mx[e], __uint_as_float(s[c + e])), __uint_as_float(s[c + 4 + e]));
+                  for (int i = 0; i < 2; ++i) s[i][4 * g + c] = s[i][4 * g + 2 + c] = __float_as_uint(NEG_INF);
           }
-          top = fmaxf(top, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.sl2);
-          if (__any_sync(0xffffffffu, top > m + MAX_GROWTH)) {
-            // the reference follows the maximum; O (of the steps before) with it
-            const float f = top == NEG_INF ? 1.f : fast_exp2(m - top);
-            m = top;
-            float a, b;
-            unpack_f32x2(l2, a, b);
-            l2 = pack_f32x2(a * f, b * f);
+          bool moved = false;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t* x = &s[i >> 1][2 * (i & 1)];
+            float a = NEG_INF, b = NEG_INF;
+#pragma unroll
+            for (int g = 0; g < 16; g += 2) {
+              a = fmaxf(fmaxf(a, __uint_as_float(x[4 * g])), __uint_as_float(x[4 * g + 1]));
+              b = fmaxf(fmaxf(b, __uint_as_float(x[4 * g + 4])), __uint_as_float(x[4 * g + 5]));
+            }
+            a = fmaxf(a, b);
+            a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
+            a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
+            top[i] = fmaxf(top[i], a * p.sl2);
+            moved = moved || top[i] > m[i] + MAX_GROWTH;
+          }
+          if (__any_sync(0xffffffffu, moved)) {
+            // the references follow the maxima; O (of the steps before) with them
+            float f[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              f[i] = top[i] == NEG_INF ? 1.f : fast_exp2(m[i] - top[i]);
+              m[i] = top[i];
+              l2[i] = mul_f32x2(l2[i], pack_f32x2(f[i], f[i]));
+            }
             if (n != it[h]) {
               if (!mbar_wait_warp(&bar.o_done[h], (n - 1) & 1, err)) {
                 failed = true;
@@ -308,38 +336,50 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
               }
               tc_fence_after();
 #pragma unroll 1
-              for (int c = 0; c < D; c += 16) {
-                uint32_t r[16];
-                tmem_ld16(o_tmem + c, r);
+              for (int c = 0; c < 2 * D; c += 16) {  // columns c mod D of rows below 16, then from 16
+                const bool up = c >= D;
+                const uint32_t at = o_tmem + ((up ? 16u : 0u) << 16) + (up ? c - D : c);
+                const float fa = up ? f[2] : f[0], fb = up ? f[3] : f[1];
+                uint32_t r[8];
+                tmem_ld_16x16(at, r);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
-                tmem_st16(o_tmem + c, r);
+                for (int e = 0; e < 8; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * ((e & 2) ? fb : fa));
+                tmem_st_16x16(at, r);
               }
-              tmem_wait_st();
             }
           }
-          const float ref = m == NEG_INF ? 0.f : -m;
-          const unsigned long long sl2 = pack_f32x2(p.sl2, p.sl2), ref2 = pack_f32x2(ref, ref);
+          const unsigned long long sl2 = pack_f32x2(p.sl2, p.sl2);
+          unsigned long long ref[4];
 #pragma unroll
-          for (int c = 0; c < KT; c += 32) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              float x, y;
-              unpack_f32x2(fma_f32x2(pack_u32x2(s[c + e], s[c + e + 1]), sl2, ref2), x, y);
-              x = fast_exp2(x);
-              y = fast_exp2(y);
-              unsigned long long xy = pack_f32x2(x, y);
-              l2 = add_f32x2(l2, xy);
-              if constexpr (BITS == 8) {
-                const float2 f = *reinterpret_cast<const float2*>(&sh.sc[gs % SC_SLOTS][1][c + e]);
-                unpack_f32x2(mul_f32x2(xy, pack_f32x2(f.x, f.y)), x, y);
-              }
-              pk[e / 2] = pack_bf16x2(x, y);
-            }
-            tmem_st16(s_tmem + c / 2, pk);
+          for (int i = 0; i < 4; ++i) {
+            const float x = m[i] == NEG_INF ? 0.f : -m[i];
+            ref[i] = pack_f32x2(x, x);
           }
+#pragma unroll
+          for (int c = 0; c < 2; ++c)  // 64 keys
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              uint32_t pk[16];
+#pragma unroll
+              for (int g = 0; g < 8; ++g) {
+                float2 vf = make_float2(1.f, 1.f);
+                if constexpr (BITS == 8) vf = *reinterpret_cast<const float2*>(&sh.sc[gs % SC_SLOTS][1][64 * c + 8 * g + 2 * q]);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {  // row r + 16 i + 8 e
+                  const uint32_t* x = &s[i][32 * c + 4 * g + 2 * e];
+                  float a, b;
+                  unpack_f32x2(fma_f32x2(pack_u32x2(x[0], x[1]), sl2, ref[2 * i + e]), a, b);
+                  a = fast_exp2(a);
+                  b = fast_exp2(b);
+                  const unsigned long long ab = pack_f32x2(a, b);
+                  l2[2 * i + e] = add_f32x2(l2[2 * i + e], ab);
+                  if constexpr (BITS == 8) unpack_f32x2(mul_f32x2(ab, pack_f32x2(vf.x, vf.y)), a, b);
+                  pk[2 * g + e] = pack_bf16x2(a, b);
+                }
+              }
+              tmem_st_16x32(s_tmem + ((uint32_t)(16 * i) << 16) + 32 * c, pk);
+            }
           tmem_wait_st();
         }
         tc_fence_before();
@@ -352,9 +392,17 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
       it[1] += n1;
       step0 += sg.nk;
       if (failed) break;
-      float la, lb;
-      unpack_f32x2(l2, la, lb);
-      float l = la + lb;
+      // from here on a row a thread: each row's maximum and sum go through shared memory
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float a, b;
+        unpack_f32x2(l2[i], a, b);
+        a += b;
+        a += __shfl_xor_sync(0xffffffffu, a, 1);
+        a += __shfl_xor_sync(0xffffffffu, a, 2);
+        if (q == 0) sh.ml[h][(warp & 3) * 32 + 8 * i + (lane >> 2)] = make_float2(m[i], a);
+      }
+      __syncwarp();
       RowOut out = row_out<D>(p, w, local, live);
       if (sg.lag == 1) {
         if (!mbar_wait_warp(&bar.o_done[h], (it[h] - 1) & 1, err)) {
@@ -363,7 +411,8 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
         }
         tc_fence_after();
         if (any) {
-          put_stats(p, out, local, m, l, true);
+          const float2 ml = sh.ml[h][trow];
+          put_stats(p, out, local, ml.x, ml.y, true);
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
             uint32_t r[32];
@@ -373,6 +422,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
           }
         }
         tc_fence_before();
+        __syncwarp();  // sh.ml has been read
       } else {
         // both streams have parts of every row: joined here, half of the columns by each warpgroup
         if (!mbar_wait_warp(&bar.o_done[0], (it[0] - 1) & 1, err) ||
@@ -380,8 +430,6 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
           failed = true;
           break;
         }
-        sh.ml[h][trow] = make_float2(m, l);
-        __syncwarp();
         if (lane == 0) mbar_arrive(&bar.x_full);
         if (!mbar_wait_warp(&bar.x_full, meets & 1, err)) {  // (the row's own log-sum-exp has been read by both)
           failed = true;
@@ -390,9 +438,9 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
         tc_fence_after();
         if (any) {
           const float2 a = sh.ml[0][trow], b = sh.ml[1][trow];
-          m = fmaxf(a.x, b.x);
+          const float m = fmaxf(a.x, b.x);
           const float f0 = a.x == NEG_INF ? 0.f : fast_exp2(a.x - m), f1 = b.x == NEG_INF ? 0.f : fast_exp2(b.x - m);
-          l = (a.x == NEG_INF ? a.y : a.y * f0) + (b.x == NEG_INF ? b.y : b.y * f1);
+          const float l = (a.x == NEG_INF ? a.y : a.y * f0) + (b.x == NEG_INF ? b.y : b.y * f1);
           put_stats(p, out, local, m, l, h == 0);
           const uint32_t o0 = tmem + lanes + 256;
 #pragma unroll 1
