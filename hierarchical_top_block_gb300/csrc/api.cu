@@ -411,8 +411,11 @@ bool encode_tensor_map(CUtensorMap* map, const void* base, int rank, const uint6
 }
 
 bool encode_byte_tensor_map(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
-                            const uint64_t* strides_bytes, const uint32_t* box) {
-  return encode(map, base, rank, dims, strides_bytes, box, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_NONE);
+                            const uint64_t* strides_bytes, const uint32_t* box, int swizzle) {
+  return encode(map, base, rank, dims, strides_bytes, box, CU_TENSOR_MAP_DATA_TYPE_UINT8,
+                swizzle == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+                : swizzle == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                : CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 }  // namespace pisa

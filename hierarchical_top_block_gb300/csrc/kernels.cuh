@@ -112,8 +112,8 @@ cudaError_t launch_wait_check(uint64_t limit_ns, uint32_t* err, cudaStream_t s);
 // Tensor-map encoding through the driver entry point (no link-time libcuda dependency).
 bool encode_tensor_map(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
                        const uint64_t* strides_bytes, const uint32_t* box);
-// The same for bytes, unswizzled.
+// The same for bytes, swizzled over rows of `swizzle` bytes (0: not, 64 or 128).
 bool encode_byte_tensor_map(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
-                            const uint64_t* strides_bytes, const uint32_t* box);
+                            const uint64_t* strides_bytes, const uint32_t* box, int swizzle);
 
 }  // namespace pisa

@@ -4,8 +4,7 @@
 //
 // Reading the prefix once for the whole group is the point: G_Q n_p query rows share each key, so
 // with few rows the reads bound the work, and with many the products do (4 d operations a row
-// and key).  Few rows: the kernel here, 16 rows a tile on mma.sync with the cache read straight into
-// registers.  Many: prefix_tc.cu.
+// and key).  Few rows: the kernel here, on mma.sync.  Many: prefix_tc.cu.
 #include <algorithm>
 
 #include "cache_attn.cuh"
@@ -17,7 +16,6 @@ namespace pisa {
 namespace {
 
 constexpr int THREADS = 128;
-constexpr int FEW_ROWS = 16;
 
 // Joins a finished row's prefix part with its own part (log-sum-exp `own`) and writes one element.
 __device__ __forceinline__ void write_out(const PrefixParams& p, size_t at, size_t row, bool write_lse, float acc,
@@ -30,55 +28,105 @@ __device__ __forceinline__ void write_out(const PrefixParams& p, size_t at, size
   if (write_lse && p.lse) p.lse[row] = lse;
 }
 
-template <int D, int BITS, bool HI>
-__global__ void __launch_bounds__(THREADS) prefix_few_kernel(PrefixParams p) {
+// Few rows: RT tiles of 16, on mma.sync.  One warp copies granules of the prefix into a ring (TMA),
+// four take them: warp w has row tile w mod RT and the granules of key part w / RT.
+template <int D, int BITS, bool HI, int RT>
+__global__ void __launch_bounds__(THREADS + 32, 2) prefix_few_kernel(const __grid_constant__ CUtensorMap mapK,
+                                                                  const __grid_constant__ CUtensorMap mapV,
+                                                                  PrefixParams p) {
   pdl_trigger();
   using Tile = CacheTile<D, BITS>;
-  __shared__ float po[4 * 16 * D];
-  __shared__ float pm[4][16], pl[4][16], bm[16], bl[16], bo[16];
+  using Ring = GranuleRing<D, BITS>;
+  constexpr int ROWS = 16 * RT, PARTS = 4 / RT;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  float* po = reinterpret_cast<float*>(smem + Ring::SLOTS * Tile::BYTES);  // [4][16][D]
+  __shared__ Ring ring;
+  __shared__ float sm[4][16], sn[4][16], sl[4][16], bo[ROWS];
+  __shared__ float2 ml[ROWS];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, q = lane & 3;
+  if (threadIdx.x == 0) ring.init(RT);
+  __syncthreads();
   PrefixWalk w;
   w.init(p, blockIdx.x, blockIdx.x == 0 && warp == 0);
+  uint32_t s0 = 0;  // granules of the segments before
+  if (warp == 4) {
+    // ------------------------------ copies ------------------------------
+    bool failed = false;
+    while (!failed && w.next(p, blockIdx.x)) {
+      const int key_end = min(w.g.len, w.k1 * PREFIX_KT);
+      for (int key0 = w.k0 * PREFIX_KT; key0 < key_end; key0 += Tile::KEYS, ++s0) {
+        if (!mbar_wait_warp(&ring.empty[s0 % Ring::SLOTS], ((s0 / Ring::SLOTS) & 1) ^ 1, p.err)) {
+          failed = true;
+          break;
+        }
+        if (lane == 0)
+          Tile::copy(smem + (s0 % Ring::SLOTS) * Tile::BYTES, &mapK, &mapV, &ring.full[s0 % Ring::SLOTS], key0,
+                     w.p * p.H_kv + w.head);
+      }
+    }
+    // copies still in flight land before shared memory goes away (bounded; the others wait for theirs too)
+    for (uint32_t u = s0 > Ring::SLOTS ? s0 - Ring::SLOTS : 0; u < s0; ++u)
+      mbar_wait_warp(&ring.full[u % Ring::SLOTS], (u / Ring::SLOTS) & 1, p.err, 100000000ull);
+    return;
+  }
+  auto sync = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
+  const int rt = warp % RT, part = warp / RT;
+  bool failed = false;
   while (w.next(p, blockIdx.x)) {
-    const int m0 = w.tile * FEW_ROWS;                       // first query row of the tile
-    const int rows = min(FEW_ROWS, w.g.n * p.GQ - m0);      // query row m: token m / G, head m % G
-    uint32_t qa[Tile::QW], qb[Tile::QW];
+    const int m0 = w.tile * ROWS;                           // first query row of the tile
+    const int rows = min(ROWS, w.g.n * p.GQ - m0);          // query row m: token m / G, head m % G
     auto q_row = [&](int i) {
       const int m = m0 + i, tok = m / p.GQ;
       return ((size_t)(w.g.first + tok) * p.H_q + (size_t)w.head * p.GQ + (m - tok * p.GQ));
     };
-    Tile::load_q(p.q + q_row(r < rows ? r : 0) * D, r < rows, q, qa);
-    Tile::load_q(p.q + q_row(r + 8 < rows ? r + 8 : 0) * D, HI && r + 8 < rows, q, qb);
+    typename Tile::Query qr;
+    {
+      const int ra = 16 * rt + r, rb = ra + 8;
+      Tile::template load_q<HI>(qr, ra < rows ? p.q + q_row(ra) * D : nullptr, rb < rows ? p.q + q_row(rb) * D : nullptr,
+                                p.sl2, q);
+    }
     const size_t ph = (size_t)w.p * p.H_kv + w.head;
-    const uint8_t* K = p.K + ph * p.N_cap * Tile::ROWB;
-    const uint8_t* V = p.V + ph * p.N_cap * Tile::ROWB;
     const float* ks = BITS == 8 ? p.ks + ph * p.N_cap : nullptr;
     const float* vs = BITS == 8 ? p.vs + ph * p.N_cap : nullptr;
     typename Tile::State st;
     Tile::clear(st);
-    const int key_end = min(w.g.len, w.k1 * PREFIX_KT);
-    for (int key0 = w.k0 * PREFIX_KT + warp * Tile::KEYS; key0 < key_end; key0 += 4 * Tile::KEYS) {
-      const int n = min(Tile::KEYS, key_end - key0);
-      typename Tile::Regs regs;
-      Tile::load(regs, K, V, ks, vs, key0, n, r, q);
-      Tile::template add<HI>(st, regs, qa, qb, n, p.sl2, q);
+    const int first = w.k0 * PREFIX_KT, key_end = min(w.g.len, w.k1 * PREFIX_KT);
+    const int granules = key_end > first ? (key_end - first + Tile::KEYS - 1) / Tile::KEYS : 0;
+    typename Tile::Scales sc, next_sc;
+    auto scales = [&](typename Tile::Scales& x, int g) {
+      if (g < granules) Tile::load_scales(x, ks, vs, first + g * Tile::KEYS, min(Tile::KEYS, key_end - first - g * Tile::KEYS), q);
+    };
+    const int g0 = (int)((part + PARTS - s0 % PARTS) % PARTS);  // the first of this warp's: s0 + g = part mod PARTS
+    scales(sc, g0);
+    for (int g = g0; g < granules && !failed; g += PARTS) {
+      const uint32_t slot = (s0 + g) % Ring::SLOTS, phase = ((s0 + g) / Ring::SLOTS) & 1;
+      scales(next_sc, g + PARTS);
+      if (!mbar_wait_warp(&ring.full[slot], phase, p.err)) {
+        failed = true;
+        break;
+      }
+      if (16 * rt < rows)
+        Tile::template add<HI>(st, smem_u32(smem + slot * Tile::BYTES), sc, qr, min(Tile::KEYS, key_end - first - g * Tile::KEYS), r, q);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ring.empty[slot]);
+      sc = next_sc;
     }
+    s0 += granules;
     // read before any row is written: lse may be lse_own
     if (threadIdx.x < rows) bo[threadIdx.x] = p.lse_own ? p.lse_own[q_row(threadIdx.x)] : NEG_INF;
-    join_warps<D, BITS, HI>(st, po, pm, pl, bm, bl, rows);
-    __syncthreads();
+    join_warps<D, BITS, HI, RT>(st, po, sm, sn, sl, ml, rows, sync);
     if (w.slot < 0) {
       for (int i = threadIdx.x; i < rows * D; i += THREADS) {
         const int row = i / D, c = i - row * D;
         const size_t orow = q_row(row);
-        write_out(p, orow * D + c, orow, c == 0, po[i], bm[row], bl[row], bo[row]);
+        write_out(p, orow * D + c, orow, c == 0, po[i], ml[row].x, ml[row].y, bo[row]);
       }
     } else {
-      float* dst = p.part_o + (size_t)w.slot * FEW_ROWS * D;
+      float* dst = p.part_o + (size_t)w.slot * ROWS * D;
       for (int i = threadIdx.x; i < rows * D; i += THREADS) dst[i] = po[i];
-      if (threadIdx.x < rows) p.part_ml[(size_t)w.slot * FEW_ROWS + threadIdx.x] = make_float2(bm[threadIdx.x], bl[threadIdx.x]);
+      if (threadIdx.x < rows) p.part_ml[(size_t)w.slot * ROWS + threadIdx.x] = ml[threadIdx.x];
     }
-    __syncthreads();  // the next segment writes the shared arrays again
+    sync();  // the next segment writes the shared arrays again
   }
 }
 
@@ -201,28 +249,48 @@ __global__ void __launch_bounds__(THREADS) prefix_join_kernel(PrefixParams p) {
 constexpr int MAX_SMS = 152;  // this GPU's: the scratch does not depend on the device at hand
 
 // Which kernel, by the query rows a group has on average (the groups' own sizes are on the device;
-// either kernel takes any).
+// any kernel takes any).
 struct Plan {
-  bool tc;
+  int tiles;   // row tiles of 16 on mma.sync; 0: the tensor-core kernel
   int rows, blocks;
 };
 Plan prefix_plan(const Problem& p) {
 #ifdef PISA_FORCE
-  const bool tc = PISA_FORCE;
+  const int tiles = PISA_FORCE;
 #else
-  const bool tc = (long long)p.N * p.GQ > 16LL * p.B;
+  const long long rows = ((long long)p.N * p.GQ + p.B - 1) / (p.B > 0 ? p.B : 1);
+  const int tiles = rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= 64 ? 4 : 0;
 #endif
-  return tc ? Plan{true, TC_ROWS, MAX_SMS} : Plan{false, FEW_ROWS, 2 * MAX_SMS};
+  return tiles ? Plan{tiles, 16 * tiles, 2 * MAX_SMS} : Plan{0, TC_ROWS, MAX_SMS};
+}
+
+template <int D, int BITS, bool HI, int RT>
+cudaError_t launch_few_t(const CUtensorMap& mapK, const CUtensorMap& mapV, const PrefixParams& p, cudaStream_t s) {
+  constexpr size_t smem = GranuleRing<D, BITS>::SLOTS * CacheTile<D, BITS>::BYTES + 4 * 16 * D * sizeof(float);
+  auto kern = prefix_few_kernel<D, BITS, HI, RT>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  kern<<<p.blocks, THREADS + 32, smem, s>>>(mapK, mapV, p);
+  return cudaGetLastError();
 }
 
 template <int D, int BITS>
-cudaError_t launch_few(const PrefixParams& p, cudaStream_t s) {
+cudaError_t launch_few(const PrefixParams& p, int tiles, cudaStream_t s) {
+  using Tile = CacheTile<D, BITS>;
+  CUtensorMap mapK, mapV;
+  const uint64_t dims[3] = {(uint64_t)D, (uint64_t)p.N_cap, (uint64_t)p.P * p.H_kv};
+  const uint64_t strides[2] = {(uint64_t)Tile::ROWB, (uint64_t)p.N_cap * Tile::ROWB};
+  const uint32_t box[3] = {BITS == 8 ? (uint32_t)D : 64u, (uint32_t)Tile::KEYS, 1};
+  auto encode = [&](CUtensorMap* map, const void* base) {
+    return BITS == 8 ? encode_byte_tensor_map(map, base, 3, dims, strides, box, Tile::SPAN)
+                     : encode_tensor_map(map, base, 3, dims, strides, box);
+  };
+  if (!encode(&mapK, p.K) || !encode(&mapV, p.V)) return cudaErrorInvalidValue;
+  if (tiles == 4) return launch_few_t<D, BITS, true, 4>(mapK, mapV, p, s);
+  if (tiles == 2) return launch_few_t<D, BITS, true, 2>(mapK, mapV, p, s);
   // a tile has rows above 8 unless all groups together are shorter
-  if ((long long)p.R * p.GQ > 8)
-    prefix_few_kernel<D, BITS, true><<<p.blocks, THREADS, 0, s>>>(p);
-  else
-    prefix_few_kernel<D, BITS, false><<<p.blocks, THREADS, 0, s>>>(p);
-  return cudaGetLastError();
+  return (long long)p.R * p.GQ > 8 ? launch_few_t<D, BITS, true, 1>(mapK, mapV, p, s)
+                                   : launch_few_t<D, BITS, false, 1>(mapK, mapV, p, s);
 }
 
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -270,12 +338,12 @@ cudaError_t launch_prefix_attn(const uint16_t* q, const void* Kp, const void* Vp
   w += up256(parts * 8);
   p.base = reinterpret_cast<long long*>(w);
   cudaError_t e;
-  if (plan.tc)
+  if (plan.tiles == 0)
     e = launch_prefix_tc(p, pr.d, s);
   else if (pr.d == 128)
-    e = k_scale ? launch_few<128, 8>(p, s) : launch_few<128, 16>(p, s);
+    e = k_scale ? launch_few<128, 8>(p, plan.tiles, s) : launch_few<128, 16>(p, plan.tiles, s);
   else
-    e = k_scale ? launch_few<64, 8>(p, s) : launch_few<64, 16>(p, s);
+    e = k_scale ? launch_few<64, 8>(p, plan.tiles, s) : launch_few<64, 16>(p, plan.tiles, s);
   if (e != cudaSuccess) return e;
   const unsigned grid = (unsigned)std::min<long long>((long long)p.R * p.H_q, (long long)num_sms * 16);
   return pr.d == 128 ? launch_pdl(prefix_join_kernel<128>, dim3(grid), dim3(THREADS), 0, s, p)

@@ -25,7 +25,6 @@
 // bounded.
 #include <algorithm>
 
-#include "cache_attn.cuh"
 #include "kernels.cuh"
 #include "pdl.cuh"
 #include "prefix_plan.cuh"
@@ -71,6 +70,16 @@ struct Shared {
   uint32_t tmem;
   __align__(16) float sc[BITS == 8 ? SC_SLOTS : 1][2][BITS == 8 ? KT : 4];  // scales of a step: keys', values'
 };
+
+// Two int8 codes in bytes 0 and 2 of y (bytes 1 and 3: anything) -> bf16x2.  A code is m - 128 s
+// (s its top bit, m the seven below): (128 + m) - 128 (1 + s), both exact bf16 numbers whose
+// bits are 0x4300 | m and 0x4300 | (code & 0x80).
+__device__ __forceinline__ uint32_t widen_codes(uint32_t y) {
+  const uint32_t a = (y & 0x007f007fu) | 0x43004300u, c = (y & 0x00800080u) | 0x43004300u;
+  uint32_t r;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(c));
+  return r;
+}
 
 template <int R>
 __device__ __forceinline__ void set_regs_up() {
@@ -712,8 +721,11 @@ cudaError_t launch_t(const PrefixParams& p, cudaStream_t s) {
   const uint64_t dims[3] = {(uint64_t)D, (uint64_t)p.N_cap, (uint64_t)p.P * p.H_kv};
   const uint64_t strides[2] = {rowb, (uint64_t)p.N_cap * rowb};
   const uint32_t box[3] = {BITS == 8 ? (uint32_t)D : 64u, (uint32_t)KT, 1};  // 128 keys
-  auto encode = BITS == 8 ? encode_byte_tensor_map : encode_tensor_map;
-  if (!encode(&mapK, p.K, 3, dims, strides, box) || !encode(&mapV, p.V, 3, dims, strides, box)) return cudaErrorInvalidValue;
+  auto encode = [&](CUtensorMap* map, const void* base) {
+    return BITS == 8 ? encode_byte_tensor_map(map, base, 3, dims, strides, box, 0)
+                     : encode_tensor_map(map, base, 3, dims, strides, box);
+  };
+  if (!encode(&mapK, p.K) || !encode(&mapV, p.V)) return cudaErrorInvalidValue;
   constexpr size_t smem = C::TILES + sizeof(Shared<BITS>);
   static_assert(smem <= 227 * 1024, "a block's shared memory");
   auto kern = prefix_tc_kernel<D, BITS>;

@@ -84,6 +84,11 @@ CASES = [  # R, H_q, H, d, N, lens, rows
     (513, 1, 1, 128, 131, [131], [0, 513]),
     (2000, 2, 1, 64, 5000, [4321], [0, 2000]),
     (90, 16, 4, 128, 3000, [2990], [0, 90]),
+    # long enough for every ring of tiles to turn many times, by few, some and many rows
+    (2, 16, 8, 128, 60000, [59999], [0, 2]),
+    (16, 16, 8, 64, 70000, [70000], [0, 16]),
+    (6, 32, 4, 128, 50001, [50001], [0, 6]),
+    (37, 16, 4, 128, 50001, [49999], [0, 37]),
 ]
 
 
