@@ -28,49 +28,40 @@ __device__ __forceinline__ void write_out(const PrefixParams& p, size_t at, size
   if (write_lse && p.lse) p.lse[row] = lse;
 }
 
-// Few rows: RT tiles of 16, on mma.sync.  One warp copies granules of the prefix into a ring (TMA),
-// four take them: warp w has row tile w mod RT and the granules of key part w / RT.
-template <int D, int BITS, bool HI, int RT>
-__global__ void __launch_bounds__(THREADS + 32, 2) prefix_few_kernel(const __grid_constant__ CUtensorMap mapK,
-                                                                  const __grid_constant__ CUtensorMap mapV,
-                                                                  PrefixParams p) {
+// Few rows: tiles of 8 NH on mma.sync.  A block's four warps take the granules of a segment in turn,
+// each with a ring of its own that it fills by TMA.
+template <int D, int BITS, int NH>
+struct FewCfg {
+  static constexpr int KEYS = BITS == 8 ? 32 : 16;
+  static constexpr int SLOTS = D == 128 ? 2 : 4;
+  using Tile = CacheTile<D, BITS, KEYS, NH>;
+  static constexpr uint32_t RING = 4 * SLOTS * Tile::BYTES, OUT = 4 * 8 * NH * D * 4;
+  static constexpr uint32_t SMEM = RING > OUT ? RING : OUT;  // the outputs meet where the granules were
+};
+
+template <int D, int BITS, int NH>
+__global__ void __launch_bounds__(THREADS, 3) prefix_few_kernel(const __grid_constant__ CUtensorMap mapK,
+                                                                const __grid_constant__ CUtensorMap mapV,
+                                                                PrefixParams p) {
   pdl_trigger();
-  using Tile = CacheTile<D, BITS>;
-  using Ring = GranuleRing<D, BITS>;
-  constexpr int ROWS = 16 * RT, PARTS = 4 / RT;
+  using C = FewCfg<D, BITS, NH>;
+  using Tile = typename C::Tile;
+  constexpr int ROWS = 8 * NH;
   extern __shared__ __align__(1024) uint8_t smem[];
-  float* po = reinterpret_cast<float*>(smem + Ring::SLOTS * Tile::BYTES);  // [4][16][D]
-  __shared__ Ring ring;
-  __shared__ float sm[4][16], sn[4][16], sl[4][16], bo[ROWS];
+  float* po = reinterpret_cast<float*>(smem);  // [4][ROWS][D]
+  __shared__ uint64_t full[4][C::SLOTS];
+  __shared__ float sn[4][16], sl[4][16], bo[ROWS];
   __shared__ float2 ml[ROWS];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, q = lane & 3;
-  if (threadIdx.x == 0) ring.init(RT);
-  __syncthreads();
+  WarpRing<Tile, C::SLOTS> ring{smem + warp * C::SLOTS * Tile::BYTES, full[warp]};
+  if (lane == 0) {
+    for (int i = 0; i < C::SLOTS; ++i) mbar_init(&full[warp][i], 1);
+    mbar_fence_init();
+  }
+  __syncwarp();
   PrefixWalk w;
   w.init(p, blockIdx.x, blockIdx.x == 0 && warp == 0);
-  uint32_t s0 = 0;  // granules of the segments before
-  if (warp == 4) {
-    // ------------------------------ copies ------------------------------
-    bool failed = false;
-    while (!failed && w.next(p, blockIdx.x)) {
-      const int key_end = min(w.g.len, w.k1 * PREFIX_KT);
-      for (int key0 = w.k0 * PREFIX_KT; key0 < key_end; key0 += Tile::KEYS, ++s0) {
-        if (!mbar_wait_warp(&ring.empty[s0 % Ring::SLOTS], ((s0 / Ring::SLOTS) & 1) ^ 1, p.err)) {
-          failed = true;
-          break;
-        }
-        if (lane == 0)
-          Tile::copy(smem + (s0 % Ring::SLOTS) * Tile::BYTES, &mapK, &mapV, &ring.full[s0 % Ring::SLOTS], key0,
-                     w.p * p.H_kv + w.head);
-      }
-    }
-    // copies still in flight land before shared memory goes away (bounded; the others wait for theirs too)
-    for (uint32_t u = s0 > Ring::SLOTS ? s0 - Ring::SLOTS : 0; u < s0; ++u)
-      mbar_wait_warp(&ring.full[u % Ring::SLOTS], (u / Ring::SLOTS) & 1, p.err, 100000000ull);
-    return;
-  }
-  auto sync = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
-  const int rt = warp % RT, part = warp / RT;
+  uint32_t s = 0, got = 0;  // granules used and fetched
   bool failed = false;
   while (w.next(p, blockIdx.x)) {
     const int m0 = w.tile * ROWS;                           // first query row of the tile
@@ -79,42 +70,39 @@ __global__ void __launch_bounds__(THREADS + 32, 2) prefix_few_kernel(const __gri
       const int m = m0 + i, tok = m / p.GQ;
       return ((size_t)(w.g.first + tok) * p.H_q + (size_t)w.head * p.GQ + (m - tok * p.GQ));
     };
+    const int ph = w.p * p.H_kv + w.head;
+    const int first = w.k0 * PREFIX_KT, key_end = min(w.g.len, w.k1 * PREFIX_KT);
+    const int granules = key_end > first ? (key_end - first + C::KEYS - 1) / C::KEYS : 0;
+#pragma unroll
+    for (int i = 0; i < C::SLOTS; ++i)
+      if (warp + 4 * i < granules && !failed) ring.fetch(got++, &mapK, &mapV, first + (warp + 4 * i) * C::KEYS, ph, lane);
     typename Tile::Query qr;
-    {
-      const int ra = 16 * rt + r, rb = ra + 8;
-      Tile::template load_q<HI>(qr, ra < rows ? p.q + q_row(ra) * D : nullptr, rb < rows ? p.q + q_row(rb) * D : nullptr,
-                                p.sl2, q);
-    }
-    const size_t ph = (size_t)w.p * p.H_kv + w.head;
-    const float* ks = BITS == 8 ? p.ks + ph * p.N_cap : nullptr;
-    const float* vs = BITS == 8 ? p.vs + ph * p.N_cap : nullptr;
+    Tile::load_q(qr, [&](int i) { return i < rows ? p.q + q_row(i) * D : nullptr; }, p.sl2, r, q);
+    const float* ks = BITS == 8 ? p.ks + (size_t)ph * p.N_cap : nullptr;
+    const float* vs = BITS == 8 ? p.vs + (size_t)ph * p.N_cap : nullptr;
     typename Tile::State st;
     Tile::clear(st);
-    const int first = w.k0 * PREFIX_KT, key_end = min(w.g.len, w.k1 * PREFIX_KT);
-    const int granules = key_end > first ? (key_end - first + Tile::KEYS - 1) / Tile::KEYS : 0;
     typename Tile::Scales sc, next_sc;
     auto scales = [&](typename Tile::Scales& x, int g) {
-      if (g < granules) Tile::load_scales(x, ks, vs, first + g * Tile::KEYS, min(Tile::KEYS, key_end - first - g * Tile::KEYS), q);
+      if (g < granules) Tile::load_scales(x, ks, vs, first + g * C::KEYS, min(C::KEYS, key_end - first - g * C::KEYS), r);
     };
-    const int g0 = (int)((part + PARTS - s0 % PARTS) % PARTS);  // the first of this warp's: s0 + g = part mod PARTS
-    scales(sc, g0);
-    for (int g = g0; g < granules && !failed; g += PARTS) {
-      const uint32_t slot = (s0 + g) % Ring::SLOTS, phase = ((s0 + g) / Ring::SLOTS) & 1;
-      scales(next_sc, g + PARTS);
-      if (!mbar_wait_warp(&ring.full[slot], phase, p.err)) {
+    scales(sc, warp);
+    for (int g = warp; g < granules && !failed; g += 4, ++s) {
+      scales(next_sc, g + 4);
+      if (!ring.wait(s, p.err)) {
         failed = true;
         break;
       }
-      if (16 * rt < rows)
-        Tile::template add<HI>(st, smem_u32(smem + slot * Tile::BYTES), sc, qr, min(Tile::KEYS, key_end - first - g * Tile::KEYS), r, q);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ring.empty[slot]);
+      Tile::add(st, ring.at(s), sc, qr, min(C::KEYS, key_end - first - g * C::KEYS), r, q);
+      __syncwarp();  // the slot has been read
+      if (g + 4 * C::SLOTS < granules) ring.fetch(got++, &mapK, &mapV, first + (g + 4 * C::SLOTS) * C::KEYS, ph, lane);
       sc = next_sc;
     }
-    s0 += granules;
+    if (failed)  // copies still in flight land before their memory is used again (bounded)
+      for (; s < got; ++s) ring.wait(s, p.err, 100000000ull);
     // read before any row is written: lse may be lse_own
     if (threadIdx.x < rows) bo[threadIdx.x] = p.lse_own ? p.lse_own[q_row(threadIdx.x)] : NEG_INF;
-    join_warps<D, BITS, HI, RT>(st, po, sm, sn, sl, ml, rows, sync);
+    join_warps<Tile, D>(st, po, sn, sl, ml, rows);
     if (w.slot < 0) {
       for (int i = threadIdx.x; i < rows * D; i += THREADS) {
         const int row = i / D, c = i - row * D;
@@ -126,7 +114,8 @@ __global__ void __launch_bounds__(THREADS + 32, 2) prefix_few_kernel(const __gri
       for (int i = threadIdx.x; i < rows * D; i += THREADS) dst[i] = po[i];
       if (threadIdx.x < rows) p.part_ml[(size_t)w.slot * ROWS + threadIdx.x] = ml[threadIdx.x];
     }
-    sync();  // the next segment writes the shared arrays again
+    fence_proxy_async();  // the next copies go where po was
+    __syncthreads();
   }
 }
 
@@ -162,7 +151,8 @@ __global__ void __launch_bounds__(THREADS) prefix_join_kernel(PrefixParams p) {
     const int mrow = (row - g.first) * p.GQ + (hq - head * p.GQ);
     const int tile = mrow / p.rows, local = mrow - tile * p.rows;
     const long long s0 = p.base[gp] + ((long long)head * g.tiles + tile) * g.steps, s1 = s0 + g.steps;
-    const int c0 = block_of(s0, len), c1 = block_of(s1 - 1, len);
+    // (in range as long as nobody changes lengths or bounds under the call)
+    const int c0 = min(block_of(s0, len), p.blocks - 1), c1 = min(block_of(s1 - 1, len), p.blocks - 1);
     if (c0 == c1) continue;  // finished by its block
     const int slot0 = 2 * c0 + (len * c0 == s0 ? 0 : 1);
     const float own = p.lse_own ? p.lse_own[i] : NEG_INF;
@@ -246,51 +236,47 @@ __global__ void __launch_bounds__(THREADS) prefix_join_kernel(PrefixParams p) {
   }
 }
 
+constexpr int FEW_PER_SM = 3;  // blocks of the few-row kernel
 constexpr int MAX_SMS = 152;  // this GPU's: the scratch does not depend on the device at hand
 
 // Which kernel, by the query rows a group has on average (the groups' own sizes are on the device;
 // any kernel takes any).
 struct Plan {
-  int tiles;   // row tiles of 16 on mma.sync; 0: the tensor-core kernel
+  bool tc;
   int rows, blocks;
 };
 Plan prefix_plan(const Problem& p) {
-#ifdef PISA_FORCE
-  const int tiles = PISA_FORCE;
-#else
   const long long rows = ((long long)p.N * p.GQ + p.B - 1) / (p.B > 0 ? p.B : 1);
-  const int tiles = rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= 64 ? 4 : 0;
+#ifdef PISA_FORCE
+  const bool tc = !PISA_FORCE;
+#else
+  const bool tc = rows > 16;
 #endif
-  return tiles ? Plan{tiles, 16 * tiles, 2 * MAX_SMS} : Plan{0, TC_ROWS, MAX_SMS};
+  return tc ? Plan{true, TC_ROWS, MAX_SMS} : Plan{false, rows > 8 ? 16 : 8, FEW_PER_SM * MAX_SMS};
 }
 
-template <int D, int BITS, bool HI, int RT>
-cudaError_t launch_few_t(const CUtensorMap& mapK, const CUtensorMap& mapV, const PrefixParams& p, cudaStream_t s) {
-  constexpr size_t smem = GranuleRing<D, BITS>::SLOTS * CacheTile<D, BITS>::BYTES + 4 * 16 * D * sizeof(float);
-  auto kern = prefix_few_kernel<D, BITS, HI, RT>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
-  kern<<<p.blocks, THREADS + 32, smem, s>>>(mapK, mapV, p);
-  return cudaGetLastError();
-}
-
-template <int D, int BITS>
-cudaError_t launch_few(const PrefixParams& p, int tiles, cudaStream_t s) {
-  using Tile = CacheTile<D, BITS>;
+template <int D, int BITS, int NH>
+cudaError_t launch_few(const PrefixParams& p, cudaStream_t s) {
+  using C = FewCfg<D, BITS, NH>;
   CUtensorMap mapK, mapV;
   const uint64_t dims[3] = {(uint64_t)D, (uint64_t)p.N_cap, (uint64_t)p.P * p.H_kv};
-  const uint64_t strides[2] = {(uint64_t)Tile::ROWB, (uint64_t)p.N_cap * Tile::ROWB};
-  const uint32_t box[3] = {BITS == 8 ? (uint32_t)D : 64u, (uint32_t)Tile::KEYS, 1};
+  const uint64_t strides[2] = {(uint64_t)C::Tile::ROWB, (uint64_t)p.N_cap * C::Tile::ROWB};
+  const uint32_t box[3] = {BITS == 8 ? (uint32_t)D : 64u, (uint32_t)C::KEYS, 1};
   auto encode = [&](CUtensorMap* map, const void* base) {
-    return BITS == 8 ? encode_byte_tensor_map(map, base, 3, dims, strides, box, Tile::SPAN)
+    return BITS == 8 ? encode_byte_tensor_map(map, base, 3, dims, strides, box, C::Tile::SPAN)
                      : encode_tensor_map(map, base, 3, dims, strides, box);
   };
   if (!encode(&mapK, p.K) || !encode(&mapV, p.V)) return cudaErrorInvalidValue;
-  if (tiles == 4) return launch_few_t<D, BITS, true, 4>(mapK, mapV, p, s);
-  if (tiles == 2) return launch_few_t<D, BITS, true, 2>(mapK, mapV, p, s);
-  // a tile has rows above 8 unless all groups together are shorter
-  return (long long)p.R * p.GQ > 8 ? launch_few_t<D, BITS, true, 1>(mapK, mapV, p, s)
-                                   : launch_few_t<D, BITS, false, 1>(mapK, mapV, p, s);
+  auto kern = prefix_few_kernel<D, BITS, NH>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+  if (e != cudaSuccess) return e;
+  kern<<<p.blocks, THREADS, C::SMEM, s>>>(mapK, mapV, p);
+  return cudaGetLastError();
+}
+template <int D>
+cudaError_t launch_few_d(const PrefixParams& p, cudaStream_t s) {
+  if (p.ks) return p.rows > 8 ? launch_few<D, 8, 2>(p, s) : launch_few<D, 8, 1>(p, s);
+  return p.rows > 8 ? launch_few<D, 16, 2>(p, s) : launch_few<D, 16, 1>(p, s);
 }
 
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -338,12 +324,10 @@ cudaError_t launch_prefix_attn(const uint16_t* q, const void* Kp, const void* Vp
   w += up256(parts * 8);
   p.base = reinterpret_cast<long long*>(w);
   cudaError_t e;
-  if (plan.tiles == 0)
+  if (plan.tc)
     e = launch_prefix_tc(p, pr.d, s);
-  else if (pr.d == 128)
-    e = k_scale ? launch_few<128, 8>(p, plan.tiles, s) : launch_few<128, 16>(p, plan.tiles, s);
   else
-    e = k_scale ? launch_few<64, 8>(p, plan.tiles, s) : launch_few<64, 16>(p, plan.tiles, s);
+    e = pr.d == 128 ? launch_few_d<128>(p, s) : launch_few_d<64>(p, s);
   if (e != cudaSuccess) return e;
   const unsigned grid = (unsigned)std::min<long long>((long long)p.R * p.H_q, (long long)num_sms * 16);
   return pr.d == 128 ? launch_pdl(prefix_join_kernel<128>, dim3(grid), dim3(THREADS), 0, s, p)
