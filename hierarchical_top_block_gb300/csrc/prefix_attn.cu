@@ -30,17 +30,23 @@ __device__ __forceinline__ void write_out(const PrefixParams& p, size_t at, size
 
 // Few rows: tiles of 8 NH on mma.sync.  A block's four warps take the granules of a segment in turn,
 // each with a ring of its own that it fills by TMA.
+constexpr int few_blocks(int d, int rows) { return rows > 8 ? 2 : d == 128 ? 4 : 3; }  // a SM
+
 template <int D, int BITS, int NH>
 struct FewCfg {
   static constexpr int KEYS = BITS == 8 ? 32 : 16;
-  static constexpr int SLOTS = D == 128 ? 2 : 4;
+  // granules a warp has under way, and blocks a SM.  Up to 8 rows more blocks beat deeper rings (8 rows x 8
+  // heads, 32768 keys of codes at d = 128: 26.5 us with 1 x 4, 27.0 with 2 x 3, 41 with 4 x 3), which the
+  // registers of 16 rows do not allow (16 rows: 33.0 us with 2 x 2, 33.8 with 1 x 3, 36.2 with 2 x 3).
+  static constexpr int SLOTS = D == 128 && NH == 1 ? 1 : 2;
+  static constexpr int PER_SM = few_blocks(D, 8 * NH);
   using Tile = CacheTile<D, BITS, KEYS, NH>;
   static constexpr uint32_t RING = 4 * SLOTS * Tile::BYTES, OUT = 4 * 8 * NH * D * 4;
   static constexpr uint32_t SMEM = RING > OUT ? RING : OUT;  // the outputs meet where the granules were
 };
 
 template <int D, int BITS, int NH>
-__global__ void __launch_bounds__(THREADS, 3) prefix_few_kernel(const __grid_constant__ CUtensorMap mapK,
+__global__ void __launch_bounds__(THREADS, FewCfg<D, BITS, NH>::PER_SM) prefix_few_kernel(const __grid_constant__ CUtensorMap mapK,
                                                                 const __grid_constant__ CUtensorMap mapV,
                                                                 PrefixParams p) {
   pdl_trigger();
@@ -55,6 +61,8 @@ __global__ void __launch_bounds__(THREADS, 3) prefix_few_kernel(const __grid_con
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, q = lane & 3;
   WarpRing<Tile, C::SLOTS> ring{smem + warp * C::SLOTS * Tile::BYTES, full[warp]};
   if (lane == 0) {
+    prefetch_map(&mapK);
+    prefetch_map(&mapV);
     for (int i = 0; i < C::SLOTS; ++i) mbar_init(&full[warp][i], 1);
     mbar_fence_init();
   }
@@ -124,16 +132,15 @@ __global__ void __launch_bounds__(THREADS, 3) prefix_few_kernel(const __grid_con
 // in flight, each warp with its own running maximum, and meet in shared memory.
 template <int D>
 __global__ void __launch_bounds__(THREADS) prefix_join_kernel(PrefixParams p) {
-  pdl_wait();
   constexpr int V = D / 32, BATCH = 8, WARPS = THREADS / 32;
   __shared__ float so[WARPS][D];
   __shared__ float2 sml[WARPS];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long len = range_len(p.base[p.P], p.blocks);
+  bool waited = false;  // the parts are written by the kernel before, the groups' bounds are not
   for (long long i = blockIdx.x; i < (long long)p.R * p.H_q; i += gridDim.x) {
     const int row = (int)(i / p.H_q), hq = (int)(i - (long long)row * p.H_q);
     int gp = 0;
-    if (p.row_start) {
+    if (p.P > 1) {
       int lo = 0, hi = p.P;  // first group with row_start[g + 1] > row
       while (lo < hi) {
         const int mid = (lo + hi) >> 1;
@@ -150,7 +157,10 @@ __global__ void __launch_bounds__(THREADS) prefix_join_kernel(PrefixParams p) {
     const int head = hq / p.GQ;
     const int mrow = (row - g.first) * p.GQ + (hq - head * p.GQ);
     const int tile = mrow / p.rows, local = mrow - tile * p.rows;
-    const long long s0 = p.base[gp] + ((long long)head * g.tiles + tile) * g.steps, s1 = s0 + g.steps;
+    if (!waited) pdl_wait();
+    waited = true;
+    const long long S = p.P > 1 ? p.base[p.P] : group_steps(p, g), len = range_len(S, p.blocks);
+    const long long s0 = (p.P > 1 ? p.base[gp] : 0) + ((long long)head * g.tiles + tile) * g.steps, s1 = s0 + g.steps;
     // (in range as long as nobody changes lengths or bounds under the call)
     const int c0 = min(block_of(s0, len), p.blocks - 1), c1 = min(block_of(s1 - 1, len), p.blocks - 1);
     if (c0 == c1) continue;  // finished by its block
@@ -234,9 +244,9 @@ __global__ void __launch_bounds__(THREADS) prefix_join_kernel(PrefixParams p) {
     }
     __syncthreads();
   }
+  if (!waited) pdl_wait();  // what comes next on the stream waits for this kernel alone
 }
 
-constexpr int FEW_PER_SM = 3;  // blocks of the few-row kernel
 constexpr int MAX_SMS = 152;  // this GPU's: the scratch does not depend on the device at hand
 
 // Which kernel, by the query rows a group has on average (the groups' own sizes are on the device;
@@ -245,14 +255,15 @@ struct Plan {
   bool tc;
   int rows, blocks;
 };
-Plan prefix_plan(const Problem& p) {
+Plan prefix_plan(const Problem& p, bool codes) {
   const long long rows = ((long long)p.N * p.GQ + p.B - 1) / (p.B > 0 ? p.B : 1);
 #ifdef PISA_FORCE
   const bool tc = !PISA_FORCE;
 #else
-  const bool tc = rows > 16;
+  const bool tc = rows > (codes ? 32 : 16);
 #endif
-  return tc ? Plan{true, TC_ROWS, MAX_SMS} : Plan{false, rows > 8 ? 16 : 8, FEW_PER_SM * MAX_SMS};
+  const int few = rows > 8 ? 16 : 8;
+  return tc ? Plan{true, TC_ROWS, MAX_SMS} : Plan{false, few, few_blocks(p.d, few) * MAX_SMS};
 }
 
 template <int D, int BITS, int NH>
@@ -284,9 +295,12 @@ size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 }  // namespace
 
 size_t prefix_workspace_bytes(const Problem& p) {
-  const Plan plan = prefix_plan(p);
-  const size_t parts = (size_t)2 * plan.blocks * plan.rows;
-  return up256(parts * p.d * 4) + up256(parts * 8) + up256((size_t)(p.B + 1) * 8);
+  size_t most = 0;  // of both kinds of cache
+  for (bool codes : {false, true}) {
+    const Plan plan = prefix_plan(p, codes);
+    most = std::max(most, (size_t)2 * plan.blocks * plan.rows);
+  }
+  return up256(most * p.d * 4) + up256(most * 8) + up256((size_t)(p.B + 1) * 8);
 }
 
 cudaError_t launch_prefix_attn(const uint16_t* q, const void* Kp, const void* Vp, const float* k_scale,
@@ -313,7 +327,7 @@ cudaError_t launch_prefix_attn(const uint16_t* q, const void* Kp, const void* Vp
   p.N_cap = pr.N_cap;
   p.sl2 = pr.scale * LOG2E;
   p.err = err;
-  const Plan plan = prefix_plan(pr);
+  const Plan plan = prefix_plan(pr, k_scale != nullptr);
   p.rows = plan.rows;
   p.blocks = plan.blocks;
   const size_t parts = (size_t)2 * p.blocks * p.rows;

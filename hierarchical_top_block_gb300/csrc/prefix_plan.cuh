@@ -27,7 +27,7 @@ struct PrefixParams {
   float* lse;                // nullable
   float* part_o;             // [2 blocks][ROWS][d] output sums relative to the row maximum
   float2* part_ml;           // [2 blocks][ROWS] row maximum (log2 units) and sum
-  long long* base;           // [P + 1] first step of each group; the last entry is S
+  long long* base;           // [P + 1] first step of each group, then S (with one group: not written)
   int P, R, H_q, H_kv, GQ, N_cap;
   int rows;                  // ROWS
   int blocks;                // thread blocks the steps are divided over
@@ -82,22 +82,31 @@ struct PrefixWalk {
   // Warp-wide.  `record`: this warp writes the groups' first steps and reports bad inputs.
   __device__ __forceinline__ void init(const PrefixParams& prm, int block, bool record) {
     const int lane = threadIdx.x & 31;
+    if (record) {
+      for (int i = lane; i < prm.P; i += 32) {
+        const int n = __ldg(prm.prefix_len + i);
+        bool bad = n < 0 || n > prm.N_cap;
+        if (prm.row_start) {
+          const int a = __ldg(prm.row_start + i), b = __ldg(prm.row_start + i + 1);
+          bad = bad || a < 0 || b < a || b > prm.R;
+        }
+        if (bad) report_error(prm.err, ERR_BAD_INDEX);
+      }
+    }
+    begun = false;
+    p = 0;
+    gbase = 0;
+    if (prm.P == 1) {  // (nobody reads the groups' first steps then)
+      g = prefix_group(prm, 0);
+      const long long S = group_steps(prm, g), len = range_len(S, prm.blocks);
+      at = min(S, len * block);
+      end = min(S, len * (block + 1));
+      return;
+    }
     long long total = 0;
     for (int i0 = 0; i0 < prm.P; i0 += 32) {
       const int i = i0 + lane;
-      long long s = 0;
-      if (i < prm.P) {
-        s = group_steps(prm, prefix_group(prm, i));
-        if (record) {
-          const int n = __ldg(prm.prefix_len + i);
-          bool bad = n < 0 || n > prm.N_cap;
-          if (prm.row_start) {
-            const int a = __ldg(prm.row_start + i), b = __ldg(prm.row_start + i + 1);
-            bad = bad || a < 0 || b < a || b > prm.R;
-          }
-          if (bad) report_error(prm.err, ERR_BAD_INDEX);
-        }
-      }
+      const long long s = i < prm.P ? group_steps(prm, prefix_group(prm, i)) : 0;
       long long x = s;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -109,9 +118,6 @@ struct PrefixWalk {
     }
     if (record && lane == 0) prm.base[prm.P] = total;
     const long long S = total, len = range_len(S, prm.blocks);
-    begun = false;
-    p = 0;
-    gbase = 0;
     at = min(S, len * block);
     end = min(S, len * (block + 1));
     if (at >= end) return;

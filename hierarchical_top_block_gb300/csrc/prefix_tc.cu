@@ -8,15 +8,20 @@
 // only when the maximum has grown by more than 2^8 past it (P stays below 2^8, far from the end of
 // bf16's and of fp32's range, and the division by l at the end is exact whatever m is).  With the
 // usual logits that happens in a job's first steps alone, so O is left where the MMA accumulates it.
-// P is rounded to bf16 (half a step, 2^-8 of each weight, the size of the output's own rounding).
+//
+// A bf16 cache: bf16 operands, P rounded to bf16 (half a step, 2^-8 of each weight, the size of the
+// output's own rounding).  An 8-bit cache: fp16 operands.  Four warps widen the codes, whole numbers,
+// into the swizzled tiles that the MMA reads (two instructions a pair; to bf16 it would be four); Q is
+// brought to at most 2 in magnitude by a power of two a row and kept as fp16 in place (exact but for
+// elements below 2^-14 of the row's largest, which keep 2^-25 of it); the key's scale multiplies the
+// fp32 logit, and the value's scale the weight before it is rounded, 2^-11 of it (2^-25 at least).  The
+// reference then covers the weight times the value's scale: log2 of the largest scale so far is
+// added to the maximum.
 //
 // Two streams keep the tensor pipe busy while the softmax of the other one runs, a warpgroup for
 // each.  With more than 128 rows a stream is a half of the rows, and both use the same tiles; with
 // fewer, both streams have all rows, one the even steps and one the odd ones, each with its own
 // m, l and O, which are joined when a job's segment ends.
-//
-// The 8-bit cache: four warps widen the codes to bf16 (exact) into the swizzled tiles that the MMA
-// reads; the key's scale multiplies the logit and the value's scale the weight, both in fp32.
 //
 // Roles: two softmax warpgroups (a row a thread); a producer warp (TMA); a warp that issues the MMAs;
 // with the 8-bit cache the widening warpgroup.  TMEM: S of stream i at 128 i (its first 64 columns
@@ -38,10 +43,17 @@ constexpr float MAX_GROWTH = 8.f;  // log2 units the maximum may pass a row's re
 template <int D, int BITS>
 struct Cfg {
   static constexpr int THREADS = BITS == 8 ? 512 : 384;
-  static constexpr int PRODUCER = BITS == 8 ? 12 : 8, ISSUER = PRODUCER + 1, WORKERS = ISSUER + 1;  // warps
+  static constexpr int PRODUCER = BITS == 8 ? 12 : 8, ISSUER = PRODUCER + 1;  // warps
   static constexpr uint32_t QT_BYTES = 128 * D * 2;     // 128 query rows
   static constexpr uint32_t TILE = KT * D * 2;          // a K or V tile in bf16
   static constexpr uint32_t RAW = KT * D;               // in codes
+  // registers a thread of the softmax, of the widening and of the producing and issuing warpgroup, of 512 x 128
+  // and 384 x 168 at launch.  The softmax holds 128 logits: with less it spills (256 tokens of 32 / 2 heads,
+  // 131072 keys: 493 us for codes with 208 / 40 / 56, 592 with 200 / 56 / 56, 653 with 192 / 56 / 72;
+  // bf16 398 us with 208 / 88, 416 with 200 / 104)
+  static constexpr int REGS_SOFTMAX = 208, REGS_WIDEN = 40, REGS_ISSUE = BITS == 8 ? 56 : 88;
+  static_assert(BITS == 8 ? 2 * REGS_SOFTMAX + REGS_WIDEN + REGS_ISSUE <= 4 * 128
+                          : 2 * REGS_SOFTMAX + REGS_ISSUE <= 3 * 168, "registers of the block");
   static constexpr int SLOTS = BITS == 8 ? 3 : 5;
   static constexpr int RSLOTS = 3;
   static constexpr size_t TILES = 2 * QT_BYTES + SLOTS * TILE + (BITS == 8 ? RSLOTS * RAW : 0);
@@ -50,7 +62,7 @@ struct Cfg {
 constexpr int SC_SLOTS = 4;
 
 struct Bars {
-  uint64_t q_full, q_empty;
+  uint64_t q_full, q_ready, q_empty;   // Q copied; brought to fp16 (8-bit cache); no longer read
   uint64_t full[5], empty[5];          // bf16 tiles
   uint64_t raw_full[3], raw_empty[3];  // tiles of codes
   uint64_t sc_full[SC_SLOTS];          // a step's scales
@@ -59,26 +71,102 @@ struct Bars {
   uint64_t drain;
 };
 
+// A softmax warp's counts so far: steps of each stream, all steps, meetings of the streams, segments.
+struct Counts {
+  uint32_t it[2], steps, meets, segs;
+};
+
+// A warp's walk over the block's segments: in its registers, or in shared memory where those are scarce.
+template <bool SHARED>
+struct Walk {
+  PrefixWalk w;
+  __device__ __forceinline__ void init(const PrefixParams& p, int block, bool record, PrefixWalk*) { w.init(p, block, record); }
+  __device__ __forceinline__ bool next(const PrefixParams& p, int block) { return w.next(p, block); }
+  __device__ __forceinline__ const PrefixWalk& now() const { return w; }
+};
+template <>
+struct Walk<true> {
+  PrefixWalk* at;
+  __device__ __forceinline__ void init(const PrefixParams& p, int block, bool record, PrefixWalk* place) {
+    PrefixWalk w;
+    w.init(p, block, record);
+    at = place;
+    keep(w);
+  }
+  __device__ __forceinline__ bool next(const PrefixParams& p, int block) {
+    PrefixWalk w = *at;
+    __syncwarp();
+    const bool more = w.next(p, block);
+    keep(w);
+    return more;
+  }
+  __device__ __forceinline__ const PrefixWalk& now() const { return *at; }
+  __device__ __forceinline__ void keep(const PrefixWalk& w) {
+    if ((threadIdx.x & 31) == 0) *at = w;
+    __syncwarp();
+  }
+};
+
+template <int BITS>
+struct ForCodes {};
+template <>
+struct ForCodes<8> {
+  __align__(16) float sc[SC_SLOTS][2][KT];  // scales of a step: keys', values'
+  uint32_t top[SC_SLOTS][4];                // largest of a widening warp's value scales, as bits
+  float q_factor[ROWS];                     // logit factor of a row: scale log2 e times its power of two
+};
+
 // What follows the tiles in shared memory (all of it dynamic: with five bf16 tiles there is room for
 // 3 KB beside them, and none for an alignment gap).
 template <int BITS>
 struct Shared {
   Bars bar;
   float2 ml[2][128];                               // the streams' maxima and sums, when they meet
-  PrefixWalk walks[BITS == 8 ? 14 : 10];           // each working warp's walk over the segments: the
-                                                   // softmax needs the registers
+  PrefixWalk walks[BITS == 8 ? 14 : 8];            // each warp's walk, where its registers are wanted
+  Counts counts[8];
   uint32_t tmem;
-  __align__(16) float sc[BITS == 8 ? SC_SLOTS : 1][2][BITS == 8 ? KT : 4];  // scales of a step: keys', values'
+  ForCodes<BITS> code;
 };
 
-// Two int8 codes in bytes 0 and 2 of y (bytes 1 and 3: anything) -> bf16x2.  A code is m - 128 s
-// (s its top bit, m the seven below): (128 + m) - 128 (1 + s), both exact bf16 numbers whose
-// bits are 0x4300 | m and 0x4300 | (code & 0x80).
-__device__ __forceinline__ uint32_t widen_codes(uint32_t y) {
-  const uint32_t a = (y & 0x007f007fu) | 0x43004300u, c = (y & 0x00800080u) | 0x43004300u;
+// Two codes with their top bit flipped (code + 128) in two bytes of x -> fp16x2: 0x6400 | u is 1024 + u.
+template <int SEL>
+__device__ __forceinline__ uint32_t widen_f16(uint32_t x) {
+  const uint32_t y = __byte_perm(x, 0x64646464u, SEL);
   uint32_t r;
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(c));
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(y), "r"(0x64806480u));  // 1152
   return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// One row of Q in its swizzled tile, bf16 -> fp16 times the power of two that brings its largest
+// element to [1, 2); returns sl2 over that power.
+template <int D>
+__device__ __forceinline__ float normalise_row(uint8_t* tile, int row, float sl2) {
+  uint32_t top = 1;  // largest exponent field
+#pragma unroll
+  for (int pass = 0; pass < 2; ++pass) {
+    const float down = __uint_as_float((254u - top) << 23);  // 2^(127 - top)
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c) {
+      uint4* at = reinterpret_cast<uint4*>(tile + (c >> 3) * (128 * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+      uint4 x = *at;
+      uint32_t* w = &x.x;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (pass == 0)
+          top = max(top, max((w[e] >> 7) & 0xffu, (w[e] >> 23) & 0xffu));
+        else
+          w[e] = pack_f16x2(bf16_lo(w[e]) * down, bf16_hi(w[e]) * down);
+      }
+      if (pass == 1) *at = x;
+    }
+    top = min(top, 253u);  // (infinities stay so)
+  }
+  return sl2 * __uint_as_float(top << 23);
 }
 
 template <int R>
@@ -198,7 +286,11 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
   uint32_t* err = p.err;
 
   if (threadIdx.x == 0) {
+    prefetch_map(&mapQ);
+    prefetch_map(&mapK);
+    prefetch_map(&mapV);
     mbar_init(&bar.q_full, 1);
+    mbar_init(&bar.q_ready, 8);
     mbar_init(&bar.q_empty, 1);
     for (int i = 0; i < C::SLOTS; ++i) {
       mbar_init(&bar.full[i], BITS == 8 ? 4 : 1);  // the widening warps; or the copy
@@ -227,57 +319,61 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
 
-  const PrefixWalk& w = sh.walks[warp < C::WORKERS ? warp : 0];
-  if (warp < C::WORKERS) {
-    PrefixWalk first;
-    first.init(p, block, block == 0 && warp == 0);
-    if (lane == 0) sh.walks[warp] = first;
-    __syncwarp();
-  }
-  auto next_segment = [&]() {
-    PrefixWalk at = sh.walks[warp];
-    __syncwarp();
-    const bool more = at.next(p, block);
-    if (lane == 0) sh.walks[warp] = at;
-    __syncwarp();
-    return more;
-  };
-
   if (warp < 8) {
     // ------------------------------ softmax ------------------------------
-    set_regs_up<BITS == 8 ? 192 : 216>();
+    set_regs_up<C::REGS_SOFTMAX>();
     const int h = warp >> 2;                                 // stream
     const int trow = (warp & 3) * 32 + lane;                 // TMEM lane
     const int q = lane & 3;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_tmem = tmem + lanes + 128 * h, o_tmem = tmem + lanes + 256 + 128 * h;
-    uint32_t it[2] = {0, 0}, step0 = 0, meets = 0;           // the streams' steps; all steps
+    Walk<true> walk;
+    walk.init(p, block, block == 0 && warp == 0, &sh.walks[warp]);
+    Counts& count = sh.counts[warp];
+    if (lane == 0) count = Counts{};
+    __syncwarp();
     bool failed = false;
-    while (!failed && next_segment()) {
+    while (!failed && walk.next(p, block)) {
+      const PrefixWalk& w = walk.now();
       const Segment sg(p, w);
       const int local = (sg.lag == 1 ? 128 * h : 0) + trow;  // row in the tile
       const bool live = local < sg.rows, any = local - lane < sg.rows;
-      // rows r, r + 8, r + 16, r + 24 of the warp's 32: a lane holds a quarter of the columns of each, so a key's
-      // scales are wanted by eight lanes only and fit in registers
-      float m[4], top[4];              // reference and maximum, log2 units
+      // rows r, r + 8, r + 16, r + 24 of the warp's 32: a lane holds a quarter of the columns of each, so it wants
+      // a quarter of the keys' scales
+      float m[4];                      // reference, log2 units
+      float sl2[4];                    // logit factor
+      float most = -100.f;             // log2 of the largest value scale so far (a bound; codes)
+      if constexpr (BITS == 8) {
+        const uint32_t seg = count.segs;
+        if (!mbar_wait_warp(&bar.q_full, seg & 1, err)) break;
+        if (sg.lag == 1 || h == 0) sh.code.q_factor[128 * h + trow] = normalise_row<D>(sQ + h * C::QT_BYTES, trow, p.sl2);
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.q_ready);
+        if (!mbar_wait_warp(&bar.q_ready, seg & 1, err)) break;
+      } else {
+        most = 0.f;
+      }
       unsigned long long l2[4];        // a lane's share of the sum, even and odd columns
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        m[i] = top[i] = NEG_INF;
+        m[i] = NEG_INF;
         l2[i] = pack_f32x2(0.f, 0.f);
+        sl2[i] = p.sl2;
+        if constexpr (BITS == 8) sl2[i] = sh.code.q_factor[(sg.lag == 1 ? 128 * h : 0) + (warp & 3) * 32 + 8 * i + (lane >> 2)];
       }
-      uint32_t n = it[h];
-      for (int j = sg.lag == 1 ? 0 : h; j < sg.nk; j += sg.lag, ++n) {
+      uint32_t n = count.it[h], gs = count.steps + (sg.lag == 1 ? 0 : h);
+      bool begun = false;  // O holds sums of this segment
+      for (int j = sg.lag == 1 ? 0 : h; j < sg.nk; j += sg.lag, ++n, gs += sg.lag) {
         const int valid = min(KT, w.g.len - (w.k0 + j) * KT);
-        const uint32_t gs = step0 + j;
-        float2 kf[BITS == 8 ? 16 : 1];
         if constexpr (BITS == 8) {
           if (!mbar_wait_warp(&bar.sc_full[gs % SC_SLOTS], (gs / SC_SLOTS) & 1, err)) {
             failed = true;
             break;
           }
-#pragma unroll
-          for (int g = 0; g < 16; ++g) kf[g] = *reinterpret_cast<const float2*>(&sh.sc[gs % SC_SLOTS][0][8 * g + 2 * q]);
+          const uint4 x = *reinterpret_cast<const uint4*>(sh.code.top[gs % SC_SLOTS]);
+          // 2^(exponent + 1) is above the largest; scales beyond 2^100 or below 2^-100 are taken as that
+          most = fmaxf(most, fminf((float)((int)(max(max(x.x, x.y), max(x.z, x.w)) >> 23) - 126), 100.f));
         }
         if (!mbar_wait_warp(&bar.s_full[h], n & 1, err)) {
           failed = true;
@@ -293,16 +389,18 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
           tmem_wait_ld();
           if constexpr (BITS == 8) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int g = 0; g < 16; ++g) {
+              const float2 kf = *reinterpret_cast<const float2*>(&sh.code.sc[gs % SC_SLOTS][0][8 * g + 2 * q]);
 #pragma unroll
-              for (int g = 0; g < 16; ++g)
+              for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; e += 2) {
                   float x, y;
-                  unpack_f32x2(mul_f32x2(pack_u32x2(s[i][4 * g + e], s[i][4 * g + e + 1]), pack_f32x2(kf[g].x, kf[g].y)), x, y);
+                  unpack_f32x2(mul_f32x2(pack_u32x2(s[i][4 * g + e], s[i][4 * g + e + 1]), pack_f32x2(kf.x, kf.y)), x, y);
                   s[i][4 * g + e] = __float_as_uint(x);
                   s[i][4 * g + e + 1] = __float_as_uint(y);
                 }
+            }
           }
           if (valid < KT) {
 #pragma unroll
@@ -314,6 +412,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
                   for (int i = 0; i < 2; ++i) s[i][4 * g + c] = s[i][4 * g + 2 + c] = __float_as_uint(NEG_INF);
           }
           bool moved = false;
+          float top[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const uint32_t* x = &s[i >> 1][2 * (i & 1)];
@@ -326,7 +425,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
             a = fmaxf(a, b);
             a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
             a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
-            top[i] = fmaxf(top[i], a * p.sl2);
+            top[i] = a * sl2[i] + most;
             moved = moved || top[i] > m[i] + MAX_GROWTH;
           }
           if (__any_sync(0xffffffffu, moved)) {
@@ -334,11 +433,12 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
             float f[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              f[i] = top[i] == NEG_INF ? 1.f : fast_exp2(m[i] - top[i]);
-              m[i] = top[i];
+              const float to = fmaxf(m[i], top[i]);
+              f[i] = to == NEG_INF ? 1.f : fast_exp2(m[i] - to);
+              m[i] = to;
               l2[i] = mul_f32x2(l2[i], pack_f32x2(f[i], f[i]));
             }
-            if (n != it[h]) {
+            if (begun) {
               if (!mbar_wait_warp(&bar.o_done[h], (n - 1) & 1, err)) {
                 failed = true;
                 break;
@@ -358,7 +458,6 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
               }
             }
           }
-          const unsigned long long sl2 = pack_f32x2(p.sl2, p.sl2);
           unsigned long long ref[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -373,18 +472,18 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
 #pragma unroll
               for (int g = 0; g < 8; ++g) {
                 float2 vf = make_float2(1.f, 1.f);
-                if constexpr (BITS == 8) vf = *reinterpret_cast<const float2*>(&sh.sc[gs % SC_SLOTS][1][64 * c + 8 * g + 2 * q]);
+                if constexpr (BITS == 8) vf = *reinterpret_cast<const float2*>(&sh.code.sc[gs % SC_SLOTS][1][64 * c + 8 * g + 2 * q]);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {  // row r + 16 i + 8 e
                   const uint32_t* x = &s[i][32 * c + 4 * g + 2 * e];
                   float a, b;
-                  unpack_f32x2(fma_f32x2(pack_u32x2(x[0], x[1]), sl2, ref[2 * i + e]), a, b);
+                  unpack_f32x2(fma_f32x2(pack_u32x2(x[0], x[1]), pack_f32x2(sl2[2 * i + e], sl2[2 * i + e]), ref[2 * i + e]), a, b);
                   a = fast_exp2(a);
                   b = fast_exp2(b);
                   const unsigned long long ab = pack_f32x2(a, b);
                   l2[2 * i + e] = add_f32x2(l2[2 * i + e], ab);
                   if constexpr (BITS == 8) unpack_f32x2(mul_f32x2(ab, pack_f32x2(vf.x, vf.y)), a, b);
-                  pk[2 * g + e] = pack_bf16x2(a, b);
+                  pk[2 * g + e] = BITS == 8 ? pack_f16x2(a, b) : pack_bf16x2(a, b);
                 }
               }
               tmem_st_16x32(s_tmem + ((uint32_t)(16 * i) << 16) + 32 * c, pk);
@@ -394,12 +493,14 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.p_full[h]);
+        begun = true;
       }
       // the streams' steps of this segment
       const uint32_t n0 = sg.lag == 1 ? sg.nk : (sg.nk + 1) / 2, n1 = sg.lag == 1 ? sg.nk : sg.nk / 2;
-      it[0] += n0;
-      it[1] += n1;
-      step0 += sg.nk;
+      const uint32_t it[2] = {count.it[0] + n0, count.it[1] + n1}, meets = count.meets;
+      __syncwarp();
+      if (lane == 0) count = Counts{{it[0], it[1]}, count.steps + sg.nk, meets + (sg.lag == 1 ? 0 : 1), count.segs + 1};
+      __syncwarp();
       if (failed) break;
       // from here on a row a thread: each row's maximum and sum go through shared memory
 #pragma unroll
@@ -474,16 +575,18 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
           failed = true;
           break;
         }
-        ++meets;
       }
     }
   } else if (warp == C::PRODUCER) {
     // ------------------------------ producer ------------------------------
-    set_regs_down<BITS == 8 ? 56 : 72>();
+    set_regs_down<C::REGS_ISSUE>();
     constexpr uint32_t N = BITS == 8 ? C::RSLOTS : C::SLOTS;
+    Walk<BITS == 8> walk;
+    walk.init(p, block, false, &sh.walks[BITS == 8 ? warp : 0]);
     uint32_t nt = 0, seg = 0;  // tiles and segments so far
     bool failed = false;
-    while (!failed && next_segment()) {
+    while (!failed && walk.next(p, block)) {
+      const PrefixWalk& w = walk.now();
       const Segment sg(p, w);
       if (!mbar_wait_warp(&bar.q_empty, (seg & 1) ^ 1, err)) break;
       if (lane == 0) {
@@ -527,9 +630,13 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
     __syncwarp();
   } else if (warp == C::ISSUER) {
     // ------------------------------ MMAs ------------------------------
-    set_regs_down<BITS == 8 ? 56 : 72>();
-    constexpr uint32_t id_qk = idesc_bf16_f32(128, KT);
-    constexpr uint32_t id_pv = idesc_bf16_f32(128, D) | (1u << 16);  // V: d contiguous, N-major
+    set_regs_down<C::REGS_ISSUE>();
+    // fp16 operands have format 0 where bf16 have 1; V: d contiguous, N-major
+    constexpr uint32_t formats = BITS == 8 ? (1u << 7) | (1u << 10) : 0u;
+    constexpr uint32_t id_qk = idesc_bf16_f32(128, KT) & ~formats;
+    constexpr uint32_t id_pv = (idesc_bf16_f32(128, D) & ~formats) | (1u << 16);
+    Walk<BITS == 8> walk;
+    walk.init(p, block, false, &sh.walks[BITS == 8 ? warp : 0]);
     uint32_t nt = 0, seg = 0, it[2] = {0, 0};
     bool failed = false;
     // tile n is here (v_valid: a V tile's keys in use)
@@ -546,29 +653,31 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
       }
       return true;
     };
-    // descriptors of the first tile and Q slot: the others differ in the address field alone (16-byte units)
-    const uint64_t q_desc = smem_desc_sw128(smem_u32(sQ), 16, 1024), k_desc = smem_desc_sw128(smem_u32(sT), 16, 1024);
-    const uint64_t v_desc = smem_desc_sw128(smem_u32(sT), KT * 128, 1024);
+    // descriptors of the first tile and Q slot: the others differ in the address field alone (16-byte units of
+    // the low word)
+    const uint64_t k_desc = smem_desc_sw128(smem_u32(sT), 16, 1024);
+    const uint32_t k_hi = (uint32_t)(k_desc >> 32), q_lo = (uint32_t)smem_desc_sw128(smem_u32(sQ), 16, 1024);
+    const uint32_t k_lo = (uint32_t)k_desc, v_lo = (uint32_t)smem_desc_sw128(smem_u32(sT), KT * 128, 1024);
+    auto desc = [&](uint32_t lo) { return pack_u32x2(lo, k_hi); };  // (8-row groups of 1024 bytes in all of them)
     auto qk = [&](int h, int qs, uint32_t n) {  // S of stream h = Q (slot qs) K^T
-      const uint64_t a = q_desc + qs * (C::QT_BYTES >> 4), b = k_desc + (n % C::SLOTS) * (C::TILE >> 4);
-      const uint32_t d = tmem + 128 * h;
+      const uint32_t a = q_lo + qs * (C::QT_BYTES >> 4), b = k_lo + (n % C::SLOTS) * (C::TILE >> 4), d = tmem + 128 * h;
 #pragma unroll
       for (int s = 0; s < D / 16; ++s)
-        umma_bf16(d, a + (((s >> 2) * (128 * 128) + (s & 3) * 32) >> 4), b + (((s >> 2) * (KT * 128) + (s & 3) * 32) >> 4),
-                       id_qk, s > 0 ? 1u : 0u);
+        umma_bf16(d, desc(a + (((s >> 2) * (128 * 128) + (s & 3) * 32) >> 4)),
+                  desc(b + (((s >> 2) * (KT * 128) + (s & 3) * 32) >> 4)), id_qk, s > 0 ? 1u : 0u);
       umma_commit(&bar.s_full[h]);
     };
     auto pv = [&](int h, uint32_t n, bool first) {  // O of stream h (+)= P V
-      const uint64_t b = v_desc + (n % C::SLOTS) * (C::TILE >> 4);
-      const uint32_t d = tmem + 256 + 128 * h, a = tmem + 128 * h;
+      const uint32_t b = v_lo + (n % C::SLOTS) * (C::TILE >> 4), d = tmem + 256 + 128 * h, a = tmem + 128 * h;
 #pragma unroll
       for (int s = 0; s < KT / 16; ++s)
-        umma_bf16_ts(d, a + 8 * s, b + ((s * 16 * 128) >> 4), id_pv, s > 0 ? 1u : first ? 0u : 1u);
+        umma_bf16_ts(d, a + 8 * s, desc(b + ((s * 16 * 128) >> 4)), id_pv, s > 0 ? 1u : first ? 0u : 1u);
       umma_commit(&bar.o_done[h]);
     };
-    while (!failed && next_segment()) {
+    while (!failed && walk.next(p, block)) {
+      const PrefixWalk& w = walk.now();
       const Segment sg(p, w);
-      if (!mbar_wait_warp(&bar.q_full, seg & 1, err)) break;
+      if (!mbar_wait_warp(BITS == 8 ? &bar.q_ready : &bar.q_full, seg & 1, err)) break;
       ++seg;
       const int head = min(sg.lag, sg.nk);
       for (int j = 0; j < head && !failed; ++j, ++nt) {
@@ -634,13 +743,16 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
     }
     __syncwarp();
   } else if (BITS == 8 && warp < 12) {
-    // ------------------------------ codes to bf16 ------------------------------
+    // ------------------------------ codes to fp16 ------------------------------
     if constexpr (BITS == 8) {
-      set_regs_down<72>();
+      set_regs_down<C::REGS_WIDEN>();
       const int t = threadIdx.x - 256;
+      Walk<true> walk;
+      walk.init(p, block, false, &sh.walks[warp]);
       uint32_t nt = 0, step0 = 0;
       bool failed = false;
-      while (!failed && next_segment()) {
+      while (!failed && walk.next(p, block)) {
+        const PrefixWalk& w = walk.now();
         const Segment sg(p, w);
         const size_t row0 = ((size_t)w.p * p.H_kv + w.head) * p.N_cap;
         for (int i = 0; i < sg.tiles(); ++i, ++nt) {
@@ -662,29 +774,26 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
             // these scales' places were last used four steps before, whose softmax is done: the slot just
             // found free held a tile that was used after it
             const uint32_t gs = step0 + j;
-            sh.sc[gs % SC_SLOTS][0][t] = ks;
-            sh.sc[gs % SC_SLOTS][1][t] = vs;
+            sh.code.sc[gs % SC_SLOTS][0][t] = ks;
+            sh.code.sc[gs % SC_SLOTS][1][t] = vs;
+            const uint32_t most = __reduce_max_sync(0xffffffffu, vs > 0.f ? __float_as_uint(vs) : 0u);  // (not of a NaN)
+            if (lane == 0) sh.code.top[gs % SC_SLOTS][warp - 8] = most;
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.sc_full[gs % SC_SLOTS]);
           }
-          const uint8_t* src = sR + rs * C::RAW;
-          uint8_t* dst = sT + cs * C::TILE;
           // 16 codes a piece; eight lanes take two rows of four pieces, so that their stores meet all banks
+          const uint8_t* src = sR + rs * C::RAW + (t >> 2) * D + (t & 3) * 16;
+          uint8_t* dst = sT + cs * C::TILE + (t >> 2) * 128;
+          const int swz = (t >> 2) & 7, c0 = ((2 * (t & 3)) ^ swz) << 4, c1 = ((2 * (t & 3) + 1) ^ swz) << 4;
 #pragma unroll
-          for (int u = 0; u < D / 16; ++u) {
-            const int row = (t >> 2) + 32 * (u & 3), c = (t & 3) + 4 * (u >> 2);
-            const uint4 x = *reinterpret_cast<const uint4*>(src + row * D + c * 16);
-            const uint32_t wd[4] = {x.x, x.y, x.z, x.w};
-            uint32_t o[8];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              o[2 * e] = widen_codes(__byte_perm(wd[e], 0, 0x4140));
-              o[2 * e + 1] = widen_codes(__byte_perm(wd[e], 0, 0x4342));
-            }
-            uint8_t* piece = dst + (u >> 2) * (KT * 128) + row * 128;
-            const int ch = 2 * (c & 3);
-            *reinterpret_cast<uint4*>(piece + ((ch ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-            *reinterpret_cast<uint4*>(piece + (((ch + 1) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+          for (int u = 0; u < D / 16; ++u) {  // rows 32 (u mod 4) further, columns 64 (u / 4)
+            const uint4 x = *reinterpret_cast<const uint4*>(src + 32 * (u & 3) * D + 64 * (u >> 2));
+            const uint32_t w0 = x.x ^ 0x80808080u, w1 = x.y ^ 0x80808080u, w2 = x.z ^ 0x80808080u, w3 = x.w ^ 0x80808080u;
+            uint8_t* row = dst + (u >> 2) * (KT * 128) + 32 * (u & 3) * 128;
+            *reinterpret_cast<uint4*>(row + c0) =
+                make_uint4(widen_f16<0x4140>(w0), widen_f16<0x4342>(w0), widen_f16<0x4140>(w1), widen_f16<0x4342>(w1));
+            *reinterpret_cast<uint4*>(row + c1) =
+                make_uint4(widen_f16<0x4140>(w2), widen_f16<0x4342>(w2), widen_f16<0x4140>(w3), widen_f16<0x4342>(w3));
           }
           fence_proxy_async();
           __syncwarp();
@@ -697,7 +806,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
       }
     }
   } else {
-    set_regs_down<BITS == 8 ? 56 : 72>();
+    set_regs_down<C::REGS_ISSUE>();
   }
   __syncthreads();
   if (warp == C::ISSUER) {

@@ -16,11 +16,6 @@ namespace pisa {
 namespace {
 
 namespace cg = cooperative_groups;
-#ifndef SPARSE_KEYS
-#define SPARSE_KEYS 32
-#define SPARSE_SLOTS 1
-#define SPARSE_F 4
-#endif
 constexpr int THREADS = 128;
 
 struct SparseParams {
@@ -70,7 +65,10 @@ struct Granules {
 
 template <int D, int NH>
 struct SparseCfg {
-  static constexpr int KEYS = SPARSE_KEYS, SLOTS = SPARSE_SLOTS;
+  // one granule of 32 keys under way a warp: four blocks a SM (8 query heads) hide more than deeper rings
+  // (64 x 8 lists of 16 blocks: 28.6 us; with two granules and three blocks 36.5; of 16 keys, two: 28.5,
+  // but 24 x 5 drafted tokens of 16 query heads take 34.1 instead of 31.0)
+  static constexpr int KEYS = 32, SLOTS = 1;
   using Tile = CacheTile<D, 8, KEYS, NH>;
   static constexpr uint32_t RING = 4 * SLOTS * Tile::BYTES, OUT = 4 * 8 * NH * D * 4;
   static constexpr uint32_t SMEM = RING > OUT ? RING : OUT;  // the outputs meet where the granules were
@@ -88,6 +86,10 @@ __global__ void __launch_bounds__(THREADS, NH == 1 ? 4 : 3) sparse_cache_kernel(
   __shared__ float sn[4][16], sl[4][16];
   __shared__ float2 ml[16];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, q = lane & 3;
+  if (lane == 0) {
+    prefetch_map(&mapK);
+    prefetch_map(&mapV);
+  }
   const int rank = blockIdx.x % cluster;
   const long long pair = blockIdx.x / cluster;  // (b, h_kv, t)
   const int t = (int)(pair % p.T);
@@ -243,9 +245,10 @@ cudaError_t launch_sparse_cache(const uint16_t* q, const int8_t* Kq, const int8_
   p.sl2 = pr.scale * LOG2E;
   p.err = err;
   const long long pairs = (long long)pr.B * pr.H_kv * pr.N;
-  // enough blocks for two an SM, while every warp keeps granules of its own
+  // up to four blocks a SM, while every warp keeps granules of its own (8 blocks: 24 x 5 drafted tokens
+  // take 39 us instead of 31, 16 x 8 lists 16 instead of 11)
   int cluster = 1;
-  while (cluster < 8 && pairs * cluster * 2 <= (long long)SPARSE_F * num_sms && 4 * cluster < 2 * pr.K) cluster *= 2;
+  while (cluster < 8 && pairs * cluster * 2 <= 4LL * num_sms && 4 * cluster < 2 * pr.K) cluster *= 2;
   const bool wide = pr.GQ > 8;
   if (pr.d == 128)
     return wide ? launch_t<128, 2>(Kq, Vq, p, pr, cluster, s) : launch_t<128, 1>(Kq, Vq, p, pr, cluster, s);

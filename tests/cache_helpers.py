@@ -7,6 +7,12 @@ a truncating sum's error a term):
   lse     an average of the logits' errors, exp2 / log2 and the sums: 2 E + 2^-18 + 2^-22 |lse|
   o       each weight is off by 2 E (its logit, the sum) and rounded to bf16 once (U), the result is
           rounded to bf16 (U):  (U + 4 E + 2^-16) sum_c w_c |v_c| + U |o|, w the softmax weights
+  o, codes   the weight times its value's scale vs_c is held in fp16: 2^-12 of it, within U, or where it is
+          below fp16's normal range half a step there, 2^-25, of numbers p_c vs_c with p_c = w_c l.  The
+          reference n of p_c = 2^(z_c - n) is at most z_top + log2(2 vs_max), so p_top >= 1 / (2 vs_max)
+          and l = p_top / w_top >= 1 / (2 vs_max w_top): 2^-25 of p_c vs_c is at most 2^-24 vs_max w_top of
+          w_c vs_c.  No error exceeds the weight itself (rounded to 0):
+          + sum_c min(2^-24 w_top vs_max / vs_c, w_c) |v_c|
 """
 import math
 
@@ -31,8 +37,9 @@ def quantise64(x):
     return code.to(torch.int8), scale, (code.float() * scale[..., None]).to(torch.bfloat16)
 
 
-def attend64(q, k, v, scale=None):
-    """q [r, d], k and v [n, d] in float64 -> o [r, d], lse [r], and the bounds on both."""
+def attend64(q, k, v, scale=None, vs=None):
+    """q [r, d], k and v [n, d] in float64 -> o [r, d], lse [r], and the bounds on both.  vs [n]: the scales of the
+    values, where they are codes."""
     d = q.shape[-1]
     scale = 1 / math.sqrt(d) if scale is None else scale
     if k.shape[0] == 0:
@@ -45,7 +52,11 @@ def attend64(q, k, v, scale=None):
     l = w.sum(1, keepdim=True)
     w = w / l
     o, lse = w @ v, (m + l.log())[:, 0]
-    return o, lse, (U + 4 * e[:, None] + 2.0 ** -16) * (w @ v.abs()) + U * o.abs(), 2 * e + 2.0 ** -18 + 2.0 ** -22 * lse.abs()
+    floor = 0.0
+    if vs is not None:
+        ratio = vs.max() / vs.clamp(min=1e-300)
+        floor = torch.minimum(2.0 ** -24 * w.amax(1, keepdim=True) * ratio, w) @ v.abs()
+    return o, lse, (U + 4 * e[:, None] + 2.0 ** -16) * (w @ v.abs()) + U * o.abs() + floor, 2 * e + 2.0 ** -18 + 2.0 ** -22 * lse.abs()
 
 
 def join64(o, lse, to, tl, o_own, lse_own):

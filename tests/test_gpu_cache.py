@@ -213,7 +213,8 @@ def sparse64(q, Kq, Vq, ks, vs, idx, ln, n, scale=None):
                 k = Kq[b, h, at].double() * ks[b, h, at].double()[:, None]
                 v = Vq[b, h, at].double() * vs[b, h, at].double()[:, None]
                 s = slice(h * G, h * G + G)
-                o[b, t, s], lse[b, t, s], to[b, t, s], tl[b, t, s] = R.attend64(q[b, t, s].double(), k, v, scale)
+                o[b, t, s], lse[b, t, s], to[b, t, s], tl[b, t, s] = R.attend64(
+                    q[b, t, s].double(), k, v, scale, vs[b, h, at].double())
     return o, lse, to, tl
 
 

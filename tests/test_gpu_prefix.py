@@ -60,7 +60,7 @@ def prefix64(q, K, V, ks, vs, lens, rows, o_own=None, lse_own=None, scale=None):
             if ks is not None:
                 k, v = k * ks[p, h, :lens[p]].double()[:, None], v * vs[p, h, :lens[p]].double()[:, None]
             s = slice(h * G, h * G + G)
-            r = R.attend64(q[a:b, s].double().reshape(-1, d), k, v, scale)
+            r = R.attend64(q[a:b, s].double().reshape(-1, d), k, v, scale, None if vs is None else vs[p, h, :lens[p]].double())
             if o_own is not None:
                 r = R.join64(*r, o_own[a:b, s].double().reshape(-1, d), lse_own[a:b, s].double().reshape(-1))
             for dst, x in zip((o, lse, to, tl), r):
@@ -205,7 +205,7 @@ def test_far_prefix(Rn):
     for h in range(H):
         k = K[P - 1, h, N - tail:].double() * ks[P - 1, h, N - tail:].double()[:, None]
         v = V[P - 1, h, N - tail:].double() * vs[P - 1, h, N - tail:].double()[:, None]
-        a, b, to, tl = R.attend64(q[1:, 2 * h:2 * h + 2].double().reshape(-1, d), k, v)
+        a, b, to, tl = R.attend64(q[1:, 2 * h:2 * h + 2].double().reshape(-1, d), k, v, vs=vs[P - 1, h, N - tail:].double())
         # the zero keys before the tail: weight 1 and value 0 each
         j = R.join64(a, b, to, tl, torch.zeros_like(a), torch.full_like(b, math.log(N - tail)))
         # a sum of 2^21 weights in at least 8 * 152 parts of at most 2^11 terms: 2^11 F relative, 2.4e-4
@@ -262,7 +262,8 @@ def test_serving_run(bits, B, H_q, H, d):
                         V8[b, h, :n].double() * t8[b, h, :n].double()[:, None])
                 for (kk, vv), og, lg in ((own, oj, lj), (own8, o8, l8)):
                     kk, vv = torch.cat([pk64[0, h], kk]), torch.cat([pv64[0, h], vv])
-                    a, l, to, tl = R.attend64(q[b, s].double(), kk, vv)
+                    # (as if all values were codes of one scale: the larger bound)
+                    a, l, to, tl = R.attend64(q[b, s].double(), kk, vv, vs=torch.ones_like(vv[:, 0]))
                     # two parts joined: the lse of each is off by tl, the own result was rounded to bf16 on its
                     # way (U of it, at most U sum w|v|, within `to` once more)
                     R.close(lg[b, s], l, 2 * tl, "lse")
