@@ -485,8 +485,9 @@ def pisa_decode_step(q, k, v, Kc, Vc, Pc, seq_len, K_sel: int, scale: float = 0.
 
 # ---- 8-bit cache ------------------------------------------------------------------------
 def _fits(t, name, shape, dtype, device):
-    """_expect, with the checks in the order that costs a valid call least."""
-    if t is not None and not (t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous()):
+    """_expect, in the order and by the calls that cost a valid argument least."""
+    if t is not None and (t.dtype is not dtype or t.shape != shape or t.get_device() != device.index
+                          or not t.is_contiguous()):
         _expect(t, name, shape, dtype, device)
 
 
@@ -498,11 +499,12 @@ def _cuda(t, name):
 
 def _call(fn, what, device, *args):
     """Calls a library function on the device's current stream, with that device current."""
-    if device.index == torch.cuda.current_device():
-        rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    i = device.index
+    if i == torch.cuda.current_device():
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(i))
     else:
-        with torch.cuda.device(device):
-            rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+        with torch.cuda.device(i):
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(i))
     if rc != PISA_OK:
         raise PisaError(rc, what)
 
@@ -628,7 +630,7 @@ def pisa_prefix_attn(q, Kp, Vp, prefix_len, row_start=None, k_scale=None, v_scal
     int8 with k_scale, v_scale [n, H_kv, N_cap]) of prefix_len [n] keys: rows row_start[p] .. row_start[p + 1] - 1
     (row_start [n + 1] int32; None: one group of all rows) are group p's.  o_own [R, H_q, d] bf16 and lse_own
     [R, H_q]: what the rows attended on their own, joined by log-sum-exp.  Returns o and lse [R, H_q] of the joined
-    result; rows of no group are left as they are (zero where allocated here)."""
+    result; rows of no group are left as they are (an o or lse allocated here holds nothing in particular there)."""
     dev = _cuda(q, "q")
     n, H_kv, N_cap, d = _cache_shape(Kp, "Kp")
     if q.dim() != 3:
@@ -647,13 +649,14 @@ def pisa_prefix_attn(q, Kp, Vp, prefix_len, row_start=None, k_scale=None, v_scal
     _fits(row_start, "row_start", (n + 1,), torch.int32, dev)
     _fits(o_own, "o_own", want, torch.bfloat16, dev)
     _fits(lse_own, "lse_own", want[:2], torch.float32, dev)
-    new = torch.empty if row_start is None and n == 1 else torch.zeros
     if o is None:
-        o = new(want, dtype=torch.bfloat16, device=dev)
-    _fits(o, "o", want, torch.bfloat16, dev)
-    if want_lse and lse is None:
-        lse = new(want[:2], dtype=torch.float32, device=dev)
-    _fits(lse, "lse", want[:2], torch.float32, dev)
+        o = torch.empty(want, dtype=torch.bfloat16, device=dev)
+    else:
+        _fits(o, "o", want, torch.bfloat16, dev)
+    if lse is not None:
+        _fits(lse, "lse", want[:2], torch.float32, dev)
+    elif want_lse:
+        lse = torch.empty(want[:2], dtype=torch.float32, device=dev)
     shape, params = pisa_shape(n, R, H_q, H_kv, d, N_cap), pisa_params(64, 2, 1, 0, float(scale), 0)
     need = lib().pisa_prefix_attn_workspace_bytes(shape, params)
     if need == 0 and R > 0:

@@ -1,6 +1,8 @@
 // Internal launchers of the PISA kernels (one per translation unit), called by api.cu.
 #pragma once
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace pisa {
@@ -108,6 +110,21 @@ cudaError_t launch_prefix_attn(const uint16_t* q, const void* Kp, const void* Vp
 
 // One CTA whose bounded waits run out after limit_ns (checks the timeout path).
 cudaError_t launch_wait_check(uint64_t limit_ns, uint32_t* err, cudaStream_t s);
+
+// Lets a kernel take `bytes` of dynamic shared memory, once for each device that it is launched on: asked for at
+// every call it is 1.5 us of a decode step's 5 us on the host.
+template <auto KERNEL>
+cudaError_t allow_shared(size_t bytes) {
+  static std::atomic<uint64_t> done{0};  // bits of the devices
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 // Tensor-map encoding through the driver entry point (no link-time libcuda dependency).
 bool encode_tensor_map(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,

@@ -249,19 +249,18 @@ __global__ void __launch_bounds__(THREADS) prefix_join_kernel(PrefixParams p) {
 
 constexpr int MAX_SMS = 152;  // this GPU's: the scratch does not depend on the device at hand
 
-// Which kernel, by the query rows a group has on average (the groups' own sizes are on the device;
-// any kernel takes any).
+// Which kernel, by the query rows a group has on average (the groups' own sizes are on the device; any kernel
+// takes any).  The few-row kernel reads the prefix again for every 16 rows, the tensor-core one pays for its
+// start (first tile in flight to first scores, 4.5 us) and for 256 rows whether they are there or not.  At
+// 8 KV heads x 32768 keys of d = 128, few-row against tensor-core kernel: bf16, 16 rows 37 : 35 us, 32 rows
+// 46 : 36; codes, 32 rows 40 : 50, 64 rows 58 : 50.
 struct Plan {
   bool tc;
   int rows, blocks;
 };
 Plan prefix_plan(const Problem& p, bool codes) {
   const long long rows = ((long long)p.N * p.GQ + p.B - 1) / (p.B > 0 ? p.B : 1);
-#ifdef PISA_FORCE
-  const bool tc = !PISA_FORCE;
-#else
   const bool tc = rows > (codes ? 32 : 16);
-#endif
   const int few = rows > 8 ? 16 : 8;
   return tc ? Plan{true, TC_ROWS, MAX_SMS} : Plan{false, few, few_blocks(p.d, few) * MAX_SMS};
 }
@@ -279,7 +278,7 @@ cudaError_t launch_few(const PrefixParams& p, cudaStream_t s) {
   };
   if (!encode(&mapK, p.K) || !encode(&mapV, p.V)) return cudaErrorInvalidValue;
   auto kern = prefix_few_kernel<D, BITS, NH>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+  const cudaError_t e = allow_shared<prefix_few_kernel<D, BITS, NH>>(C::SMEM);
   if (e != cudaSuccess) return e;
   kern<<<p.blocks, THREADS, C::SMEM, s>>>(mapK, mapV, p);
   return cudaGetLastError();

@@ -838,7 +838,7 @@ cudaError_t launch_t(const PrefixParams& p, cudaStream_t s) {
   constexpr size_t smem = C::TILES + sizeof(Shared<BITS>);
   static_assert(smem <= 227 * 1024, "a block's shared memory");
   auto kern = prefix_tc_kernel<D, BITS>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = allow_shared<prefix_tc_kernel<D, BITS>>(smem);
   if (e != cudaSuccess) return e;
   kern<<<p.blocks, C::THREADS, smem, s>>>(mapQ, mapK, mapV, p);
   return cudaGetLastError();

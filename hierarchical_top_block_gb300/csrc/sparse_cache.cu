@@ -205,7 +205,7 @@ cudaError_t launch_t(const int8_t* Kq, const int8_t* Vq, const SparseParams& p, 
       !encode_byte_tensor_map(&mapV, Vq, 3, dims, strides, box, C::Tile::SPAN))
     return cudaErrorInvalidValue;
   auto kern = sparse_cache_kernel<D, NH>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+  cudaError_t e = allow_shared<sparse_cache_kernel<D, NH>>(C::SMEM);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((long long)pr.B * pr.H_kv * pr.N * cluster));
