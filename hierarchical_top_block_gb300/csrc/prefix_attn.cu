@@ -159,12 +159,13 @@ __global__ void __launch_bounds__(THREADS) prefix_join_kernel(PrefixParams p) {
     const int tile = mrow / p.rows, local = mrow - tile * p.rows;
     if (!waited) pdl_wait();
     waited = true;
-    const long long S = p.P > 1 ? p.base[p.P] : group_steps(p, g), len = range_len(S, p.blocks);
-    const long long s0 = (p.P > 1 ? p.base[gp] : 0) + ((long long)head * g.tiles + tile) * g.steps, s1 = s0 + g.steps;
+    const PrefixCut cut = p.P > 1 ? PrefixCut{p.base[p.P], (int)p.base[p.P + 1]} : prefix_cut_one(p, g);
+    // the job's steps, counted from the first block's first
+    const long long s0 = (p.P > 1 ? p.base[gp] : 0) + ((long long)head * g.tiles + tile) * (g.steps + cut.extra), s1 = s0 + g.steps;
     // (in range as long as nobody changes lengths or bounds under the call)
-    const int c0 = min(block_of(s0, len), p.blocks - 1), c1 = min(block_of(s1 - 1, len), p.blocks - 1);
+    const int c0 = (int)min(quotient(s0, cut.len), (long long)p.blocks - 1), c1 = (int)min(quotient(s1 - 1, cut.len), (long long)p.blocks - 1);
     if (c0 == c1) continue;  // finished by its block
-    const int slot0 = 2 * c0 + (len * c0 == s0 ? 0 : 1);
+    const int slot0 = 2 * c0 + (cut.len * c0 >= s0 - cut.extra ? 0 : 1);  // 1: the block had a job before
     const float own = p.lse_own ? p.lse_own[i] : NEG_INF;
     float m = NEG_INF, l = 0.f, acc[V];
 #pragma unroll
@@ -256,13 +257,13 @@ constexpr int MAX_SMS = 152;  // this GPU's: the scratch does not depend on the 
 // 46 : 36; codes, 32 rows 40 : 50, 64 rows 58 : 50.
 struct Plan {
   bool tc;
-  int rows, blocks;
+  int rows, blocks, stop;
 };
 Plan prefix_plan(const Problem& p, bool codes) {
   const long long rows = ((long long)p.N * p.GQ + p.B - 1) / (p.B > 0 ? p.B : 1);
   const bool tc = rows > (codes ? 32 : 16);
   const int few = rows > 8 ? 16 : 8;
-  return tc ? Plan{true, TC_ROWS, MAX_SMS} : Plan{false, few, few_blocks(p.d, few) * MAX_SMS};
+  return tc ? Plan{true, TC_ROWS, MAX_SMS, 3} : Plan{false, few, few_blocks(p.d, few) * MAX_SMS, 1};
 }
 
 template <int D, int BITS, int NH>
@@ -299,7 +300,7 @@ size_t prefix_workspace_bytes(const Problem& p) {
     const Plan plan = prefix_plan(p, codes);
     most = std::max(most, (size_t)2 * plan.blocks * plan.rows);
   }
-  return up256(most * p.d * 4) + up256(most * 8) + up256((size_t)(p.B + 1) * 8);
+  return up256(most * p.d * 4) + up256(most * 8) + up256((size_t)(p.B + 2) * 8);
 }
 
 cudaError_t launch_prefix_attn(const uint16_t* q, const void* Kp, const void* Vp, const float* k_scale,
@@ -329,6 +330,7 @@ cudaError_t launch_prefix_attn(const uint16_t* q, const void* Kp, const void* Vp
   const Plan plan = prefix_plan(pr, k_scale != nullptr);
   p.rows = plan.rows;
   p.blocks = plan.blocks;
+  p.stop = plan.stop;
   const size_t parts = (size_t)2 * p.blocks * p.rows;
   uint8_t* w = static_cast<uint8_t*>(ws);
   p.part_o = reinterpret_cast<float*>(w);

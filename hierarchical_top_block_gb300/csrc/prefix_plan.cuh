@@ -1,12 +1,17 @@
 // How the attention over shared prefixes is divided over thread blocks.
 //
 // A job is (group p, KV head, tile of ROWS query rows); it takes the group's prefix in steps of
-// PREFIX_KT keys.  The jobs' steps, one job after the other, form one line of S steps, cut into
-// equal ranges, one a block: whatever the number of groups, rows and keys, every block gets the
-// same number of steps (to within one).  A job that lies in one block is finished there; of a job
-// that spans blocks, each block stores its part (row maxima, sums and output sums), and a second
-// kernel joins them.  A block has at most two such parts: the first job of its range and the last.
-// The cut depends on the sizes alone, so results are the same in every run.
+// PREFIX_KT keys.  The jobs' steps, one job after the other, form one line, cut into equal ranges,
+// one a block: whatever the number of groups, rows and keys, every block gets the same work.  A job
+// that lies in one block is finished there; of a job that spans blocks, each block stores its part
+// (row maxima, sums and output sums), and a second kernel joins them.  A block has at most two such
+// parts: the first job of its range and the last.  The cut depends on the sizes alone, so results
+// are the same in every run.
+//
+// A block that meets a second job stops for it: the rows of the first are written, those of the
+// next fetched.  On the line every job but the first therefore begins with `extra` empty steps,
+// as long as that stop; where the jobs end on the blocks' bounds anyway, or the empty steps would
+// make the ranges longer than a stop does, there are none.
 #pragma once
 
 #include "common.cuh"
@@ -27,10 +32,11 @@ struct PrefixParams {
   float* lse;                // nullable
   float* part_o;             // [2 blocks][ROWS][d] output sums relative to the row maximum
   float2* part_ml;           // [2 blocks][ROWS] row maximum (log2 units) and sum
-  long long* base;           // [P + 1] first step of each group, then S (with one group: not written)
+  long long* base;           // [P + 2] first step of each group, a range's steps, `extra` (with one group: not written)
   int P, R, H_q, H_kv, GQ, N_cap;
   int rows;                  // ROWS
   int blocks;                // thread blocks the steps are divided over
+  int stop;                  // steps that a second job in a block costs
   float sl2;
   uint32_t* err;
 };
@@ -54,18 +60,35 @@ __device__ __forceinline__ PrefixGroup prefix_group(const PrefixParams& p, int i
   g.steps = max(1, (g.len + PREFIX_KT - 1) / PREFIX_KT);
   return g;
 }
-__device__ __forceinline__ long long group_steps(const PrefixParams& p, const PrefixGroup& g) {
-  return (long long)p.H_kv * g.tiles * g.steps;
+__device__ __forceinline__ long long group_jobs(const PrefixParams& p, const PrefixGroup& g) {
+  return (long long)p.H_kv * g.tiles;
 }
 
-// Block c's range of the line of S steps: [c len, (c + 1) len).  Every block up to the last in use
-// has a step, so a job's parts are in consecutive blocks.
-__device__ __forceinline__ long long range_len(long long S, int blocks) {
-  return (S >> 31) ? (S + blocks - 1) / blocks : (long long)(((uint32_t)S + (uint32_t)blocks - 1) / (uint32_t)blocks);
+// a / b of numbers >= 0, in 32 bits where they fit (a fifth of the time).
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return (a >> 32) || (b >> 32) ? a / b : (long long)((uint32_t)a / (uint32_t)b);
 }
-// The block that holds step s.
-__device__ __forceinline__ int block_of(long long s, long long len) {
-  return (s >> 32) || (len >> 32) ? (int)(s / len) : (int)((uint32_t)s / (uint32_t)len);
+
+// The line's cut.  Block c has the positions [len c, len (c + 1)) + extra; job j of a group that starts at
+// position `base` has its steps from base + j (steps + extra) + extra on.
+struct PrefixCut {
+  long long len;
+  int extra;
+};
+__device__ __forceinline__ long long range_len(long long S, int blocks) { return quotient(S + blocks - 1, blocks); }
+// S steps in so many jobs; `even(len)`: no range of len steps meets a second job.
+template <class Even>
+__device__ __forceinline__ PrefixCut prefix_cut(const PrefixParams& p, long long S, long long jobs, Even even) {
+  PrefixCut c{range_len(S, p.blocks), 0};
+  if (jobs > 1 && !even(c.len)) {
+    const long long len = range_len(S + (jobs - 1) * p.stop, p.blocks);
+    if (len < c.len + p.stop) c = PrefixCut{len, p.stop};
+  }
+  return c;
+}
+__device__ __forceinline__ PrefixCut prefix_cut_one(const PrefixParams& p, const PrefixGroup& g) {
+  return prefix_cut(p, group_jobs(p, g) * g.steps, group_jobs(p, g),
+                    [&](long long len) { return len == 1 || quotient(g.steps, len) * len == g.steps; });
 }
 
 // Walks a block's range job by job.  Every thread of a warp holds the same state.
@@ -73,6 +96,7 @@ struct PrefixWalk {
   long long at, end;      // next step and end of the range
   long long gbase;        // first step of the current group
   int p;                  // current group
+  short extra;            // empty steps before a job's own
   bool begun;             // a segment of the range is behind
   PrefixGroup g;
   // current segment
@@ -96,48 +120,67 @@ struct PrefixWalk {
     begun = false;
     p = 0;
     gbase = 0;
-    if (prm.P == 1) {  // (nobody reads the groups' first steps then)
+    if (prm.P == 1) {  // (nobody reads `base` then)
       g = prefix_group(prm, 0);
-      const long long S = group_steps(prm, g), len = range_len(S, prm.blocks);
-      at = min(S, len * block);
-      end = min(S, len * (block + 1));
+      const PrefixCut cut = prefix_cut_one(prm, g);
+      extra = (short)cut.extra;
+      const long long total = group_jobs(prm, g) * (g.steps + extra);
+      at = min(total, cut.len * block + extra);
+      end = min(total, cut.len * (block + 1) + extra);
       return;
     }
-    long long total = 0;
-    for (int i0 = 0; i0 < prm.P; i0 += 32) {
-      const int i = i0 + lane;
-      const long long s = i < prm.P ? group_steps(prm, prefix_group(prm, i)) : 0;
-      long long x = s;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      if (record && i < prm.P) prm.base[i] = total + x - s;
-      total += __shfl_sync(0xffffffffu, x, 31);
+    long long S = 0, jobs = 0;
+    for (int i = lane; i < prm.P; i += 32) {
+      const PrefixGroup x = prefix_group(prm, i);
+      jobs += group_jobs(prm, x);
+      S += group_jobs(prm, x) * x.steps;
     }
-    if (record && lane == 0) prm.base[prm.P] = total;
-    const long long S = total, len = range_len(S, prm.blocks);
-    at = min(S, len * block);
-    end = min(S, len * (block + 1));
-    if (at >= end) return;
-    // the group that holds step `at`
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      S += __shfl_xor_sync(0xffffffffu, S, o);
+      jobs += __shfl_xor_sync(0xffffffffu, jobs, o);
+    }
+    const PrefixCut cut = prefix_cut(prm, S, jobs, [&](long long len) {
+      if (len == 1) return true;
+      bool even = true;
+      for (int i = lane; i < prm.P; i += 32) {
+        const PrefixGroup x = prefix_group(prm, i);
+        even = even && (x.tiles == 0 || quotient(x.steps, len) * len == x.steps);
+      }
+      return (bool)__all_sync(0xffffffffu, even);
+    });
+    extra = (short)cut.extra;
+    const long long line = S + jobs * extra;
+    at = min(line, cut.len * block + extra);
+    end = min(line, cut.len * (block + 1) + extra);
+    if (record && lane == 0) {
+      prm.base[prm.P] = cut.len;
+      prm.base[prm.P + 1] = extra;
+    }
+    if (at >= end && !record) return;
+    // the group that holds position `at`
     long long before = 0;
-    for (int i0 = 0; i0 < prm.P; i0 += 32) {
+    bool found = false;
+    for (int i0 = 0; i0 < prm.P && !(found && !record); i0 += 32) {
       const int i = i0 + lane;
-      const long long s = i < prm.P ? group_steps(prm, prefix_group(prm, i)) : 0;
+      long long s = 0;
+      if (i < prm.P) {
+        const PrefixGroup x = prefix_group(prm, i);
+        s = group_jobs(prm, x) * (x.steps + extra);
+      }
       long long x = s;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const long long y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
       }
+      if (record && i < prm.P) prm.base[i] = before + x - s;
       const unsigned past = __ballot_sync(0xffffffffu, before + x > at);
-      if (past) {
+      if (past && !found) {
         const int l = __ffs(past) - 1;
         p = i0 + l;
         gbase = before + __shfl_sync(0xffffffffu, x - s, l);
-        break;
+        found = true;
       }
       before += __shfl_sync(0xffffffffu, x, 31);
     }
@@ -147,15 +190,24 @@ struct PrefixWalk {
   // Moves to the next segment; false at the end of the range.
   __device__ __forceinline__ bool next(const PrefixParams& prm, int block) {
     if (at >= end) return false;
-    while (at >= gbase + group_steps(prm, g)) {
-      gbase += group_steps(prm, g);
-      g = prefix_group(prm, ++p);  // at < end <= S: a later group holds it
+    long long job, off;  // of the group; position in the job
+    for (;;) {
+      const long long span = g.steps + extra;
+      const long long all = group_jobs(prm, g) * span;
+      if (at >= gbase + all) {
+        gbase += all;
+        g = prefix_group(prm, ++p);  // at < end <= the line's length: a later group holds it
+        continue;
+      }
+      job = quotient(at - gbase, span);
+      off = at - gbase - job * span;
+      if (off >= extra) break;
+      at = min(end, at + extra - off);  // the empty steps
+      if (at == end) return false;
     }
-    const long long off = at - gbase;
-    const int job = (int)(off / g.steps);
-    head = job / g.tiles;
-    tile = job - head * g.tiles;
-    k0 = (int)(off - (long long)job * g.steps);
+    head = (int)quotient(job, g.tiles);
+    tile = (int)(job - (long long)head * g.tiles);
+    k0 = (int)(off - extra);
     k1 = (int)min((long long)g.steps, k0 + (end - at));
     slot = (k0 == 0 && k1 == g.steps) ? -1 : 2 * block + (begun ? 1 : 0);
     begun = true;

@@ -80,18 +80,16 @@ struct Counts {
 template <bool SHARED>
 struct Walk {
   PrefixWalk w;
-  __device__ __forceinline__ void init(const PrefixParams& p, int block, bool record, PrefixWalk*) { w.init(p, block, record); }
+  __device__ __forceinline__ void start(const PrefixWalk& from, PrefixWalk*) { w = from; }
   __device__ __forceinline__ bool next(const PrefixParams& p, int block) { return w.next(p, block); }
   __device__ __forceinline__ const PrefixWalk& now() const { return w; }
 };
 template <>
 struct Walk<true> {
   PrefixWalk* at;
-  __device__ __forceinline__ void init(const PrefixParams& p, int block, bool record, PrefixWalk* place) {
-    PrefixWalk w;
-    w.init(p, block, record);
+  __device__ __forceinline__ void start(const PrefixWalk& from, PrefixWalk* place) {
     at = place;
-    keep(w);
+    keep(from);
   }
   __device__ __forceinline__ bool next(const PrefixParams& p, int block) {
     PrefixWalk w = *at;
@@ -146,25 +144,27 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 // element to [1, 2); returns sl2 over that power.
 template <int D>
 __device__ __forceinline__ float normalise_row(uint8_t* tile, int row, float sl2) {
-  uint32_t top = 1;  // largest exponent field
+  auto at = [&](int c) {
+    return reinterpret_cast<uint4*>(tile + (c >> 3) * (128 * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+  };
+  uint4 x[D / 8];
 #pragma unroll
-  for (int pass = 0; pass < 2; ++pass) {
-    const float down = __uint_as_float((254u - top) << 23);  // 2^(127 - top)
+  for (int c = 0; c < D / 8; ++c) x[c] = *at(c);
+  uint32_t most[2] = {0, 0};  // largest magnitudes of two halves of a word each: as integers they are in order
 #pragma unroll
-    for (int c = 0; c < D / 8; ++c) {
-      uint4* at = reinterpret_cast<uint4*>(tile + (c >> 3) * (128 * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4));
-      uint4 x = *at;
-      uint32_t* w = &x.x;
+  for (int c = 0; c < D / 8; ++c) {
+    most[0] = __vmaxu2(most[0], __vmaxu2(x[c].x & 0x7fff7fffu, x[c].y & 0x7fff7fffu));
+    most[1] = __vmaxu2(most[1], __vmaxu2(x[c].z & 0x7fff7fffu, x[c].w & 0x7fff7fffu));
+  }
+  const uint32_t both = __vmaxu2(most[0], most[1]);
+  const uint32_t top = min(max(max(both >> 23, (both >> 7) & 0x1ffu), 1u), 253u);  // exponent (infinities stay so)
+  const float down = __uint_as_float((254u - top) << 23);                          // 2^(127 - top)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (pass == 0)
-          top = max(top, max((w[e] >> 7) & 0xffu, (w[e] >> 23) & 0xffu));
-        else
-          w[e] = pack_f16x2(bf16_lo(w[e]) * down, bf16_hi(w[e]) * down);
-      }
-      if (pass == 1) *at = x;
-    }
-    top = min(top, 253u);  // (infinities stay so)
+  for (int c = 0; c < D / 8; ++c) {
+    uint32_t* w = &x[c].x;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = pack_f16x2(bf16_lo(w[e]) * down, bf16_hi(w[e]) * down);
+    *at(c) = x[c];
   }
   return sl2 * __uint_as_float(top << 23);
 }
@@ -205,66 +205,57 @@ struct Segment {
   }
 };
 
-// Where a finished query row goes: the output (the whole job was this segment) or a part's slot.
+// Where a finished query row goes: the output (the whole job was this segment) or a part's slot.  The output
+// sums are read from tensor memory in the accumulators' layout (a lane has pairs of columns of rows r and
+// r + 8), so that a store fills whole 32-byte sectors of eight rows: a row a thread it took twice as long.
 struct RowOut {
   bool live;
-  int slot;
   size_t orow;
-  float own;         // the row's own log-sum-exp
-  float fa, fo;
-  float* part;
+  float fa, fo;  // factors of the sums and of the row's own output
 };
-template <int D>
-__device__ __forceinline__ RowOut row_out(const PrefixParams& p, const PrefixWalk& w, int local, bool live) {
+// The row's place and factors; `stats`: this lane writes its log-sum-exp, or maximum and sum.  Warp-wide.
+__device__ __forceinline__ RowOut row_out(const PrefixParams& p, const PrefixWalk& w, int local, bool live, float m, float l,
+                                          bool stats) {
   RowOut r;
   r.live = live;
-  r.slot = w.slot;
+  r.fa = 1.f;
+  r.fo = 0.f;
+  if (w.slot >= 0) {
+    r.orow = (size_t)w.slot * ROWS + local;
+    if (live && stats) p.part_ml[r.orow] = make_float2(m, l);
+    return r;
+  }
   const int mrow = w.tile * ROWS + local, tok = mrow / p.GQ;
   r.orow = (size_t)(w.g.first + tok) * p.H_q + (size_t)w.head * p.GQ + (mrow - tok * p.GQ);
-  r.own = live && w.slot < 0 && p.lse_own ? p.lse_own[r.orow] : NEG_INF;
-  r.part = p.part_o + ((size_t)(w.slot < 0 ? 0 : w.slot) * ROWS + local) * D;
-  r.fa = r.fo = 0.f;
+  float lse;
+  join_own(m, l, live && p.lse_own ? p.lse_own[r.orow] : NEG_INF, r.fa, r.fo, lse);
+  __syncwarp();  // lse may be lse_own: all four lanes of a row have read it
+  if (live && stats && p.lse) p.lse[r.orow] = lse;
   return r;
 }
-// The row's factors, and (stats) its log-sum-exp or maximum and sum.
-__device__ __forceinline__ void put_stats(const PrefixParams& p, RowOut& r, int local, float m, float l, bool stats) {
-  if (!r.live) return;
-  if (r.slot < 0) {
-    float lse;
-    join_own(m, l, r.own, r.fa, r.fo, lse);
-    if (stats && p.lse) p.lse[r.orow] = lse;
-  } else if (stats) {
-    p.part_ml[(size_t)r.slot * ROWS + local] = make_float2(m, l);
-  }
-}
-// 32 columns from c on of the row's output sums, relative to its maximum.
+// 32 columns from c on of rows r and r + 8 of a half of 16, x[4 g + 2 e + i]: column c + 8 g + 2 q + i of row r + 8 e.
 template <int D>
-__device__ __forceinline__ void put_columns(const PrefixParams& p, const RowOut& r, int c, const uint32_t (&x)[32]) {
-  if (!r.live) return;
-  if (r.slot < 0) {
+__device__ __forceinline__ void put_columns(const PrefixParams& p, const PrefixWalk& w, const RowOut (&r)[2], int c, int q,
+                                            const uint32_t (&x)[16]) {
 #pragma unroll
-    for (int j = 0; j < 32; j += 8) {
-      uint4 own = make_uint4(0, 0, 0, 0);
-      const bool with = p.o_own && r.fo != 0.f;
-      if (with) own = *reinterpret_cast<const uint4*>(p.o_own + r.orow * D + c + j);
-      const uint32_t ow[4] = {own.x, own.y, own.z, own.w};
-      uint32_t v[4];
+  for (int e = 0; e < 2; ++e) {
+    if (!r[e].live) continue;
+    const size_t at = r[e].orow * D + c + 2 * q;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float a = r.fa == 0.f ? 0.f : __uint_as_float(x[j + 2 * e]) * r.fa;
-        float b = r.fa == 0.f ? 0.f : __uint_as_float(x[j + 2 * e + 1]) * r.fa;
-        if (with) {
-          a += bf16_lo(ow[e]) * r.fo;
-          b += bf16_hi(ow[e]) * r.fo;
-        }
-        v[e] = pack_bf16x2(a, b);
+    for (int g = 0; g < 4; ++g) {
+      const float a = __uint_as_float(x[4 * g + 2 * e]), b = __uint_as_float(x[4 * g + 2 * e + 1]);
+      if (w.slot >= 0) {
+        *reinterpret_cast<float2*>(p.part_o + at + 8 * g) = make_float2(a, b);
+        continue;
       }
-      *reinterpret_cast<uint4*>(p.o + r.orow * D + c + j) = make_uint4(v[0], v[1], v[2], v[3]);
+      float v0 = r[e].fa == 0.f ? 0.f : a * r[e].fa, v1 = r[e].fa == 0.f ? 0.f : b * r[e].fa;
+      if (p.o_own && r[e].fo != 0.f) {
+        const uint32_t own = *reinterpret_cast<const uint32_t*>(p.o_own + at + 8 * g);
+        v0 += bf16_lo(own) * r[e].fo;
+        v1 += bf16_hi(own) * r[e].fo;
+      }
+      *reinterpret_cast<uint32_t*>(p.o + at + 8 * g) = pack_bf16x2(v0, v1);
     }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 32; j += 4)
-      *reinterpret_cast<uint4*>(r.part + c + j) = make_uint4(x[j], x[j + 1], x[j + 2], x[j + 3]);
   }
 }
 
@@ -285,39 +276,49 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
   const int block = blockIdx.x;
   uint32_t* err = p.err;
 
-  if (threadIdx.x == 0) {
-    prefetch_map(&mapQ);
-    prefetch_map(&mapK);
-    prefetch_map(&mapV);
-    mbar_init(&bar.q_full, 1);
-    mbar_init(&bar.q_ready, 8);
-    mbar_init(&bar.q_empty, 1);
-    for (int i = 0; i < C::SLOTS; ++i) {
-      mbar_init(&bar.full[i], BITS == 8 ? 4 : 1);  // the widening warps; or the copy
-      mbar_init(&bar.empty[i], 1);
+  // The producer sets up the barriers and starts to fetch at once; the others meet when they and the tensor
+  // memory are there.
+  if (warp == C::PRODUCER) {
+    if (lane == 0) {
+      prefetch_map(&mapQ);
+      prefetch_map(&mapK);
+      prefetch_map(&mapV);
+      mbar_init(&bar.q_full, 1);
+      mbar_init(&bar.q_ready, 8);
+      mbar_init(&bar.q_empty, 1);
+      for (int i = 0; i < C::SLOTS; ++i) {
+        mbar_init(&bar.full[i], BITS == 8 ? 4 : 1);  // the widening warps; or the copy
+        mbar_init(&bar.empty[i], 1);
+      }
+      for (int i = 0; i < C::RSLOTS; ++i) {
+        mbar_init(&bar.raw_full[i], 1);
+        mbar_init(&bar.raw_empty[i], 4);
+      }
+      for (int i = 0; i < SC_SLOTS; ++i) mbar_init(&bar.sc_full[i], 4);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&bar.s_full[i], 1);
+        mbar_init(&bar.p_full[i], 4);
+        mbar_init(&bar.o_done[i], 1);
+      }
+      mbar_init(&bar.x_full, 8);
+      mbar_init(&bar.x_done, 8);
+      mbar_init(&bar.drain, 1);
+      mbar_fence_init();
     }
-    for (int i = 0; i < C::RSLOTS; ++i) {
-      mbar_init(&bar.raw_full[i], 1);
-      mbar_init(&bar.raw_empty[i], 4);
-    }
-    for (int i = 0; i < SC_SLOTS; ++i) mbar_init(&bar.sc_full[i], 4);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&bar.s_full[i], 1);
-      mbar_init(&bar.p_full[i], 4);
-      mbar_init(&bar.o_done[i], 1);
-    }
-    mbar_init(&bar.x_full, 8);
-    mbar_init(&bar.x_done, 8);
-    mbar_init(&bar.drain, 1);
-    mbar_fence_init();
-  }
-  if (warp == C::ISSUER) {
+    __syncwarp();
+    asm volatile("barrier.cta.arrive 1, %0;" ::"n"(C::THREADS) : "memory");
+  } else if (warp == C::ISSUER) {
     tmem_alloc(&sh.tmem, 512);
     tmem_relinquish();
   }
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = sh.tmem;
+  PrefixWalk first;
+  first.init(p, block, block == 0 && warp == 0);
+  uint32_t tmem = 0;
+  if (warp != C::PRODUCER) {
+    asm volatile("barrier.cta.sync 1, %0;" ::"n"(C::THREADS) : "memory");
+    tc_fence_after();
+    tmem = sh.tmem;
+  }
 
   if (warp < 8) {
     // ------------------------------ softmax ------------------------------
@@ -328,7 +329,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_tmem = tmem + lanes + 128 * h, o_tmem = tmem + lanes + 256 + 128 * h;
     Walk<true> walk;
-    walk.init(p, block, block == 0 && warp == 0, &sh.walks[warp]);
+    walk.start(first, &sh.walks[warp]);
     Counts& count = sh.counts[warp];
     if (lane == 0) count = Counts{};
     __syncwarp();
@@ -337,7 +338,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
       const PrefixWalk& w = walk.now();
       const Segment sg(p, w);
       const int local = (sg.lag == 1 ? 128 * h : 0) + trow;  // row in the tile
-      const bool live = local < sg.rows, any = local - lane < sg.rows;
+      const bool any = local - lane < sg.rows;
       // rows r, r + 8, r + 16, r + 24 of the warp's 32: a lane holds a quarter of the columns of each, so it wants
       // a quarter of the keys' scales
       float m[4];                      // reference, log2 units
@@ -502,70 +503,86 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
       if (lane == 0) count = Counts{{it[0], it[1]}, count.steps + sg.nk, meets + (sg.lag == 1 ? 0 : 1), count.segs + 1};
       __syncwarp();
       if (failed) break;
-      // from here on a row a thread: each row's maximum and sum go through shared memory
+      float l[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         float a, b;
         unpack_f32x2(l2[i], a, b);
         a += b;
         a += __shfl_xor_sync(0xffffffffu, a, 1);
-        a += __shfl_xor_sync(0xffffffffu, a, 2);
-        if (q == 0) sh.ml[h][(warp & 3) * 32 + 8 * i + (lane >> 2)] = make_float2(m[i], a);
+        l[i] = a + __shfl_xor_sync(0xffffffffu, a, 2);
       }
-      __syncwarp();
-      RowOut out = row_out<D>(p, w, local, live);
+      const int row0 = (sg.lag == 1 ? 128 * h : 0) + (warp & 3) * 32 + (lane >> 2);  // the first of the lane's rows
       if (sg.lag == 1) {
         if (!mbar_wait_warp(&bar.o_done[h], (it[h] - 1) & 1, err)) {
           failed = true;
           break;
         }
         tc_fence_after();
-        if (any) {
-          const float2 ml = sh.ml[h][trow];
-          put_stats(p, out, local, ml.x, ml.y, true);
+        if (any)
+#pragma unroll
+          for (int i = 0; i < 4; i += 2) {
+            RowOut out[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int row = row0 + 8 * (i + e);
+              out[e] = row_out(p, w, row, row < sg.rows, m[i + e], l[i + e], q == 0);
+            }
 #pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            uint32_t r[32];
-            tmem_ld32(o_tmem + c, r);
-            tmem_wait_ld();
-            put_columns<D>(p, out, c, r);
+            for (int c = 0; c < D; c += 32) {
+              uint32_t r[16];
+              tmem_ld_16x32(o_tmem + ((uint32_t)(8 * i) << 16) + c, r);
+              tmem_wait_ld();
+              put_columns<D>(p, w, out, c, q, r);
+            }
           }
-        }
         tc_fence_before();
-        __syncwarp();  // sh.ml has been read
       } else {
-        // both streams have parts of every row: joined here, half of the columns by each warpgroup
+        // both streams have parts of every row: joined here, rows below 16 of 32 by one warpgroup, the others by
+        // the other one
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (q == 0) sh.ml[h][row0 + 8 * i] = make_float2(m[i], l[i]);
+        __syncwarp();
         if (!mbar_wait_warp(&bar.o_done[0], (it[0] - 1) & 1, err) ||
             (n1 > 0 && !mbar_wait_warp(&bar.o_done[1], (it[1] - 1) & 1, err))) {
           failed = true;
           break;
         }
         if (lane == 0) mbar_arrive(&bar.x_full);
-        if (!mbar_wait_warp(&bar.x_full, meets & 1, err)) {  // (the row's own log-sum-exp has been read by both)
+        if (!mbar_wait_warp(&bar.x_full, meets & 1, err)) {
           failed = true;
           break;
         }
         tc_fence_after();
         if (any) {
-          const float2 a = sh.ml[0][trow], b = sh.ml[1][trow];
-          const float m = fmaxf(a.x, b.x);
-          const float f0 = a.x == NEG_INF ? 0.f : fast_exp2(a.x - m), f1 = b.x == NEG_INF ? 0.f : fast_exp2(b.x - m);
-          const float l = (a.x == NEG_INF ? a.y : a.y * f0) + (b.x == NEG_INF ? b.y : b.y * f1);
-          put_stats(p, out, local, m, l, h == 0);
-          const uint32_t o0 = tmem + lanes + 256;
+          RowOut out[2];
+          float f0[2], f1[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int row = row0 + 16 * h + 8 * e;
+            const float2 a = sh.ml[0][row], b = sh.ml[1][row];
+            const float top = fmaxf(a.x, b.x);
+            f0[e] = a.x == NEG_INF ? 0.f : fast_exp2(a.x - top);
+            f1[e] = b.x == NEG_INF ? 0.f : fast_exp2(b.x - top);
+            const float sum = (a.x == NEG_INF ? a.y : a.y * f0[e]) + (b.x == NEG_INF ? b.y : b.y * f1[e]);
+            out[e] = row_out(p, w, row, row < sg.rows, top, sum, q == 0);
+          }
+          const uint32_t o0 = tmem + lanes + 256 + ((uint32_t)(16 * h) << 16);
 #pragma unroll 1
-          for (int c = h * (D / 2); c < (h + 1) * (D / 2); c += 32) {
-            uint32_t r[32], r1[32];
-            tmem_ld32(o0 + c, r);
-            if (n1 > 0) tmem_ld32(o0 + 128 + c, r1);
+          for (int c = 0; c < D; c += 32) {
+            uint32_t r[16], r1[16];
+            tmem_ld_16x32(o0 + c, r);
+            if (n1 > 0) tmem_ld_16x32(o0 + 128 + c, r1);
             tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              float x = __uint_as_float(r[e]) * f0;
-              if (n1 > 0) x = fmaf(__uint_as_float(r1[e]), f1, x);
-              r[e] = __float_as_uint(x);
+            for (int k = 0; k < 16; ++k) {
+              const int e = (k >> 1) & 1;
+              float x = __uint_as_float(r[k]) * f0[e];
+              if (n1 > 0) x = fmaf(__uint_as_float(r1[k]), f1[e], x);
+              r[k] = __float_as_uint(x);
             }
-            put_columns<D>(p, out, c, r);
+            put_columns<D>(p, w, out, c, q, r);
           }
         }
         tc_fence_before();
@@ -582,7 +599,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
     set_regs_down<C::REGS_ISSUE>();
     constexpr uint32_t N = BITS == 8 ? C::RSLOTS : C::SLOTS;
     Walk<BITS == 8> walk;
-    walk.init(p, block, false, &sh.walks[BITS == 8 ? warp : 0]);
+    walk.start(first, &sh.walks[BITS == 8 ? warp : 0]);
     uint32_t nt = 0, seg = 0;  // tiles and segments so far
     bool failed = false;
     while (!failed && walk.next(p, block)) {
@@ -636,7 +653,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
     constexpr uint32_t id_qk = idesc_bf16_f32(128, KT) & ~formats;
     constexpr uint32_t id_pv = (idesc_bf16_f32(128, D) & ~formats) | (1u << 16);
     Walk<BITS == 8> walk;
-    walk.init(p, block, false, &sh.walks[BITS == 8 ? warp : 0]);
+    walk.start(first, &sh.walks[BITS == 8 ? warp : 0]);
     uint32_t nt = 0, seg = 0, it[2] = {0, 0};
     bool failed = false;
     // tile n is here (v_valid: a V tile's keys in use)
@@ -748,7 +765,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
       set_regs_down<C::REGS_WIDEN>();
       const int t = threadIdx.x - 256;
       Walk<true> walk;
-      walk.init(p, block, false, &sh.walks[warp]);
+      walk.start(first, &sh.walks[warp]);
       uint32_t nt = 0, step0 = 0;
       bool failed = false;
       while (!failed && walk.next(p, block)) {
