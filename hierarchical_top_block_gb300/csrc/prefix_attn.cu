@@ -127,18 +127,27 @@ __global__ void __launch_bounds__(THREADS, FewCfg<D, BITS, NH>::PER_SM) prefix_f
   }
 }
 
-// Joins the parts of every job that spans blocks: a block a (row, query head).  A part is D floats,
-// one 16-byte (8-byte) piece a lane; the block's four warps take the parts in turn, BATCH of them
-// in flight, each warp with its own running maximum, and meet in shared memory.
-template <int D>
-__global__ void __launch_bounds__(THREADS) prefix_join_kernel(PrefixParams p) {
-  constexpr int V = D / 32, BATCH = 8, WARPS = THREADS / 32;
-  __shared__ float so[WARPS][D];
-  __shared__ float2 sml[WARPS];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// Joins the parts of every job that spans blocks.  A (row, query head) is joined by WARPS warps of a block's four: a
+// part is D floats, one 16-byte (8-byte) piece a lane; the warps take the parts in turn, BATCH of them in
+// flight, each with its own running maximum, and meet in shared memory.  Latency bounds it (launch, bounds,
+// maxima, sums), so few rows have all four warps each, and many have two, so that all rows are under way at
+// once (64 tokens of 32 heads, 19 parts a row: JOIN_FIGURES).
+template <int D, int WARPS>
+__global__ void __launch_bounds__(THREADS, 8) prefix_join_kernel(PrefixParams p) {
+  constexpr int V = D / 32, BATCH = 8, PER = THREADS / 32 / WARPS;  // rows a block
+  __shared__ float so[PER][WARPS][D];
+  __shared__ float2 sml[PER][WARPS];
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % WARPS, sub = (threadIdx.x >> 5) / WARPS;
+  static_assert(PER <= 2, "a barrier each");
+  auto meet = [&] {
+    if (sub == 0)
+      asm volatile("barrier.cta.sync 1, %0;" ::"n"(32 * WARPS) : "memory");
+    else
+      asm volatile("barrier.cta.sync 2, %0;" ::"n"(32 * WARPS) : "memory");
+  };
   bool waited = false;  // the parts are written by the kernel before, the groups' bounds are not
-  for (long long i = blockIdx.x; i < (long long)p.R * p.H_q; i += gridDim.x) {
-    const int row = (int)(i / p.H_q), hq = (int)(i - (long long)row * p.H_q);
+  for (long long i = (long long)blockIdx.x * PER + sub; i < (long long)p.R * p.H_q; i += (long long)gridDim.x * PER) {
+    const int row = (int)quotient(i, p.H_q), hq = (int)(i - (long long)row * p.H_q);
     int gp = 0;
     if (p.P > 1) {
       int lo = 0, hi = p.P;  // first group with row_start[g + 1] > row
@@ -157,16 +166,39 @@ __global__ void __launch_bounds__(THREADS) prefix_join_kernel(PrefixParams p) {
     const int head = hq / p.GQ;
     const int mrow = (row - g.first) * p.GQ + (hq - head * p.GQ);
     const int tile = mrow / p.rows, local = mrow - tile * p.rows;
-    if (!waited) pdl_wait();
-    waited = true;
-    const PrefixCut cut = p.P > 1 ? PrefixCut{p.base[p.P], (int)p.base[p.P + 1]} : prefix_cut_one(p, g);
+    PrefixCut cut;
+    long long s0 = 0;
+    if (p.P == 1) {
+      cut = prefix_cut_one(p, g);
+    } else {
+      if (!waited) pdl_wait();
+      waited = true;
+      cut = PrefixCut{p.base[p.P], (int)p.base[p.P + 1]};
+      s0 = p.base[gp];
+    }
     // the job's steps, counted from the first block's first
-    const long long s0 = (p.P > 1 ? p.base[gp] : 0) + ((long long)head * g.tiles + tile) * (g.steps + cut.extra), s1 = s0 + g.steps;
+    s0 += ((long long)head * g.tiles + tile) * (g.steps + cut.extra);
+    const long long s1 = s0 + g.steps;
     // (in range as long as nobody changes lengths or bounds under the call)
     const int c0 = (int)min(quotient(s0, cut.len), (long long)p.blocks - 1), c1 = (int)min(quotient(s1 - 1, cut.len), (long long)p.blocks - 1);
     if (c0 == c1) continue;  // finished by its block
     const int slot0 = 2 * c0 + (cut.len * c0 >= s0 - cut.extra ? 0 : 1);  // 1: the block had a job before
-    const float own = p.lse_own ? p.lse_own[i] : NEG_INF;
+    const size_t at = (size_t)i * D + lane * V;
+    float own = NEG_INF, own_o[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) own_o[j] = 0.f;
+    if (warp == 0 && p.lse_own) {  // (rows that the kernel before finished are others)
+      own = p.lse_own[i];
+      if constexpr (V == 4) {
+        const uint2 x = *reinterpret_cast<const uint2*>(p.o_own + at);
+        own_o[0] = bf16_lo(x.x), own_o[1] = bf16_hi(x.x), own_o[2] = bf16_lo(x.y), own_o[3] = bf16_hi(x.y);
+      } else {
+        const uint32_t x = *reinterpret_cast<const uint32_t*>(p.o_own + at);
+        own_o[0] = bf16_lo(x), own_o[1] = bf16_hi(x);
+      }
+    }
+    if (!waited) pdl_wait();
+    waited = true;
     float m = NEG_INF, l = 0.f, acc[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) acc[j] = 0.f;
@@ -206,19 +238,19 @@ __global__ void __launch_bounds__(THREADS) prefix_join_kernel(PrefixParams p) {
       }
     }
 #pragma unroll
-    for (int j = 0; j < V; ++j) so[warp][lane * V + j] = acc[j];
-    if (lane == 0) sml[warp] = make_float2(m, l);
-    __syncthreads();
+    for (int j = 0; j < V; ++j) so[sub][warp][lane * V + j] = acc[j];
+    if (lane == 0) sml[sub][warp] = make_float2(m, l);
+    meet();
     if (warp == 0) {
       m = NEG_INF;
 #pragma unroll
-      for (int u = 0; u < WARPS; ++u) m = fmaxf(m, sml[u].x);
+      for (int u = 0; u < WARPS; ++u) m = fmaxf(m, sml[sub][u].x);
       l = 0.f;
 #pragma unroll
       for (int j = 0; j < V; ++j) acc[j] = 0.f;
 #pragma unroll
       for (int u = 0; u < WARPS; ++u) {
-        const float2 ml = sml[u];
+        const float2 ml = sml[sub][u];
         if (ml.x == NEG_INF) {
           l += ml.y;
           continue;
@@ -226,24 +258,24 @@ __global__ void __launch_bounds__(THREADS) prefix_join_kernel(PrefixParams p) {
         const float f = fast_exp2(ml.x - m);
         l += ml.y * f;
 #pragma unroll
-        for (int j = 0; j < V; ++j) acc[j] += so[u][lane * V + j] * f;
+        for (int j = 0; j < V; ++j) acc[j] += so[sub][u][lane * V + j] * f;
       }
       float fa, fo, lse;
       join_own(m, l, own, fa, fo, lse);
-      const size_t at = (size_t)i * D + lane * V;
       float v[V];
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         v[j] = fa == 0.f ? 0.f : acc[j] * fa;
-        if (p.o_own && fo != 0.f) v[j] += bf16_to_f32(p.o_own[at + j]) * fo;
+        if (fo != 0.f) v[j] += own_o[j] * fo;
       }
       if constexpr (V == 4)
         *reinterpret_cast<uint2*>(p.o + at) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
       else
         *reinterpret_cast<uint32_t*>(p.o + at) = pack_bf16x2(v[0], v[1]);
-      if (p.lse && lane == 0) p.lse[i] = lse;  // lse may be lse_own: read above, before the block met
+      __syncwarp();  // lse may be lse_own: every lane has read it
+      if (p.lse && lane == 0) p.lse[i] = lse;
     }
-    __syncthreads();
+    meet();
   }
   if (!waited) pdl_wait();  // what comes next on the stream waits for this kernel alone
 }
@@ -344,9 +376,12 @@ cudaError_t launch_prefix_attn(const uint16_t* q, const void* Kp, const void* Vp
   else
     e = pr.d == 128 ? launch_few_d<128>(p, s) : launch_few_d<64>(p, s);
   if (e != cudaSuccess) return e;
-  const unsigned grid = (unsigned)std::min<long long>((long long)p.R * p.H_q, (long long)num_sms * 16);
-  return pr.d == 128 ? launch_pdl(prefix_join_kernel<128>, dim3(grid), dim3(THREADS), 0, s, p)
-                     : launch_pdl(prefix_join_kernel<64>, dim3(grid), dim3(THREADS), 0, s, p);
+  const long long rows = (long long)p.R * p.H_q;
+  const int warps = rows <= 8ll * num_sms ? 4 : 2;  // a row
+  const dim3 grid((unsigned)std::min<long long>((rows * warps + 3) / 4, (long long)num_sms * 16));
+  auto join = pr.d == 128 ? (warps == 4 ? prefix_join_kernel<128, 4> : prefix_join_kernel<128, 2>)
+                          : (warps == 4 ? prefix_join_kernel<64, 4> : prefix_join_kernel<64, 2>);
+  return launch_pdl(join, grid, dim3(THREADS), 0, s, p);
 }
 
 }  // namespace pisa

@@ -129,9 +129,11 @@ struct PrefixWalk {
       end = min(total, cut.len * (block + 1) + extra);
       return;
     }
+    const PrefixGroup mine = prefix_group(prm, min(lane, prm.P - 1));
+    auto group = [&](int i) { return i < 32 ? mine : prefix_group(prm, i); };  // a lane's own
     long long S = 0, jobs = 0;
     for (int i = lane; i < prm.P; i += 32) {
-      const PrefixGroup x = prefix_group(prm, i);
+      const PrefixGroup x = group(i);
       jobs += group_jobs(prm, x);
       S += group_jobs(prm, x) * x.steps;
     }
@@ -144,7 +146,7 @@ struct PrefixWalk {
       if (len == 1) return true;
       bool even = true;
       for (int i = lane; i < prm.P; i += 32) {
-        const PrefixGroup x = prefix_group(prm, i);
+        const PrefixGroup x = group(i);
         even = even && (x.tiles == 0 || quotient(x.steps, len) * len == x.steps);
       }
       return (bool)__all_sync(0xffffffffu, even);
@@ -165,7 +167,7 @@ struct PrefixWalk {
       const int i = i0 + lane;
       long long s = 0;
       if (i < prm.P) {
-        const PrefixGroup x = prefix_group(prm, i);
+        const PrefixGroup x = group(i);
         s = group_jobs(prm, x) * (x.steps + extra);
       }
       long long x = s;

@@ -311,8 +311,9 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
     tmem_alloc(&sh.tmem, 512);
     tmem_relinquish();
   }
-  PrefixWalk first;
+  PrefixWalk first;  // (the first segment is found here: with all registers, and in one piece of code)
   first.init(p, block, block == 0 && warp == 0);
+  const bool any_work = first.next(p, block);
   uint32_t tmem = 0;
   if (warp != C::PRODUCER) {
     asm volatile("barrier.cta.sync 1, %0;" ::"n"(C::THREADS) : "memory");
@@ -334,7 +335,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
     if (lane == 0) count = Counts{};
     __syncwarp();
     bool failed = false;
-    while (!failed && walk.next(p, block)) {
+    for (bool more_work = any_work; !failed && more_work; more_work = walk.next(p, block)) {
       const PrefixWalk& w = walk.now();
       const Segment sg(p, w);
       const int local = (sg.lag == 1 ? 128 * h : 0) + trow;  // row in the tile
@@ -602,7 +603,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
     walk.start(first, &sh.walks[BITS == 8 ? warp : 0]);
     uint32_t nt = 0, seg = 0;  // tiles and segments so far
     bool failed = false;
-    while (!failed && walk.next(p, block)) {
+    for (bool more_work = any_work; !failed && more_work; more_work = walk.next(p, block)) {
       const PrefixWalk& w = walk.now();
       const Segment sg(p, w);
       if (!mbar_wait_warp(&bar.q_empty, (seg & 1) ^ 1, err)) break;
@@ -691,7 +692,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
         umma_bf16_ts(d, a + 8 * s, desc(b + ((s * 16 * 128) >> 4)), id_pv, s > 0 ? 1u : first ? 0u : 1u);
       umma_commit(&bar.o_done[h]);
     };
-    while (!failed && walk.next(p, block)) {
+    for (bool more_work = any_work; !failed && more_work; more_work = walk.next(p, block)) {
       const PrefixWalk& w = walk.now();
       const Segment sg(p, w);
       if (!mbar_wait_warp(BITS == 8 ? &bar.q_ready : &bar.q_full, seg & 1, err)) break;
@@ -768,7 +769,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
       walk.start(first, &sh.walks[warp]);
       uint32_t nt = 0, step0 = 0;
       bool failed = false;
-      while (!failed && walk.next(p, block)) {
+      for (bool more_work = any_work; !failed && more_work; more_work = walk.next(p, block)) {
         const PrefixWalk& w = walk.now();
         const Segment sg(p, w);
         const size_t row0 = ((size_t)w.p * p.H_kv + w.head) * p.N_cap;
