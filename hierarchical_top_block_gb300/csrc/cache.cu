@@ -24,6 +24,19 @@ namespace {
 constexpr int THREADS = 256;
 constexpr int RPT = 4;  // rows a thread has in flight
 
+// n / d of n < 2^31 as one product: with 2^(s-1) < d <= 2^s and m = ceil(2^(31+s) / d) < 2^32 + 1, n m / 2^(31+s)
+// exceeds n / d by n (m d - 2^(31+s)) / (d 2^(31+s)) < 2^31 2^s / (d 2^(31+s)) = 1 / d: the whole part is that of n / d.
+struct Divisor {
+  uint64_t m;
+  uint32_t d, shift;
+};
+Divisor divisor(uint32_t d) {
+  uint32_t s = 0;
+  while ((1ull << s) < d) ++s;
+  return {((1ull << (31 + s)) + d - 1) / d, d, 31 + s};
+}
+__device__ __forceinline__ uint32_t quotient(uint32_t n, const Divisor& d) { return (uint32_t)((n * d.m) >> d.shift); }
+
 struct CacheParams {
   const uint16_t* x[2];  // write: K and V rows in
   uint16_t* y[2];        // values out (read: the rows; write: nullable)
@@ -31,17 +44,18 @@ struct CacheParams {
   float* s[2];
   const int32_t* start;  // first cache row of each sequence (nullable: 0)
   const int32_t* count;  // rows of each sequence in use (nullable: T)
-  uint32_t rows;         // B * H * T
-  int H, T, N_cap;
+  uint32_t rows;         // B * H * T, below 2^31
+  Divisor H, T;
+  int N_cap;
   uint32_t* err;
 };
 
 // The place of row `row` of [B][H][T]: its cache row, or -1 where there is none (behind the
 // sequence's count, or a sequence whose rows do not fit: nothing of it is read or written).
 __device__ __forceinline__ long long cache_row(const CacheParams& p, uint32_t row) {
-  const uint32_t bh = row / (uint32_t)p.T, t = row - bh * (uint32_t)p.T, b = bh / (uint32_t)p.H;
-  const int first = p.start ? __ldg(p.start + b) : 0, n = p.count ? __ldg(p.count + b) : p.T;
-  if (first < 0 || n < 0 || n > p.T || first > p.N_cap - n) {
+  const uint32_t bh = quotient(row, p.T), t = row - bh * p.T.d, b = quotient(bh, p.H);
+  const int first = p.start ? __ldg(p.start + b) : 0, n = p.count ? __ldg(p.count + b) : (int)p.T.d;
+  if (first < 0 || n < 0 || n > (int)p.T.d || first > p.N_cap - n) {
     report_error(p.err, ERR_BAD_INDEX);
     return -1;
   }
@@ -68,34 +82,40 @@ __global__ void __launch_bounds__(THREADS) cache_write_kernel(CacheParams p) {
     }
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
-      const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-      // the largest |x| by its bits (bf16 magnitudes order as integers; NaN above infinity)
+      uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+      // the largest |x| by its bits (bf16 magnitudes order as integers; NaN above infinity), two at a time
       uint32_t a = 0;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) a = max(a, max(u[j] & 0x7fffu, (u[j] >> 16) & 0x7fffu));
+      for (int j = 0; j < 4; ++j) a = __vmaxu2(a, u[j] & 0x7fff7fffu);
 #pragma unroll
-      for (int o = LANES / 2; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
+      for (int o = LANES / 2; o > 0; o >>= 1) a = __vmaxu2(a, __shfl_xor_sync(0xffffffffu, a, o));
+      a = max(a >> 16, a & 0xffffu);
       const float amax = __uint_as_float(a << 16);
       const bool finite = a < 0x7f80u;
       const float scale = finite ? __fdiv_rn(amax, 127.f) : __uint_as_float(0x7fc00000u);
       // 127 / a overflows below 2^-121: both sides times 2^64 there (exact)
       const float up = amax < 5.421010862427522e-20f ? 1.8446744073709552e19f : 1.f;
-      const float inv = (a == 0 || !finite) ? 0.f : __fdiv_rn(127.f, amax * up) * (1.f + 9.5367431640625e-07f);
-      float t[8];
+      const float inv = a == 0 || !finite ? 0.f : __fdiv_rn(127.f, amax * up) * (1.f + 9.5367431640625e-07f);
+      float t[8];         // the codes
+      uint32_t bits[8];   // the codes in their low bytes
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float lo = bf16_lo(u[j]), hi = bf16_hi(u[j]);
-        t[2 * j] = inv > 0.f ? truncf(fmaf(lo * up, inv, copysignf(0.5f, lo))) : 0.f;
-        t[2 * j + 1] = inv > 0.f ? truncf(fmaf(hi * up, inv, copysignf(0.5f, hi))) : 0.f;
+      for (int j = 0; j < 8; ++j) {
+        if (j % 2 == 0 && !finite) u[j / 2] = 0;
+        float v = j % 2 ? bf16_hi(u[j / 2]) : bf16_lo(u[j / 2]);
+        if (up != 1.f) v *= up;
+        // |v inv| + 1/2 is cut to a whole number by its sum with 2^23 towards zero, and the code, subtracted
+        // from that again, is left in two's complement by a sum with 1.5 2^23
+        const uint32_t sign = __float_as_uint(v) & 0x80000000u;
+        const float big = __uint_as_float(0x4b000000u | sign);
+        t[j] = __fadd_rn(__fadd_rz(__fmaf_rn(v, inv, __uint_as_float(0x3f000000u | sign)), big), -big);
+        bits[j] = __float_as_uint(__fadd_rn(t[j], 12582912.f));
       }
       if (at[i] < 0) continue;
       uint32_t code[2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t b01 = __byte_perm((uint32_t)(int)t[4 * h], (uint32_t)(int)t[4 * h + 1], 0x0040);
-        const uint32_t b23 = __byte_perm((uint32_t)(int)t[4 * h + 2], (uint32_t)(int)t[4 * h + 3], 0x0040);
-        code[h] = __byte_perm(b01, b23, 0x5410);
-      }
+      for (int h = 0; h < 2; ++h)
+        code[h] = __byte_perm(__byte_perm(bits[4 * h], bits[4 * h + 1], 0x0040),
+                              __byte_perm(bits[4 * h + 2], bits[4 * h + 3], 0x0040), 0x5410);
       *reinterpret_cast<uint2*>(q + at[i] * D + 8 * part) = make_uint2(code[0], code[1]);
       if (part == 0) s[at[i]] = scale;
       if (VALUES) {
@@ -158,8 +178,8 @@ unsigned blocks_for(uint32_t rows, int rows_per_step, int num_sms) {
 CacheParams params_of(const Problem& p, uint32_t* err) {
   CacheParams c{};
   c.rows = (uint32_t)p.B * (uint32_t)p.H_kv * (uint32_t)p.N;
-  c.H = p.H_kv;
-  c.T = p.N;
+  c.H = divisor((uint32_t)p.H_kv);
+  c.T = divisor((uint32_t)p.N);
   c.N_cap = p.N_cap;
   c.err = err;
   return c;

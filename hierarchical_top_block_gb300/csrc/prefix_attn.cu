@@ -295,7 +295,7 @@ Plan prefix_plan(const Problem& p, bool codes) {
   const long long rows = ((long long)p.N * p.GQ + p.B - 1) / (p.B > 0 ? p.B : 1);
   const bool tc = rows > (codes ? 32 : 16);
   const int few = rows > 8 ? 16 : 8;
-  return tc ? Plan{true, TC_ROWS, MAX_SMS, 3} : Plan{false, few, few_blocks(p.d, few) * MAX_SMS, 1};
+  return tc ? Plan{true, TC_ROWS, MAX_SMS, 3} : Plan{false, few, few_blocks(p.d, few) * MAX_SMS, 2};
 }
 
 template <int D, int BITS, int NH>
