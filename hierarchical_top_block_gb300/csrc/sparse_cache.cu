@@ -65,17 +65,18 @@ struct Granules {
 
 template <int D, int NH>
 struct SparseCfg {
-  // one granule of 32 keys under way a warp: four blocks a SM (8 query heads) hide more than deeper rings
-  // (64 x 8 lists of 16 blocks: 28.6 us; with two granules and three blocks 36.5; of 16 keys, two: 28.5,
-  // but 24 x 5 drafted tokens of 16 query heads take 34.1 instead of 31.0)
-  static constexpr int KEYS = 32, SLOTS = 1;
+  // Up to eight query heads: one granule of 32 keys under way a warp and four blocks a SM hide more than deeper
+  // rings (64 x 8 lists of 16 blocks: 27.5 us; with two granules and three blocks 33.7).  Sixteen: the state
+  // takes twice the registers, and two granules with two blocks are better (24 x 5 drafted tokens, lists of
+  // 32 blocks: 29.3 us; one granule and three blocks 35.3, three and two 29.6).
+  static constexpr int KEYS = 32, SLOTS = NH, PER_SM = NH == 1 ? 4 : 2;
   using Tile = CacheTile<D, 8, KEYS, NH>;
   static constexpr uint32_t RING = 4 * SLOTS * Tile::BYTES, OUT = 4 * 8 * NH * D * 4;
   static constexpr uint32_t SMEM = RING > OUT ? RING : OUT;  // the outputs meet where the granules were
 };
 
 template <int D, int NH>
-__global__ void __launch_bounds__(THREADS, NH == 1 ? 4 : 3) sparse_cache_kernel(const __grid_constant__ CUtensorMap mapK,
+__global__ void __launch_bounds__(THREADS, SparseCfg<D, NH>::PER_SM) sparse_cache_kernel(const __grid_constant__ CUtensorMap mapK,
                                                                     const __grid_constant__ CUtensorMap mapV,
                                                                     SparseParams p, int cluster) {
   using C = SparseCfg<D, NH>;
@@ -245,11 +246,12 @@ cudaError_t launch_sparse_cache(const uint16_t* q, const int8_t* Kq, const int8_
   p.sl2 = pr.scale * LOG2E;
   p.err = err;
   const long long pairs = (long long)pr.B * pr.H_kv * pr.N;
-  // up to four blocks a SM, while every warp keeps granules of its own (8 blocks: 24 x 5 drafted tokens
-  // take 39 us instead of 31, 16 x 8 lists 16 instead of 11)
-  int cluster = 1;
-  while (cluster < 8 && pairs * cluster * 2 <= 4LL * num_sms && 4 * cluster < 2 * pr.K) cluster *= 2;
+  // Blocks in a cluster: as many as are resident at once, while every warp keeps granules of its own.  (A cluster
+  // costs two meetings and the other blocks' outputs, so lists that fill the SMs get one block each: 24 x 5
+  // drafted tokens take 29 us with one block, 44 with two; one list of 16 blocks 7.8 us with eight and 14.4 with one.)
   const bool wide = pr.GQ > 8;
+  int cluster = 1;
+  while (cluster < 8 && pairs * cluster * 2 <= (wide ? 2LL : 4LL) * num_sms && 4 * cluster < 2 * pr.K) cluster *= 2;
   if (pr.d == 128)
     return wide ? launch_t<128, 2>(Kq, Vq, p, pr, cluster, s) : launch_t<128, 1>(Kq, Vq, p, pr, cluster, s);
   return wide ? launch_t<64, 2>(Kq, Vq, p, pr, cluster, s) : launch_t<64, 1>(Kq, Vq, p, pr, cluster, s);
