@@ -43,7 +43,7 @@ def no_error():
 
 # ---- write -------------------------------------------------------------------------------
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("B,H,T,N", [(1, 1, 1, 1), (3, 2, 1, 65), (2, 3, 17, 40), (1, 8, 1000, 1003), (5, 1, 129, 700)])
+@pytest.mark.parametrize("B,H,T,N", [(1, 1, 1, 1), (3, 2, 1, 65), (2, 3, 17, 40), (1, 8, 1000, 1003), (5, 1, 129, 700), (3, 5, 4001, 4100)])
 @pytest.mark.parametrize("ragged", [False, True])
 def test_write(d, B, H, T, N, ragged):
     g = gen(T * 7 + d)
@@ -164,7 +164,7 @@ def test_write_lengths_that_do_not_fit(ln, n):
 
 # ---- read --------------------------------------------------------------------------------
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("B,H,T,N", [(1, 1, 1, 1), (2, 3, 7, 100), (3, 2, 333, 500), (4, 8, 64, 64)])
+@pytest.mark.parametrize("B,H,T,N", [(1, 1, 1, 1), (2, 3, 7, 100), (3, 2, 333, 500), (4, 8, 64, 64), (3, 5, 4001, 4100)])
 @pytest.mark.parametrize("ragged", [False, True])
 def test_read(d, B, H, T, N, ragged):
     g = gen(T + d)
@@ -235,7 +235,8 @@ def lists(g, B, H, T, K, N, ln):
 @pytest.mark.parametrize("B,T,H_q,H,d,K,N", [
     (1, 1, 1, 1, 64, 1, 1), (1, 1, 16, 1, 128, 16, 4096), (2, 1, 4, 4, 64, 4, 333), (3, 1, 32, 8, 128, 16, 2000),
     (1, 5, 16, 1, 64, 32, 3001), (2, 3, 8, 1, 128, 8, 700), (40, 2, 16, 8, 128, 8, 130), (2, 8, 32, 2, 128, 32, 2500),
-    (1, 1, 2, 1, 128, 32, 5000), (300, 1, 2, 1, 64, 3, 200)])
+    (1, 1, 2, 1, 128, 32, 5000), (300, 1, 2, 1, 64, 3, 200),
+    (60, 2, 32, 2, 128, 9, 1500), (90, 1, 32, 2, 64, 17, 1999)])
 @pytest.mark.parametrize("ragged", [False, True])
 def test_sparse(B, T, H_q, H, d, K, N, ragged):
     g = gen(B + 10 * T + K)

@@ -89,6 +89,12 @@ CASES = [  # R, H_q, H, d, N, lens, rows
     (16, 16, 8, 64, 70000, [70000], [0, 16]),
     (6, 32, 4, 128, 50001, [50001], [0, 6]),
     (37, 16, 4, 128, 50001, [49999], [0, 37]),
+    # blocks that meet two jobs and more, of groups of different sizes
+    (150, 16, 8, 128, 6000, [5000, 6000, 3], [0, 60, 140, 150]),
+    (9, 16, 8, 128, 20000, [19999, 777, 20000], [0, 3, 8, 9]),
+    (12, 32, 8, 64, 20000, [19000, 5, 20000, 64], [0, 4, 4, 9, 12]),
+    (1600, 8, 8, 64, 700, list(range(100, 700, 15)), list(range(0, 1601, 40))),
+    (64, 32, 8, 64, 4000, [3999], [0, 64]),
 ]
 
 
