@@ -484,27 +484,26 @@ def pisa_decode_step(q, k, v, Kc, Vc, Pc, seq_len, K_sel: int, scale: float = 0.
 
 
 # ---- 8-bit cache ------------------------------------------------------------------------
-def _fits(t, name, shape, dtype, device):
-    """_expect, in the order and by the calls that cost a valid argument least."""
-    if t is not None and (t.dtype is not dtype or t.shape != shape or t.get_device() != device.index
-                          or not t.is_contiguous()):
-        _expect(t, name, shape, dtype, device)
+def _fits(t, name, shape, dtype, dev):
+    """_expect on CUDA device number dev, in the order and by the calls that cost a valid argument least."""
+    if t is not None and (t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous()):
+        _expect(t, name, shape, dtype, torch.device("cuda", dev))
 
 
 def _cuda(t, name):
+    """The number of the device that t is on."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    return t.device
+    return t.get_device()
 
 
-def _call(fn, what, device, *args):
+def _call(fn, what, dev, *args):
     """Calls a library function on the device's current stream, with that device current."""
-    i = device.index
-    if i == torch.cuda.current_device():
-        rc = fn(*args, torch._C._cuda_getCurrentRawStream(i))
+    if dev == torch._C._cuda_getDevice():  # (a tensor is on it: it is initialised)
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
-        with torch.cuda.device(i):
-            rc = fn(*args, torch._C._cuda_getCurrentRawStream(i))
+        with torch.cuda.device(dev):
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     if rc != PISA_OK:
         raise PisaError(rc, what)
 
@@ -650,7 +649,7 @@ def pisa_prefix_attn(q, Kp, Vp, prefix_len, row_start=None, k_scale=None, v_scal
     _fits(o_own, "o_own", want, torch.bfloat16, dev)
     _fits(lse_own, "lse_own", want[:2], torch.float32, dev)
     if o is None:
-        o = torch.empty(want, dtype=torch.bfloat16, device=dev)
+        o = torch.empty_like(q)
     else:
         _fits(o, "o", want, torch.bfloat16, dev)
     if lse is not None:
@@ -661,7 +660,7 @@ def pisa_prefix_attn(q, Kp, Vp, prefix_len, row_start=None, k_scale=None, v_scal
     need = lib().pisa_prefix_attn_workspace_bytes(shape, params)
     if need == 0 and R > 0:
         raise PisaError(2, "pisa_prefix_attn: unsupported shape or parameters")
-    ws = _workspace(ws, need, dev)
+    ws = _workspace(ws, need, torch.device("cuda", dev))
     _call(lib().pisa_prefix_attn, "pisa_prefix_attn", dev, q.data_ptr(), Kp.data_ptr(), Vp.data_ptr(), _addr(k_scale),
           _addr(v_scale), prefix_len.data_ptr(), _addr(row_start), _addr(o_own), _addr(lse_own), o.data_ptr(),
           _addr(lse if want_lse else None), ws.data_ptr(), ws.numel(), shape, params)

@@ -295,7 +295,11 @@ Plan prefix_plan(const Problem& p, bool codes) {
   const long long rows = ((long long)p.N * p.GQ + p.B - 1) / (p.B > 0 ? p.B : 1);
   const bool tc = rows > (codes ? 32 : 16);
   const int few = rows > 8 ? 16 : 8;
-  return tc ? Plan{true, TC_ROWS, MAX_SMS, 3} : Plan{false, few, few_blocks(p.d, few) * MAX_SMS, 2};
+  Plan plan = tc ? Plan{true, TC_ROWS, MAX_SMS, 3} : Plan{false, few, few_blocks(p.d, few) * MAX_SMS, 2};
+  // no more blocks (and scratch) than there can be steps: every group has at most one tile that is not full
+  const long long tiles = (long long)p.N * p.GQ / plan.rows + p.B, steps = (p.N_cap + PREFIX_KT - 1) / PREFIX_KT;
+  plan.blocks = (int)std::min<long long>(plan.blocks, p.H_kv * tiles * steps);
+  return plan;
 }
 
 template <int D, int BITS, int NH>
