@@ -30,16 +30,17 @@ __device__ __forceinline__ void write_out(const PrefixParams& p, size_t at, size
 
 // Few rows: tiles of 8 NH on mma.sync.  A block's four warps take the granules of a segment in turn,
 // each with a ring of its own that it fills by TMA.
-constexpr int few_blocks(int d, int rows) { return rows > 8 ? 2 : d == 128 ? 4 : 3; }  // a SM
+constexpr int few_blocks(int rows) { return rows > 8 ? 2 : 4; }  // a SM
 
 template <int D, int BITS, int NH>
 struct FewCfg {
-  static constexpr int KEYS = BITS == 8 ? 32 : 16;
-  // granules a warp has under way, and blocks a SM.  Up to 8 rows more blocks beat deeper rings (8 rows x 8
-  // heads, 32768 keys of codes at d = 128: 26.5 us with 1 x 4, 27.0 with 2 x 3, 41 with 4 x 3), which the
-  // registers of 16 rows do not allow (16 rows: 33.0 us with 2 x 2, 33.8 with 1 x 3, 36.2 with 2 x 3).
-  static constexpr int SLOTS = D == 128 && NH == 1 ? 1 : 2;
-  static constexpr int PER_SM = few_blocks(D, 8 * NH);
+  // A granule: 4 KB of K and of V, at most 32 keys (d = 64, bf16: 8 rows x 8 heads, 32768 keys take 12.2 us with 32
+  // keys and 13.3 with 16).  Granules a warp has under way: one with 8 KB and the registers of 8 rows, where
+  // four blocks a SM hide more than deeper rings with three (d = 128, codes, 26.5 against 27.0 and with four
+  // granules 41 when measured; 16 rows, two blocks: 32.0 with two granules, 34.4 with one).
+  static constexpr int KEYS = D * BITS <= 1024 ? 32 : 16;
+  static constexpr int SLOTS = D * BITS == 512 || (NH == 2 && D == 128) ? 2 : 1;
+  static constexpr int PER_SM = few_blocks(8 * NH);
   using Tile = CacheTile<D, BITS, KEYS, NH>;
   static constexpr uint32_t RING = 4 * SLOTS * Tile::BYTES, OUT = 4 * 8 * NH * D * 4;
   static constexpr uint32_t SMEM = RING > OUT ? RING : OUT;  // the outputs meet where the granules were
@@ -129,9 +130,10 @@ __global__ void __launch_bounds__(THREADS, FewCfg<D, BITS, NH>::PER_SM) prefix_f
 
 // Joins the parts of every job that spans blocks.  A (row, query head) is joined by WARPS warps of a block's four: a
 // part is D floats, one 16-byte (8-byte) piece a lane; the warps take the parts in turn, BATCH of them in
-// flight, each with its own running maximum, and meet in shared memory.  Latency bounds it (launch, bounds,
-// maxima, sums), so few rows have all four warps each, and many have two, so that all rows are under way at
-// once (64 tokens of 32 heads, 19 parts a row: JOIN_FIGURES).
+// flight, each with its own running maximum, and meet in shared memory.  Latency bounds it (launch 1 us, wait
+// for the kernel before 1.7, bounds 1, sums 1-2), so few rows have all four warps each, and many have two, so that
+// all rows are under way at once (217 tokens of 16 heads in five groups: the call takes 35.1 us, with four
+// warps 38.6; 4 tokens of 32 heads, 38 parts a row: 23.0 with four, 25.4 with two).
 template <int D, int WARPS>
 __global__ void __launch_bounds__(THREADS, 8) prefix_join_kernel(PrefixParams p) {
   constexpr int V = D / 32, BATCH = 8, PER = THREADS / 32 / WARPS;  // rows a block
@@ -284,9 +286,9 @@ constexpr int MAX_SMS = 152;  // this GPU's: the scratch does not depend on the 
 
 // Which kernel, by the query rows a group has on average (the groups' own sizes are on the device; any kernel
 // takes any).  The few-row kernel reads the prefix again for every 16 rows, the tensor-core one pays for its
-// start (first tile in flight to first scores, 4.5 us) and for 256 rows whether they are there or not.  At
-// 8 KV heads x 32768 keys of d = 128, few-row against tensor-core kernel: bf16, 16 rows 37 : 35 us, 32 rows
-// 46 : 36; codes, 32 rows 40 : 50, 64 rows 58 : 50.
+// start (first scores after 6 us) and for 256 rows whether they are there or not.  At 8 KV heads x 32768 keys
+// of d = 128, few-row against tensor-core kernel: codes, 32 rows 32 : 37 us, 48 rows 42 : 38; bf16, 16 rows 32 : 35,
+// 32 rows 47 : 36; d = 64: codes, 32 rows 24 : 29, 64 rows 39 : 30; bf16, 16 rows 16 : 21, 32 rows 24 : 21.
 struct Plan {
   bool tc;
   int rows, blocks, stop;
@@ -295,7 +297,7 @@ Plan prefix_plan(const Problem& p, bool codes) {
   const long long rows = ((long long)p.N * p.GQ + p.B - 1) / (p.B > 0 ? p.B : 1);
   const bool tc = rows > (codes ? 32 : 16);
   const int few = rows > 8 ? 16 : 8;
-  Plan plan = tc ? Plan{true, TC_ROWS, MAX_SMS, 3} : Plan{false, few, few_blocks(p.d, few) * MAX_SMS, 2};
+  Plan plan = tc ? Plan{true, TC_ROWS, MAX_SMS, 3} : Plan{false, few, few_blocks(few) * MAX_SMS, 2};
   // no more blocks (and scratch) than there can be steps: every group has at most one tile that is not full
   const long long tiles = (long long)p.N * p.GQ / plan.rows + p.B, steps = (p.N_cap + PREFIX_KT - 1) / PREFIX_KT;
   plan.blocks = (int)std::min<long long>(plan.blocks, p.H_kv * tiles * steps);

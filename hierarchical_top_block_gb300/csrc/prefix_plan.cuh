@@ -11,7 +11,9 @@
 // A block that meets a second job stops for it: the rows of the first are written, those of the
 // next fetched.  On the line every job but the first therefore begins with `extra` empty steps,
 // as long as that stop; where the jobs end on the blocks' bounds anyway, or the empty steps would
-// make the ranges longer than a stop does, there are none.
+// make the ranges longer than a stop does, there are none.  (64 tokens of 32 / 8 heads after 32768 codes, eight
+// jobs of 256 steps over 152 blocks: 49.0 us with a stop of 3 steps, 47.8 with 4, 54.7 with none; five groups
+// of bf16 prefixes, 20 jobs of 79 steps: 34.8, 34.0 and 38.8.)
 #pragma once
 
 #include "common.cuh"

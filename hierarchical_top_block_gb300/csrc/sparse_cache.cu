@@ -5,8 +5,14 @@
 // Work: K * 64 rows of 2 d + 8 bytes a (b, h_kv, t) against 4 G_Q d operations a row, at most 60 a
 // byte: the reads bound it, so what counts is bytes in flight.  A block of four warps per (b, h_kv, t): the
 // warps take the list's granules (KEYS keys) in turn, each with a ring of its own that it fills by TMA
-// as far ahead as the ring goes.  Where there are few (b, h_kv, t), a cluster of up to eight blocks shares one list and the partial results meet through distributed shared memory, so
-// that every size is one launch and needs no scratch memory.
+// as far ahead as the ring goes.  Where there are few (b, h_kv, t), a cluster of up to eight blocks shares
+// one list and the partial results meet through distributed shared memory, so that every size is one
+// launch and needs no scratch memory.
+//
+// Measured: 64 x 8 lists of 16 blocks (four query heads each, d = 128, 139 MB) 27.4 us, 5.1 TB/s; one list of 16
+// blocks under 16 heads 7.8 us, where launch, list, first copy and the cluster's two meetings follow one
+// another; 24 x 5 drafted tokens x 2 lists of 32 blocks 29 us, bound by the instructions of a warp's
+// granules (1.6 us each; 240 lists leave SMs with one block and with two).
 #include <cooperative_groups.h>
 
 #include "cache_attn.cuh"
