@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(THREADS, FewCfg<D, BITS, NH>::PER_SM) prefix_f
     const int m0 = w.tile * ROWS;                           // first query row of the tile
     const int rows = min(ROWS, w.g.n * p.GQ - m0);          // query row m: token m / G, head m % G
     auto q_row = [&](int i) {
-      const int m = m0 + i, tok = m / p.GQ;
+      const int m = m0 + i, tok = m >> p.gq_bits;
       return ((size_t)(w.g.first + tok) * p.H_q + (size_t)w.head * p.GQ + (m - tok * p.GQ));
     };
     const int ph = w.p * p.H_kv + w.head;
@@ -165,9 +165,9 @@ __global__ void __launch_bounds__(THREADS, 8) prefix_join_kernel(PrefixParams p)
     }
     const PrefixGroup g = prefix_group(p, gp);
     if (row < g.first || row >= g.first + g.n) continue;
-    const int head = hq / p.GQ;
+    const int head = hq >> p.gq_bits;
     const int mrow = (row - g.first) * p.GQ + (hq - head * p.GQ);
-    const int tile = mrow / p.rows, local = mrow - tile * p.rows;
+    const int tile = mrow >> p.row_bits, local = mrow - (tile << p.row_bits);
     PrefixCut cut;
     long long s0 = 0;
     if (p.P == 1) {
@@ -175,16 +175,14 @@ __global__ void __launch_bounds__(THREADS, 8) prefix_join_kernel(PrefixParams p)
     } else {
       if (!waited) pdl_wait();
       waited = true;
-      cut = PrefixCut{p.base[p.P], (int)p.base[p.P + 1]};
+      cut = prefix_cut(p, p.base[p.P], (int)p.base[p.P + 1]);
       s0 = p.base[gp];
     }
-    // the job's steps, counted from the first block's first
-    s0 += ((long long)head * g.tiles + tile) * (g.steps + cut.extra);
-    const long long s1 = s0 + g.steps;
+    s0 += ((long long)head * g.tiles + tile) * (g.steps + cut.extra);  // the job's first position; its steps follow `extra`
     // (in range as long as nobody changes lengths or bounds under the call)
-    const int c0 = (int)min(quotient(s0, cut.len), (long long)p.blocks - 1), c1 = (int)min(quotient(s1 - 1, cut.len), (long long)p.blocks - 1);
+    const int c0 = min(cut.block_of(s0 + cut.extra), p.blocks - 1), c1 = min(cut.block_of(s0 + cut.extra + g.steps - 1), p.blocks - 1);
     if (c0 == c1) continue;  // finished by its block
-    const int slot0 = 2 * c0 + (cut.len * c0 >= s0 - cut.extra ? 0 : 1);  // 1: the block had a job before
+    const int slot0 = 2 * c0 + (cut.start(c0) >= s0 ? 0 : 1);  // 1: the block had a job before
     const size_t at = (size_t)i * D + lane * V;
     float own = NEG_INF, own_o[V];
 #pragma unroll
@@ -211,7 +209,7 @@ __global__ void __launch_bounds__(THREADS, 8) prefix_join_kernel(PrefixParams p)
       for (int u = 0; u < BATCH; ++u) {
         const int cc = c + u * WARPS;
         const bool in = cc <= c1;
-        const size_t at = (size_t)(cc == c0 || !in ? slot0 : 2 * cc) * p.rows + local;
+        const size_t at = ((size_t)(cc == c0 || !in ? slot0 : 2 * cc) << p.row_bits) + local;
         ml[u] = in ? p.part_ml[at] : make_float2(NEG_INF, 0.f);
         const float* src = p.part_o + at * D + lane * V;
         if constexpr (V == 4)
@@ -324,8 +322,8 @@ cudaError_t launch_few(const PrefixParams& p, cudaStream_t s) {
 }
 template <int D>
 cudaError_t launch_few_d(const PrefixParams& p, cudaStream_t s) {
-  if (p.ks) return p.rows > 8 ? launch_few<D, 8, 2>(p, s) : launch_few<D, 8, 1>(p, s);
-  return p.rows > 8 ? launch_few<D, 16, 2>(p, s) : launch_few<D, 16, 1>(p, s);
+  if (p.ks) return p.row_bits > 3 ? launch_few<D, 8, 2>(p, s) : launch_few<D, 8, 1>(p, s);
+  return p.row_bits > 3 ? launch_few<D, 16, 2>(p, s) : launch_few<D, 16, 1>(p, s);
 }
 
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -366,10 +364,16 @@ cudaError_t launch_prefix_attn(const uint16_t* q, const void* Kp, const void* Vp
   p.sl2 = pr.scale * LOG2E;
   p.err = err;
   const Plan plan = prefix_plan(pr, k_scale != nullptr);
-  p.rows = plan.rows;
+  auto bits = [](int x) {  // of a power of two
+    int b = 0;
+    while ((1 << b) < x) ++b;
+    return b;
+  };
+  p.gq_bits = bits(pr.GQ);
+  p.row_bits = bits(plan.rows);
   p.blocks = plan.blocks;
   p.stop = plan.stop;
-  const size_t parts = (size_t)2 * p.blocks * p.rows;
+  const size_t parts = (size_t)2 * p.blocks * plan.rows;
   uint8_t* w = static_cast<uint8_t*>(ws);
   p.part_o = reinterpret_cast<float*>(w);
   w += up256(parts * pr.d * 4);

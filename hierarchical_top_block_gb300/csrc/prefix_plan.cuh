@@ -8,12 +8,17 @@
 // parts: the first job of its range and the last.  The cut depends on the sizes alone, so results
 // are the same in every run.
 //
+// The ranges begin at S b / blocks, rounded down, not at multiples of a rounded length: the jobs of one
+// head (tiles of its query rows) read the same keys, and with the exact quotient their blocks begin at
+// few different keys, walk over the prefix side by side, and all but the first find it in the L2 (256
+// tokens of 32 / 2 heads after 131072 bf16 keys, 32 jobs over 152 blocks: 388 us, with multiples 403).
+//
 // A block that meets a second job stops for it: the rows of the first are written, those of the
-// next fetched.  On the line every job but the first therefore begins with `extra` empty steps,
-// as long as that stop; where the jobs end on the blocks' bounds anyway, or the empty steps would
-// make the ranges longer than a stop does, there are none.  (64 tokens of 32 / 8 heads after 32768 codes, eight
-// jobs of 256 steps over 152 blocks: 49.0 us with a stop of 3 steps, 47.8 with 4, 54.7 with none; five groups
-// of bf16 prefixes, 20 jobs of 79 steps: 34.8, 34.0 and 38.8.)
+// next fetched.  On the line every job therefore begins with `extra` empty steps, as long as that stop;
+// where the jobs end on the blocks' bounds anyway, or the empty steps would make the ranges longer than
+// a stop does, there are none.  (64 tokens of 32 / 8 heads after 32768 codes, eight jobs of 256 steps over
+// 152 blocks: 49.0 us with a stop of 3 steps, 47.8 with 4, 54.7 with none; five groups of bf16 prefixes,
+// 20 jobs of 79 steps: 34.8, 34.0 and 38.8.)
 #pragma once
 
 #include "common.cuh"
@@ -34,9 +39,9 @@ struct PrefixParams {
   float* lse;                // nullable
   float* part_o;             // [2 blocks][ROWS][d] output sums relative to the row maximum
   float2* part_ml;           // [2 blocks][ROWS] row maximum (log2 units) and sum
-  long long* base;           // [P + 2] first step of each group, a range's steps, `extra` (with one group: not written)
+  long long* base;           // [P + 2] first step of each group, the line's length, `extra` (with one group: not written)
   int P, R, H_q, H_kv, GQ, N_cap;
-  int rows;                  // ROWS
+  int gq_bits, row_bits;     // G_Q and ROWS are 2 to these
   int blocks;                // thread blocks the steps are divided over
   int stop;                  // steps that a second job in a block costs
   float sl2;
@@ -58,7 +63,7 @@ __device__ __forceinline__ PrefixGroup prefix_group(const PrefixParams& p, int i
   g.first = lo;
   g.n = hi - lo;
   g.len = min(max(__ldg(p.prefix_len + i), 0), p.N_cap);
-  g.tiles = (int)(((long long)g.n * p.GQ + p.rows - 1) / p.rows);
+  g.tiles = (int)((((long long)g.n << p.gq_bits) + (1 << p.row_bits) - 1) >> p.row_bits);
   g.steps = max(1, (g.len + PREFIX_KT - 1) / PREFIX_KT);
   return g;
 }
@@ -71,26 +76,31 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
   return (a >> 32) || (b >> 32) ? a / b : (long long)((uint32_t)a / (uint32_t)b);
 }
 
-// The line's cut.  Block c has the positions [len c, len (c + 1)) + extra; job j of a group that starts at
-// position `base` has its steps from base + j (steps + extra) + extra on.
+// The line's cut: S positions over `blocks` blocks.  Job j of a group whose first position is `base` has its
+// steps from base + j (steps + extra) + extra on.
 struct PrefixCut {
-  long long len;
-  int extra;
+  long long S;
+  int blocks, extra;
+  __device__ __forceinline__ long long start(int block) const { return quotient(S * block, blocks); }
+  // The block that holds position s: the last one that starts at or before it.
+  __device__ __forceinline__ int block_of(long long s) const { return (int)quotient((s + 1) * blocks - 1, S); }
 };
-__device__ __forceinline__ long long range_len(long long S, int blocks) { return quotient(S + blocks - 1, blocks); }
-// S steps in so many jobs; `even(len)`: no range of len steps meets a second job.
+// Every block in use has a position, so a job's parts are in consecutive blocks.
+__device__ __forceinline__ PrefixCut prefix_cut(const PrefixParams& p, long long S, int extra) {
+  return PrefixCut{S, (int)max(min(S, (long long)p.blocks), 1ll), extra};
+}
+// S steps in so many jobs; `even(len)`: ranges of len steps never meet a second job.
 template <class Even>
 __device__ __forceinline__ PrefixCut prefix_cut(const PrefixParams& p, long long S, long long jobs, Even even) {
-  PrefixCut c{range_len(S, p.blocks), 0};
-  if (jobs > 1 && !even(c.len)) {
-    const long long len = range_len(S + (jobs - 1) * p.stop, p.blocks);
-    if (len < c.len + p.stop) c = PrefixCut{len, p.stop};
-  }
-  return c;
+  const PrefixCut c = prefix_cut(p, S, 0);
+  const long long len = quotient(S, c.blocks), with = S + jobs * p.stop;
+  if (jobs <= 1 || (len * c.blocks == S && even(len))) return c;
+  // the longest range, with its stop or with the empty steps
+  return with <= (len + p.stop) * c.blocks ? prefix_cut(p, with, p.stop) : c;
 }
 __device__ __forceinline__ PrefixCut prefix_cut_one(const PrefixParams& p, const PrefixGroup& g) {
   return prefix_cut(p, group_jobs(p, g) * g.steps, group_jobs(p, g),
-                    [&](long long len) { return len == 1 || quotient(g.steps, len) * len == g.steps; });
+                    [&](long long len) { return quotient(g.steps, len) * len == g.steps; });
 }
 
 // Walks a block's range job by job.  Every thread of a warp holds the same state.
@@ -126,9 +136,7 @@ struct PrefixWalk {
       g = prefix_group(prm, 0);
       const PrefixCut cut = prefix_cut_one(prm, g);
       extra = (short)cut.extra;
-      const long long total = group_jobs(prm, g) * (g.steps + extra);
-      at = min(total, cut.len * block + extra);
-      end = min(total, cut.len * (block + 1) + extra);
+      range(cut, block);
       return;
     }
     const PrefixGroup mine = prefix_group(prm, min(lane, prm.P - 1));
@@ -145,7 +153,6 @@ struct PrefixWalk {
       jobs += __shfl_xor_sync(0xffffffffu, jobs, o);
     }
     const PrefixCut cut = prefix_cut(prm, S, jobs, [&](long long len) {
-      if (len == 1) return true;
       bool even = true;
       for (int i = lane; i < prm.P; i += 32) {
         const PrefixGroup x = group(i);
@@ -154,11 +161,9 @@ struct PrefixWalk {
       return (bool)__all_sync(0xffffffffu, even);
     });
     extra = (short)cut.extra;
-    const long long line = S + jobs * extra;
-    at = min(line, cut.len * block + extra);
-    end = min(line, cut.len * (block + 1) + extra);
+    range(cut, block);
     if (record && lane == 0) {
-      prm.base[prm.P] = cut.len;
+      prm.base[prm.P] = cut.S;
       prm.base[prm.P + 1] = extra;
     }
     if (at >= end && !record) return;
@@ -189,6 +194,13 @@ struct PrefixWalk {
       before += __shfl_sync(0xffffffffu, x, 31);
     }
     g = prefix_group(prm, p);
+  }
+
+  __device__ __forceinline__ void range(const PrefixCut& cut, int block) {
+    at = end = 0;
+    if (block >= cut.blocks) return;
+    at = cut.start(block);
+    end = cut.start(block + 1);
   }
 
   // Moves to the next segment; false at the end of the range.

@@ -29,8 +29,8 @@
 // next S is issued right behind its O += P V, which reads P from the same columns.  Every wait is
 // bounded.
 //
-// Measured (d = 128): 256 tokens of 32 / 2 heads after 131072 bf16 keys 398-410 us, 1.35-1.38 PFLOP/s; a step of
-// 256 rows takes 3400 clocks, of which the products alone would take 2048 and their operands' way through
+// Measured (d = 128): 256 tokens of 32 / 2 heads after 131072 bf16 keys 388 us, 1.42 PFLOP/s; a step of
+// 256 rows takes 3300 clocks, of which the products alone would take 2048 and their operands' way through
 // shared memory, with the copies, up to 2560; the rest is the softmax's latency that two streams do
 // not hide.  (Weights handed over in halves, so that O += P V starts earlier: no gain.  Pairs of SMs
 // that share the tiles, halving the operands' reads: slower, each step then waits for the other SM.)  With
@@ -234,7 +234,7 @@ __device__ __forceinline__ RowOut row_out(const PrefixParams& p, const PrefixWal
     if (live && stats) p.part_ml[r.orow] = make_float2(m, l);
     return r;
   }
-  const int mrow = w.tile * ROWS + local, tok = mrow / p.GQ;
+  const int mrow = w.tile * ROWS + local, tok = mrow >> p.gq_bits;
   r.orow = (size_t)(w.g.first + tok) * p.H_q + (size_t)w.head * p.GQ + (mrow - tok * p.GQ);
   float lse;
   join_own(m, l, live && p.lse_own ? p.lse_own[r.orow] : NEG_INF, r.fa, r.fo, lse);
@@ -622,7 +622,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
         for (int h = 0; h < streams; ++h)
           for (int c = 0; c < DH; ++c)
             tma_load_4d(sQ + h * C::QT_BYTES + c * (128 * 128), &mapQ, &bar.q_full, 64 * c, 0, w.head,
-                        w.g.first + (w.tile * ROWS + h * 128) / p.GQ);
+                        w.g.first + ((w.tile * ROWS + h * 128) >> p.gq_bits));
       }
       ++seg;
       const int ph = w.p * p.H_kv + w.head;
