@@ -235,7 +235,7 @@ struct CacheTile {
     float lv[BITS == 8 ? G8 : 1];
     if constexpr (BITS == 8) {
 #pragma unroll
-      for (int i = 0; i < G8; ++i) lv[i] = fmaxf(fast_log2(sc.v[i]), -100.f);
+      for (int i = 0; i < G8; ++i) lv[i] = fmaxf(fast_log2(fabsf(sc.v[i])), -100.f);
     }
     bool moved = false;
     float top[NH][2];
@@ -264,14 +264,17 @@ struct CacheTile {
     if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
       for (int h = 0; h < NH; ++h) {
-        float f[2];
+        float f[2], l[2];
+        unpack_f32x2(st.l[h], l[0], l[1]);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float to = fmaxf(st.n[h][e], top[h][e]);
-          f[e] = to == NEG_INF ? 1.f : fast_exp2(st.n[h][e] - to);  // 0 before the first keys
+          const float to = fmaxf(st.n[h][e], top[h][e]), by = to == NEG_INF ? 0.f : st.n[h][e] - to;
+          f[e] = fast_exp2(by);  // 0 before the first keys
+          // (n covers the values' scales too: where those rise by far, l is large and may keep what f does not)
+          l[e] = times_exp2(l[e], by);
           st.n[h][e] = to;
         }
-        st.l[h] = mul_f32x2(st.l[h], pack_f32x2(f[0], f[1]));
+        st.l[h] = pack_f32x2(l[0], l[1]);
 #pragma unroll
         for (int t = 0; t < DT; ++t) {
           st.o[t][h][0] *= f[0];
@@ -406,7 +409,7 @@ __device__ __forceinline__ void join_warps(typename Tile::State& st, float* po, 
 #pragma unroll
       for (int k = 0; k < 4; ++k) {  // without a reference a sum is 0, or NaN where every logit was
         const float a = sn[k][row], b = sl[k][row];
-        l += a == NEG_INF ? b : b * fast_exp2(a - n);
+        l += a == NEG_INF ? b : times_exp2(b, a - n);
       }
       if (warp == 0 && r == 0 && row < rows) ml[row] = make_float2(n, l);
       const float f = st.n[h][e] == NEG_INF ? 0.f : fast_exp2(st.n[h][e] - n);

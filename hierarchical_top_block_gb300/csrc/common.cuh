@@ -88,6 +88,11 @@ __device__ __forceinline__ float fast_exp2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// x 2^e where 2^e alone may be below fp32's range (e > -252).
+__device__ __forceinline__ float times_exp2(float x, float e) {
+  const float h = fast_exp2(0.5f * e);
+  return x * h * h;
+}
 __device__ __forceinline__ float fast_log2(float x) {
   float y;
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

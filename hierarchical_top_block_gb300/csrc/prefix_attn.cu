@@ -133,10 +133,11 @@ __global__ void __launch_bounds__(THREADS, FewCfg<D, BITS, NH>::PER_SM) prefix_f
 // flight, each with its own running maximum, and meet in shared memory.  Latency bounds it (launch 1 us, wait
 // for the kernel before 1.7, bounds 1, sums 1-2), so few rows have all four warps each, and many have two, so that
 // all rows are under way at once (217 tokens of 16 heads in five groups: the call takes 35.1 us, with four
-// warps 38.6; 4 tokens of 32 heads, 38 parts a row: 23.0 with four, 25.4 with two).
+// warps 38.6; 4 tokens of 32 heads, 38 parts a row: 23.0 with four, 25.4 with two).  BATCH 5: 64 tokens of 32 heads,
+// 19 parts a row, take 47.0 us, with 8 (the registers spill) 48.8, with 4 48.7.
 template <int D, int WARPS>
 __global__ void __launch_bounds__(THREADS, 8) prefix_join_kernel(PrefixParams p) {
-  constexpr int V = D / 32, BATCH = 8, PER = THREADS / 32 / WARPS;  // rows a block
+  constexpr int V = D / 32, BATCH = 5, PER = THREADS / 32 / WARPS;  // rows a block
   __shared__ float so[PER][WARPS][D];
   __shared__ float2 sml[PER][WARPS];
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % WARPS, sub = (threadIdx.x >> 5) / WARPS;
@@ -220,8 +221,10 @@ __global__ void __launch_bounds__(THREADS, 8) prefix_join_kernel(PrefixParams p)
       float top = m;
 #pragma unroll
       for (int u = 0; u < BATCH; ++u) top = fmaxf(top, ml[u].x);
-      const float f0 = m == NEG_INF ? 0.f : fast_exp2(m - top);
-      if (m != NEG_INF) l *= f0;
+      // sums in two factors of 2^(m - top): with value scales that differ by far it may be below fp32's range
+      // where the sum times it is not
+      const float h0 = m == NEG_INF ? 0.f : fast_exp2(0.5f * (m - top)), f0 = h0 * h0;
+      if (m != NEG_INF) l = l * h0 * h0;
       m = top;
 #pragma unroll
       for (int j = 0; j < V; ++j) acc[j] *= f0;
@@ -231,8 +234,8 @@ __global__ void __launch_bounds__(THREADS, 8) prefix_join_kernel(PrefixParams p)
           l += ml[u].y;  // 0, or NaN where every logit was
           continue;
         }
-        const float f = fast_exp2(ml[u].x - m);
-        l += ml[u].y * f;
+        const float h = fast_exp2(0.5f * (ml[u].x - m)), f = h * h;
+        l += ml[u].y * h * h;
 #pragma unroll
         for (int j = 0; j < V; ++j) acc[j] += x[u][j] * f;
       }
@@ -255,8 +258,8 @@ __global__ void __launch_bounds__(THREADS, 8) prefix_join_kernel(PrefixParams p)
           l += ml.y;
           continue;
         }
-        const float f = fast_exp2(ml.x - m);
-        l += ml.y * f;
+        const float h = fast_exp2(0.5f * (ml.x - m)), f = h * h;
+        l += ml.y * h * h;
 #pragma unroll
         for (int j = 0; j < V; ++j) acc[j] += so[sub][u][lane * V + j] * f;
       }

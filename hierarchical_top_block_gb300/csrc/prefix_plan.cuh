@@ -242,7 +242,7 @@ __device__ __forceinline__ void join_own(float m, float l, float own, float& f_a
   float M = fmaxf(m, mo);
   if (M == NEG_INF) M = 0.f;
   const float a = fast_exp2(m - M), b = own == NEG_INF ? 0.f : fast_exp2(mo - M);
-  const float t = l * a + b;
+  const float t = times_exp2(l, m - M) + b;
   f_acc = t == 0.f ? 0.f : a / t;
   f_own = b == 0.f ? 0.f : b / t;
   lse = t == 0.f ? NEG_INF : (M + log2f(t)) * LN2;

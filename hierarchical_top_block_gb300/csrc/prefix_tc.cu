@@ -444,10 +444,11 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
             float f[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const float to = fmaxf(m[i], top[i]);
-              f[i] = to == NEG_INF ? 1.f : fast_exp2(m[i] - to);
+              const float to = fmaxf(m[i], top[i]), by = to == NEG_INF ? 0.f : m[i] - to;
+              f[i] = fast_exp2(by);
               m[i] = to;
-              l2[i] = mul_f32x2(l2[i], pack_f32x2(f[i], f[i]));
+              const float h = fast_exp2(0.5f * by);  // (l times 2^by, where l is large and 2^by below fp32's range too)
+              l2[i] = mul_f32x2(mul_f32x2(l2[i], pack_f32x2(h, h)), pack_f32x2(h, h));
             }
             if (begun) {
               if (!mbar_wait_warp(&bar.o_done[h], (n - 1) & 1, err)) {
@@ -575,7 +576,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
             const float top = fmaxf(a.x, b.x);
             f0[e] = a.x == NEG_INF ? 0.f : fast_exp2(a.x - top);
             f1[e] = b.x == NEG_INF ? 0.f : fast_exp2(b.x - top);
-            const float sum = (a.x == NEG_INF ? a.y : a.y * f0[e]) + (b.x == NEG_INF ? b.y : b.y * f1[e]);
+            const float sum = (a.x == NEG_INF ? a.y : times_exp2(a.y, a.x - top)) + (b.x == NEG_INF ? b.y : times_exp2(b.y, b.x - top));
             out[e] = row_out(p, w, row, row < sg.rows, top, sum, q == 0);
           }
           const uint32_t o0 = tmem + lanes + 256 + ((uint32_t)(16 * h) << 16);
@@ -803,7 +804,8 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
             const uint32_t gs = step0 + j;
             sh.code.sc[gs % SC_SLOTS][0][t] = ks;
             sh.code.sc[gs % SC_SLOTS][1][t] = vs;
-            const uint32_t most = __reduce_max_sync(0xffffffffu, vs > 0.f ? __float_as_uint(vs) : 0u);  // (not of a NaN)
+            const uint32_t mag = __float_as_uint(vs) & 0x7fffffffu;
+            const uint32_t most = __reduce_max_sync(0xffffffffu, mag <= 0x7f800000u ? mag : 0u);  // (not of a NaN)
             if (lane == 0) sh.code.top[gs % SC_SLOTS][warp - 8] = most;
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.sc_full[gs % SC_SLOTS]);

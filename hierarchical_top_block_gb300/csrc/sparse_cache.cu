@@ -190,9 +190,8 @@ __global__ void __launch_bounds__(THREADS, SparseCfg<D, NH>::PER_SM) sparse_cach
           l += x[c].y;  // 0, or NaN where every logit was
           continue;
         }
-        const float f = fast_exp2(x[c].x - m);
-        l += x[c].y * f;
-        acc += a[c] * f;
+        l += times_exp2(x[c].y, x[c].x - m);
+        acc += a[c] * fast_exp2(x[c].x - m);
       }
     p.o[row0 * D + i] = f32_to_bf16_rne(l > 0.f ? acc / l : l == 0.f ? 0.f : l);
     if (p.lse && i % D == 0) p.lse[row0 + row] = l == 0.f ? NEG_INF : (m + log2f(l)) * LN2;

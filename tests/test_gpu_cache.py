@@ -305,6 +305,26 @@ def test_sparse_extreme_logits():
     assert O.isnan().all() and L.isnan().all()
 
 
+@pytest.mark.parametrize("spread", [5, 90])
+@pytest.mark.parametrize("H_q", [4, 16])
+def test_sparse_value_scales_far_apart(spread, H_q):
+    """Value scales 2^-spread .. 2^spread times their own, rising and falling over the keys; some of 0."""
+    g = gen(14)
+    N, d, K = 640, 128, 10
+    Kq, Vq, ks, vs = filled_cache(g, 2, 1, N, d)
+    ramp = torch.linspace(-spread, spread, N, device=DEV).round().exp2()
+    vs[0] *= ramp
+    vs[1] *= ramp.flip(0)
+    vs[:, :, 3::89] = 0
+    q = normal(g, 2, 1, H_q, d)
+    idx = torch.arange(K, dtype=torch.int32, device=DEV).expand(2, 1, 1, K).contiguous()
+    ln, n = i32(N - 1, N - 1), i32(1, 1)
+    O, lse = pisa.pisa_sparse_attn_cache(q, Kq, Vq, ks, vs, idx, ln)
+    o, l, to, tl = sparse64(q, Kq, Vq, ks, vs, idx, ln, n)
+    R.close(O, o, to, "O")
+    R.close(lse, l, tl, "LSE")
+
+
 def test_sparse_lengths_that_do_not_fit():
     g = gen(5)
     Kq, Vq, ks, vs = filled_cache(g, 3, 1, 100, 64)

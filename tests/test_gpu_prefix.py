@@ -193,6 +193,29 @@ def test_extreme_logits(own, bits, Rn):
     no_error()
 
 
+@pytest.mark.parametrize("spread", [5, 90])
+@pytest.mark.parametrize("Rn,P", [(1, 1), (40, 1), (2, 2), (140, 2)])
+def test_value_scales_far_apart(spread, Rn, P):
+    """Scales 2^-spread .. 2^spread, rising over one prefix and falling over the other; some of 0."""
+    g = gen(13)
+    N, d = 1280, 64
+    q = normal(g, Rn, 4, d)
+    lens, rows = [N, N - 1][:P], [0, Rn] if P == 1 else [0, Rn // 2, Rn]
+    K, V, ks, vs = prefix(g, P, 2, N, d, 8, lens, behind=False)
+    ramp = torch.linspace(-spread, spread, N, device=DEV).round().exp2()
+    vs[0] = ramp
+    vs[P - 1, 1] = ramp.flip(0)
+    vs[:, :, 5::97] = 0
+    oo, ll = normal(g, Rn, 4, d), torch.randn((Rn, 4), generator=g, device=DEV) * 3 + 7
+    for own in ((None, None), (oo, ll)):
+        want = prefix64(q, K, V, ks, vs, lens, rows, *own)
+        o, lse = pisa.pisa_prefix_attn(q, K, V, i32(*lens), row_start=i32(*rows), k_scale=ks, v_scale=vs, o_own=own[0],
+                                       lse_own=own[1])
+        R.close(lse, want[1], want[3], "lse")
+        R.close(o, want[0], want[2], "o")
+    no_error()
+
+
 @pytest.mark.parametrize("Rn", [4, 150])
 def test_far_prefix(Rn):
     """Offsets past 32 bits: the last prefixes and keys of a cache of more than 4 GB."""
