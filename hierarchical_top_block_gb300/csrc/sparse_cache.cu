@@ -9,10 +9,10 @@
 // one list and the partial results meet through distributed shared memory, so that every size is one
 // launch and needs no scratch memory.
 //
-// Measured: 64 x 8 lists of 16 blocks (four query heads each, d = 128, 139 MB) 27.4 us, 5.1 TB/s; one list of 16
-// blocks under 16 heads 7.8 us, where launch, list, first copy and the cluster's two meetings follow one
-// another; 24 x 5 drafted tokens x 2 lists of 32 blocks 29 us, bound by the instructions of a warp's
-// granules (1.6 us each; 240 lists leave SMs with one block and with two).
+// Measured (d = 128): 64 x 8 lists of 16 blocks, four query heads each (139 MB) 27.3 us, 5.1 TB/s; 152 x 2 lists of
+// 32, sixteen heads each (164 MB) 34.3 us, 4.8 TB/s; 24 x 5 drafted tokens x 2 lists of 32 29-31 us (126 MB, a third
+// of it from HBM); one list of 16 blocks under 16 heads 7.2 us, where launch, list, first copy and the
+// cluster's two meetings follow one another.
 #include <cooperative_groups.h>
 
 #include "cache_attn.cuh"
@@ -169,17 +169,19 @@ __global__ void __launch_bounds__(THREADS, SparseCfg<D, NH>::PER_SM) sparse_cach
   }
   cg::cluster_group cl = cg::this_cluster();
   cl.sync();
-  for (int i = rank * THREADS + threadIdx.x; i < p.GQ * D; i += THREADS * cluster) {
+  // four columns a thread: one round trip to the other blocks where a column each took up to eight
+  for (int i = 4 * (rank * THREADS + threadIdx.x); i < p.GQ * D; i += 4 * THREADS * cluster) {
     const int row = i / D;
     float2 x[8];
-    float a[8];
+    float4 a[8];
 #pragma unroll
     for (int c = 0; c < 8; ++c)  // all of them under way at once
       if (c < cluster) {
         x[c] = *cl.map_shared_rank(&ml[row], c);
-        a[c] = *cl.map_shared_rank(&po[i], c);
+        a[c] = *cl.map_shared_rank(reinterpret_cast<float4*>(&po[i]), c);
       }
-    float m = NEG_INF, l = 0.f, acc = 0.f;
+    float m = NEG_INF, l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int c = 0; c < 8; ++c)
       if (c < cluster) m = fmaxf(m, x[c].x);
@@ -191,9 +193,15 @@ __global__ void __launch_bounds__(THREADS, SparseCfg<D, NH>::PER_SM) sparse_cach
           continue;
         }
         l += times_exp2(x[c].y, x[c].x - m);
-        acc += a[c] * fast_exp2(x[c].x - m);
+        const float f = fast_exp2(x[c].x - m);
+        acc.x += a[c].x * f;
+        acc.y += a[c].y * f;
+        acc.z += a[c].z * f;
+        acc.w += a[c].w * f;
       }
-    p.o[row0 * D + i] = f32_to_bf16_rne(l > 0.f ? acc / l : l == 0.f ? 0.f : l);
+    const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
+    *reinterpret_cast<uint2*>(p.o + row0 * D + i) =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
     if (p.lse && i % D == 0) p.lse[row0 + row] = l == 0.f ? NEG_INF : (m + log2f(l)) * LN2;
   }
   cl.sync();  // no block leaves while another reads its shared memory
@@ -251,12 +259,16 @@ cudaError_t launch_sparse_cache(const uint16_t* q, const int8_t* Kq, const int8_
   p.sl2 = pr.scale * LOG2E;
   p.err = err;
   const long long pairs = (long long)pr.B * pr.H_kv * pr.N;
-  // Blocks in a cluster: as many as are resident at once, while every warp keeps granules of its own.  (A cluster
-  // costs two meetings and the other blocks' outputs, so lists that fill the SMs get one block each: 24 x 5
-  // drafted tokens take 29 us with one block, 44 with two; one list of 16 blocks 7.8 us with eight and 14.4 with one.)
+  // Blocks in a cluster, while every warp keeps granules of its own: two as long as all of them are resident at
+  // once, more only while they are with half of the room left, since a cluster's blocks need free places in one
+  // group of SMs.  (d = 128, lists of 32 blocks, 16 heads each: 38 lists 12.0 us with four blocks and 18.2 with
+  // eight, 76 lists 15.1 with two and 21.6 with four, 152 lists 19.5 with two and 22.0 with one; lists of 16
+  // blocks, four heads each: 32 lists 6.8 us with eight, 72 7.8 with four and 8.5 with eight, 152 10.0 with two
+  // and 13.7 with four, 304 15.1 with two and 16.0 with one.)
   const bool wide = pr.GQ > 8;
+  const long long room = (wide ? 2LL : 4LL) * num_sms;
   int cluster = 1;
-  while (cluster < 8 && pairs * cluster * 2 <= (wide ? 2LL : 4LL) * num_sms && 4 * cluster < 2 * pr.K) cluster *= 2;
+  while (cluster < 8 && pairs * cluster * 2 <= (cluster == 1 ? room : room / 2) && 4 * cluster < 2 * pr.K) cluster *= 2;
   if (pr.d == 128)
     return wide ? launch_t<128, 2>(Kq, Vq, p, pr, cluster, s) : launch_t<128, 1>(Kq, Vq, p, pr, cluster, s);
   return wide ? launch_t<64, 2>(Kq, Vq, p, pr, cluster, s) : launch_t<64, 1>(Kq, Vq, p, pr, cluster, s);
