@@ -34,7 +34,7 @@
 // shared memory, with the copies, up to 2560; the rest is the softmax's latency that two streams do
 // not hide.  (Weights handed over in halves, so that O += P V starts earlier: no gain.  Pairs of SMs
 // that share the tiles, halving the operands' reads: slower, each step then waits for the other SM.)  With
-// codes a step takes 4200 clocks (482 us): the widened tiles are written and read once more.  Short
+// codes a step takes 4100 clocks (466 us): the widened tiles are written and read once more.  Short
 // prefixes pay for the start (7 us to the first scores of codes, 5 of bf16), the parts' 128 KB a SM
 // (3-5 us) and the join (5 us).
 #include <algorithm>
@@ -58,9 +58,9 @@ struct Cfg {
   static constexpr uint32_t RAW = KT * D;               // in codes
   // registers a thread of the softmax, of the widening and of the producing and issuing warpgroup, of 512 x 128
   // and 384 x 168 at launch.  The softmax holds 128 logits: with less it spills (256 tokens of 32 / 2 heads,
-  // 131072 keys: 493 us for codes with 208 / 40 / 56, 592 with 200 / 56 / 56, 653 with 192 / 56 / 72;
+  // 131072 keys: 466 us for codes with 208 / 56 / 40, 478 with 208 / 40 / 56; with 200 a fifth more, with 192 a third;
   // bf16 398 us with 208 / 88, 416 with 200 / 104)
-  static constexpr int REGS_SOFTMAX = 208, REGS_WIDEN = 40, REGS_ISSUE = BITS == 8 ? 56 : 88;
+  static constexpr int REGS_SOFTMAX = 208, REGS_WIDEN = 56, REGS_ISSUE = BITS == 8 ? 40 : 88;
   static_assert(BITS == 8 ? 2 * REGS_SOFTMAX + REGS_WIDEN + REGS_ISSUE <= 4 * 128
                           : 2 * REGS_SOFTMAX + REGS_ISSUE <= 3 * 168, "registers of the block");
   static constexpr int SLOTS = BITS == 8 ? 3 : 5;
