@@ -8,6 +8,7 @@ stream.  If the library is missing, every call raises: there is no fallback path
 from __future__ import annotations
 
 import ctypes as ct
+import functools
 import math
 import os
 
@@ -524,8 +525,9 @@ def _check_cache(Kq, Vq, k_scale, v_scale, device):
         raise ValueError("k_scale and v_scale must be given")
     _fits(Kq, "Kq", shape, torch.int8, device)
     _fits(Vq, "Vq", shape, torch.int8, device)
-    _fits(k_scale, "k_scale", shape[:3], torch.float32, device)
-    _fits(v_scale, "v_scale", shape[:3], torch.float32, device)
+    rows = shape[:3]
+    _fits(k_scale, "k_scale", rows, torch.float32, device)
+    _fits(v_scale, "v_scale", rows, torch.float32, device)
     return shape
 
 
@@ -623,6 +625,16 @@ def pisa_prefix_attn_workspace_bytes(shape: pisa_shape, params: pisa_params) -> 
     return int(lib().pisa_prefix_attn_workspace_bytes(shape, params))
 
 
+@functools.lru_cache(maxsize=256)
+def _prefix_sizes(n, R, H_q, H_kv, d, N_cap, scale):
+    """The shape and parameters of a call, and the bytes of scratch it wants (at least 256)."""
+    shape, params = pisa_shape(n, R, H_q, H_kv, d, N_cap), pisa_params(64, 2, 1, 0, scale, 0)
+    need = lib().pisa_prefix_attn_workspace_bytes(shape, params)
+    if need == 0 and R > 0:
+        raise PisaError(2, "pisa_prefix_attn: unsupported shape or parameters")
+    return shape, params, max(need, 256)
+
+
 def pisa_prefix_attn(q, Kp, Vp, prefix_len, row_start=None, k_scale=None, v_scale=None, o_own=None, lse_own=None,
                      scale: float = 0.0, o=None, lse=None, want_lse: bool = True, ws=None):
     """Attention of R query rows q [R, H_q, d] in n groups over the prefixes Kp, Vp [n, H_kv, N_cap, d] (bf16, or
@@ -638,10 +650,11 @@ def pisa_prefix_attn(q, Kp, Vp, prefix_len, row_start=None, k_scale=None, v_scal
     want = (R, H_q, d)
     _fits(q, "q", want, torch.bfloat16, dev)
     dtype = torch.bfloat16 if k_scale is None else torch.int8
-    _fits(Kp, "Kp", Kp.shape, dtype, dev)
-    _fits(Vp, "Vp", Kp.shape, dtype, dev)
-    _fits(k_scale, "k_scale", Kp.shape[:3], torch.float32, dev)
-    _fits(v_scale, "v_scale", Kp.shape[:3], torch.float32, dev)
+    whole, rows = (n, H_kv, N_cap, d), (n, H_kv, N_cap)
+    _fits(Kp, "Kp", whole, dtype, dev)
+    _fits(Vp, "Vp", whole, dtype, dev)
+    _fits(k_scale, "k_scale", rows, torch.float32, dev)
+    _fits(v_scale, "v_scale", rows, torch.float32, dev)
     if prefix_len is None:
         raise ValueError("prefix_len must be given")
     _fits(prefix_len, "prefix_len", (n,), torch.int32, dev)
@@ -656,11 +669,11 @@ def pisa_prefix_attn(q, Kp, Vp, prefix_len, row_start=None, k_scale=None, v_scal
         _fits(lse, "lse", want[:2], torch.float32, dev)
     elif want_lse:
         lse = torch.empty(want[:2], dtype=torch.float32, device=dev)
-    shape, params = pisa_shape(n, R, H_q, H_kv, d, N_cap), pisa_params(64, 2, 1, 0, float(scale), 0)
-    need = lib().pisa_prefix_attn_workspace_bytes(shape, params)
-    if need == 0 and R > 0:
-        raise PisaError(2, "pisa_prefix_attn: unsupported shape or parameters")
-    ws = _workspace(ws, need, torch.device("cuda", dev))
+    shape, params, need = _prefix_sizes(n, R, H_q, H_kv, d, N_cap, float(scale))
+    if ws is None:
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    else:
+        ws = _workspace(ws, need, torch.device("cuda", dev))
     _call(lib().pisa_prefix_attn, "pisa_prefix_attn", dev, q.data_ptr(), Kp.data_ptr(), Vp.data_ptr(), _addr(k_scale),
           _addr(v_scale), prefix_len.data_ptr(), _addr(row_start), _addr(o_own), _addr(lse_own), o.data_ptr(),
           _addr(lse if want_lse else None), ws.data_ptr(), ws.numel(), shape, params)
