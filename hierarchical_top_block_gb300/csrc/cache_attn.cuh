@@ -33,9 +33,7 @@
 // lanes of a quarter-warp read eight different 16-byte columns in both.
 #pragma once
 
-#include <cuda_fp16.h>
-
-#include "common.cuh"
+#include "codes.cuh"
 
 namespace pisa {
 
@@ -54,24 +52,10 @@ __device__ __forceinline__ void product_bf16(float (&c)[4], uint32_t a0, uint32_
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 // An 8 x 8 matrix of 16-bit elements, row r in lanes 4 r .. 4 r + 3, transposed.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
-  return r;
-}
-
-// Codes with their top bit flipped (code + 128) in two bytes of x -> fp16x2: 0x6400 | u is 1024 + u.
-template <int SEL>
-__device__ __forceinline__ uint32_t widen_f16(uint32_t x) {
-  const uint32_t y = __byte_perm(x, 0x64646464u, SEL);
-  uint32_t r;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(y), "r"(0x64806480u));  // 1152
   return r;
 }
 
