@@ -5,8 +5,9 @@
 // Formulas, for query row i and key c with codes k8, v8 and row scales ks, vs (a bf16 cache: k, v
 // themselves and scales 1):
 //   z_ic = scale ks_c (q_i . k8_c),   p_ic = 2^(z_ic - n_i),   l_i = sum_c p_ic,   o_i = sum_c (p_ic vs_c) v8_c
-// (z in log2 units): one pass over the keys.  n is a reference that the largest z + log2 vs passes by
-// 2^8 at most: it is raised, and o and l multiplied by 2^(old - new), only when that has grown by more.
+// (z in log2 units): one pass over the keys.  n is a reference that the largest z (of codes: z + log2 vs, less
+// WEIGHT_ROOM) passes by 2^8 at most: it is raised, and o and l multiplied by 2^(old - new), only when that
+// has grown by more.
 // The result is o_i / l_i, and n_i + log2 l_i the log-sum-exp, whatever n is.
 //
 // The products run on mma.sync (m16n8k16, fp32 sums) with the keys as rows and the query rows as the
@@ -18,7 +19,7 @@
 // instructions a pair away (bf16 takes four, and its weights carry 8 bits); q is brought to at most
 // 2 in magnitude by a power of two a row, so that it is exact but for elements below 2^-14 of the row's
 // largest, which keep 2^-25 of it; and the weight with its value's scale, p vs, is rounded to fp16:
-// 2^-11 of it, and 2^-25 of the row's largest one at least.  A bf16 cache keeps bf16 operands, and
+// 2^-11 of it, and 2^-32 of the row's largest one at least (codes.cuh).  A bf16 cache keeps bf16 operands, and
 // its weights are rounded to bf16 (2^-8).  l sums the unrounded weights.
 //
 // A granule of 32 or 16 keys lies in shared memory as TMA wrote it, rows of 128 bytes (64 for codes of
@@ -214,12 +215,11 @@ struct CacheTile {
           }
         }
     }
-    // logits, and the maximum of z + log2 vs (log2 vs of a value row of zeros, or of tiny ones: -100, so
-    // that p stays in fp32's range)
+    // logits, and the maximum of them with the values' scales
     float lv[BITS == 8 ? G8 : 1];
     if constexpr (BITS == 8) {
 #pragma unroll
-      for (int i = 0; i < G8; ++i) lv[i] = fmaxf(fast_log2(fabsf(sc.v[i])), -100.f);
+      for (int i = 0; i < G8; ++i) lv[i] = scale_log2(sc.v[i]);
     }
     bool moved = false;
     float top[NH][2];

@@ -19,4 +19,18 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
+
+// The weight of a key times its value's scale, p vs, is rounded to fp16, so a row's reference n (p = 2^(z - n)) has
+// to follow the largest z + log2 vs over its keys: jointly, since a key with a large logit and a small value
+// (attention sinks are such keys) would push the others below fp16's least number, where each loses what the sum l
+// counts.  WEIGHT_ROOM: the reference stays so far (log2) below that maximum, and is raised when the maximum has
+// grown by 2^8 past it.  Products thus reach 2^15 of fp16's 2^16, and half of its least number is at most 2^-32 of
+// the row's largest product, where without the room it is 2^-25: over 2^17 keys that adds up to 2^-8.
+// SCALE_FLOOR: what log2 vs counts as for values of 0 and of less.  p is then at most 2^(8 + 7 + 87), and its sum over
+// a prefix (fewer than 2^25 keys) below 2^127.
+constexpr float WEIGHT_ROOM = 7.f, SCALE_FLOOR = -87.f;
+
+// What a key's value scale adds to its logit (log2) for the reference.
+__device__ __forceinline__ float scale_log2(float vs) { return fmaxf(fast_log2(fabsf(vs)), SCALE_FLOOR) - WEIGHT_ROOM; }
+
 }  // namespace pisa

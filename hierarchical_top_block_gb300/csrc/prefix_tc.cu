@@ -14,9 +14,11 @@
 // into the swizzled tiles that the MMA reads (two instructions a pair; to bf16 it would be four); Q is
 // brought to at most 2 in magnitude by a power of two a row and kept as fp16 in place (exact but for
 // elements below 2^-14 of the row's largest, which keep 2^-25 of it); the key's scale multiplies the
-// fp32 logit, and the value's scale the weight before it is rounded, 2^-11 of it (2^-25 at least).  The
-// reference then covers the weight times the value's scale: log2 of the largest scale so far is
-// added to the maximum.
+// fp32 logit, and the value's scale the weight before it is rounded, 2^-11 of it (2^-32 of the row's
+// largest at least, codes.cuh).  The reference then follows the largest product of a weight and its value's
+// scale.  A step's largest logit and largest scale together bound that; only where the bound asks for a raise
+// are logits and scales added key by key (in a job's first steps, and in later ones whose largest belong to
+// different keys).
 //
 // Two streams keep the tensor pipe busy while the softmax of the other one runs, a warpgroup for
 // each.  With more than 128 rows a stream is a half of the rows, and both use the same tiles; with
@@ -49,6 +51,7 @@ namespace {
 
 constexpr int ROWS = TC_ROWS, KT = PREFIX_KT;
 constexpr float MAX_GROWTH = 8.f;  // log2 units the maximum may pass a row's reference
+constexpr float SCALE_CEILING = 100.f;  // what log2 of larger value scales counts as (their rows' outputs may overflow)
 
 template <int D, int BITS>
 struct Cfg {
@@ -119,7 +122,7 @@ template <int BITS>
 struct ForCodes {};
 template <>
 struct ForCodes<8> {
-  __align__(16) float sc[SC_SLOTS][2][KT];  // scales of a step: keys', values'
+  __align__(16) float sc[SC_SLOTS][3][KT];  // scales of a step: keys', values'; what the values' add to a logit (log2)
   uint32_t top[SC_SLOTS][4];                // largest of a widening warp's value scales, as bits
   float q_factor[ROWS];                     // logit factor of a row: scale log2 e times its power of two
 };
@@ -340,7 +343,6 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
       // a quarter of the keys' scales
       float m[4];                      // reference, log2 units
       float sl2[4];                    // logit factor
-      float most = -100.f;             // log2 of the largest value scale so far (a bound; codes)
       if constexpr (BITS == 8) {
         const uint32_t seg = count.segs;
         if (!mbar_wait_warp(&bar.q_full, seg & 1, err)) break;
@@ -349,8 +351,6 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.q_ready);
         if (!mbar_wait_warp(&bar.q_ready, seg & 1, err)) break;
-      } else {
-        most = 0.f;
       }
       unsigned long long l2[4];        // a lane's share of the sum, even and odd columns
 #pragma unroll
@@ -364,14 +364,16 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
       bool begun = false;  // O holds sums of this segment
       for (int j = sg.lag == 1 ? 0 : h; j < sg.nk; j += sg.lag, ++n, gs += sg.lag) {
         const int valid = min(KT, w.g.len - (w.k0 + j) * KT);
+        float most = 0.f;  // codes: what the step's largest value scale adds to a logit (a bound)
         if constexpr (BITS == 8) {
           if (!mbar_wait_warp(&bar.sc_full[gs % SC_SLOTS], (gs / SC_SLOTS) & 1, err)) {
             failed = true;
             break;
           }
           const uint4 x = *reinterpret_cast<const uint4*>(sh.code.top[gs % SC_SLOTS]);
-          // 2^(exponent + 1) is above the largest; scales beyond 2^100 or below 2^-100 are taken as that
-          most = fmaxf(most, fminf((float)((int)(max(max(x.x, x.y), max(x.z, x.w)) >> 23) - 126), 100.f));
+          // 2^(exponent + 1) is above the largest; scales beyond 2^100 are taken as that
+          const float log2_above = (float)((int)(max(max(x.x, x.y), max(x.z, x.w)) >> 23) - 126);
+          most = fminf(fmaxf(log2_above, SCALE_FLOOR), SCALE_CEILING) - WEIGHT_ROOM;
         }
         if (!mbar_wait_warp(&bar.s_full[h], n & 1, err)) {
           failed = true;
@@ -426,7 +428,33 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
             top[i] = a * sl2[i] + most;
             moved = moved || top[i] > m[i] + MAX_GROWTH;
           }
-          if (__any_sync(0xffffffffu, moved)) {
+          bool raise = __any_sync(0xffffffffu, moved);
+          if constexpr (BITS == 8) {
+            if (raise) {  // the maxima themselves
+#pragma unroll
+              for (int i = 0; i < 4; ++i) top[i] = NEG_INF;
+#pragma unroll
+              for (int g = 0; g < 16; ++g) {
+                const float2 lv = *reinterpret_cast<const float2*>(&sh.code.sc[gs % SC_SLOTS][2][8 * g + 2 * q]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const uint32_t* x = &s[i >> 1][4 * g + 2 * (i & 1)];
+                  float a, b;
+                  unpack_f32x2(fma_f32x2(pack_u32x2(x[0], x[1]), pack_f32x2(sl2[i], sl2[i]), pack_f32x2(lv.x, lv.y)), a, b);
+                  top[i] = fmaxf(fmaxf(top[i], a), b);
+                }
+              }
+              moved = false;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
+                top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
+                moved = moved || top[i] > m[i] + MAX_GROWTH;
+              }
+              raise = __any_sync(0xffffffffu, moved);
+            }
+          }
+          if (raise) {
             // the references follow the maxima; O (of the steps before) with them
             float f[4];
 #pragma unroll
@@ -791,6 +819,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
             const uint32_t gs = step0 + j;
             sh.code.sc[gs % SC_SLOTS][0][t] = ks;
             sh.code.sc[gs % SC_SLOTS][1][t] = vs;
+            sh.code.sc[gs % SC_SLOTS][2][t] = fminf(scale_log2(vs), SCALE_CEILING - WEIGHT_ROOM);
             const uint32_t mag = __float_as_uint(vs) & 0x7fffffffu;
             const uint32_t most = __reduce_max_sync(0xffffffffu, mag <= 0x7f800000u ? mag : 0u);  // (not of a NaN)
             if (lane == 0) sh.code.top[gs % SC_SLOTS][warp - 8] = most;
