@@ -59,6 +59,14 @@ def attend(q, kc, ks, vc, vs):
     return o, lse, bound, 2 * e + s + 2.0 ** -18 + 2.0 ** -22 * lse.abs()
 
 
+def both(q, kc, ks, vc, vs):
+    """[R, 4, d] queries over one KV head's codes [n, d]: the prefix's answer and the definition's."""
+    n, d = kc.shape
+    o, lse = pisa.pisa_prefix_attn(q, kc[None, None], vc[None, None], i32(n), k_scale=ks[None, None], v_scale=vs[None, None])
+    want, l, to, tl = attend(q.reshape(-1, d), kc, ks, vc, vs)
+    return o.reshape(-1, d), lse.reshape(-1), want, l, to, tl
+
+
 def dominant(N, at, value, d=64):
     """A key 17.5 nats above N - 1 equal ones of value +-1; its own values are `value` and 0 in turn."""
     kc, vc = (torch.zeros((N, d), dtype=torch.int8, device=DEV) for _ in range(2))
@@ -100,6 +108,37 @@ def test_selected_keys_under_a_dominant_one(H_q, value):
     N, d, K = 2048, 64, 32
     kc, ks, vc, vs = dominant(N, 77, value)
     q = torch.ones((1, H_q, d), dtype=torch.bfloat16, device=DEV)
+    idx = torch.arange(K, dtype=torch.int32, device=DEV).reshape(1, 1, K)
+    O, L = pisa.pisa_sparse_attn_cache(q, kc[None, None], vc[None, None], ks[None, None], vs[None, None], idx, i32(N - 1))
+    o, l, to, tl = attend(q[0], kc, ks, vc, vs)
+    R.close(L[0], l, tl, "LSE")
+    R.close(O[0], o, to, "O")
+    no_error()
+
+
+@pytest.mark.parametrize("N", [2, 3, 5, 17, 100, 700])
+@pytest.mark.parametrize("Rn", ROWS)
+@pytest.mark.parametrize("d", [64, 128])
+def test_weights_of_few_keys(d, Rn, N):
+    """Few keys: a weight's rounding is not averaged away, and values of both signs leave it in the result."""
+    g = gen(N + Rn + d)
+    kc, ks, _ = R.quantise64(normal(g, N, d))
+    vc, vs, _ = R.quantise64(normal(g, N, d))
+    o, lse, want, l, to, tl = both(normal(g, Rn, 4, d, scale=1.5), kc, ks, vc, vs)
+    R.close(lse, l, tl, "lse")
+    R.close(o, want, to, "o")
+    no_error()
+
+
+@pytest.mark.parametrize("N", [2, 3, 5, 17, 100, 700])
+@pytest.mark.parametrize("H_q", [4, 16])
+@pytest.mark.parametrize("d", [64, 128])
+def test_weights_of_few_selected_keys(d, H_q, N):
+    g = gen(N + H_q + d)
+    kc, ks, _ = R.quantise64(normal(g, N, d))
+    vc, vs, _ = R.quantise64(normal(g, N, d))
+    q = normal(g, 1, H_q, d, scale=1.5)
+    K = -(-N // 64)
     idx = torch.arange(K, dtype=torch.int32, device=DEV).reshape(1, 1, K)
     O, L = pisa.pisa_sparse_attn_cache(q, kc[None, None], vc[None, None], ks[None, None], vs[None, None], idx, i32(N - 1))
     o, l, to, tl = attend(q[0], kc, ks, vc, vs)
