@@ -21,6 +21,8 @@
 // 20 jobs of 79 steps: 34.8, 34.0 and 38.8.)
 #pragma once
 
+#include <cfloat>
+
 #include "common.cuh"
 
 namespace pisa {
@@ -235,17 +237,20 @@ struct PrefixWalk {
 // One (row, head): joins its prefix part (maximum m and sum l, log2 units; acc relative to m) with
 // what the row attended on its own.  Returns the factors of acc and of the own output, and the
 // joined log-sum-exp (natural).  Rows that nothing was attended for: both 0, -inf.  Without an
-// own part (own = -inf) its factor is 0 whatever the prefix part holds, NaN included.
+// own part (own = -inf) its factor is 0 whatever the prefix part holds, NaN included; where nothing
+// was attended for in the prefix, the own part is returned as it is.
 __device__ __forceinline__ void join_own(float m, float l, float own, float& f_acc, float& f_own, float& lse) {
-  // prefix part: weight l at scale 2^m; own part: weight 1 at scale 2^(own log2 e)
-  const float mo = own * LOG2E;
+  // prefix part: weight l at scale 2^m; own part: weight 1 at scale 2^(own log2 e), which is finite where own is
+  // (a mask of the type's lowest value may stand behind it)
+  float mo = own * LOG2E;
+  if (fabsf(own) <= FLT_MAX) mo = fminf(fmaxf(mo, -FLT_MAX), FLT_MAX);
   float M = fmaxf(m, mo);
   if (M == NEG_INF) M = 0.f;
   const float a = fast_exp2(m - M), b = own == NEG_INF ? 0.f : fast_exp2(mo - M);
-  const float t = times_exp2(l, m - M) + b;
+  const float prefix = times_exp2(l, m - M), t = prefix + b;
   f_acc = t == 0.f ? 0.f : a / t;
   f_own = b == 0.f ? 0.f : b / t;
-  lse = t == 0.f ? NEG_INF : (M + log2f(t)) * LN2;
+  lse = prefix == 0.f ? own : (M + log2f(t)) * LN2;
 }
 
 // The tensor-core kernel (prefix_tc.cu): tiles of TC_ROWS rows, one block a SM.

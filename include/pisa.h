@@ -331,7 +331,8 @@ PISA_API pisa_status pisa_sparse_attn_cache(const uint16_t* q, const int8_t* Kq,
  *               row_start[p+1] - 1 are group p's; rows before the first and behind the last
  *               are left as they are.  NULL with n = 1: all rows.
  *   o_own [R][H_q][d] bf16, lse_own [R][H_q] fp32: both or neither.  o = o_own and lse = lse_own
- *               are allowed.  A row with lse_own = -inf takes nothing of o_own.
+ *               are allowed.  A row with lse_own = -inf takes nothing of o_own; a row that sees no key of
+ *               its prefix gives o_own and lse_own as they are, whatever finite value lse_own has.
  *   lse         [R][H_q] fp32 out, nullable (natural log, of the joined result).
  *   ws          device scratch, 256-B aligned, ws_bytes >= pisa_prefix_attn_workspace_bytes();
  *               not to be used by other work until the call has run (two captured graphs that
