@@ -30,7 +30,11 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 // a prefix (fewer than 2^25 keys) below 2^127.
 constexpr float WEIGHT_ROOM = 7.f, SCALE_FLOOR = -87.f;
 
-// What a key's value scale adds to its logit (log2) for the reference.
-__device__ __forceinline__ float scale_log2(float vs) { return fmaxf(fast_log2(fabsf(vs)), SCALE_FLOOR) - WEIGHT_ROOM; }
+// What a key's value scale adds to its logit (log2) for the reference.  A scale that is no number says nothing about
+// the weights (an infinite reference would make all of them 0): it shows in the products.
+__device__ __forceinline__ float scale_log2(float vs) {
+  const float x = fast_log2(fabsf(vs));
+  return (x < 128.f ? fmaxf(x, SCALE_FLOOR) : SCALE_FLOOR) - WEIGHT_ROOM;
+}
 
 }  // namespace pisa

@@ -268,7 +268,8 @@ PISA_API pisa_status pisa_decode_step_ws(const uint16_t* q, const uint16_t* k, c
  * The attention over it (pisa_sparse_attn_cache, pisa_prefix_attn) holds each weight times its value's
  * scale in fp16: rounded by up to 2^-11 of itself, and 2^-32 of the row's largest such product.  Sums are
  * fp32.  Value scales are taken up to 2^100 in magnitude (values of 2^107): beyond, a row's output may
- * overflow.
+ * overflow.  One that is infinite or NaN makes the outputs it takes part in infinite or NaN; the LSE does not
+ * depend on value scales.
  * Bases are 16-byte aligned, as everywhere (int32 arrays and LSE: 4-byte aligned).  No argument
  * may overlap another unless this says so. */
 
