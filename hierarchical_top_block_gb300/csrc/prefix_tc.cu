@@ -620,171 +620,6 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
         }
       }
     }
-  } else if (warp == C::PRODUCER) {
-    // ------------------------------ producer ------------------------------
-    set_regs_down<C::REGS_ISSUE>();
-    constexpr uint32_t N = BITS == 8 ? C::RSLOTS : C::SLOTS;
-    Walk<BITS == 8> walk;
-    walk.start(first, &sh.walks[BITS == 8 ? warp : 0]);
-    uint32_t nt = 0, seg = 0;  // tiles and segments so far
-    bool failed = false;
-    for (bool more_work = any_work; !failed && more_work; more_work = walk.next(p, block)) {
-      const PrefixWalk& w = walk.now();
-      const Segment sg(p, w);
-      if (!mbar_wait_warp(&bar.q_empty, (seg & 1) ^ 1, err)) break;
-      if (lane == 0) {
-        const int streams = sg.lag == 1 ? 2 : 1;
-        mbar_arrive_expect_tx(&bar.q_full, streams * C::QT_BYTES);
-        for (int h = 0; h < streams; ++h)
-          for (int c = 0; c < DH; ++c)
-            tma_load_4d(sQ + h * C::QT_BYTES + c * (128 * 128), &mapQ, &bar.q_full, 64 * c, 0, w.head,
-                        w.g.first + ((w.tile * ROWS + h * 128) >> p.gq_bits));
-      }
-      ++seg;
-      const int ph = w.p * p.H_kv + w.head;
-      for (int i = 0; i < sg.tiles(); ++i, ++nt) {
-        bool is_v;
-        const int key0 = (w.k0 + sg.tile(i, is_v)) * KT;
-        const int st = nt % N;
-        uint64_t* full = BITS == 8 ? &bar.raw_full[st] : &bar.full[st];
-        if (!mbar_wait_warp(BITS == 8 ? &bar.raw_empty[st] : &bar.empty[st], ((nt / N) & 1) ^ 1, err)) {
-          failed = true;
-          break;
-        }
-        if (lane == 0) {
-          if constexpr (BITS == 8) {
-            mbar_arrive_expect_tx(full, C::RAW);
-            uint8_t* dst = sR + st * C::RAW;
-            tma_load_3d(dst, is_v ? &mapV : &mapK, full, 0, key0, ph);
-          } else {
-            mbar_arrive_expect_tx(full, C::TILE);
-            uint8_t* dst = sT + st * C::TILE;
-            for (int c = 0; c < DH; ++c) tma_load_3d(dst + c * (KT * 128), is_v ? &mapV : &mapK, full, 64 * c, key0, ph);
-          }
-        }
-      }
-    }
-    // copies still in flight land before shared memory goes away (bounded; at once unless a wait failed)
-    if (lane == 0) {
-      if (seg > 0) mbar_wait(&bar.q_full, (seg - 1) & 1, err, 100000000ull);
-      for (uint32_t u = nt > N ? nt - N : 0; u < nt; ++u)
-        mbar_wait(BITS == 8 ? &bar.raw_full[u % N] : &bar.full[u % N], (u / N) & 1, err, 100000000ull);
-    }
-    __syncwarp();
-  } else if (warp == C::ISSUER) {
-    // ------------------------------ MMAs ------------------------------
-    set_regs_down<C::REGS_ISSUE>();
-    // fp16 operands have format 0 where bf16 have 1; V: d contiguous, N-major
-    constexpr uint32_t formats = BITS == 8 ? (1u << 7) | (1u << 10) : 0u;
-    constexpr uint32_t id_qk = idesc_bf16_f32(128, KT) & ~formats;
-    constexpr uint32_t id_pv = (idesc_bf16_f32(128, D) & ~formats) | (1u << 16);
-    Walk<BITS == 8> walk;
-    walk.start(first, &sh.walks[BITS == 8 ? warp : 0]);
-    uint32_t nt = 0, seg = 0, it[2] = {0, 0};
-    bool failed = false;
-    // tile n is here (v_valid: a V tile's keys in use)
-    auto tile_here = [&](uint32_t n, int v_valid) {
-      if (!mbar_wait_warp(&bar.full[n % C::SLOTS], (n / C::SLOTS) & 1, err)) return false;
-      if (BITS == 16 && v_valid < KT) {
-        // values past the prefix's end are multiplied by weights of 0: they have to be finite
-        uint8_t* t = sT + (n % C::SLOTS) * C::TILE;
-        for (int c = 0; c < DH; ++c)
-          for (int i = max(0, v_valid) * 8 + lane; i < KT * 8; i += 32)
-            *reinterpret_cast<uint4*>(t + c * (KT * 128) + i * 16) = make_uint4(0, 0, 0, 0);
-        fence_proxy_async();
-        __syncwarp();
-      }
-      return true;
-    };
-    // descriptors of the first tile and Q slot: the others differ in the address field alone (16-byte units of
-    // the low word)
-    const uint64_t k_desc = smem_desc_sw128(smem_u32(sT), 16, 1024);
-    const uint32_t k_hi = (uint32_t)(k_desc >> 32), q_lo = (uint32_t)smem_desc_sw128(smem_u32(sQ), 16, 1024);
-    const uint32_t k_lo = (uint32_t)k_desc, v_lo = (uint32_t)smem_desc_sw128(smem_u32(sT), KT * 128, 1024);
-    auto desc = [&](uint32_t lo) { return pack_u32x2(lo, k_hi); };  // (8-row groups of 1024 bytes in all of them)
-    auto qk = [&](int h, int qs, uint32_t n) {  // S of stream h = Q (slot qs) K^T
-      const uint32_t a = q_lo + qs * (C::QT_BYTES >> 4), b = k_lo + (n % C::SLOTS) * (C::TILE >> 4), d = tmem + 128 * h;
-#pragma unroll
-      for (int s = 0; s < D / 16; ++s)
-        umma_bf16(d, desc(a + (((s >> 2) * (128 * 128) + (s & 3) * 32) >> 4)),
-                  desc(b + (((s >> 2) * (KT * 128) + (s & 3) * 32) >> 4)), id_qk, s > 0 ? 1u : 0u);
-      umma_commit(&bar.s_full[h]);
-    };
-    auto pv = [&](int h, uint32_t n, bool first) {  // O of stream h (+)= P V
-      const uint32_t b = v_lo + (n % C::SLOTS) * (C::TILE >> 4), d = tmem + 256 + 128 * h, a = tmem + 128 * h;
-#pragma unroll
-      for (int s = 0; s < KT / 16; ++s)
-        umma_bf16_ts(d, a + 8 * s, desc(b + ((s * 16 * 128) >> 4)), id_pv, s > 0 ? 1u : first ? 0u : 1u);
-      umma_commit(&bar.o_done[h]);
-    };
-    for (bool more_work = any_work; !failed && more_work; more_work = walk.next(p, block)) {
-      const PrefixWalk& w = walk.now();
-      const Segment sg(p, w);
-      if (!mbar_wait_warp(BITS == 8 ? &bar.q_ready : &bar.q_full, seg & 1, err)) break;
-      ++seg;
-      const int head = min(sg.lag, sg.nk);
-      for (int j = 0; j < head && !failed; ++j, ++nt) {
-        if (!tile_here(nt, KT)) {
-          failed = true;
-          break;
-        }
-        tc_fence_after();
-        if (elect_one()) {
-          if (sg.lag == 1) {
-            qk(0, 0, nt);
-            qk(1, 1, nt);
-          } else {
-            qk(j, 0, nt);
-          }
-          umma_commit(&bar.empty[nt % C::SLOTS]);
-          if (j == sg.nk - 1) umma_commit(&bar.q_empty);
-        }
-        __syncwarp();
-      }
-      for (int j = 0; j < sg.nk && !failed; ++j) {
-        const uint32_t nv = nt++;
-        const bool more = j + sg.lag < sg.nk;
-        const uint32_t nn = more ? nt++ : 0;
-        if (!tile_here(nv, w.g.len - (w.k0 + j) * KT)) {
-          failed = true;
-          break;
-        }
-        const int h0 = sg.lag == 1 ? 0 : j & 1, h1 = sg.lag == 1 ? 1 : h0;
-        for (int h = h0; h <= h1; ++h) {
-          if (!mbar_wait_warp(&bar.p_full[h], it[h] & 1, err)) {
-            failed = true;
-            break;
-          }
-          ++it[h];
-          tc_fence_after();
-          if (elect_one()) {
-            pv(h, nv, j < sg.lag);
-            if (h == h1) umma_commit(&bar.empty[nv % C::SLOTS]);
-          }
-          __syncwarp();
-          if (more) {
-            if (h == h0 && !tile_here(nn, KT)) {
-              failed = true;
-              break;
-            }
-            tc_fence_after();
-            if (elect_one()) {
-              qk(h, sg.lag == 1 ? h : 0, nn);
-              if (h == h1) {
-                umma_commit(&bar.empty[nn % C::SLOTS]);
-                if (j + sg.lag == sg.nk - 1) umma_commit(&bar.q_empty);
-              }
-            }
-            __syncwarp();
-          }
-        }
-      }
-    }
-    if (elect_one()) {  // every MMA issued has completed before the tensor memory is released (bounded)
-      umma_commit(&bar.drain);
-      mbar_wait(&bar.drain, 0, err);
-    }
-    __syncwarp();
   } else if (BITS == 8 && warp < 12) {
     // ------------------------------ codes to fp16 ------------------------------
     if constexpr (BITS == 8) {
@@ -851,7 +686,172 @@ __global__ void __launch_bounds__(Cfg<D, BITS>::THREADS, 1)
       }
     }
   } else {
+    // The producing and issuing warps are two of one warpgroup: all of it changes its registers by one instruction.
     set_regs_down<C::REGS_ISSUE>();
+    if (warp == C::PRODUCER) {
+      // ------------------------------ producer ------------------------------
+      constexpr uint32_t N = BITS == 8 ? C::RSLOTS : C::SLOTS;
+      Walk<BITS == 8> walk;
+      walk.start(first, &sh.walks[BITS == 8 ? warp : 0]);
+      uint32_t nt = 0, seg = 0;  // tiles and segments so far
+      bool failed = false;
+      for (bool more_work = any_work; !failed && more_work; more_work = walk.next(p, block)) {
+        const PrefixWalk& w = walk.now();
+        const Segment sg(p, w);
+        if (!mbar_wait_warp(&bar.q_empty, (seg & 1) ^ 1, err)) break;
+        if (lane == 0) {
+          const int streams = sg.lag == 1 ? 2 : 1;
+          mbar_arrive_expect_tx(&bar.q_full, streams * C::QT_BYTES);
+          for (int h = 0; h < streams; ++h)
+            for (int c = 0; c < DH; ++c)
+              tma_load_4d(sQ + h * C::QT_BYTES + c * (128 * 128), &mapQ, &bar.q_full, 64 * c, 0, w.head,
+                          w.g.first + ((w.tile * ROWS + h * 128) >> p.gq_bits));
+        }
+        ++seg;
+        const int ph = w.p * p.H_kv + w.head;
+        for (int i = 0; i < sg.tiles(); ++i, ++nt) {
+          bool is_v;
+          const int key0 = (w.k0 + sg.tile(i, is_v)) * KT;
+          const int st = nt % N;
+          uint64_t* full = BITS == 8 ? &bar.raw_full[st] : &bar.full[st];
+          if (!mbar_wait_warp(BITS == 8 ? &bar.raw_empty[st] : &bar.empty[st], ((nt / N) & 1) ^ 1, err)) {
+            failed = true;
+            break;
+          }
+          if (lane == 0) {
+            if constexpr (BITS == 8) {
+              mbar_arrive_expect_tx(full, C::RAW);
+              uint8_t* dst = sR + st * C::RAW;
+              tma_load_3d(dst, is_v ? &mapV : &mapK, full, 0, key0, ph);
+            } else {
+              mbar_arrive_expect_tx(full, C::TILE);
+              uint8_t* dst = sT + st * C::TILE;
+              for (int c = 0; c < DH; ++c) tma_load_3d(dst + c * (KT * 128), is_v ? &mapV : &mapK, full, 64 * c, key0, ph);
+            }
+          }
+        }
+      }
+      // copies still in flight land before shared memory goes away (bounded; at once unless a wait failed)
+      if (lane == 0) {
+        if (seg > 0) mbar_wait(&bar.q_full, (seg - 1) & 1, err, 100000000ull);
+        for (uint32_t u = nt > N ? nt - N : 0; u < nt; ++u)
+          mbar_wait(BITS == 8 ? &bar.raw_full[u % N] : &bar.full[u % N], (u / N) & 1, err, 100000000ull);
+      }
+      __syncwarp();
+    } else if (warp == C::ISSUER) {
+      // ------------------------------ MMAs ------------------------------
+      // fp16 operands have format 0 where bf16 have 1; V: d contiguous, N-major
+      constexpr uint32_t formats = BITS == 8 ? (1u << 7) | (1u << 10) : 0u;
+      constexpr uint32_t id_qk = idesc_bf16_f32(128, KT) & ~formats;
+      constexpr uint32_t id_pv = (idesc_bf16_f32(128, D) & ~formats) | (1u << 16);
+      Walk<BITS == 8> walk;
+      walk.start(first, &sh.walks[BITS == 8 ? warp : 0]);
+      uint32_t nt = 0, seg = 0, it[2] = {0, 0};
+      bool failed = false;
+      // tile n is here (v_valid: a V tile's keys in use)
+      auto tile_here = [&](uint32_t n, int v_valid) {
+        if (!mbar_wait_warp(&bar.full[n % C::SLOTS], (n / C::SLOTS) & 1, err)) return false;
+        if (BITS == 16 && v_valid < KT) {
+          // values past the prefix's end are multiplied by weights of 0: they have to be finite
+          uint8_t* t = sT + (n % C::SLOTS) * C::TILE;
+          for (int c = 0; c < DH; ++c)
+            for (int i = max(0, v_valid) * 8 + lane; i < KT * 8; i += 32)
+              *reinterpret_cast<uint4*>(t + c * (KT * 128) + i * 16) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async();
+          __syncwarp();
+        }
+        return true;
+      };
+      // descriptors of the first tile and Q slot: the others differ in the address field alone (16-byte units of
+      // the low word)
+      const uint64_t k_desc = smem_desc_sw128(smem_u32(sT), 16, 1024);
+      const uint32_t k_hi = (uint32_t)(k_desc >> 32), q_lo = (uint32_t)smem_desc_sw128(smem_u32(sQ), 16, 1024);
+      const uint32_t k_lo = (uint32_t)k_desc, v_lo = (uint32_t)smem_desc_sw128(smem_u32(sT), KT * 128, 1024);
+      auto desc = [&](uint32_t lo) { return pack_u32x2(lo, k_hi); };  // (8-row groups of 1024 bytes in all of them)
+      auto qk = [&](int h, int qs, uint32_t n) {  // S of stream h = Q (slot qs) K^T
+        const uint32_t a = q_lo + qs * (C::QT_BYTES >> 4), b = k_lo + (n % C::SLOTS) * (C::TILE >> 4), d = tmem + 128 * h;
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s)
+          umma_bf16(d, desc(a + (((s >> 2) * (128 * 128) + (s & 3) * 32) >> 4)),
+                    desc(b + (((s >> 2) * (KT * 128) + (s & 3) * 32) >> 4)), id_qk, s > 0 ? 1u : 0u);
+        umma_commit(&bar.s_full[h]);
+      };
+      auto pv = [&](int h, uint32_t n, bool first) {  // O of stream h (+)= P V
+        const uint32_t b = v_lo + (n % C::SLOTS) * (C::TILE >> 4), d = tmem + 256 + 128 * h, a = tmem + 128 * h;
+#pragma unroll
+        for (int s = 0; s < KT / 16; ++s)
+          umma_bf16_ts(d, a + 8 * s, desc(b + ((s * 16 * 128) >> 4)), id_pv, s > 0 ? 1u : first ? 0u : 1u);
+        umma_commit(&bar.o_done[h]);
+      };
+      for (bool more_work = any_work; !failed && more_work; more_work = walk.next(p, block)) {
+        const PrefixWalk& w = walk.now();
+        const Segment sg(p, w);
+        if (!mbar_wait_warp(BITS == 8 ? &bar.q_ready : &bar.q_full, seg & 1, err)) break;
+        ++seg;
+        const int head = min(sg.lag, sg.nk);
+        for (int j = 0; j < head && !failed; ++j, ++nt) {
+          if (!tile_here(nt, KT)) {
+            failed = true;
+            break;
+          }
+          tc_fence_after();
+          if (elect_one()) {
+            if (sg.lag == 1) {
+              qk(0, 0, nt);
+              qk(1, 1, nt);
+            } else {
+              qk(j, 0, nt);
+            }
+            umma_commit(&bar.empty[nt % C::SLOTS]);
+            if (j == sg.nk - 1) umma_commit(&bar.q_empty);
+          }
+          __syncwarp();
+        }
+        for (int j = 0; j < sg.nk && !failed; ++j) {
+          const uint32_t nv = nt++;
+          const bool more = j + sg.lag < sg.nk;
+          const uint32_t nn = more ? nt++ : 0;
+          if (!tile_here(nv, w.g.len - (w.k0 + j) * KT)) {
+            failed = true;
+            break;
+          }
+          const int h0 = sg.lag == 1 ? 0 : j & 1, h1 = sg.lag == 1 ? 1 : h0;
+          for (int h = h0; h <= h1; ++h) {
+            if (!mbar_wait_warp(&bar.p_full[h], it[h] & 1, err)) {
+              failed = true;
+              break;
+            }
+            ++it[h];
+            tc_fence_after();
+            if (elect_one()) {
+              pv(h, nv, j < sg.lag);
+              if (h == h1) umma_commit(&bar.empty[nv % C::SLOTS]);
+            }
+            __syncwarp();
+            if (more) {
+              if (h == h0 && !tile_here(nn, KT)) {
+                failed = true;
+                break;
+              }
+              tc_fence_after();
+              if (elect_one()) {
+                qk(h, sg.lag == 1 ? h : 0, nn);
+                if (h == h1) {
+                  umma_commit(&bar.empty[nn % C::SLOTS]);
+                  if (j + sg.lag == sg.nk - 1) umma_commit(&bar.q_empty);
+                }
+              }
+              __syncwarp();
+            }
+          }
+        }
+      }
+      if (elect_one()) {  // every MMA issued has completed before the tensor memory is released (bounded)
+        umma_commit(&bar.drain);
+        mbar_wait(&bar.drain, 0, err);
+      }
+      __syncwarp();
+    }
   }
   __syncthreads();
   if (warp == C::ISSUER) {
