@@ -10,9 +10,9 @@
 // Rounding half away from zero makes the codes exact with one fp32 reciprocal a row: with
 // X, M < 2^8 the integer significands of x and a and e the difference of their exponents,
 // 127 |x| / a = 127 X / (M 2^e), so a value that is not half-way between two codes is at least
-// 2^-(e+8) from half-way, while its size is below 2^(8-e).  Multiplying by (127 / a)(1 + 2^-20)
-// moves it by less than 2^(8.3-e-20) (the two roundings included), too little to cross, and
-// moves an exact half-way value up, never down.
+// 1 / (2 M 2^e) > 2^-(e+9) from half-way, while its size is below 2^(8-e).  Multiplying by
+// (127 / a)(1 + 2^-20) moves it by less than 2^(8.3-e-20) = 2^-(e+11.7) (the two roundings included), too
+// little to cross, and moves an exact half-way value up, never down.
 //
 // Both kernels move bytes: 16 lanes (d = 128) or 8 lanes (d = 64) take a row, 8 values a lane, so
 // every access of a warp is whole 128-byte lines; a thread has RPT rows in flight, four when there are
