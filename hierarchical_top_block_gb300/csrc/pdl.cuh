@@ -4,8 +4,10 @@
 // still draining: its CTAs are scheduled once every CTA of that kernel has signalled
 // pdl_trigger() (or exited), and pdl_wait() then blocks until that kernel has completed and
 // its memory writes are visible.  Each kernel of the chain therefore calls pdl_wait() before
-// it reads or writes anything, and pdl_trigger() at its start so that the next one's launch
-// overlaps its run.  Both instructions are no-ops for a kernel launched without the attribute.
+// it reads what an earlier kernel on the stream writes and before it writes anything, and pdl_trigger() at
+// its start so that the next one's launch overlaps its run.  What may be read before pdl_wait(): the inputs of
+// a chain whose first kernel was launched without the attribute, since all that came before on the stream was
+// complete when that one started.  Both instructions are no-ops for a kernel launched without the attribute.
 // The trigger only lets the next grid launch: since it fires once all CTAs of this grid are
 // resident, the next grid's waiting CTAs can never keep one of this grid's CTAs off an SM.
 #pragma once

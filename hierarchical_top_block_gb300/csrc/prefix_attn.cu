@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(THREADS, FewCfg<D, BITS, NH>::PER_SM) prefix_f
 // for the kernel before 1.7, bounds 1, sums 1-2), so few rows have all four warps each, and many have two, so that
 // all rows are under way at once (217 tokens of 16 heads in five groups: the call takes 35.1 us, with four
 // warps 38.6; 4 tokens of 32 heads, 38 parts a row: 23.0 with four, 25.4 with two).  BATCH 5: 64 tokens of 32 heads,
-// 19 parts a row, take 47.0 us, with 8 (the registers spill) 48.8, with 4 48.7.
+// 19 parts a row, took 47.0 us when chosen, with 8 (the registers spill) 48.8, with 4 48.7.
 template <int D, int WARPS>
 __global__ void __launch_bounds__(THREADS, 8) prefix_join_kernel(PrefixParams p) {
   constexpr int V = D / 32, BATCH = 5, PER = THREADS / 32 / WARPS;  // rows a block
@@ -288,8 +288,10 @@ constexpr int MAX_SMS = 152;  // this GPU's: the scratch does not depend on the 
 // Which kernel, by the query rows a group has on average (the groups' own sizes are on the device; any kernel
 // takes any).  The few-row kernel reads the prefix again for every 16 rows, the tensor-core one pays for its
 // start (first scores after 6 us) and for 256 rows whether they are there or not.  At 8 KV heads x 32768 keys
-// of d = 128, few-row against tensor-core kernel: codes, 32 rows 32 : 37 us, 48 rows 42 : 38; bf16, 16 rows 32 : 35,
+// of d = 128, few-row against tensor-core kernel: codes, 32 rows 31 : 37 us, 48 rows 42 : 38; bf16, 16 rows 32 : 35,
 // 32 rows 47 : 36; d = 64: codes, 32 rows 24 : 29, 64 rows 39 : 30; bf16, 16 rows 16 : 21, 32 rows 24 : 21.
+// Uneven groups, one of 200 tokens among 60 of one, 16 / 4 heads, for which the average says few rows: 1024 codes each
+// 52 : 82 us, 8192 codes 280 : 280.
 struct Plan {
   bool tc;
   int rows, blocks, stop;
@@ -383,6 +385,8 @@ cudaError_t launch_prefix_attn(const uint16_t* q, const void* Kp, const void* Vp
   p.part_ml = reinterpret_cast<float2*>(w);
   w += up256(parts * 8);
   p.base = reinterpret_cast<long long*>(w);
+  // Launched without the programmatic attribute: the call's inputs are there when the kernel starts, so the join,
+  // launched with it, may read them before it waits for the parts.
   cudaError_t e;
   if (plan.tc)
     e = launch_prefix_tc(p, pr.d, s);

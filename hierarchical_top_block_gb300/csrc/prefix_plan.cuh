@@ -16,9 +16,10 @@
 // A block that meets a second job stops for it: the rows of the first are written, those of the
 // next fetched.  On the line every job therefore begins with `extra` empty steps, as long as that stop;
 // where the jobs end on the blocks' bounds anyway, or the empty steps would make the ranges longer than
-// a stop does, there are none.  (64 tokens of 32 / 8 heads after 32768 codes, eight jobs of 256 steps over
-// 152 blocks: 49.0 us with a stop of 3 steps, 47.8 with 4, 54.7 with none; five groups of bf16 prefixes,
-// 20 jobs of 79 steps: 34.8, 34.0 and 38.8.)
+// a stop does, there are none.  (Five groups of 217 tokens of 16 / 4 heads in all, d = 128, 20 jobs of up to 79
+// steps over 152 blocks: codes 43.0 us with a stop of 3 steps, 44.9 with 2, 43.1 with 4 and 5, 48.0 with none;
+// bf16 33.7, 34.2, 34.0 and 34.6, 36.5.  One prefix of 32768 keys differs by less than 1%.  Few rows, three groups of
+// two tokens over 20000 codes: 28.1 us with 2, 28.3 with 1, 28.7 with 3, 29.9 with none.)
 #pragma once
 
 #include <cfloat>

@@ -31,12 +31,12 @@
 // next S is issued right behind its O += P V, which reads P from the same columns.  Every wait is
 // bounded.
 //
-// Measured (d = 128): 256 tokens of 32 / 2 heads after 131072 bf16 keys 388 us, 1.42 PFLOP/s; a step of
+// Measured (d = 128): 256 tokens of 32 / 2 heads after 131072 bf16 keys 379-392 us, 1.40-1.45 PFLOP/s; a step of
 // 256 rows takes 3300 clocks, of which the products alone would take 2048 and their operands' way through
 // shared memory, with the copies, up to 2560; the rest is the softmax's latency that two streams do
 // not hide.  (Weights handed over in halves, so that O += P V starts earlier: no gain.  Pairs of SMs
 // that share the tiles, halving the operands' reads: slower, each step then waits for the other SM.)  With
-// codes a step takes 4100 clocks (466 us): the widened tiles are written and read once more.  Short
+// codes a step takes 4100 clocks (472 us): the widened tiles are written and read once more.  Short
 // prefixes pay for the start (7 us to the first scores of codes, 5 of bf16), the parts' 128 KB a SM
 // (3-5 us) and the join (5 us).
 #include <algorithm>

@@ -9,9 +9,9 @@
 // one list and the partial results meet through distributed shared memory, so that every size is one
 // launch and needs no scratch memory.
 //
-// Measured (d = 128): 64 x 8 lists of 16 blocks, four query heads each (139 MB) 27.3 us, 5.1 TB/s; 152 x 2 lists of
-// 32, sixteen heads each (164 MB) 34.3 us, 4.8 TB/s; 24 x 5 drafted tokens x 2 lists of 32 29-31 us (126 MB, a third
-// of it from HBM); one list of 16 blocks under 16 heads 7.2 us, where launch, list, first copy and the
+// Measured (d = 128): 64 x 8 lists of 16 blocks, four query heads each (139 MB) 28.5 us, 4.9 TB/s; 152 x 2 lists of
+// 32, sixteen heads each (164 MB) 33.6 us, 4.9 TB/s; 24 x 5 drafted tokens x 2 lists of 32 30-31 us (126 MB, a third
+// of it from HBM); one list of 16 blocks under 16 heads 7.3 us, where launch, list, first copy and the
 // cluster's two meetings follow one another.
 #include <cooperative_groups.h>
 
@@ -72,7 +72,7 @@ struct Granules {
 template <int D, int NH>
 struct SparseCfg {
   // Up to eight query heads: one granule of 32 keys under way a warp and four blocks a SM hide more than deeper
-  // rings (64 x 8 lists of 16 blocks: 27.5 us; with two granules and three blocks 33.7).  Sixteen: the state
+  // rings (64 x 8 lists of 16 blocks: 27.5 us when chosen; with two granules and three blocks 33.7).  Sixteen: the state
   // takes twice the registers, and two granules with two blocks are better (24 x 5 drafted tokens, lists of
   // 32 blocks: 29.3 us; one granule and three blocks 35.3, three and two 29.6).
   static constexpr int KEYS = 32, SLOTS = NH, PER_SM = NH == 1 ? 4 : 2;

@@ -302,8 +302,9 @@ PISA_API pisa_status pisa_cache_read(const int8_t* Kq, const int8_t* Vq, const f
  *   z_c = scale k_scale_c (q . Kq_c),  o = sum_c softmax(z)_c v_scale_c Vq_c,  LSE = log sum_c exp z_c.
  * The new tokens' own rows are in the cache already (pisa_cache_write with the same seq_len), so
  * T > 1 tokens (drafted ones, a chunk of a prompt) see each other as far as their lists name
- * their blocks.  The lists may come from the step that attended last, another layer or a rule of the
- * caller's own; a block listed twice counts twice.
+ * their blocks.  No call selects blocks over the 8-bit cache itself: pisa_decode_step and pisa_select_prefill
+ * read bf16 keys and their pyramid.  The lists come from a step that attended before, another layer or a rule
+ * of the caller's own; a block listed twice counts twice.
  *   q, O [B][T][H_q][d] bf16;  idx [B][H_kv][T][K] int32, entries < 0 skipped, entries >=
  *   ceil(N_cap/C) skipped and flagged (PISA_ERR_BAD_INDEX);  LSE [B][T][H_q] fp32, nullable.
  *   new_len as for pisa_cache_write: rows t >= new_len[b] of O and LSE are left as they are.
@@ -338,8 +339,10 @@ PISA_API pisa_status pisa_sparse_attn_cache(const uint16_t* q, const int8_t* Kq,
  *   ws          device scratch, 256-B aligned, ws_bytes >= pisa_prefix_attn_workspace_bytes();
  *               not to be used by other work until the call has run (two captured graphs that
  *               may run at once need one each).
- * A row that sees nothing gives o = 0 and lse = -inf.  Lengths or bounds out of range are brought
- * into range and flagged (PISA_ERR_BAD_INDEX).  Results are the same in every run. */
+ * A row that sees nothing gives o = 0 and lse = -inf.  Weights are rounded to bf16 over bf16 prefixes (2^-8 of
+ * each) and to fp16 over codes (see above); logits, sums and joins are fp32.  Lengths or bounds out of
+ * range are brought into range and flagged (PISA_ERR_BAD_INDEX); rows that decreasing bounds give to two groups
+ * hold the result of either, element by element.  Otherwise results are the same in every run. */
 /* 0 for arguments pisa_prefix_attn refuses. */
 PISA_API size_t pisa_prefix_attn_workspace_bytes(pisa_shape shape, pisa_params params);
 PISA_API pisa_status pisa_prefix_attn(const uint16_t* q, const void* Kp, const void* Vp, const float* k_scale,
