@@ -493,7 +493,7 @@ def _fits(t, name, shape, dtype, dev):
 
 def _cuda(t, name):
     """The number of the device that t is on."""
-    if not t.is_cuda:
+    if t is None or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     return t.get_device()
 
@@ -514,15 +514,15 @@ def _addr(t):
 
 
 def _cache_shape(Kq, name):
-    if Kq.dim() != 4:
+    if Kq is None or Kq.dim() != 4:
         raise ValueError(f"{name} must be [B, H_kv, N_cap, d]")
     return Kq.shape
 
 
 def _check_cache(Kq, Vq, k_scale, v_scale, device):
     shape = _cache_shape(Kq, "Kq")
-    if k_scale is None or v_scale is None:
-        raise ValueError("k_scale and v_scale must be given")
+    if Vq is None or k_scale is None or v_scale is None:
+        raise ValueError("Vq, k_scale and v_scale must be given")
     _fits(Kq, "Kq", shape, torch.int8, device)
     _fits(Vq, "Vq", shape, torch.int8, device)
     rows = shape[:3]
@@ -546,8 +546,8 @@ def pisa_cache_write(k, v, Kq, Vq, k_scale, v_scale, seq_len, new_len=None, k_ou
     _fits(v, "v", want, torch.bfloat16, dev)
     _fits(k_out, "k_out", want, torch.bfloat16, dev)
     _fits(v_out, "v_out", want, torch.bfloat16, dev)
-    if seq_len is None:
-        raise ValueError("seq_len must be given")
+    if v is None or seq_len is None:
+        raise ValueError("v and seq_len must be given")
     _fits(seq_len, "seq_len", (B,), torch.int32, dev)
     _fits(new_len, "new_len", (B,), torch.int32, dev)
     _call(lib().pisa_cache_write, "pisa_cache_write", dev, k.data_ptr(), v.data_ptr(), Kq.data_ptr(), Vq.data_ptr(),
@@ -596,6 +596,8 @@ def pisa_sparse_attn_cache(q, Kq, Vq, k_scale, v_scale, idx, seq_len, new_len=No
     t >= new_len[b], and sequences whose lengths do not fit, are left as they are (zero where allocated here)."""
     dev = _cuda(q, "q")
     B, H_kv, N_cap, d = _check_cache(Kq, Vq, k_scale, v_scale, dev)
+    if idx is None or seq_len is None:
+        raise ValueError("idx and seq_len must be given")
     one = q.dim() == 3
     if q.dim() not in (3, 4) or idx.dim() != q.dim():
         raise ValueError("q must be [B, T, H_q, d] with idx [B, H_kv, T, K], or [B, H_q, d] with idx [B, H_kv, K]")
@@ -603,8 +605,6 @@ def pisa_sparse_attn_cache(q, Kq, Vq, k_scale, v_scale, idx, seq_len, new_len=No
     want = (B, H_q, d) if one else (B, T, H_q, d)
     _fits(q, "q", want, torch.bfloat16, dev)
     _fits(idx, "idx", (B, H_kv, K_sel) if one else (B, H_kv, T, K_sel), torch.int32, dev)
-    if seq_len is None:
-        raise ValueError("seq_len must be given")
     _fits(seq_len, "seq_len", (B,), torch.int32, dev)
     _fits(new_len, "new_len", (B,), torch.int32, dev)
     if O is None:
@@ -655,8 +655,8 @@ def pisa_prefix_attn(q, Kp, Vp, prefix_len, row_start=None, k_scale=None, v_scal
     _fits(Vp, "Vp", whole, dtype, dev)
     _fits(k_scale, "k_scale", rows, torch.float32, dev)
     _fits(v_scale, "v_scale", rows, torch.float32, dev)
-    if prefix_len is None:
-        raise ValueError("prefix_len must be given")
+    if Vp is None or prefix_len is None:
+        raise ValueError("Vp and prefix_len must be given")
     _fits(prefix_len, "prefix_len", (n,), torch.int32, dev)
     _fits(row_start, "row_start", (n + 1,), torch.int32, dev)
     _fits(o_own, "o_own", want, torch.bfloat16, dev)
