@@ -266,9 +266,9 @@ PISA_API pisa_status pisa_decode_step_ws(const uint16_t* q, const uint16_t* k, c
  * reads back as NaN.  What a row reads back as is bf16(code * scale), both roundings to nearest.
  *   Kq, Vq            [B][H_kv][N_cap][d] int8;   k_scale, v_scale [B][H_kv][N_cap] fp32.
  * The attention over it (pisa_sparse_attn_cache, pisa_prefix_attn) holds each weight times its value's
- * scale in fp16: rounded by up to 2^-11 of itself, and 2^-32 of the row's largest such product.  Sums are
- * fp32.  Value scales are taken up to 2^100 in magnitude (values of 2^107): beyond, a row's output may
- * overflow.  One that is infinite or NaN makes the outputs it takes part in infinite or NaN; the LSE does not
+ * scale in fp16: rounded by up to 2^-11 of itself, and 2^-32 of the row's largest such product, where a value
+ * scale below 2^-87 counts as 2^-87.  Sums are fp32.  Value scales are taken up to 2^100 in magnitude
+ * (values of 2^107): beyond, a row's output may overflow.  One that is infinite or NaN makes the outputs it takes part in infinite or NaN; the LSE does not
  * depend on value scales.
  * Bases are 16-byte aligned, as everywhere (int32 arrays and LSE: 4-byte aligned).  No argument
  * may overlap another unless this says so. */

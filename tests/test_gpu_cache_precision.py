@@ -5,7 +5,7 @@ over many keys.
 Bounds: U = 2^-8 is half a step of bf16, F = 2^-23.  With e the error of a logit (d products summed in fp32, and
 three factors), w the softmax weights, vs the value scales and c the codes, o is off by at most
   (2^-11 + 4 e + 2^-16) sum w |v|     a weight's rounding to fp16, its logit and the sum's, exp2
-  + sum min(2^-32 W, w vs) |c|        the least weight; W = max w vs
+  + sum min(2^-32 W, w vs) |c|        the least weight; W = max w max(vs, 2^-87)
   + 2 s sum w |v| + U |o|             the sums; the result's rounding
 where s = N 2^-27: of N weights a lane adds N / 8 at most, a half step (2^-24) each, and the products are added up
 16 keys at a time, a step each.  The log-sum-exp is off by s, 2 e and its own rounding.
@@ -53,7 +53,8 @@ def attend(q, kc, ks, vc, vs):
     w = w / l
     wv = w * vs
     o, mag = wv @ vc, wv.abs() @ vc.abs()
-    least = torch.minimum(2.0 ** -32 * wv.abs().amax(1, keepdim=True), wv.abs()) @ vc.abs()
+    top = (w * vs.abs().clamp(min=2.0 ** -87)).amax(1, keepdim=True)
+    least = torch.minimum(2.0 ** -32 * top, wv.abs()) @ vc.abs()
     lse, s = (m + l.log())[:, 0], kc.shape[0] * 2.0 ** -27
     bound = (2.0 ** -11 + 4 * e[:, None] + 2.0 ** -16 + 2 * s) * mag + least + R.U * o.abs()
     return o, lse, bound, 2 * e + s + 2.0 ** -18 + 2.0 ** -22 * lse.abs()
@@ -160,4 +161,21 @@ def test_values_of_zero_over_many_keys(Rn):
     # number below 128 whose last place is 2^-17: that place once, and a rounding of the result
     want = math.log(N)
     assert (lse.double() - want).abs().max() <= 2.0 ** -17 + 2.0 ** -24 * want
+    no_error()
+
+
+@pytest.mark.parametrize("e", [-60, -87, -95, -105, -115])
+@pytest.mark.parametrize("Rn", ROWS)
+def test_tiny_values(Rn, e):
+    """Value scales down to where they are less than the least that the reference follows."""
+    N, d = 300, 64
+    g = gen(Rn)
+    kc, ks, _ = R.quantise64(normal(g, N, d))
+    vc, vs, _ = R.quantise64(normal(g, N, d))
+    vs *= 2.0 ** e
+    o, lse, want, l, to, tl = both(normal(g, Rn, 4, d, scale=1.5), kc, ks, vc, vs)
+    R.close(lse, l, tl + 2.0 ** -17, "lse")  # a logarithm of a sum up to 2^127: its last place
+    up = 2.0 ** -e
+    # the output itself is a normal bf16 number or off by half of bf16's least, 2^-134
+    R.close(o.double() * up, want * up, (to + 2.0 ** -134) * up, "o")
     no_error()
