@@ -38,6 +38,10 @@ class pisa_shape(ct.Structure):
                 ("N_cap", ct.c_int)]
 
 
+class pisa_pages(ct.Structure):
+    _fields_ = [("pages", ct.c_int), ("page_size", ct.c_int), ("max_pages", ct.c_int)]
+
+
 _lib = None
 _P = ct.c_void_p
 
@@ -96,6 +100,18 @@ def lib() -> ct.CDLL:
         L.pisa_prefix_attn_workspace_bytes.argtypes = [pisa_shape, pisa_params]
         L.pisa_prefix_attn.restype = ct.c_int
         L.pisa_prefix_attn.argtypes = [_P] * 12 + [ct.c_size_t, pisa_shape, pisa_params, _P]
+        L.pisa_paged_write.restype = ct.c_int
+        L.pisa_paged_write.argtypes = [_P] * 8 + [ct.c_longlong] * 2 + [pisa_shape, pisa_pages, _P]
+        L.pisa_paged_attn_workspace_bytes.restype = ct.c_size_t
+        L.pisa_paged_attn_workspace_bytes.argtypes = [pisa_shape, pisa_params, pisa_pages]
+        L.pisa_paged_attn.restype = ct.c_int
+        L.pisa_paged_attn.argtypes = [_P] * 9 + [ct.c_size_t, ct.c_longlong, pisa_shape, pisa_params, pisa_pages, _P]
+        L.pisa_paged_weights.restype = ct.c_int
+        L.pisa_paged_weights.argtypes = [_P] * 7 + [ct.c_int, ct.c_longlong, pisa_shape, pisa_params, pisa_pages, _P]
+        L.pisa_paged_evict_workspace_bytes.restype = ct.c_size_t
+        L.pisa_paged_evict_workspace_bytes.argtypes = [pisa_shape, pisa_pages, ct.c_int]
+        L.pisa_paged_evict.restype = ct.c_int
+        L.pisa_paged_evict.argtypes = [_P] * 9 + [ct.c_size_t] + [ct.c_int] * 4 + [pisa_shape, pisa_pages, _P]
         L.pisa_status_string.restype = ct.c_char_p
         L.pisa_status_string.argtypes = [ct.c_int]
         L.pisa_get_last_device_error.restype = ct.c_int
@@ -678,3 +694,152 @@ def pisa_prefix_attn(q, Kp, Vp, prefix_len, row_start=None, k_scale=None, v_scal
           _addr(v_scale), prefix_len.data_ptr(), _addr(row_start), _addr(o_own), _addr(lse_own), o.data_ptr(),
           _addr(lse if want_lse else None), ws.data_ptr(), ws.numel(), shape, params)
     return o, (lse if want_lse else None)
+
+
+# ---- paged cache ----------------------------------------------------------------------------
+def _token_rows(t, name, R, H, d, dev):
+    """Elements between the token rows of t [R, H, d], whose heads lie together (a part of a fused projection's
+    output will do)."""
+    if t is None or t.dtype is not torch.bfloat16 or t.get_device() != dev or t.shape != (R, H, d):
+        raise ValueError(f"{name} must be a torch.bfloat16 tensor of shape {(R, H, d)} on cuda:{dev}")
+    rows, heads, cols = t.stride()
+    if R <= 1:
+        rows = H * d
+    if cols != 1 or (heads != d and H > 1) or rows < H * d or rows % 8:
+        raise ValueError(f"{name}'s heads must lie together and its rows a multiple of 8 elements apart; got strides {t.stride()}")
+    return rows
+
+
+def _page_pool(Kp, Vp, page_table, seq_len, row_start, dev):
+    if Kp is None or Kp.dim() != 4:
+        raise ValueError("Kp must be [pages, H_kv, page_size, d]")
+    if page_table is None or page_table.dim() != 2 or seq_len is None:
+        raise ValueError("page_table must be [B, max_pages] and seq_len [B]")
+    P, H_kv, S, d = Kp.shape
+    B, M = page_table.shape
+    _fits(Kp, "Kp", Kp.shape, torch.bfloat16, dev)
+    _fits(Vp, "Vp", Kp.shape, torch.bfloat16, dev)
+    _fits(page_table, "page_table", (B, M), torch.int32, dev)
+    _fits(seq_len, "seq_len", (B,), torch.int32, dev)
+    _fits(row_start, "row_start", (B + 1,), torch.int32, dev)
+    return B, H_kv, d, pisa_pages(P, S, M)
+
+
+def pisa_paged_write(k, v, Kp, Vp, page_table, seq_len, row_start=None, w=None) -> None:
+    """Put the new tokens' rows k, v [R, H_kv, d] bf16 (parts of a fused projection's output will do) into the pages Kp,
+    Vp [pages, H_kv, page_size, d] of their sequences: rows row_start[b] .. row_start[b + 1] - 1 (row_start [B + 1]
+    int32; None: R / B rows each) are keys seq_len[b] + t of sequence b, whose pages are page_table[b]
+    ([B, max_pages] int32).  w [pages, H_kv, page_size] fp32: accumulated weights, cleared for the new keys."""
+    dev = _cuda(k, "k")
+    if Vp is None:
+        raise ValueError("Vp must be given")
+    B, H_kv, d, pages = _page_pool(Kp, Vp, page_table, seq_len, row_start, dev)
+    R = k.shape[0]
+    k_stride, v_stride = _token_rows(k, "k", R, H_kv, d, dev), _token_rows(v, "v", R, H_kv, d, dev)
+    _fits(w, "w", Kp.shape[:3], torch.float32, dev)
+    _call(lib().pisa_paged_write, "pisa_paged_write", dev, k.data_ptr(), v.data_ptr(), Kp.data_ptr(), Vp.data_ptr(),
+          _addr(w), page_table.data_ptr(), seq_len.data_ptr(), _addr(row_start), k_stride, v_stride,
+          pisa_shape(B, R, H_kv, H_kv, d, 0), pages)
+
+
+def pisa_paged_attn_workspace_bytes(shape: pisa_shape, params: pisa_params, pages: pisa_pages) -> int:
+    return int(lib().pisa_paged_attn_workspace_bytes(shape, params, pages))
+
+
+@functools.lru_cache(maxsize=256)
+def _paged_sizes(B, R, H_q, H_kv, d, causal, scale, P, S, M):
+    """The shape, parameters and pages of a call, and the bytes of scratch its attention wants (at least 256)."""
+    shape, params = pisa_shape(B, R, H_q, H_kv, d, 0), pisa_params(64, 2, 1, causal, scale, 0)
+    pages = pisa_pages(P, S, M)
+    need = lib().pisa_paged_attn_workspace_bytes(shape, params, pages)
+    if need == 0 and B > 0 and R > 0:
+        raise PisaError(2, "paged cache: unsupported shape or parameters")
+    return shape, params, pages, max(need, 256)
+
+
+def pisa_paged_attn(q, Kp, Vp, page_table, seq_len, row_start=None, causal: bool = True, scale: float = 0.0, o=None,
+                    lse=None, want_lse: bool = True, ws=None):
+    """Attention of the new tokens q [R, H_q, d] over the pages of their sequences (see pisa_paged_write, which has put
+    their own rows there): token t of sequence b sees its keys 0 .. seq_len[b] + t, or with causal = False all
+    seq_len[b] + n_b.  Returns o [R, H_q, d] and lse [R, H_q]; rows of no sequence are left as they are (an o or
+    lse allocated here holds nothing in particular there)."""
+    dev = _cuda(q, "q")
+    if q.dim() != 3:
+        raise ValueError("q must be [R, H_q, d]")
+    if Vp is None:
+        raise ValueError("Vp must be given")
+    B, H_kv, d, pages = _page_pool(Kp, Vp, page_table, seq_len, row_start, dev)
+    R, H_q = q.shape[:2]
+    q_stride = _token_rows(q, "q", R, H_q, d, dev)
+    want = (R, H_q, d)
+    if o is None:
+        o = torch.empty(want, dtype=torch.bfloat16, device=q.device)
+    else:
+        _fits(o, "o", want, torch.bfloat16, dev)
+    if lse is not None:
+        _fits(lse, "lse", want[:2], torch.float32, dev)
+    elif want_lse:
+        lse = torch.empty(want[:2], dtype=torch.float32, device=q.device)
+    shape, params, pages, need = _paged_sizes(B, R, H_q, H_kv, d, 1 if causal else 0, float(scale), pages.pages,
+                                              pages.page_size, pages.max_pages)
+    if ws is None:
+        ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+    else:
+        ws = _workspace(ws, need, q.device)
+    _call(lib().pisa_paged_attn, "pisa_paged_attn", dev, q.data_ptr(), Kp.data_ptr(), Vp.data_ptr(),
+          page_table.data_ptr(), seq_len.data_ptr(), _addr(row_start), o.data_ptr(), _addr(lse if want_lse else None),
+          ws.data_ptr(), ws.numel(), q_stride, shape, params, pages)
+    return o, (lse if want_lse else None)
+
+
+def pisa_paged_weights(q, lse, Kp, w, page_table, seq_len, row_start=None, accumulate: bool = True, causal: bool = True,
+                       scale: float = 0.0) -> None:
+    """Add to w [pages, H_kv, page_size] fp32 (accumulate = False: put there) the attention weight that every key of
+    the sequences got from the new tokens q [R, H_q, d], summed over them and the query heads of its KV head.  lse
+    [R, H_q]: pisa_paged_attn's of the same tokens, with the same causal and scale."""
+    dev = _cuda(q, "q")
+    if q.dim() != 3:
+        raise ValueError("q must be [R, H_q, d]")
+    if lse is None or w is None:
+        raise ValueError("lse and w must be given")
+    B, H_kv, d, pages = _page_pool(Kp, None, page_table, seq_len, row_start, dev)
+    R, H_q = q.shape[:2]
+    q_stride = _token_rows(q, "q", R, H_q, d, dev)
+    _fits(lse, "lse", (R, H_q), torch.float32, dev)
+    _fits(w, "w", Kp.shape[:3], torch.float32, dev)
+    _call(lib().pisa_paged_weights, "pisa_paged_weights", dev, q.data_ptr(), lse.data_ptr(), Kp.data_ptr(), w.data_ptr(),
+          page_table.data_ptr(), seq_len.data_ptr(), _addr(row_start), 1 if accumulate else 0, q_stride,
+          pisa_shape(B, R, H_q, H_kv, d, 0), pisa_params(64, 2, 1, 1 if causal else 0, float(scale), 0), pages)
+
+
+def pisa_paged_evict_workspace_bytes(shape: pisa_shape, pages: pisa_pages, keep: int) -> int:
+    return int(lib().pisa_paged_evict_workspace_bytes(shape, pages, keep))
+
+
+def pisa_paged_evict(Kp, Vp, w, page_table, seq_len, new_table, keep: int, sinks: int = 0, recent: int = 0, new_len=None,
+                     kept=None, want_kept: bool = True, ws=None):
+    """Cut every sequence's seq_len[b] keys down to `keep`, for each KV head by itself: the first `sinks` and the last
+    `recent` stay, and of the others those of the largest weights w (ties to the lower index).  Their rows of Kp, Vp
+    and w are copied, in their order, to the pages new_table [B, new_max_pages] (other pages than any in use by
+    page_table).  Returns new_len [B] int32 and kept [B, H_kv, keep] int32, the old places of the rows (-1 behind
+    the last); want_kept = False: None, and ws (uint8, allocated when None) holds them meanwhile."""
+    dev = _cuda(Kp, "Kp")
+    if Vp is None or w is None or new_table is None or new_table.dim() != 2:
+        raise ValueError("Vp, w and new_table [B, new_max_pages] must be given")
+    B, H_kv, d, pages = _page_pool(Kp, Vp, page_table, seq_len, None, dev)
+    _fits(w, "w", Kp.shape[:3], torch.float32, dev)
+    _fits(new_table, "new_table", (B, new_table.shape[1]), torch.int32, dev)
+    if new_len is None:
+        new_len = torch.zeros(B, dtype=torch.int32, device=Kp.device)
+    _fits(new_len, "new_len", (B,), torch.int32, dev)
+    if kept is None and want_kept:
+        kept = torch.empty((B, H_kv, max(keep, 0)), dtype=torch.int32, device=Kp.device)
+    _fits(kept, "kept", (B, H_kv, keep), torch.int32, dev)
+    shape = pisa_shape(B, 0, H_kv, H_kv, d, 0)
+    if kept is None:
+        ws = _workspace(ws, pisa_paged_evict_workspace_bytes(shape, pages, keep), Kp.device)
+    _call(lib().pisa_paged_evict, "pisa_paged_evict", dev, Kp.data_ptr(), Vp.data_ptr(), w.data_ptr(),
+          page_table.data_ptr(), seq_len.data_ptr(), new_table.data_ptr(), new_len.data_ptr(), _addr(kept),
+          _addr(ws if kept is None else None), 0 if kept is not None else ws.numel(), keep, sinks, recent,
+          new_table.shape[1], shape, pages)
+    return new_len, kept

@@ -78,10 +78,12 @@ DeviceState g_dev[MAX_DEVICES];
 // While enabled, each entry point records a CUDA event on its stream at the start of its work
 // and after each kernel phase; pisa_phase_times() resolves the events and sums the phases.
 enum Phase { PH_PYRAMID, PH_STAGE1, PH_CLUSTER, PH_LEAF_LSE, PH_TOPK, PH_ATTN, PH_BSA, PH_DECODE, PH_BACKWARD,
-             PH_CACHE_WRITE, PH_CACHE_READ, PH_ATTN_CACHE, PH_PREFIX, NPHASE };
+             PH_CACHE_WRITE, PH_CACHE_READ, PH_ATTN_CACHE, PH_PREFIX, PH_PAGED_WRITE, PH_PAGED_ATTN, PH_PAGED_WEIGHTS,
+             PH_PAGED_EVICT, NPHASE };
 const char* const PHASE_NAMES[NPHASE] = {"pyramid", "stage1", "cluster", "leaf_lse", "topk",
                                          "sparse_attn", "bsa_select", "decode", "attn_backward",
-                                         "cache_write", "cache_read", "sparse_attn_cache", "prefix_attn"};
+                                         "cache_write", "cache_read", "sparse_attn_cache", "prefix_attn",
+                                         "paged_write", "paged_attn", "paged_weights", "paged_evict"};
 
 std::atomic<bool> g_timing{false};
 
@@ -927,6 +929,167 @@ pisa_status pisa_prefix_attn(const uint16_t* q, const void* Kp, const void* Vp, 
   const cudaError_t e = launch_prefix_attn(q, Kp, Vp, k_scale, v_scale, prefix_len, row_start, o_own, lse_own, o, lse,
                                            ws, p, st->num_sms, st->err, static_cast<cudaStream_t>(stream));
   tm.mark(PH_PREFIX);
+  return cuda_status(e);
+}
+
+namespace {
+
+// The paged cache's entry points: B sequences, N new rows (all sequences together).  Without `params` H_q does not count.
+pisa_status check_paged(const pisa_shape& shape, const pisa_params* params, const pisa_pages& pages, Problem* p, Pages* pg) {
+  if (shape.N < 0 || shape.N_cap != 0) return PISA_ERR_INVALID_ARG;
+  pisa_shape s = shape;
+  s.N = 0;
+  if (!params) s.H_q = s.H_kv;
+  const pisa_params none{64, 2, 1, 1, 0.f, 0};
+  const pisa_status rc = check_params(s, params ? *params : none, p);
+  if (rc != PISA_OK) return rc;
+  if (pages.pages <= 0 || pages.page_size <= 0 || pages.max_pages <= 0) return PISA_ERR_INVALID_ARG;
+  if (pages.page_size < 16 || (pages.page_size & (pages.page_size - 1)) != 0) return PISA_ERR_UNSUPPORTED;
+  if ((long long)pages.page_size * pages.max_pages >= (1LL << 25)) return PISA_ERR_UNSUPPORTED;
+  if ((long long)shape.N * s.H_q >= (1LL << 31) || (long long)shape.B * s.H_kv >= (1LL << 16)) return PISA_ERR_UNSUPPORTED;
+  p->N = p->t_hi = shape.N;
+  pg->P = pages.pages;
+  pg->M = pages.max_pages;
+  pg->s_bits = 0;
+  while ((1 << pg->s_bits) < pages.page_size) ++pg->s_bits;
+  return PISA_OK;
+}
+
+// Elements between token rows: 0 for `width`; else at least that and whole 16-byte pieces.
+bool row_stride(long long* stride, long long width) {
+  if (*stride == 0) *stride = width;
+  return *stride >= width && *stride % 8 == 0 && *stride < (1LL << 31);
+}
+
+}  // namespace
+
+pisa_status pisa_paged_write(const uint16_t* k, const uint16_t* v, uint16_t* Kp, uint16_t* Vp, float* w,
+                             const int32_t* page_table, const int32_t* seq_len, const int32_t* row_start,
+                             long long k_stride, long long v_stride, pisa_shape shape, pisa_pages pages,
+                             pisa_stream stream) {
+  Problem p;
+  Pages pg;
+  pisa_status rc = check_paged(shape, nullptr, pages, &p, &pg);
+  if (rc != PISA_OK) return rc;
+  if (p.B == 0 || p.N == 0) return PISA_OK;
+  if (!k || !v || !Kp || !Vp || !page_table || !seq_len) return PISA_ERR_INVALID_ARG;
+  if (!row_start && p.N % p.B != 0) return PISA_ERR_INVALID_ARG;
+  if (!row_stride(&k_stride, (long long)p.H_kv * p.d) || !row_stride(&v_stride, (long long)p.H_kv * p.d))
+    return PISA_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(Kp) || !aligned16(Vp) || !aligned16(w) || !aligned4(page_table) ||
+      !aligned4(seq_len) || !aligned4(row_start))
+    return PISA_ERR_INVALID_ARG;
+  DeviceState* st;
+  if ((rc = device_state(&st)) != PISA_OK) return rc;
+  PhaseTimer tm(static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_paged_write(k, v, k_stride, v_stride, Kp, Vp, w, page_table, seq_len, row_start, p, pg,
+                                           st->num_sms, st->err, static_cast<cudaStream_t>(stream));
+  tm.mark(PH_PAGED_WRITE);
+  return cuda_status(e);
+}
+
+size_t pisa_paged_attn_workspace_bytes(pisa_shape shape, pisa_params params, pisa_pages pages) {
+  Problem p;
+  Pages pg;
+  if (check_paged(shape, &params, pages, &p, &pg) != PISA_OK || p.B == 0) return 0;
+  return paged_workspace_bytes(p, pg);
+}
+
+pisa_status pisa_paged_attn(const uint16_t* q, const uint16_t* Kp, const uint16_t* Vp, const int32_t* page_table,
+                            const int32_t* seq_len, const int32_t* row_start, uint16_t* o, float* lse, void* ws,
+                            size_t ws_bytes, long long q_stride, pisa_shape shape, pisa_params params, pisa_pages pages,
+                            pisa_stream stream) {
+  Problem p;
+  Pages pg;
+  pisa_status rc = check_paged(shape, &params, pages, &p, &pg);
+  if (rc != PISA_OK) return rc;
+  if (p.B == 0 || p.N == 0) return PISA_OK;
+  if (!q || !Kp || !Vp || !page_table || !seq_len || !o || !ws) return PISA_ERR_INVALID_ARG;
+  if (!row_start && p.N % p.B != 0) return PISA_ERR_INVALID_ARG;
+  if (!row_stride(&q_stride, (long long)p.H_q * p.d)) return PISA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(Kp) || !aligned16(Vp) || !aligned4(page_table) || !aligned4(seq_len) ||
+      !aligned4(row_start) || !aligned16(o) || !aligned4(lse) || (reinterpret_cast<uintptr_t>(ws) & 255u))
+    return PISA_ERR_INVALID_ARG;
+  if (ws_bytes < paged_workspace_bytes(p, pg)) return PISA_ERR_WORKSPACE;
+  DeviceState* st;
+  if ((rc = device_state(&st)) != PISA_OK) return rc;
+  PhaseTimer tm(static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_paged_attn(q, q_stride, Kp, Vp, page_table, seq_len, row_start, o, lse, ws, p, pg,
+                                          st->num_sms, st->err, static_cast<cudaStream_t>(stream));
+  tm.mark(PH_PAGED_ATTN);
+  return cuda_status(e);
+}
+
+pisa_status pisa_paged_weights(const uint16_t* q, const float* lse, const uint16_t* Kp, float* w, const int32_t* page_table,
+                               const int32_t* seq_len, const int32_t* row_start, int accumulate, long long q_stride,
+                               pisa_shape shape, pisa_params params, pisa_pages pages, pisa_stream stream) {
+  Problem p;
+  Pages pg;
+  pisa_status rc = check_paged(shape, &params, pages, &p, &pg);
+  if (rc != PISA_OK) return rc;
+  if (accumulate != 0 && accumulate != 1) return PISA_ERR_INVALID_ARG;
+  if (p.B == 0 || (p.N == 0 && accumulate)) return PISA_OK;
+  if ((p.N > 0 && (!q || !lse)) || !Kp || !w || !page_table || !seq_len) return PISA_ERR_INVALID_ARG;
+  if (!row_start && p.N % p.B != 0) return PISA_ERR_INVALID_ARG;
+  if (!row_stride(&q_stride, (long long)p.H_q * p.d)) return PISA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned4(lse) || !aligned16(Kp) || !aligned16(w) || !aligned4(page_table) ||
+      !aligned4(seq_len) || !aligned4(row_start))
+    return PISA_ERR_INVALID_ARG;
+  DeviceState* st;
+  if ((rc = device_state(&st)) != PISA_OK) return rc;
+  PhaseTimer tm(static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_paged_weights(q, q_stride, lse, Kp, w, page_table, seq_len, row_start, accumulate != 0, p,
+                                             pg, st->err, static_cast<cudaStream_t>(stream));
+  tm.mark(PH_PAGED_WEIGHTS);
+  return cuda_status(e);
+}
+
+namespace {
+
+pisa_status check_evict(const pisa_shape& shape, const pisa_pages& pages, int keep, int sinks, int recent,
+                        int new_max_pages, Problem* p, Pages* pg) {
+  pisa_shape s = shape;
+  s.N = 0;
+  const pisa_status rc = check_paged(s, nullptr, pages, p, pg);
+  if (rc != PISA_OK) return rc;
+  if (keep <= 0 || sinks < 0 || recent < 0 || sinks > keep - recent || new_max_pages <= 0) return PISA_ERR_INVALID_ARG;
+  if ((long long)new_max_pages * pages.page_size < keep) return PISA_ERR_INVALID_ARG;
+  if (keep >= (1 << 25)) return PISA_ERR_UNSUPPORTED;
+  return PISA_OK;
+}
+
+}  // namespace
+
+size_t pisa_paged_evict_workspace_bytes(pisa_shape shape, pisa_pages pages, int keep) {
+  Problem p;
+  Pages pg;
+  if (check_evict(shape, pages, keep, 0, 0, keep, &p, &pg) != PISA_OK) return 0;
+  return paged_evict_workspace_bytes(p, keep);
+}
+
+pisa_status pisa_paged_evict(uint16_t* Kp, uint16_t* Vp, float* w, const int32_t* page_table, const int32_t* seq_len,
+                             const int32_t* new_table, int32_t* new_len, int32_t* kept, void* ws, size_t ws_bytes, int keep,
+                             int sinks, int recent, int new_max_pages, pisa_shape shape, pisa_pages pages,
+                             pisa_stream stream) {
+  Problem p;
+  Pages pg;
+  pisa_status rc = check_evict(shape, pages, keep, sinks, recent, new_max_pages, &p, &pg);
+  if (rc != PISA_OK) return rc;
+  if (p.B == 0) return PISA_OK;
+  if (!Kp || !Vp || !w || !page_table || !seq_len || !new_table || !new_len || (!kept && !ws)) return PISA_ERR_INVALID_ARG;
+  if (!aligned16(Kp) || !aligned16(Vp) || !aligned16(w) || !aligned4(page_table) || !aligned4(seq_len) ||
+      !aligned4(new_table) || !aligned4(new_len) || !aligned4(kept) || (reinterpret_cast<uintptr_t>(ws) & 255u))
+    return PISA_ERR_INVALID_ARG;
+  if (!kept) {
+    if (ws_bytes < paged_evict_workspace_bytes(p, keep)) return PISA_ERR_WORKSPACE;
+    kept = static_cast<int32_t*>(ws);
+  }
+  DeviceState* st;
+  if ((rc = device_state(&st)) != PISA_OK) return rc;
+  PhaseTimer tm(static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_paged_evict(Kp, Vp, w, page_table, seq_len, new_table, new_len, kept, keep, sinks, recent,
+                                           new_max_pages, p, pg, st->err, static_cast<cudaStream_t>(stream));
+  tm.mark(PH_PAGED_EVICT);
   return cuda_status(e);
 }
 

@@ -180,9 +180,11 @@ struct CacheTile {
     return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
   }
 
-  // Adds the first `n` keys of the granule at `g` in shared memory.
+  // Adds the first `n` keys of the granule at `g` in shared memory.  LIMITS: row 8 h + 2 q + e sees the first
+  // lim[h][e] of them alone.
+  template <bool LIMITS = false>
   __device__ static __forceinline__ void add(State& st, const uint8_t* g, const Scales& sc, const Query& qr, int n, int r,
-                                             int q) {
+                                             int q, const int (*lim)[2] = nullptr) {
     float s[MT][NH][4];  // keys of groups 2 i (elements 0, 1: rows 2 q, 2 q + 1) and 2 i + 1 (2, 3)
     const int krow = key_of(r);
 #pragma unroll
@@ -233,6 +235,10 @@ struct CacheTile {
         unsigned long long y = mul_f32x2(pack_f32x2(z[0], z[1]), BITS == 8 ? mul_f32x2(f, pack_f32x2(sc.k[i], sc.k[i])) : f);
         unpack_f32x2(y, z[0], z[1]);
         if (8 * i + krow >= n) z[0] = z[1] = NEG_INF;
+        if constexpr (LIMITS) {
+          if (8 * i + krow >= lim[h][0]) z[0] = NEG_INF;
+          if (8 * i + krow >= lim[h][1]) z[1] = NEG_INF;
+        }
         float a = z[0], b = z[1];
         if constexpr (BITS == 8) {
           a += lv[i];

@@ -108,6 +108,31 @@ cudaError_t launch_prefix_attn(const uint16_t* q, const void* Kp, const void* Vp
                                const uint16_t* o_own, const float* lse_own, uint16_t* o, float* lse, void* ws,
                                const Problem& p, int num_sms, uint32_t* err, cudaStream_t s);
 
+// The paged cache: P pages of 2^s_bits tokens, M table entries a sequence.
+struct Pages {
+  int P, M, s_bits;
+};
+// p.N new tokens' rows into their pages; w (nullable): the weights beside the pages, cleared there.
+cudaError_t launch_paged_write(const uint16_t* k, const uint16_t* v, long long k_stride, long long v_stride, uint16_t* Kp,
+                               uint16_t* Vp, float* w, const int32_t* table, const int32_t* seq_len,
+                               const int32_t* row_start, const Problem& p, const Pages& pg, int num_sms, uint32_t* err,
+                               cudaStream_t s);
+// Attention of p.N new tokens of p.B sequences over their pages.
+size_t paged_workspace_bytes(const Problem& p, const Pages& pg);
+cudaError_t launch_paged_attn(const uint16_t* q, long long q_stride, const uint16_t* Kp, const uint16_t* Vp,
+                              const int32_t* table, const int32_t* seq_len, const int32_t* row_start, uint16_t* o,
+                              float* lse, void* ws, const Problem& p, const Pages& pg, int num_sms, uint32_t* err,
+                              cudaStream_t s);
+// The attention weight of every key, summed over the new tokens.
+cudaError_t launch_paged_weights(const uint16_t* q, long long q_stride, const float* lse, const uint16_t* Kp, float* w,
+                                 const int32_t* table, const int32_t* seq_len, const int32_t* row_start, bool accumulate,
+                                 const Problem& p, const Pages& pg, uint32_t* err, cudaStream_t s);
+// The keys of the largest weights into new pages.
+size_t paged_evict_workspace_bytes(const Problem& p, int keep);
+cudaError_t launch_paged_evict(uint16_t* Kp, uint16_t* Vp, float* w, const int32_t* table, const int32_t* seq_len,
+                               const int32_t* new_table, int32_t* new_len, int32_t* kept, int keep, int sinks, int recent,
+                               int new_max_pages, const Problem& p, const Pages& pg, uint32_t* err, cudaStream_t s);
+
 // One CTA whose bounded waits run out after limit_ns (checks the timeout path).
 cudaError_t launch_wait_check(uint64_t limit_ns, uint32_t* err, cudaStream_t s);
 

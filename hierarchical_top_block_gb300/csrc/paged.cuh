@@ -1,0 +1,283 @@
+// The paged cache, and how the attention over it is divided over thread blocks.
+//
+// Keys and values of all sequences lie in pages [P][H_kv][S][d], S = 2^s_bits tokens; key c of sequence b is row
+// c mod S of page table[b][c / S].  Sequence b has L = seq_len[b] keys before its n new tokens, whose
+// query rows are first .. first + n - 1; token t sees the keys 0 .. L + t (or all L + n).
+//
+// A job is (sequence, KV head, tile of ROWS query rows: ROWS / G_Q tokens of G_Q heads); it takes the keys that its
+// last token sees in steps of PAGED_KT.  The jobs' steps, one job after the other, form one line that is cut into
+// equal ranges, one a block: whatever the lengths, every block gets the same work.  A job that lies in one block
+// is finished there; of one that spans blocks each stores its part (row maxima, sums and output sums), and a
+// second kernel joins them.  A block has at most two such parts: the first job of its range and the last.  On
+// the line every job begins with `extra` empty steps, as long as a block stops for it (rows written, others
+// fetched).  The cut depends on the sizes alone, so results are the same in every run.
+//
+// With the causal mask the jobs of a head have different numbers of steps; their sums have a closed form:
+// a tile of TT tokens (a power of two) ends at token (i + 1) TT, so it takes floor((L + 127 + (i + 1) TT) / 128)
+// steps, which is floor((a + i + 1) / c) with c = 128 / TT and a = floor((L + 127) / TT).
+#pragma once
+
+#include "common.cuh"
+
+namespace pisa {
+
+constexpr int PAGED_KT = 128;  // keys a step
+
+struct PagedParams {
+  const uint16_t* q;
+  const uint16_t* K;
+  const uint16_t* V;
+  const int32_t* table;      // [B][M]
+  const int32_t* seq_len;    // [B]
+  const int32_t* row_start;  // [B + 1], nullable: R / B rows each
+  uint16_t* o;
+  float* lse;                // nullable
+  float* part_o;             // [2 blocks][ROWS][d] output sums relative to the row maximum
+  float2* part_ml;           // [2 blocks][ROWS] row maximum (log2 units) and sum
+  long long* base;           // [B + 2] first position of each sequence, the line's length, `extra`
+  long long q_stride;        // elements between rows of q
+  int B, R, H_q, H_kv, GQ, P, M;
+  int s_bits, gq_bits, row_bits;  // S, G_Q and ROWS are 2 to these
+  int causal;
+  int blocks, stop;          // thread blocks the line is cut for; steps that a second job in a block costs
+  float sl2;
+  uint32_t* err;
+};
+
+struct PagedSeq {
+  int first, n, L;  // first row, rows (0 where the lengths do not fit: the sequence is left out), keys before them
+};
+// `bad`: the inputs are out of range.
+__device__ __forceinline__ PagedSeq paged_seq(const int32_t* row_start, const int32_t* seq_len, int B, int R, int cap,
+                                              int b, bool& bad) {
+  PagedSeq s;
+  int lo = row_start ? __ldg(row_start + b) : b * (R / B), hi = row_start ? __ldg(row_start + b + 1) : lo + R / B;
+  bad = lo < 0 || hi < lo || hi > R;
+  lo = min(max(lo, 0), R);
+  hi = min(max(hi, lo), R);
+  s.first = lo;
+  s.n = hi - lo;
+  s.L = __ldg(seq_len + b);
+  if (s.L < 0 || s.L > cap - s.n) {
+    bad = true;
+    s.n = s.L = 0;
+  }
+  return s;
+}
+__device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int b, bool& bad) {
+  return paged_seq(p.row_start, p.seq_len, p.B, p.R, p.M << p.s_bits, b, bad);
+}
+
+// a / b of numbers >= 0, in 32 bits where they fit.
+__device__ __forceinline__ long long whole_quotient(long long a, long long b) {
+  return (a >> 32) || (b >> 32) ? a / b : (long long)((uint32_t)a / (uint32_t)b);
+}
+
+// The steps of a sequence's jobs, the same for each of its KV heads.
+struct PagedJobs {
+  int tiles, tt_bits;  // tiles a head; tokens a tile, 2 to this
+  int L, n, causal;
+  __device__ __forceinline__ PagedJobs(const PagedParams& p, const PagedSeq& s) {
+    tt_bits = p.row_bits - p.gq_bits;
+    tiles = (s.n + (1 << tt_bits) - 1) >> tt_bits;
+    L = s.L;
+    n = s.n;
+    causal = p.causal;
+  }
+  // Keys that the last token of tile i sees.
+  __device__ __forceinline__ int keys(int i) const { return L + (causal ? min(n, (i + 1) << tt_bits) : n); }
+  __device__ __forceinline__ int steps(int i) const { return (keys(i) + PAGED_KT - 1) / PAGED_KT; }
+  // Steps of the tiles before tile k <= tiles.
+  __device__ __forceinline__ long long before(int k) const {
+    if (k == 0) return 0;
+    if (!causal) return (long long)k * steps(0);
+    const int last = k == tiles ? steps(k - 1) : -1;  // (it may be ragged)
+    if (last >= 0 && --k == 0) return last;
+    long long sum;
+    const int a0 = L + PAGED_KT - 1;
+    if (tt_bits >= 8) {
+      sum = (long long)k * (a0 / PAGED_KT) + ((long long)k * (k + 1) << (tt_bits - 8));
+    } else {
+      const int a = a0 >> tt_bits;
+      sum = floors(a + k) - floors(a);
+    }
+    return sum + max(last, 0);
+  }
+  // sum of floor(j / c) for j = 0 .. m, c = 128 / TT
+  __device__ __forceinline__ long long floors(int m) const {
+    const int c_bits = 7 - tt_bits, q = m >> c_bits, r = m - (q << c_bits);
+    return ((long long)q * (q - 1) >> 1 << c_bits) + (long long)q * (r + 1);
+  }
+  __device__ __forceinline__ long long span(int extra) const { return before(tiles) + (long long)tiles * extra; }
+  // The tile that holds position x < span(extra) of a head.
+  __device__ __forceinline__ int tile_at(long long x, int extra) const {
+    int lo = 0, hi = tiles - 1;  // the last tile that begins at or before x
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (before(mid) + (long long)mid * extra <= x)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    return lo;
+  }
+};
+
+// The cut of S positions over `blocks` blocks: every block in use has one at least, so a job's parts are in
+// consecutive blocks.
+struct PagedCut {
+  long long S;
+  int blocks, extra;
+  __device__ __forceinline__ long long start(int block) const { return whole_quotient(S * block, blocks); }
+  // The block that holds position s: the last one that starts at or before it.
+  __device__ __forceinline__ int block_of(long long s) const { return (int)whole_quotient((s + 1) * blocks - 1, S); }
+};
+__device__ __forceinline__ PagedCut paged_cut(const PagedParams& p, long long S, int extra) {
+  return PagedCut{S, (int)max(min(S, (long long)p.blocks), 1ll), extra};
+}
+__device__ __forceinline__ PagedCut paged_cut_of(const PagedParams& p, long long S, long long jobs) {
+  const PagedCut c = paged_cut(p, S, 0);
+  const long long len = whole_quotient(S, c.blocks), with = S + jobs * p.stop;
+  // the longest range, with its stop or with the empty steps
+  return jobs > 1 && with <= (len + p.stop) * c.blocks ? paged_cut(p, with, p.stop) : c;
+}
+
+// Walks a block's range job by job.  Every thread of a warp holds the same state.
+struct PagedWalk {
+  long long at, end;  // next position and end of the range
+  long long gbase;    // first position of the current sequence
+  int b;              // current sequence
+  int extra;          // empty steps before a job's own
+  bool begun;         // a segment of the range is behind
+  PagedSeq s;
+  // current segment
+  int head, tile, k0, k1;  // KV head, tile, steps [k0, k1) of the job
+  int slot;                // -1: the whole job; else the part's slot (2 block + 0 or 1)
+
+  // Warp-wide.  `record`: this warp writes the sequences' first positions and reports bad inputs.
+  __device__ __forceinline__ void init(const PagedParams& p, int block, bool record) {
+    const int lane = threadIdx.x & 31;
+    begun = false;
+    b = 0;
+    gbase = 0;
+    bool bad = false, any_bad = false;
+    const PagedSeq mine = paged_seq(p, min(lane, p.B - 1), bad);
+    any_bad = bad;
+    auto seq = [&](int i) {  // a lane's own
+      if (i < 32) return mine;
+      bool x;
+      const PagedSeq s = paged_seq(p, i, x);
+      any_bad = any_bad || x;
+      return s;
+    };
+    long long S = 0, jobs = 0;
+    for (int i = lane; i < p.B; i += 32) {
+      const PagedJobs j(p, seq(i));
+      jobs += (long long)p.H_kv * j.tiles;
+      S += p.H_kv * j.before(j.tiles);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      S += __shfl_xor_sync(0xffffffffu, S, o);
+      jobs += __shfl_xor_sync(0xffffffffu, jobs, o);
+    }
+    if (record && any_bad) report_error(p.err, ERR_BAD_INDEX);
+    const PagedCut cut = paged_cut_of(p, S, jobs);
+    extra = cut.extra;
+    at = end = 0;
+    if (block < cut.blocks) {
+      at = cut.start(block);
+      end = cut.start(block + 1);
+    }
+    if (record && lane == 0) {
+      p.base[p.B] = cut.S;
+      p.base[p.B + 1] = extra;
+    }
+    if (at >= end && !record) return;
+    // the sequence that holds position `at`
+    long long before = 0;
+    bool found = false;
+    for (int i0 = 0; i0 < p.B && !(found && !record); i0 += 32) {
+      const int i = i0 + lane;
+      const long long mine_all = i < p.B ? p.H_kv * PagedJobs(p, seq(i)).span(extra) : 0;
+      long long x = mine_all;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (record && i < p.B) p.base[i] = before + x - mine_all;
+      const unsigned past = __ballot_sync(0xffffffffu, before + x > at);
+      if (past && !found) {
+        const int l = __ffs(past) - 1;
+        b = i0 + l;
+        gbase = before + __shfl_sync(0xffffffffu, x - mine_all, l);
+        found = true;
+      }
+      before += __shfl_sync(0xffffffffu, x, 31);
+    }
+    s = paged_seq(p, b, bad);
+  }
+
+  // Moves to the next segment; false at the end of the range.
+  __device__ __forceinline__ bool next(const PagedParams& p, int block) {
+    for (;;) {
+      if (at >= end) return false;
+      const PagedJobs j(p, s);
+      const long long span = j.span(extra);
+      long long off = at - gbase;
+      if (off >= p.H_kv * span) {  // at < end <= the line's length: a later sequence holds it
+        gbase += p.H_kv * span;
+        if (++b >= p.B) return false;  // (unless somebody changes the lengths under the call)
+        bool bad;
+        s = paged_seq(p, b, bad);
+        continue;
+      }
+      head = (int)whole_quotient(off, span);
+      off -= head * span;
+      tile = j.tile_at(off, extra);
+      off -= j.before(tile) + (long long)tile * extra;
+      if (off < extra) {  // the empty steps
+        at = min(end, at + extra - off);
+        continue;
+      }
+      const int steps = j.steps(tile);
+      k0 = (int)(off - extra);
+      k1 = (int)min((long long)steps, k0 + (end - at));
+      slot = (k0 == 0 && k1 == steps) ? -1 : 2 * block + (begun ? 1 : 0);
+      begun = true;
+      at += k1 - k0;
+      return true;
+    }
+  }
+  // Keys that query row `row` of the tile sees.
+  __device__ __forceinline__ int seen(const PagedParams& p, int row) const {
+    const int tok = min(((tile << p.row_bits) + row) >> p.gq_bits, s.n - 1);
+    return s.L + (p.causal ? tok + 1 : s.n);
+  }
+  // Query rows of the tile, and the place of one among all rows and heads.
+  __device__ __forceinline__ int rows(const PagedParams& p) const {
+    return min(1 << p.row_bits, (s.n << p.gq_bits) - (tile << p.row_bits));
+  }
+  __device__ __forceinline__ size_t row_at(const PagedParams& p, int row) const {
+    const int m = (tile << p.row_bits) + row, tok = m >> p.gq_bits;
+    return (size_t)(s.first + tok) * p.H_q + (size_t)head * p.GQ + (m - (tok << p.gq_bits));
+  }
+};
+
+// The page of keys from c0 on (c0 < cap): its number, or P (whose rows a copy reads as zeros) where the entry names
+// none; no row sees those keys.  Entries from P on are reported.
+__device__ __forceinline__ int page_of(const int32_t* table, int P, int entry, uint32_t* err) {
+  const int page = __ldg(table + entry);
+  if (page >= P) report_error(err, ERR_BAD_INDEX);
+  return page < 0 || page >= P ? P : page;
+}
+
+// The tensor-core kernel (paged_tc.cu): tiles of PAGED_TC_ROWS rows, one block a SM.
+constexpr int PAGED_TC_ROWS = 256;
+cudaError_t launch_paged_tc(const PagedParams& p, int d, cudaStream_t s);
+
+// A map over pages [P][H_kv][S][d]: boxes of `keys` rows of 64 columns.
+bool encode_page_map(CUtensorMap* map, const void* base, int d, int S, int H_kv, int P, int keys);
+
+}  // namespace pisa

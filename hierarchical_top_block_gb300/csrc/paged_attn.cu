@@ -1,0 +1,379 @@
+// Attention of new tokens over the paged cache of their sequences: one token (decode), a few (drafts), a chunk of a
+// prompt or a whole one, in ragged batches.
+//
+//   z_tc = scale q_t . k_c for the keys c that token t sees,   o_t = sum_c softmax(z_t)_c v_c,   lse_t = log sum_c e^z_tc
+//
+// in one pass over the keys with a running reference (cache_attn.cuh, paged_tc.cu).  Few query rows a sequence
+// (G_Q heads x tokens): the kernel here, on mma.sync, bound by the bytes of the cache.  Many: paged_tc.cu.
+#include <algorithm>
+
+#include "cache_attn.cuh"
+#include "kernels.cuh"
+#include "paged.cuh"
+#include "pdl.cuh"
+
+namespace pisa {
+
+bool encode_page_map(CUtensorMap* map, const void* base, int d, int S, int H_kv, int P, int keys) {
+  const uint64_t dims[4] = {(uint64_t)d, (uint64_t)S, (uint64_t)H_kv, (uint64_t)P};
+  const uint64_t strides[3] = {(uint64_t)d * 2, (uint64_t)S * d * 2, (uint64_t)H_kv * S * d * 2};
+  const uint32_t box[4] = {64, (uint32_t)keys, 1, 1};
+  return encode_tensor_map(map, base, 4, dims, strides, box);
+}
+
+namespace {
+
+constexpr int THREADS = 128;
+constexpr int few_blocks(int rows) { return rows > 8 ? 2 : 4; }  // a SM
+
+// A finished row: the factor of its output sums, and its log-sum-exp.
+__device__ __forceinline__ float finish_row(float m, float l, float& lse) {
+  lse = l == 0.f ? NEG_INF : (m + log2f(l)) * LN2;
+  return l == 0.f ? 0.f : 1.f / l;
+}
+
+// Tiles of 8 NH rows.  A block's four warps take the granules of a segment in turn, each with a ring of its own that
+// it fills by TMA.  A granule lies in one page (KEYS <= S).
+template <int D, int KEYS, int NH>
+struct FewCfg {
+  static constexpr int SLOTS = (D == 64 && KEYS == 32) || (NH == 2 && D == 128) ? 2 : KEYS * D == 1024 ? 2 : 1;
+  static constexpr int PER_SM = few_blocks(8 * NH);
+  using Tile = CacheTile<D, 16, KEYS, NH>;
+  static constexpr uint32_t RING = 4 * SLOTS * Tile::BYTES, OUT = 4 * 8 * NH * D * 4;
+  static constexpr uint32_t SMEM = RING > OUT ? RING : OUT;  // the outputs meet where the granules were
+};
+
+template <int D, int KEYS, int NH>
+__global__ void __launch_bounds__(THREADS, FewCfg<D, KEYS, NH>::PER_SM)
+    paged_few_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV, PagedParams p) {
+  pdl_trigger();
+  using C = FewCfg<D, KEYS, NH>;
+  using Tile = typename C::Tile;
+  constexpr int ROWS = 8 * NH;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  float* po = reinterpret_cast<float*>(smem);  // [4][ROWS][D]
+  __shared__ uint64_t full[4][C::SLOTS];
+  __shared__ float sn[4][16], sl[4][16];
+  __shared__ float2 ml[ROWS];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, q = lane & 3;
+  uint8_t* ring = smem + warp * C::SLOTS * Tile::BYTES;
+  if (lane == 0) {
+    prefetch_map(&mapK);
+    prefetch_map(&mapV);
+    for (int i = 0; i < C::SLOTS; ++i) mbar_init(&full[warp][i], 1);
+    mbar_fence_init();
+  }
+  __syncwarp();
+  PagedWalk w;
+  w.init(p, blockIdx.x, blockIdx.x == 0 && warp == 0);
+  uint32_t s = 0, got = 0;  // granules used and fetched
+  bool failed = false;
+  while (w.next(p, blockIdx.x)) {
+    const int rows = w.rows(p);
+    const int first = w.k0 * PAGED_KT, key_end = min(w.seen(p, rows - 1), w.k1 * PAGED_KT);
+    const int granules = (key_end - first + KEYS - 1) / KEYS, mine = max(0, (granules - warp + 3) >> 2);
+    const int32_t* table = p.table + (size_t)w.b * p.M;
+    int pages = p.P;  // of the 32 granules of this warp from `batch` on, one a lane
+    auto look = [&](int batch) {
+      const int g = batch + lane;
+      pages = g < mine ? page_of(table, p.P, (first + (warp + 4 * g) * KEYS) >> p.s_bits, p.err) : p.P;
+    };
+    uint32_t none = 0;  // slots whose granule has no page
+    auto fetch = [&](int i) {  // granule i of this warp
+      if ((i & 31) == 0) look(i);
+      const int page = __shfl_sync(0xffffffffu, pages, i & 31), slot = got % C::SLOTS;
+      none = page == p.P ? none | 1u << slot : none & ~(1u << slot);
+      if (lane == 0) {
+        const int row = (first + (warp + 4 * i) * KEYS) & ((1 << p.s_bits) - 1);
+        uint8_t* dst = ring + slot * Tile::BYTES;
+        mbar_arrive_expect_tx(&full[warp][slot], Tile::BYTES);
+#pragma unroll
+        for (int c = 0; c < Tile::PIECES; ++c) {
+          tma_load_4d(dst + c * (KEYS * 128), &mapK, &full[warp][slot], 64 * c, row, w.head, page);
+          tma_load_4d(dst + Tile::SIDE + c * (KEYS * 128), &mapV, &full[warp][slot], 64 * c, row, w.head, page);
+        }
+      }
+      ++got;
+    };
+    auto wait = [&](uint32_t n, uint64_t limit = WAIT_LIMIT_NS) {
+      return mbar_wait_warp(&full[warp][n % C::SLOTS], (n / C::SLOTS) & 1, p.err, limit);
+    };
+#pragma unroll
+    for (int i = 0; i < C::SLOTS; ++i)
+      if (i < mine && !failed) fetch(i);
+    typename Tile::Query qr;
+    Tile::load_q(qr, [&](int i) {
+      if (i >= rows) return (const uint16_t*)nullptr;
+      const int m = w.tile * ROWS + i, tok = m >> p.gq_bits;
+      return p.q + (w.s.first + tok) * p.q_stride + ((size_t)w.head * p.GQ + (m - (tok << p.gq_bits))) * D;
+    }, p.sl2, r, q);
+    int seen[NH][2];
+    const int least = w.seen(p, 0);
+#pragma unroll
+    for (int h = 0; h < NH; ++h)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) seen[h][e] = w.seen(p, 8 * h + 2 * q + e);
+    typename Tile::State st;
+    Tile::clear(st);
+    const typename Tile::Scales sc{};
+    for (int i = 0; i < mine && !failed; ++i, ++s) {
+      if (!wait(s)) {
+        failed = true;
+        break;
+      }
+      const int key = first + (warp + 4 * i) * KEYS, slot = s % C::SLOTS, n = min(KEYS, key_end - key);
+      if (!(none >> slot & 1)) {
+        if (key + KEYS <= least) {
+          Tile::add(st, ring + slot * Tile::BYTES, sc, qr, n, r, q);
+        } else {
+          int lim[NH][2];
+#pragma unroll
+          for (int h = 0; h < NH; ++h) lim[h][0] = seen[h][0] - key, lim[h][1] = seen[h][1] - key;
+          Tile::template add<true>(st, ring + slot * Tile::BYTES, sc, qr, n, r, q, lim);
+        }
+      }
+      __syncwarp();  // the slot has been read
+      if (i + C::SLOTS < mine) fetch(i + C::SLOTS);
+    }
+    if (failed)  // copies still in flight land before their memory is used again (bounded)
+      for (; s < got; ++s) wait(s, 100000000ull);
+    join_warps<Tile, D>(st, po, sn, sl, ml, rows);
+    if (w.slot < 0) {
+      for (int i = threadIdx.x; i < rows * D / 2; i += THREADS) {
+        const int row = 2 * i / D, c = 2 * i - row * D;
+        const size_t at = w.row_at(p, row);
+        float lse;
+        const float f = finish_row(ml[row].x, ml[row].y, lse);
+        const float2 x = *reinterpret_cast<const float2*>(po + 2 * i);
+        *reinterpret_cast<uint32_t*>(p.o + at * D + c) = f == 0.f ? 0u : pack_bf16x2(x.x * f, x.y * f);
+        if (c == 0 && p.lse) p.lse[at] = lse;
+      }
+    } else {
+      float* dst = p.part_o + (size_t)w.slot * ROWS * D;
+      for (int i = threadIdx.x; i < rows * D; i += THREADS) dst[i] = po[i];
+      if (threadIdx.x < rows) p.part_ml[(size_t)w.slot * ROWS + threadIdx.x] = ml[threadIdx.x];
+    }
+    fence_proxy_async();  // the next copies go where po was
+    __syncthreads();
+  }
+}
+
+// Joins the parts of the jobs that span blocks.  blockIdx.x: the block in which such a job begins; its rows are
+// taken by WARPS warps each, which take the parts in turn, BATCH of them in flight, and meet in shared memory.
+template <int D, int WARPS>
+__global__ void __launch_bounds__(THREADS, 8) paged_join_kernel(PagedParams p) {
+  constexpr int V = D / 32, BATCH = 5, PER = THREADS / 32 / WARPS;  // rows a block at a time
+  __shared__ float so[PER][WARPS][D];
+  __shared__ float2 sml[PER][WARPS];
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % WARPS, sub = (threadIdx.x >> 5) / WARPS;
+  const int c0 = blockIdx.x;
+  pdl_wait();
+  const PagedCut cut = paged_cut(p, p.base[p.B], (int)p.base[p.B + 1]);
+  if (c0 >= cut.blocks || cut.S == 0) return;
+  // the job that holds the last position of block c0
+  PagedWalk w;
+  const long long last = cut.start(c0 + 1) - 1;
+  int lo = 0, hi = p.B - 1;  // the last sequence that begins at or before it
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (p.base[mid] <= last)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  bool bad;
+  w.b = lo;
+  w.s = paged_seq(p, lo, bad);
+  if (w.s.n == 0) return;
+  const PagedJobs j(p, w.s);
+  long long off = last - p.base[lo];
+  const long long span = j.span(cut.extra);
+  w.head = (int)whole_quotient(off, span);
+  off -= w.head * span;
+  w.tile = j.tile_at(off, cut.extra);
+  const long long s0 = last - off + j.before(w.tile) + (long long)w.tile * cut.extra, s1 = s0 + cut.extra;  // its first position and step
+  if (cut.block_of(s1) != c0) return;
+  // (in range as long as nobody changes the lengths under the call)
+  const int c1 = min(cut.block_of(s1 + j.steps(w.tile) - 1), p.blocks - 1);
+  if (c1 <= c0) return;
+  const int slot0 = 2 * c0 + (cut.start(c0) >= s0 ? 0 : 1);  // 1: the block had a job before
+  const int rows = w.rows(p);
+  for (int row0 = blockIdx.y * PER; row0 < rows; row0 += gridDim.y * PER) {
+    const int row = min(row0 + sub, rows - 1);
+    float m = NEG_INF, l = 0.f, acc[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = 0.f;
+    for (int c = c0 + warp; c <= c1; c += WARPS * BATCH) {
+      float2 ml[BATCH];
+      float x[BATCH][V];
+#pragma unroll
+      for (int u = 0; u < BATCH; ++u) {
+        const int cc = c + u * WARPS;
+        const bool in = cc <= c1;
+        const size_t at = ((size_t)(cc == c0 || !in ? slot0 : 2 * cc) << p.row_bits) + row;
+        ml[u] = in ? p.part_ml[at] : make_float2(NEG_INF, 0.f);
+        const float* src = p.part_o + at * D + lane * V;
+        if constexpr (V == 4)
+          *reinterpret_cast<float4*>(x[u]) = *reinterpret_cast<const float4*>(src);
+        else
+          *reinterpret_cast<float2*>(x[u]) = *reinterpret_cast<const float2*>(src);
+      }
+      float top = m;
+#pragma unroll
+      for (int u = 0; u < BATCH; ++u) top = fmaxf(top, ml[u].x);
+      const float f0 = m == NEG_INF ? 0.f : fast_exp2(m - top);
+      if (m != NEG_INF) l *= f0;
+      m = top;
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] *= f0;
+#pragma unroll
+      for (int u = 0; u < BATCH; ++u) {
+        if (ml[u].x == NEG_INF) {
+          l += ml[u].y;  // 0, or NaN where every logit was
+          continue;
+        }
+        const float f = fast_exp2(ml[u].x - m);
+        l += ml[u].y * f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] += x[u][i] * f;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) so[sub][warp][lane * V + i] = acc[i];
+    if (lane == 0) sml[sub][warp] = make_float2(m, l);
+    __syncthreads();
+    if (warp == 0 && row0 + sub < rows) {
+      m = NEG_INF;
+#pragma unroll
+      for (int u = 0; u < WARPS; ++u) m = fmaxf(m, sml[sub][u].x);
+      l = 0.f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] = 0.f;
+#pragma unroll
+      for (int u = 0; u < WARPS; ++u) {
+        const float2 ml = sml[sub][u];
+        const float f = ml.x == NEG_INF ? 0.f : fast_exp2(ml.x - m);
+        l += ml.x == NEG_INF ? ml.y : ml.y * f;
+        if (f != 0.f)
+#pragma unroll
+          for (int i = 0; i < V; ++i) acc[i] += so[sub][u][lane * V + i] * f;
+      }
+      float lse;
+      const float f = finish_row(m, l, lse);
+      const size_t at = w.row_at(p, row);
+      uint32_t y[V / 2];
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) y[i] = f == 0.f ? 0u : pack_bf16x2(acc[2 * i] * f, acc[2 * i + 1] * f);
+      uint16_t* dst = p.o + at * D + lane * V;
+      if constexpr (V == 4)
+        *reinterpret_cast<uint2*>(dst) = make_uint2(y[0], y[1]);
+      else
+        *reinterpret_cast<uint32_t*>(dst) = y[0];
+      if (p.lse && lane == 0) p.lse[at] = lse;
+    }
+    __syncthreads();
+  }
+}
+
+constexpr int MAX_SMS = 152;  // this GPU's: the scratch does not depend on the device at hand
+
+struct Plan {
+  bool tc;
+  int rows, blocks, stop;
+};
+Plan paged_plan(const Problem& p, const Pages& pg) {
+  const long long rows = ((long long)p.N * p.GQ + p.B - 1) / (p.B > 0 ? p.B : 1);  // a sequence has on average
+  const int few = rows > 8 || p.GQ > 8 ? 16 : 8;
+  Plan plan{false, few, few_blocks(few) * MAX_SMS, 2};
+  // no more blocks (and scratch) than there can be steps: every sequence has at most one tile that is not full
+  const long long tiles = (long long)p.N * p.GQ / plan.rows + p.B;
+  const long long steps = (((long long)pg.M << pg.s_bits) + PAGED_KT - 1) / PAGED_KT;
+  plan.blocks = (int)std::min<long long>(plan.blocks, p.H_kv * tiles * steps);
+  return plan;
+}
+
+template <int D, int KEYS, int NH>
+cudaError_t launch_few(const PagedParams& p, cudaStream_t s) {
+  using C = FewCfg<D, KEYS, NH>;
+  CUtensorMap mapK, mapV;
+  if (!encode_page_map(&mapK, p.K, D, 1 << p.s_bits, p.H_kv, p.P, KEYS) ||
+      !encode_page_map(&mapV, p.V, D, 1 << p.s_bits, p.H_kv, p.P, KEYS))
+    return cudaErrorInvalidValue;
+  auto kern = paged_few_kernel<D, KEYS, NH>;
+  const cudaError_t e = allow_shared<paged_few_kernel<D, KEYS, NH>>(C::SMEM);
+  if (e != cudaSuccess) return e;
+  kern<<<p.blocks, THREADS, C::SMEM, s>>>(mapK, mapV, p);
+  return cudaGetLastError();
+}
+template <int D, int KEYS>
+cudaError_t launch_few_rows(const PagedParams& p, cudaStream_t s) {
+  return p.row_bits > 3 ? launch_few<D, KEYS, 2>(p, s) : launch_few<D, KEYS, 1>(p, s);
+}
+
+size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+int bits_of(int x) {  // of a power of two
+  int b = 0;
+  while ((1 << b) < x) ++b;
+  return b;
+}
+
+}  // namespace
+
+size_t paged_workspace_bytes(const Problem& p, const Pages& pg) {
+  const Plan plan = paged_plan(p, pg);
+  const size_t parts = (size_t)2 * plan.blocks * plan.rows;
+  return up256(parts * p.d * 4) + up256(parts * 8) + up256((size_t)(p.B + 2) * 8);
+}
+
+cudaError_t launch_paged_attn(const uint16_t* q, long long q_stride, const uint16_t* Kp, const uint16_t* Vp,
+                              const int32_t* table, const int32_t* seq_len, const int32_t* row_start, uint16_t* o,
+                              float* lse, void* ws, const Problem& pr, const Pages& pg, int num_sms, uint32_t* err,
+                              cudaStream_t s) {
+  PagedParams p;
+  p.q = q;
+  p.K = Kp;
+  p.V = Vp;
+  p.table = table;
+  p.seq_len = seq_len;
+  p.row_start = row_start;
+  p.o = o;
+  p.lse = lse;
+  p.q_stride = q_stride;
+  p.B = pr.B;
+  p.R = pr.N;
+  p.H_q = pr.H_q;
+  p.H_kv = pr.H_kv;
+  p.GQ = pr.GQ;
+  p.P = pg.P;
+  p.M = pg.M;
+  p.s_bits = pg.s_bits;
+  p.causal = pr.causal;
+  p.sl2 = pr.scale * LOG2E;
+  p.err = err;
+  const Plan plan = paged_plan(pr, pg);
+  p.gq_bits = bits_of(pr.GQ);
+  p.row_bits = bits_of(plan.rows);
+  p.blocks = plan.blocks;
+  p.stop = plan.stop;
+  const size_t parts = (size_t)2 * p.blocks * plan.rows;
+  uint8_t* at = static_cast<uint8_t*>(ws);
+  p.part_o = reinterpret_cast<float*>(at);
+  at += up256(parts * pr.d * 4);
+  p.part_ml = reinterpret_cast<float2*>(at);
+  at += up256(parts * 8);
+  p.base = reinterpret_cast<long long*>(at);
+  cudaError_t e;
+  if (pr.d == 128)
+    e = launch_few_rows<128, 16>(p, s);
+  else
+    e = pg.s_bits > 4 ? launch_few_rows<64, 32>(p, s) : launch_few_rows<64, 16>(p, s);
+  if (e != cudaSuccess) return e;
+  const int warps = plan.rows <= 16 ? 4 : 2, per = 4 / warps;  // a row; rows a block
+  const dim3 grid((unsigned)p.blocks, (unsigned)std::min(plan.rows / per, std::max(1, num_sms * 16 / p.blocks)));
+  auto join = pr.d == 128 ? (warps == 4 ? paged_join_kernel<128, 4> : paged_join_kernel<128, 2>)
+                          : (warps == 4 ? paged_join_kernel<64, 4> : paged_join_kernel<64, 2>);
+  return launch_pdl(join, grid, dim3(THREADS), 0, s, p);
+}
+
+}  // namespace pisa

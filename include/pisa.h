@@ -350,6 +350,84 @@ PISA_API pisa_status pisa_prefix_attn(const uint16_t* q, const void* Kp, const v
                                       const uint16_t* o_own, const float* lse_own, uint16_t* o, float* lse, void* ws,
                                       size_t ws_bytes, pisa_shape shape, pisa_params params, pisa_stream stream);
 
+/* ---- paged key/value cache --------------------------------------------------------------- */
+
+/* Keys and values of many sequences in pages of one pool, so that a sequence grows and shrinks without being moved (the
+ * paper has no counterpart).  Dense attention of new tokens over it (a decode step, drafted tokens, a chunk of a prompt
+ * or a whole one, mixed in one ragged batch), the attention weight that its keys got, and the eviction of those that
+ * got least.
+ *   Kp, Vp      [P][H_kv][S][d] bf16;  w [P][H_kv][S] fp32: accumulated attention weights, kept beside the pages.
+ *   page_table  [B][M] int32 (device): key c of sequence b is row c mod S of page page_table[b][c / S].  Entries
+ *               behind a sequence's last key are not read.
+ *   seq_len     [B] int32 (device): keys of each sequence before its new tokens; not changed by any call.
+ *   row_start   [B + 1] int32 (device), not decreasing, within 0 .. R: rows row_start[b] .. row_start[b+1] - 1 of q, k,
+ *               v, o and lse are sequence b's new tokens, token t at position seq_len[b] + t; other rows are neither
+ *               read nor written.  NULL where B divides R: R / B rows each.
+ * pages.pages = P, pages.page_size = S (a power of two from 16), pages.max_pages = M, M S < 2^25; shape.B sequences,
+ * shape.N = R rows in all, R H_q < 2^31, B H_kv < 2^16, shape.N_cap = 0.  A cache [B][H_kv][S][d] of one page a sequence
+ * (page_table[b][0] = b) is the layout of the other entry points.
+ * *_stride: elements between token rows of q [R][H_q][d], k or v [R][H_kv][d], whose heads lie together (parts of
+ * one fused projection are passed as they are); a multiple of 8, 0 for rows that follow one another.
+ * A sequence whose seq_len is negative or whose keys do not fit in M S is left as it is, decreasing row bounds are
+ * brought into range, and both are flagged (PISA_ERR_BAD_INDEX).  A table entry that names no page: keys there are seen
+ * by no row; from P on it is flagged as well (a negative one may stand for a page that is gone).  No argument may
+ * overlap another unless this says so, and no page may be written for two sequences (it would hold rows of
+ * either).  Results are the same in every run. */
+typedef struct {
+  int pages;      /* P, pages in the pool */
+  int page_size;  /* S, tokens a page */
+  int max_pages;  /* M, entries of a row of page_table */
+} pisa_pages;
+
+/* Puts the new tokens' rows k, v [R][H_kv][d] bf16 into their pages and, unless w is NULL, clears their weights.  A row
+ * whose table entry names no page is left out and flagged.  shape.H_q is ignored. */
+PISA_API pisa_status pisa_paged_write(const uint16_t* k, const uint16_t* v, uint16_t* Kp, uint16_t* Vp, float* w,
+                                      const int32_t* page_table, const int32_t* seq_len, const int32_t* row_start,
+                                      long long k_stride, long long v_stride, pisa_shape shape, pisa_pages pages,
+                                      pisa_stream stream);
+
+/* Attention of the new tokens, whose own rows are in the pages already: token t of sequence b sees its keys 0 ..
+ * seq_len[b] + t (params.causal = 1) or all seq_len[b] + n_b (0),
+ *   z_c = scale (q . k_c),  o = sum_c softmax(z)_c v_c,  lse = log sum_c exp z_c.
+ *   q, o [R][H_q][d] bf16 (o's rows follow one another);  lse [R][H_q] fp32, nullable.
+ *   ws   device scratch, 256-B aligned, ws_bytes >= pisa_paged_attn_workspace_bytes(); not to be used by other work
+ *        until the call has run (two captured graphs that may run at once need one each).
+ * A row that sees no key gives o = 0 and lse = -inf.  Weights are rounded to bf16 (2^-9 of each); logits and sums are
+ * fp32.  Keys behind a sequence's last may hold anything; a value that is infinite or NaN shows in the rows that
+ * see its key, and may show in others of its sequence.  params.scale and causal are used. */
+PISA_API size_t pisa_paged_attn_workspace_bytes(pisa_shape shape, pisa_params params, pisa_pages pages);
+PISA_API pisa_status pisa_paged_attn(const uint16_t* q, const uint16_t* Kp, const uint16_t* Vp, const int32_t* page_table,
+                                     const int32_t* seq_len, const int32_t* row_start, uint16_t* o, float* lse, void* ws,
+                                     size_t ws_bytes, long long q_stride, pisa_shape shape, pisa_params params,
+                                     pisa_pages pages, pisa_stream stream);
+
+/* The attention weight that every key of the sequences (the new tokens' own included) got from the new tokens,
+ *   w_c = sum over the tokens t that see c and the G_Q query heads of its KV head of  exp(scale (q_t . k_c) - lse_t),
+ * added to w (accumulate = 1) or put in its place (0).  lse [R][H_q] is pisa_paged_attn's; a row with lse = -inf saw
+ * nothing and gives nothing.  Weights of other keys and pages are left as they are.  Exponents and sums are fp32. */
+PISA_API pisa_status pisa_paged_weights(const uint16_t* q, const float* lse, const uint16_t* Kp, float* w,
+                                        const int32_t* page_table, const int32_t* seq_len, const int32_t* row_start,
+                                        int accumulate, long long q_stride, pisa_shape shape, pisa_params params,
+                                        pisa_pages pages, pisa_stream stream);
+
+/* Cuts every sequence down to `keep` keys, for each KV head by itself: the first `sinks` and the last `recent` of its
+ * seq_len[b] keys (here all of its keys) stay, and of the others those of the largest weights w, ties to the
+ * lower index, a NaN below every number; a sequence of no more keys keeps all.  Their rows of Kp, Vp and w are
+ * copied, in their order, to rows 0 .. new_len[b] - 1 of the pages of new_table [B][new_max_pages], whose entries
+ * in use name other pages than any that the call reads; a sequence's old pages are left as they are (they may be shared with
+ * others, and are free for new keys after the call).
+ *   new_len  [B] int32 out: min(keep, keys of seq_len[b] that are there); not seq_len.
+ *   kept     [B][H_kv][keep] int32 out, nullable: which key is now row j, -1 behind the last.
+ *   ws       scratch where kept is NULL: 256-B aligned, pisa_paged_evict_workspace_bytes() bytes.
+ * sinks + recent <= keep <= new_max_pages S.  Rows whose new_table entry names no page are left out and flagged.
+ * A sequence whose seq_len does not fit is flagged, its new_len is left as it is and kept is -1.  shape.H_q and N
+ * are ignored. */
+PISA_API size_t pisa_paged_evict_workspace_bytes(pisa_shape shape, pisa_pages pages, int keep);
+PISA_API pisa_status pisa_paged_evict(uint16_t* Kp, uint16_t* Vp, float* w, const int32_t* page_table,
+                                      const int32_t* seq_len, const int32_t* new_table, int32_t* new_len, int32_t* kept,
+                                      void* ws, size_t ws_bytes, int keep, int sinks, int recent, int new_max_pages,
+                                      pisa_shape shape, pisa_pages pages, pisa_stream stream);
+
 /* ---- status ---------------------------------------------------------------------------- */
 
 PISA_API const char* pisa_status_string(pisa_status status);
@@ -364,7 +442,8 @@ PISA_API pisa_status pisa_get_last_device_error(pisa_stream stream);
 /* While enabled, every compute entry point records a CUDA event on its stream when its work
  * starts and after each of its kernel phases: pyramid, Stage 1 (with the clustering histogram),
  * clustering, Stage 2 leaf LSE, top-K, sparse attention, BSA selection, decode step, attention
- * backward, 8-bit cache write, read and sparse attention, prefix attention.  The records cost a few microseconds per call and add no ordering beyond the
+ * backward, 8-bit cache write, read and sparse attention, prefix attention, paged cache
+ * write, attention, weights and eviction.  The records cost a few microseconds per call and add no ordering beyond the
  * stream's own.  Events are recorded on the device current at the call.
  * pisa_phase_timing(1) enables recording and clears the current device's totals; (0) disables
  * it (the totals are kept).  Returns PISA_ERR_CUDA if resolving earlier records failed.
