@@ -277,6 +277,14 @@ __device__ __forceinline__ int page_of(const int32_t* table, int P, int entry, u
 constexpr int PAGED_TC_ROWS = 256;
 cudaError_t launch_paged_tc(const PagedParams& p, int d, cudaStream_t s);
 
+// A finished row: the factor of its output sums, and its log-sum-exp.
+__device__ __forceinline__ float finish_row(float m, float l, float& lse) {
+  lse = l == 0.f ? NEG_INF : (m + log2f(l)) * LN2;
+  return l == 0.f ? 0.f : 1.f / l;
+}
+
+// A map over the query rows of one KV head's group: boxes of 128, (64 columns, G_Q heads, 1 KV head, 128 / G_Q tokens).
+bool encode_token_map(CUtensorMap* map, const uint16_t* q, int d, int GQ, int H_kv, int R, long long q_stride);
 // A map over pages [P][H_kv][S][d]: boxes of `keys` rows of 64 columns.
 bool encode_page_map(CUtensorMap* map, const void* base, int d, int S, int H_kv, int P, int keys);
 

@@ -21,16 +21,17 @@ bool encode_page_map(CUtensorMap* map, const void* base, int d, int S, int H_kv,
   return encode_tensor_map(map, base, 4, dims, strides, box);
 }
 
+bool encode_token_map(CUtensorMap* map, const uint16_t* q, int d, int GQ, int H_kv, int R, long long q_stride) {
+  const uint64_t dims[4] = {(uint64_t)d, (uint64_t)GQ, (uint64_t)H_kv, (uint64_t)R};
+  const uint64_t strides[3] = {(uint64_t)d * 2, (uint64_t)GQ * d * 2, (uint64_t)q_stride * 2};
+  const uint32_t box[4] = {64, (uint32_t)GQ, 1, (uint32_t)(128 / GQ)};
+  return encode_tensor_map(map, q, 4, dims, strides, box);
+}
+
 namespace {
 
 constexpr int THREADS = 128;
 constexpr int few_blocks(int rows) { return rows > 8 ? 2 : 4; }  // a SM
-
-// A finished row: the factor of its output sums, and its log-sum-exp.
-__device__ __forceinline__ float finish_row(float m, float l, float& lse) {
-  lse = l == 0.f ? NEG_INF : (m + log2f(l)) * LN2;
-  return l == 0.f ? 0.f : 1.f / l;
-}
 
 // Tiles of 8 NH rows.  A block's four warps take the granules of a segment in turn, each with a ring of its own that
 // it fills by TMA.  A granule lies in one page (KEYS <= S).
@@ -284,7 +285,7 @@ struct Plan {
 Plan paged_plan(const Problem& p, const Pages& pg) {
   const long long rows = ((long long)p.N * p.GQ + p.B - 1) / (p.B > 0 ? p.B : 1);  // a sequence has on average
   const int few = rows > 8 || p.GQ > 8 ? 16 : 8;
-  Plan plan{false, few, few_blocks(few) * MAX_SMS, 2};
+  Plan plan = rows > 16 ? Plan{true, PAGED_TC_ROWS, MAX_SMS, 3} : Plan{false, few, few_blocks(few) * MAX_SMS, 2};
   // no more blocks (and scratch) than there can be steps: every sequence has at most one tile that is not full
   const long long tiles = (long long)p.N * p.GQ / plan.rows + p.B;
   const long long steps = (((long long)pg.M << pg.s_bits) + PAGED_KT - 1) / PAGED_KT;
@@ -364,7 +365,9 @@ cudaError_t launch_paged_attn(const uint16_t* q, long long q_stride, const uint1
   at += up256(parts * 8);
   p.base = reinterpret_cast<long long*>(at);
   cudaError_t e;
-  if (pr.d == 128)
+  if (plan.tc)
+    e = launch_paged_tc(p, pr.d, s);
+  else if (pr.d == 128)
     e = launch_few_rows<128, 16>(p, s);
   else
     e = pg.s_bits > 4 ? launch_few_rows<64, 32>(p, s) : launch_few_rows<64, 16>(p, s);
