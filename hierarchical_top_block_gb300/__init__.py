@@ -107,7 +107,9 @@ def lib() -> ct.CDLL:
         L.pisa_paged_attn.restype = ct.c_int
         L.pisa_paged_attn.argtypes = [_P] * 9 + [ct.c_size_t, ct.c_longlong, pisa_shape, pisa_params, pisa_pages, _P]
         L.pisa_paged_weights.restype = ct.c_int
-        L.pisa_paged_weights.argtypes = [_P] * 7 + [ct.c_int, ct.c_longlong, pisa_shape, pisa_params, pisa_pages, _P]
+        L.pisa_paged_weights.argtypes = [_P] * 8 + [ct.c_size_t, ct.c_int, ct.c_longlong, pisa_shape, pisa_params, pisa_pages, _P]
+        L.pisa_paged_weights_workspace_bytes.restype = ct.c_size_t
+        L.pisa_paged_weights_workspace_bytes.argtypes = [pisa_shape, pisa_params, pisa_pages]
         L.pisa_paged_evict_workspace_bytes.restype = ct.c_size_t
         L.pisa_paged_evict_workspace_bytes.argtypes = [pisa_shape, pisa_pages, ct.c_int]
         L.pisa_paged_evict.restype = ct.c_int
@@ -792,8 +794,12 @@ def pisa_paged_attn(q, Kp, Vp, page_table, seq_len, row_start=None, causal: bool
     return o, (lse if want_lse else None)
 
 
+def pisa_paged_weights_workspace_bytes(shape: pisa_shape, params: pisa_params, pages: pisa_pages) -> int:
+    return int(lib().pisa_paged_weights_workspace_bytes(shape, params, pages))
+
+
 def pisa_paged_weights(q, lse, Kp, w, page_table, seq_len, row_start=None, accumulate: bool = True, causal: bool = True,
-                       scale: float = 0.0) -> None:
+                       scale: float = 0.0, ws=None) -> None:
     """Add to w [pages, H_kv, page_size] fp32 (accumulate = False: put there) the attention weight that every key of
     the sequences got from the new tokens q [R, H_q, d], summed over them and the query heads of its KV head.  lse
     [R, H_q]: pisa_paged_attn's of the same tokens, with the same causal and scale."""
@@ -807,9 +813,11 @@ def pisa_paged_weights(q, lse, Kp, w, page_table, seq_len, row_start=None, accum
     q_stride = _token_rows(q, "q", R, H_q, d, dev)
     _fits(lse, "lse", (R, H_q), torch.float32, dev)
     _fits(w, "w", Kp.shape[:3], torch.float32, dev)
+    shape, params = pisa_shape(B, R, H_q, H_kv, d, 0), pisa_params(64, 2, 1, 1 if causal else 0, float(scale), 0)
+    ws = _workspace(ws, lib().pisa_paged_weights_workspace_bytes(shape, params, pages), q.device)
     _call(lib().pisa_paged_weights, "pisa_paged_weights", dev, q.data_ptr(), lse.data_ptr(), Kp.data_ptr(), w.data_ptr(),
-          page_table.data_ptr(), seq_len.data_ptr(), _addr(row_start), 1 if accumulate else 0, q_stride,
-          pisa_shape(B, R, H_q, H_kv, d, 0), pisa_params(64, 2, 1, 1 if causal else 0, float(scale), 0), pages)
+          page_table.data_ptr(), seq_len.data_ptr(), _addr(row_start), ws.data_ptr(), ws.numel(), 1 if accumulate else 0,
+          q_stride, shape, params, pages)
 
 
 def pisa_paged_evict_workspace_bytes(shape: pisa_shape, pages: pisa_pages, keep: int) -> int:

@@ -1020,25 +1020,32 @@ pisa_status pisa_paged_attn(const uint16_t* q, const uint16_t* Kp, const uint16_
   return cuda_status(e);
 }
 
+size_t pisa_paged_weights_workspace_bytes(pisa_shape shape, pisa_params params, pisa_pages pages) {
+  Problem p;
+  Pages pg;
+  return check_paged(shape, &params, pages, &p, &pg) == PISA_OK ? paged_weights_workspace_bytes(p) : 0;
+}
+
 pisa_status pisa_paged_weights(const uint16_t* q, const float* lse, const uint16_t* Kp, float* w, const int32_t* page_table,
-                               const int32_t* seq_len, const int32_t* row_start, int accumulate, long long q_stride,
-                               pisa_shape shape, pisa_params params, pisa_pages pages, pisa_stream stream) {
+                               const int32_t* seq_len, const int32_t* row_start, void* ws, size_t ws_bytes, int accumulate,
+                               long long q_stride, pisa_shape shape, pisa_params params, pisa_pages pages, pisa_stream stream) {
   Problem p;
   Pages pg;
   pisa_status rc = check_paged(shape, &params, pages, &p, &pg);
   if (rc != PISA_OK) return rc;
   if (accumulate != 0 && accumulate != 1) return PISA_ERR_INVALID_ARG;
   if (p.B == 0 || (p.N == 0 && accumulate)) return PISA_OK;
-  if ((p.N > 0 && (!q || !lse)) || !Kp || !w || !page_table || !seq_len) return PISA_ERR_INVALID_ARG;
+  if ((p.N > 0 && (!q || !lse)) || !Kp || !w || !page_table || !seq_len || !ws) return PISA_ERR_INVALID_ARG;
   if (!row_start && p.N % p.B != 0) return PISA_ERR_INVALID_ARG;
   if (!row_stride(&q_stride, (long long)p.H_q * p.d)) return PISA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned4(lse) || !aligned16(Kp) || !aligned16(w) || !aligned4(page_table) ||
-      !aligned4(seq_len) || !aligned4(row_start))
+      !aligned4(seq_len) || !aligned4(row_start) || (reinterpret_cast<uintptr_t>(ws) & 255u))
     return PISA_ERR_INVALID_ARG;
+  if (ws_bytes < paged_weights_workspace_bytes(p)) return PISA_ERR_WORKSPACE;
   DeviceState* st;
   if ((rc = device_state(&st)) != PISA_OK) return rc;
   PhaseTimer tm(static_cast<cudaStream_t>(stream));
-  const cudaError_t e = launch_paged_weights(q, q_stride, lse, Kp, w, page_table, seq_len, row_start, accumulate != 0, p,
+  const cudaError_t e = launch_paged_weights(q, q_stride, lse, Kp, w, page_table, seq_len, row_start, accumulate != 0, ws, p,
                                              pg, st->err, static_cast<cudaStream_t>(stream));
   tm.mark(PH_PAGED_WEIGHTS);
   return cuda_status(e);

@@ -124,9 +124,10 @@ cudaError_t launch_paged_attn(const uint16_t* q, long long q_stride, const uint1
                               float* lse, void* ws, const Problem& p, const Pages& pg, int num_sms, uint32_t* err,
                               cudaStream_t s);
 // The attention weight of every key, summed over the new tokens.
+size_t paged_weights_workspace_bytes(const Problem& p);
 cudaError_t launch_paged_weights(const uint16_t* q, long long q_stride, const float* lse, const uint16_t* Kp, float* w,
                                  const int32_t* table, const int32_t* seq_len, const int32_t* row_start, bool accumulate,
-                                 const Problem& p, const Pages& pg, uint32_t* err, cudaStream_t s);
+                                 void* ws, const Problem& p, const Pages& pg, uint32_t* err, cudaStream_t s);
 // The keys of the largest weights into new pages.
 size_t paged_evict_workspace_bytes(const Problem& p, int keep);
 cudaError_t launch_paged_evict(uint16_t* Kp, uint16_t* Vp, float* w, const int32_t* table, const int32_t* seq_len,

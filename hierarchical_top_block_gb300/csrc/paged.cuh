@@ -27,6 +27,8 @@ struct PagedParams {
   const uint16_t* q;
   const uint16_t* K;
   const uint16_t* V;
+  float* w;                  // (the weights' kernels)
+  const float* lse_in;       // (the same)
   const int32_t* table;      // [B][M]
   const int32_t* seq_len;    // [B]
   const int32_t* row_start;  // [B + 1], nullable: R / B rows each
@@ -38,7 +40,7 @@ struct PagedParams {
   long long q_stride;        // elements between rows of q
   int B, R, H_q, H_kv, GQ, P, M;
   int s_bits, gq_bits, row_bits;  // S, G_Q and ROWS are 2 to these
-  int causal;
+  int causal, accumulate;
   int blocks, stop;          // thread blocks the line is cut for; steps that a second job in a block costs
   float sl2;
   uint32_t* err;
@@ -71,6 +73,20 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int b, bool&
 // a / b of numbers >= 0, in 32 bits where they fit.
 __device__ __forceinline__ long long whole_quotient(long long a, long long b) {
   return (a >> 32) || (b >> 32) ? a / b : (long long)((uint32_t)a / (uint32_t)b);
+}
+
+// The tile of a head that holds its position x < span(extra).
+template <class Jobs>
+__device__ __forceinline__ int tile_of(const Jobs& j, long long x, int extra) {
+  int lo = 0, hi = j.tiles - 1;  // the last tile that begins at or before x
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (j.before(mid) + (long long)mid * extra <= x)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo;
 }
 
 // The steps of a sequence's jobs, the same for each of its KV heads.
@@ -109,18 +125,7 @@ struct PagedJobs {
     return ((long long)q * (q - 1) >> 1 << c_bits) + (long long)q * (r + 1);
   }
   __device__ __forceinline__ long long span(int extra) const { return before(tiles) + (long long)tiles * extra; }
-  // The tile that holds position x < span(extra) of a head.
-  __device__ __forceinline__ int tile_at(long long x, int extra) const {
-    int lo = 0, hi = tiles - 1;  // the last tile that begins at or before x
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (before(mid) + (long long)mid * extra <= x)
-        lo = mid;
-      else
-        hi = mid - 1;
-    }
-    return lo;
-  }
+  __device__ __forceinline__ int tile_at(long long x, int extra) const { return tile_of(*this, x, extra); }
 };
 
 // The cut of S positions over `blocks` blocks: every block in use has one at least, so a job's parts are in
@@ -143,7 +148,8 @@ __device__ __forceinline__ PagedCut paged_cut_of(const PagedParams& p, long long
 }
 
 // Walks a block's range job by job.  Every thread of a warp holds the same state.
-struct PagedWalk {
+template <class Jobs>
+struct PagedLine {
   long long at, end;  // next position and end of the range
   long long gbase;    // first position of the current sequence
   int b;              // current sequence
@@ -172,7 +178,7 @@ struct PagedWalk {
     };
     long long S = 0, jobs = 0;
     for (int i = lane; i < p.B; i += 32) {
-      const PagedJobs j(p, seq(i));
+      const Jobs j(p, seq(i));
       jobs += (long long)p.H_kv * j.tiles;
       S += p.H_kv * j.before(j.tiles);
     }
@@ -199,7 +205,7 @@ struct PagedWalk {
     bool found = false;
     for (int i0 = 0; i0 < p.B && !(found && !record); i0 += 32) {
       const int i = i0 + lane;
-      const long long mine_all = i < p.B ? p.H_kv * PagedJobs(p, seq(i)).span(extra) : 0;
+      const long long mine_all = i < p.B ? p.H_kv * Jobs(p, seq(i)).span(extra) : 0;
       long long x = mine_all;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -223,7 +229,7 @@ struct PagedWalk {
   __device__ __forceinline__ bool next(const PagedParams& p, int block) {
     for (;;) {
       if (at >= end) return false;
-      const PagedJobs j(p, s);
+      const Jobs j(p, s);
       const long long span = j.span(extra);
       long long off = at - gbase;
       if (off >= p.H_kv * span) {  // at < end <= the line's length: a later sequence holds it
@@ -250,6 +256,42 @@ struct PagedWalk {
       return true;
     }
   }
+
+  // For the kernel that joins: moves to the job that begins in block c0 and goes on behind it, if there is one.  Its
+  // parts: slot0 of block c0, then the first slots of blocks c0 + 1 .. c1.
+  __device__ __forceinline__ bool split_job(const PagedParams& p, int c0, int& c1, int& slot0) {
+    const PagedCut cut = paged_cut(p, p.base[p.B], (int)p.base[p.B + 1]);
+    if (c0 >= cut.blocks || cut.S == 0) return false;
+    const long long last = cut.start(c0 + 1) - 1;  // the job that holds the block's last position
+    int lo = 0, hi = p.B - 1;                      // the last sequence that begins at or before it
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (p.base[mid] <= last)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    bool bad;
+    b = lo;
+    s = paged_seq(p, lo, bad);
+    const Jobs j(p, s);
+    if (j.tiles == 0) return false;
+    long long off = last - p.base[lo];
+    const long long span = j.span(cut.extra);
+    head = (int)whole_quotient(off, span);
+    off -= head * span;
+    tile = j.tile_at(off, cut.extra);
+    const long long s0 = last - off + j.before(tile) + (long long)tile * cut.extra, s1 = s0 + cut.extra;  // its first position and step
+    if (cut.block_of(s1) != c0) return false;
+    // (in range as long as nobody changes the lengths under the call)
+    c1 = min(cut.block_of(s1 + j.steps(tile) - 1), p.blocks - 1);
+    slot0 = 2 * c0 + (cut.start(c0) >= s0 ? 0 : 1);  // 1: the block had a job before
+    return c1 > c0;
+  }
+};
+
+// The attention's: jobs of query tiles.
+struct PagedWalk : PagedLine<PagedJobs> {
   // Keys that query row `row` of the tile sees.
   __device__ __forceinline__ int seen(const PagedParams& p, int row) const {
     const int tok = min(((tile << p.row_bits) + row) >> p.gq_bits, s.n - 1);
@@ -283,8 +325,8 @@ __device__ __forceinline__ float finish_row(float m, float l, float& lse) {
   return l == 0.f ? 0.f : 1.f / l;
 }
 
-// A map over the query rows of one KV head's group: boxes of 128, (64 columns, G_Q heads, 1 KV head, 128 / G_Q tokens).
-bool encode_token_map(CUtensorMap* map, const uint16_t* q, int d, int GQ, int H_kv, int R, long long q_stride);
+// A map over the query rows of one KV head's group: boxes of `rows`, (64 columns, G_Q heads, 1 KV head, rows / G_Q tokens).
+bool encode_token_map(CUtensorMap* map, const uint16_t* q, int d, int GQ, int H_kv, int R, long long q_stride, int rows);
 // A map over pages [P][H_kv][S][d]: boxes of `keys` rows of 64 columns.
 bool encode_page_map(CUtensorMap* map, const void* base, int d, int S, int H_kv, int P, int keys);
 

@@ -21,10 +21,10 @@ bool encode_page_map(CUtensorMap* map, const void* base, int d, int S, int H_kv,
   return encode_tensor_map(map, base, 4, dims, strides, box);
 }
 
-bool encode_token_map(CUtensorMap* map, const uint16_t* q, int d, int GQ, int H_kv, int R, long long q_stride) {
+bool encode_token_map(CUtensorMap* map, const uint16_t* q, int d, int GQ, int H_kv, int R, long long q_stride, int rows) {
   const uint64_t dims[4] = {(uint64_t)d, (uint64_t)GQ, (uint64_t)H_kv, (uint64_t)R};
   const uint64_t strides[3] = {(uint64_t)d * 2, (uint64_t)GQ * d * 2, (uint64_t)q_stride * 2};
-  const uint32_t box[4] = {64, (uint32_t)GQ, 1, (uint32_t)(128 / GQ)};
+  const uint32_t box[4] = {64, (uint32_t)GQ, 1, (uint32_t)(rows / GQ)};
   return encode_tensor_map(map, q, 4, dims, strides, box);
 }
 
@@ -169,35 +169,9 @@ __global__ void __launch_bounds__(THREADS, 8) paged_join_kernel(PagedParams p) {
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % WARPS, sub = (threadIdx.x >> 5) / WARPS;
   const int c0 = blockIdx.x;
   pdl_wait();
-  const PagedCut cut = paged_cut(p, p.base[p.B], (int)p.base[p.B + 1]);
-  if (c0 >= cut.blocks || cut.S == 0) return;
-  // the job that holds the last position of block c0
   PagedWalk w;
-  const long long last = cut.start(c0 + 1) - 1;
-  int lo = 0, hi = p.B - 1;  // the last sequence that begins at or before it
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (p.base[mid] <= last)
-      lo = mid;
-    else
-      hi = mid - 1;
-  }
-  bool bad;
-  w.b = lo;
-  w.s = paged_seq(p, lo, bad);
-  if (w.s.n == 0) return;
-  const PagedJobs j(p, w.s);
-  long long off = last - p.base[lo];
-  const long long span = j.span(cut.extra);
-  w.head = (int)whole_quotient(off, span);
-  off -= w.head * span;
-  w.tile = j.tile_at(off, cut.extra);
-  const long long s0 = last - off + j.before(w.tile) + (long long)w.tile * cut.extra, s1 = s0 + cut.extra;  // its first position and step
-  if (cut.block_of(s1) != c0) return;
-  // (in range as long as nobody changes the lengths under the call)
-  const int c1 = min(cut.block_of(s1 + j.steps(w.tile) - 1), p.blocks - 1);
-  if (c1 <= c0) return;
-  const int slot0 = 2 * c0 + (cut.start(c0) >= s0 ? 0 : 1);  // 1: the block had a job before
+  int c1, slot0;
+  if (!w.split_job(p, c0, c1, slot0)) return;
   const int rows = w.rows(p);
   for (int row0 = blockIdx.y * PER; row0 < rows; row0 += gridDim.y * PER) {
     const int row = min(row0 + sub, rows - 1);
@@ -331,7 +305,7 @@ cudaError_t launch_paged_attn(const uint16_t* q, long long q_stride, const uint1
                               const int32_t* table, const int32_t* seq_len, const int32_t* row_start, uint16_t* o,
                               float* lse, void* ws, const Problem& pr, const Pages& pg, int num_sms, uint32_t* err,
                               cudaStream_t s) {
-  PagedParams p;
+  PagedParams p = {};
   p.q = q;
   p.K = Kp;
   p.V = Vp;

@@ -652,7 +652,7 @@ cudaError_t launch_t(const PagedParams& p, cudaStream_t s) {
   using C = Cfg<D>;
   CUtensorMap mapQ, mapK, mapV;
   const int box = 1 << std::min(p.s_bits, 7);
-  if (!encode_token_map(&mapQ, p.q, D, p.GQ, p.H_kv, p.R, p.q_stride) ||
+  if (!encode_token_map(&mapQ, p.q, D, p.GQ, p.H_kv, p.R, p.q_stride, 128) ||
       !encode_page_map(&mapK, p.K, D, 1 << p.s_bits, p.H_kv, p.P, box) ||
       !encode_page_map(&mapV, p.V, D, 1 << p.s_bits, p.H_kv, p.P, box))
     return cudaErrorInvalidValue;

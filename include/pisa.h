@@ -404,10 +404,12 @@ PISA_API pisa_status pisa_paged_attn(const uint16_t* q, const uint16_t* Kp, cons
 /* The attention weight that every key of the sequences (the new tokens' own included) got from the new tokens,
  *   w_c = sum over the tokens t that see c and the G_Q query heads of its KV head of  exp(scale (q_t . k_c) - lse_t),
  * added to w (accumulate = 1) or put in its place (0).  lse [R][H_q] is pisa_paged_attn's; a row with lse = -inf saw
- * nothing and gives nothing.  Weights of other keys and pages are left as they are.  Exponents and sums are fp32. */
+ * nothing and gives nothing.  Weights of other keys and pages are left as they are.  Exponents and sums are fp32.  ws as
+ * for the attention, of pisa_paged_weights_workspace_bytes(). */
+PISA_API size_t pisa_paged_weights_workspace_bytes(pisa_shape shape, pisa_params params, pisa_pages pages);
 PISA_API pisa_status pisa_paged_weights(const uint16_t* q, const float* lse, const uint16_t* Kp, float* w,
                                         const int32_t* page_table, const int32_t* seq_len, const int32_t* row_start,
-                                        int accumulate, long long q_stride, pisa_shape shape, pisa_params params,
+                                        void* ws, size_t ws_bytes, int accumulate, long long q_stride, pisa_shape shape, pisa_params params,
                                         pisa_pages pages, pisa_stream stream);
 
 /* Cuts every sequence down to `keep` keys, for each KV head by itself: the first `sinks` and the last `recent` of its

@@ -11,7 +11,7 @@ A = 0x1000  # an aligned address that nothing reads: every call made with it is 
 
 # tensors, which of them may be NULL, whether parameters follow
 CALLS = {"pisa_paged_write": (8, {4, 7}, False), "pisa_paged_attn": (9, {5, 7}, True),
-         "pisa_paged_weights": (7, {6}, True), "pisa_paged_evict": (9, {7, 8}, False)}
+         "pisa_paged_weights": (8, {6}, True), "pisa_paged_evict": (9, {7, 8}, False)}
 
 
 def shape(**kw):
@@ -34,7 +34,7 @@ def call(name, null=(), odd=(), ws_bytes=1 << 40, s=None, p=None, pages=(10, 16,
     elif name == "pisa_paged_attn":
         a += [ws_bytes] + (extra or [0])
     elif name == "pisa_paged_weights":
-        a += extra or [1, 0]
+        a += [ws_bytes] + (extra or [1, 0])
     else:
         a += [ws_bytes] + (extra or [8, 1, 2, 1])
     a += [s] + ([p] if CALLS[name][2] else []) + [pisa.pisa_pages(*pages), None]
@@ -110,6 +110,10 @@ def test_scratch():
     assert call("pisa_paged_attn", ws_bytes=need - 1) == WORKSPACE
     assert pisa.pisa_paged_attn_workspace_bytes(shape(d=96), par(), pages) == 0
     assert pisa.pisa_paged_attn_workspace_bytes(shape(B=0), par(), pages) == 0
+    need = pisa.pisa_paged_weights_workspace_bytes(shape(), par(), pages)
+    assert need > 0
+    assert call("pisa_paged_weights", ws_bytes=need - 1) == WORKSPACE
+    assert pisa.pisa_paged_weights_workspace_bytes(shape(d=96), par(), pages) == 0
     need = pisa.pisa_paged_evict_workspace_bytes(shape(), pages, 8)
     assert need >= 2 * 8 * 4
     assert call("pisa_paged_evict", null={7}, ws_bytes=need - 1) == WORKSPACE
