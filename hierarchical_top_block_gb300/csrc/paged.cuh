@@ -152,8 +152,9 @@ template <class Jobs>
 struct PagedLine {
   long long at, end;  // next position and end of the range
   long long gbase;    // first position of the current sequence
+  long long job_end;  // the position behind the current job
   int b;              // current sequence
-  int extra;          // empty steps before a job's own
+  short extra;        // empty steps before a job's own
   bool begun;         // a segment of the range is behind
   PagedSeq s;
   // current segment
@@ -166,6 +167,7 @@ struct PagedLine {
     begun = false;
     b = 0;
     gbase = 0;
+    job_end = -1;
     bool bad = false, any_bad = false;
     const PagedSeq mine = paged_seq(p, min(lane, p.B - 1), bad);
     any_bad = bad;
@@ -189,7 +191,7 @@ struct PagedLine {
     }
     if (record && any_bad) report_error(p.err, ERR_BAD_INDEX);
     const PagedCut cut = paged_cut_of(p, S, jobs);
-    extra = cut.extra;
+    extra = (short)cut.extra;
     at = end = 0;
     if (block < cut.blocks) {
       at = cut.start(block);
@@ -230,19 +232,29 @@ struct PagedLine {
     for (;;) {
       if (at >= end) return false;
       const Jobs j(p, s);
-      const long long span = j.span(extra);
-      long long off = at - gbase;
-      if (off >= p.H_kv * span) {  // at < end <= the line's length: a later sequence holds it
-        gbase += p.H_kv * span;
-        if (++b >= p.B) return false;  // (unless somebody changes the lengths under the call)
-        bool bad;
-        s = paged_seq(p, b, bad);
-        continue;
+      long long off;  // in the job
+      if (at == job_end && tile + 1 < j.tiles) {  // the head's next
+        ++tile;
+        off = 0;
+        job_end += extra + j.steps(tile);
+      } else if (at >= job_end) {
+        const long long span = j.span(extra);
+        off = at - gbase;
+        if (off >= p.H_kv * span) {  // at < end <= the line's length: a later sequence holds it
+          gbase += p.H_kv * span;
+          if (++b >= p.B) return false;  // (unless somebody changes the lengths under the call)
+          bool bad;
+          s = paged_seq(p, b, bad);
+          continue;
+        }
+        head = (int)whole_quotient(off, span);
+        off -= head * span;
+        tile = j.tile_at(off, extra);
+        off -= j.before(tile) + (long long)tile * extra;
+        job_end = at - off + extra + j.steps(tile);
+      } else {
+        off = extra;  // behind the job's empty steps
       }
-      head = (int)whole_quotient(off, span);
-      off -= head * span;
-      tile = j.tile_at(off, extra);
-      off -= j.before(tile) + (long long)tile * extra;
       if (off < extra) {  // the empty steps
         at = min(end, at + extra - off);
         continue;

@@ -12,7 +12,7 @@
 // steps form one line that is cut into equal ranges, as the attention's (paged.cuh); of a job that spans blocks each
 // stores its sums, and a second kernel adds them in order.  Results are the same in every run.
 //
-// Roles: eight epilogue warps (a warpgroup a half of the keys), a producer (TMA: K by pages, Q), a warp that issues the
+// Roles: epilogue warps, a producer (TMA: K by pages, Q), a warp that issues the
 // MMAs, a warp that puts the rows' log-sum-exps into shared memory.  TMEM: two stages of two halves of 128 columns.
 // Every wait is bounded.
 #include <algorithm>
@@ -25,8 +25,9 @@ namespace pisa {
 namespace {
 
 constexpr int KEYS = 256;                   // a job
-constexpr int THREADS = 352, PRODUCER = 8, ISSUER = 9;  // warps
-constexpr int K_SLOTS = 2, L_SLOTS = 4;
+// Epilogue warps: sixteen, a warpgroup a stage and half of the keys, or for few rows eight, a warpgroup a half.
+constexpr int epilogue_warps(int nq) { return nq > 16 ? 16 : 8; }
+constexpr int K_SLOTS = 2, L_SLOTS = 3;
 
 // Jobs of key tiles: tile i has the keys 256 i .., and begins with the first tile of query rows that sees one of them.
 // p.row_bits: rows of a query tile.
@@ -63,13 +64,16 @@ template <int D, int NQ>
 struct Cfg {
   static constexpr uint32_t K_BYTES = KEYS * D * 2, Q_BYTES = NQ * D * 2;
   static constexpr int Q_SLOTS = 3;
+  static constexpr int EPILOGUE = epilogue_warps(NQ), PRODUCER = EPILOGUE, ISSUER = EPILOGUE + 1;  // warps
+  static constexpr int THREADS = 32 * (EPILOGUE + 3);
   static constexpr size_t TILES = K_SLOTS * K_BYTES + Q_SLOTS * Q_BYTES;
 };
 
 struct Shared {
   uint64_t k_full[K_SLOTS], k_empty[K_SLOTS], q_full[3], q_empty[3];
-  uint64_t l_full[L_SLOTS], l_empty[L_SLOTS], s_full[2][2], s_empty[2][2], drain;
+  uint64_t l_full[L_SLOTS], l_empty[L_SLOTS], s_full[2][2], s_empty[2][2], x_full[2], x_empty[2], drain;
   __align__(16) float neg[L_SLOTS][128];  // -lse log2 e of a tile's rows
+  float sum[2][128];                      // of the second stage's warps, for the first's
   uint32_t tmem;
 };
 
@@ -81,6 +85,9 @@ __device__ __forceinline__ void put_weight(const PagedParams& p, const KeyWalk& 
   float* at = p.w + (((size_t)page * p.H_kv + w.head) << p.s_bits) + (c & ((1 << p.s_bits) - 1));
   *at = p.accumulate ? *at + sum : sum;
 }
+
+__device__ __forceinline__ void load_columns(uint32_t at, uint32_t (&x)[32]) { tmem_ld32(at, x); }
+__device__ __forceinline__ void load_columns(uint32_t at, uint32_t (&x)[16]) { tmem_ld16(at, x); }
 
 // Adds COLS columns of x (from column c on of the tile) with the rows' terms at `neg`; MASK: columns lo .. hi - 1 alone.
 template <int COLS, bool MASK>
@@ -104,7 +111,7 @@ __device__ __forceinline__ void add_columns(const uint32_t (&x)[COLS], const flo
 }
 
 template <int D, int NQ>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
     paged_weights_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapQ, PagedParams p) {
   pdl_trigger();
   using C = Cfg<D, NQ>;
@@ -115,7 +122,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   Shared& sh = *reinterpret_cast<Shared*>(smem + C::TILES);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint32_t* err = p.err;
-  if (warp == PRODUCER) {
+  if (warp == C::PRODUCER) {
     if (lane == 0) {
       prefetch_map(&mapK);
       prefetch_map(&mapQ);
@@ -129,18 +136,22 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       for (int i = 0; i < L_SLOTS; ++i) {
         mbar_init(&sh.l_full[i], 1);
-        mbar_init(&sh.l_empty[i], 8);
+        mbar_init(&sh.l_empty[i], 8);  // (two warpgroups use a tile's)
       }
       for (int i = 0; i < 2; ++i)
         for (int g = 0; g < 2; ++g) {
           mbar_init(&sh.s_full[i][g], 1);
           mbar_init(&sh.s_empty[i][g], 4);
         }
+      for (int g = 0; g < 2; ++g) {
+        mbar_init(&sh.x_full[g], 4);
+        mbar_init(&sh.x_empty[g], 4);
+      }
       mbar_init(&sh.drain, 1);
       mbar_fence_init();
     }
     __syncwarp();
-  } else if (warp == ISSUER) {
+  } else if (warp == C::ISSUER) {
     tmem_alloc(&sh.tmem, 512);
     tmem_relinquish();
   }
@@ -153,9 +164,9 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint32_t nt = 0, jobs = 0;  // steps and jobs so far
   bool failed = false;
 
-  if (warp < 8) {
+  if (warp < C::EPILOGUE) {
     // ------------------------------ epilogue ------------------------------
-    const int half = warp >> 2, key = 128 * half + (warp & 3) * 32 + lane;
+    const int half = (warp >> 2) & 1, mine = warp >> 3, key = 128 * half + (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const unsigned long long sl2 = pack_f32x2(p.sl2, p.sl2);
     while (!failed && w.next(p, blockIdx.x)) {
@@ -163,6 +174,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int c = w.tile * KEYS + key, t0 = j.first(w.tile) + w.k0;
       float total = 0.f;
       for (int t = w.k0; t < w.k1; ++t, ++nt) {
+        if (C::EPILOGUE == 16 && (int)(nt & 1) != mine) continue;
         const int m0 = (t0 + t - w.k0) * NQ, hi = (w.s.n << p.gq_bits) - m0;  // rows in use: those before hi
         const int lo = p.causal ? ((c - w.s.L) << p.gq_bits) - m0 : 0;        // that see the key: from lo on
         const uint32_t st = nt & 1, ls = nt % L_SLOTS;
@@ -179,10 +191,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
         for (int cc = 0; cc < NQ; cc += COLS) {
           uint32_t x[COLS];
-          if constexpr (COLS == 32)
-            tmem_ld32(at + cc, x);
-          else
-            tmem_ld16(at + cc, x);
+          load_columns(at + cc, x);
           tmem_wait_ld();
           if (!mask)
             add_columns<COLS, false>(x, sh.neg[ls] + cc, sl2, 0, 0, sum);
@@ -201,12 +210,27 @@ __global__ void __launch_bounds__(THREADS, 1)
         total += (a + b) + (e + f);
       }
       if (failed) break;
+      if constexpr (C::EPILOGUE == 16) {  // the two stages' sums meet
+        if (mine == 1) {
+          if (!mbar_wait_warp(&sh.x_empty[half], (jobs & 1) ^ 1, err)) break;
+          sh.sum[half][key & 127] = total;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.x_full[half]);
+          ++jobs;
+          continue;
+        }
+        if (!mbar_wait_warp(&sh.x_full[half], jobs & 1, err)) break;
+        total += sh.sum[half][key & 127];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.x_empty[half]);
+        ++jobs;
+      }
       if (w.slot < 0)
         put_weight(p, w, c, total);
       else
         p.part_o[(size_t)w.slot * KEYS + key] = total;
     }
-  } else if (warp == PRODUCER) {
+  } else if (warp == C::PRODUCER) {
     // ------------------------------ producer ------------------------------
     const int box_bits = min(p.s_bits, 7);
     const int piece = lane & (DH - 1), box = lane / DH;  // this lane's copy of a K tile (256 keys: at most 16 copies)
@@ -248,7 +272,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         mbar_wait(&sh.q_full[u % C::Q_SLOTS], (u / C::Q_SLOTS) & 1, err, 100000000ull);
     }
     __syncwarp();
-  } else if (warp == ISSUER) {
+  } else if (warp == C::ISSUER) {
     // ------------------------------ MMAs ------------------------------
     constexpr uint32_t id = idesc_bf16_f32(128, NQ);
     while (!failed && w.next(p, blockIdx.x)) {
@@ -291,24 +315,33 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncwarp();
   } else {
     // ------------------------------ the rows' log-sum-exps ------------------------------
+    constexpr int PER = (NQ + 31) / 32;
     while (!failed && w.next(p, blockIdx.x)) {
       const KeyJobs j(p, w.s);
       const int t0 = j.first(w.tile);
-      for (int t = w.k0; t < w.k1; ++t, ++nt) {
-        const uint32_t ls = nt % L_SLOTS;
-        float x[(NQ + 31) / 32];
+      auto read = [&](int t, float (&x)[PER]) {
 #pragma unroll
-        for (int i = 0; i < (NQ + 31) / 32; ++i) {
+        for (int i = 0; i < PER; ++i) {
           const int m = (t0 + t) * NQ + 32 * i + lane, tok = m >> p.gq_bits;
           x[i] = NEG_INF;
-          if (tok < w.s.n) x[i] = __ldg(p.lse_in + (size_t)(w.s.first + tok) * p.H_q + w.head * p.GQ + (m - (tok << p.gq_bits)));
+          if (t < w.k1 && tok < w.s.n)
+            x[i] = __ldg(p.lse_in + (size_t)(w.s.first + tok) * p.H_q + w.head * p.GQ + (m - (tok << p.gq_bits)));
         }
+      };
+      float next[PER];
+      read(w.k0, next);
+      for (int t = w.k0; t < w.k1; ++t, ++nt) {
+        const uint32_t ls = nt % L_SLOTS;
+        float x[PER];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) x[i] = next[i];
+        read(t + 1, next);
         if (!mbar_wait_warp(&sh.l_empty[ls], ((nt / L_SLOTS) & 1) ^ 1, err)) {
           failed = true;
           break;
         }
 #pragma unroll
-        for (int i = 0; i < (NQ + 31) / 32; ++i)  // a row that saw nothing gives nothing
+        for (int i = 0; i < PER; ++i)  // a row that saw nothing gives nothing
           if (32 * i + lane < NQ) sh.neg[ls][32 * i + lane] = x[i] == NEG_INF ? NEG_INF : -x[i] * LOG2E;
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.l_full[ls]);
@@ -317,7 +350,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == ISSUER) {
+  if (warp == C::ISSUER) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -349,7 +382,7 @@ cudaError_t launch_t(const PagedParams& p, cudaStream_t s) {
   static_assert(smem <= 227 * 1024, "a block's shared memory");
   const cudaError_t e = allow_shared<paged_weights_kernel<D, NQ>>(smem);
   if (e != cudaSuccess) return e;
-  paged_weights_kernel<D, NQ><<<p.blocks, THREADS, smem, s>>>(mapK, mapQ, p);
+  paged_weights_kernel<D, NQ><<<p.blocks, C::THREADS, smem, s>>>(mapK, mapQ, p);
   return cudaGetLastError();
 }
 
