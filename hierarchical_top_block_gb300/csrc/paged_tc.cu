@@ -18,10 +18,10 @@
 // the sequence's last key, are given a page number past the pool and read as zeros.  Logits are masked by row only
 // in steps that pass the last key which the warp's first row sees, and in steps with such a page.
 //
-// Roles: two softmax warpgroups; a producer warp (TMA); a warp that issues the MMAs.  TMEM: S of stream i at 128 i
-// (its first 64 columns hold P afterwards), O of stream i at 256 + 128 i.  The MMAs of one thread run in order, so a
-// stream's next S is issued right behind its O += P V, which reads P from the same columns.  Every wait is
-// bounded.
+// Roles: two softmax warpgroups; a producer warp (TMA); a warp that issues the MMAs.  TMEM: NB buffers of 128 columns
+// for S (the first 64 of one hold P afterwards), then O of both streams.  With d = 64 there is room for a third buffer,
+// so that a stream finds its next S made when it has handed over its P.  The MMAs of one thread run in order, so the next
+// S of a buffer is issued right behind the O += P V that reads P from it.  Every wait is bounded.
 #include <algorithm>
 
 #include "kernels.cuh"
@@ -38,31 +38,35 @@ constexpr int THREADS = 384, PRODUCER = 8, ISSUER = 9;  // warps
 // Registers a thread of the softmax and of the other warpgroup, of 384 x 168 at launch: the softmax holds 128 logits.
 constexpr int REGS_SOFTMAX = 208, REGS_ISSUE = 88;
 static_assert(2 * REGS_SOFTMAX + REGS_ISSUE <= 3 * 168, "registers of the block");
-constexpr int SLOTS = 5;
 
 template <int D>
 struct Cfg {
+  static constexpr int NB = D == 64 ? 3 : 2;         // buffers of S
+  static constexpr int SLOTS = D == 64 ? 9 : 5;      // K and V tiles
   static constexpr uint32_t QT_BYTES = 128 * D * 2;  // 128 query rows
   static constexpr uint32_t TILE = KT * D * 2;       // a K or V tile
   static constexpr size_t TILES = 2 * QT_BYTES + SLOTS * TILE;
+  static_assert(NB * 128 + 2 * D <= 512, "tensor memory");
 };
 
+template <int D>
 struct Bars {
   uint64_t q_full, q_empty;             // Q copied; no longer read
-  uint64_t full[SLOTS], empty[SLOTS];   // K and V tiles
-  uint64_t s_full[2], p_full[2], o_done[2];
+  uint64_t full[Cfg<D>::SLOTS], empty[Cfg<D>::SLOTS];  // K and V tiles
+  uint64_t s_full[Cfg<D>::NB], p_full[Cfg<D>::NB], o_done[Cfg<D>::NB];  // of a buffer of S: made, P in it, O += P V made
   uint64_t x_full, x_done;              // the streams' meeting at the end of a segment
   uint64_t drain;
 };
 
-// A softmax warp's counts so far: steps of each stream, meetings of the streams.
+// A softmax warp's counts so far: products, meetings of the streams.
 struct Counts {
-  uint32_t it[2], meets;
+  uint32_t made, meets;
 };
 
 // What follows the tiles in shared memory.
+template <int D>
 struct Shared {
-  Bars bar;
+  Bars<D> bar;
   float2 ml[2][128];      // the streams' maxima and sums, when they meet
   PagedWalk walks[10];    // each warp's walk: registers are wanted elsewhere
   Counts counts[8];
@@ -99,19 +103,24 @@ __device__ __forceinline__ void set_regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
 
-// A segment's streams: by rows (`lag` 1: both use every tile) or by steps (`lag` 2: stream = step mod 2).  The tiles'
-// order is that of their use: K 0 .. lag - 1, then V j and K j + lag.
+// A segment's streams: by rows (`lag` 1: both use every tile) or by steps (`lag` 2: stream = step mod 2).  Its products
+// are numbered in the order in which they are made, streams in turn: product u is of stream u mod 2 and step u / 2 (by
+// rows) or u (by steps), and S of u lies in buffer (products before the segment + u) mod NB.  S of u + NB is issued right
+// behind the O += P V of u, which reads P from the same buffer.  So the tiles are wanted in this order: K of the first
+// `head` steps, then V j and K j + head.
 struct Segment {
-  int rows, nk, lag;
-  __device__ __forceinline__ Segment(const PagedParams& p, const PagedWalk& w) {
+  int rows, nk, lag, head;
+  __device__ __forceinline__ Segment(const PagedParams& p, const PagedWalk& w, int buffers) {
     rows = w.rows(p);
     nk = w.k1 - w.k0;
     lag = rows > ROWS / 2 ? 1 : 2;
+    head = min(lag == 1 ? (buffers + 1) / 2 : buffers, nk);
   }
   __device__ __forceinline__ int tiles() const { return 2 * nk; }
+  __device__ __forceinline__ int products() const { return lag == 1 ? 2 * nk : nk; }
   // Tile i of the order: returns its step, and whether it is a V.
   __device__ __forceinline__ int tile(int i, bool& is_v) const {
-    const int head = min(lag, nk), both = 2 * (nk - head);
+    const int both = 2 * (nk - head);
     if (i < head) {
       is_v = false;
       return i;
@@ -180,8 +189,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sQ = smem;
   uint8_t* sT = sQ + 2 * C::QT_BYTES;
-  Shared& sh = *reinterpret_cast<Shared*>(smem + C::TILES);
-  Bars& bar = sh.bar;
+  Shared<D>& sh = *reinterpret_cast<Shared<D>*>(smem + C::TILES);
+  Bars<D>& bar = sh.bar;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int block = blockIdx.x;
   uint32_t* err = p.err;
@@ -196,11 +205,11 @@ __global__ void __launch_bounds__(THREADS, 1)
       prefetch_map(&mapV);
       mbar_init(&bar.q_full, 1);
       mbar_init(&bar.q_empty, 1);
-      for (int i = 0; i < SLOTS; ++i) {
+      for (int i = 0; i < C::SLOTS; ++i) {
         mbar_init(&bar.full[i], 1);
         mbar_init(&bar.empty[i], 1);
       }
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < C::NB; ++i) {
         mbar_init(&bar.s_full[i], 1);
         mbar_init(&bar.p_full[i], 4);
         mbar_init(&bar.o_done[i], 1);
@@ -232,7 +241,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int h = warp >> 2;                                 // stream
     const int q = lane & 3;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t s_tmem = tmem + lanes + 128 * h, o_tmem = tmem + lanes + 256 + 128 * h;
+    const uint32_t o_tmem = tmem + lanes + 128 * C::NB + D * h;
     Walk walk;
     walk.start(first, &sh.walks[warp]);
     Counts& count = sh.counts[warp];
@@ -241,7 +250,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     bool failed = false;
     for (bool more_work = any_work; !failed && more_work; more_work = walk.next(p, block)) {
       const PagedWalk& w = walk.now();
-      const Segment sg(p, w);
+      const Segment sg(p, w, C::NB);
       const int warp_row = (sg.lag == 1 ? 128 * h : 0) + (warp & 3) * 32;  // the warp's first row in the tile
       const int row0 = warp_row + (lane >> 2);                             // the first of the lane's four, 8 apart
       const bool any = warp_row < sg.rows;
@@ -260,14 +269,19 @@ __global__ void __launch_bounds__(THREADS, 1)
         l2[i] = pack_f32x2(0.f, 0.f);
       }
       const unsigned long long sl2 = pack_f32x2(p.sl2, p.sl2);
-      uint32_t n = count.it[h];
+      const uint32_t made = count.made;  // products before the segment
+      uint32_t u = made + h;
+      // O += P V of product v has been made.  (A wait may not be two phases ahead of its barrier.  The one before it in
+      // v's buffer, of product v - NB, is known to be done: S of v was issued behind it.)
+      auto o_done = [&](uint32_t v) { return mbar_wait_warp(&bar.o_done[v % C::NB], (v / C::NB) & 1, err); };
       bool begun = false;  // O holds sums of this segment
       bool gone = look(sg.lag == 1 ? 0 : h);
-      for (int j = sg.lag == 1 ? 0 : h; j < sg.nk; j += sg.lag, ++n) {
+      for (int j = sg.lag == 1 ? 0 : h; j < sg.nk; j += sg.lag, u += 2) {
+        const uint32_t buf = u % C::NB, s_tmem = tmem + lanes + 128 * buf;
         const int key0 = (w.k0 + j) * KT;
         const unsigned none = __ballot_sync(0xffffffffu, gone);
         gone = look(j + sg.lag);
-        if (!mbar_wait_warp(&bar.s_full[h], n & 1, err)) {
+        if (!mbar_wait_warp(&bar.s_full[buf], (u / C::NB) & 1, err)) {
           failed = true;
           break;
         }
@@ -327,7 +341,7 @@ __global__ void __launch_bounds__(THREADS, 1)
               l2[i] = mul_f32x2(l2[i], pack_f32x2(f[i], f[i]));
             }
             if (begun) {
-              if (!mbar_wait_warp(&bar.o_done[h], (n - 1) & 1, err)) {
+              if (!o_done(u - 2)) {
                 failed = true;
                 break;
               }
@@ -375,14 +389,13 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.p_full[h]);
+        if (lane == 0) mbar_arrive(&bar.p_full[buf]);
         begun = true;
       }
-      // the streams' steps of this segment
-      const uint32_t n0 = sg.lag == 1 ? sg.nk : (sg.nk + 1) / 2, n1 = sg.lag == 1 ? sg.nk : sg.nk / 2;
-      const uint32_t it[2] = {count.it[0] + n0, count.it[1] + n1}, meets = count.meets;
+      const uint32_t all = sg.products(), meets = count.meets;
+      const bool both = all > 1;  // the second stream has steps
       __syncwarp();
-      if (lane == 0) count = Counts{{it[0], it[1]}, meets + (sg.lag == 1 ? 0 : 1)};
+      if (lane == 0) count = Counts{made + all, meets + (sg.lag == 1 ? 0 : 1)};
       __syncwarp();
       if (failed) break;
       float l[4];
@@ -395,7 +408,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         l[i] = a + __shfl_xor_sync(0xffffffffu, a, 2);
       }
       if (sg.lag == 1) {
-        if (!mbar_wait_warp(&bar.o_done[h], (it[h] - 1) & 1, err)) {
+        if (!o_done(made + all - 2 + h)) {
           failed = true;
           break;
         }
@@ -425,8 +438,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int i = 0; i < 4; ++i)
           if (q == 0) sh.ml[h][row0 + 8 * i] = make_float2(m[i], l[i]);
         __syncwarp();
-        if (!mbar_wait_warp(&bar.o_done[0], (it[0] - 1) & 1, err) ||
-            (n1 > 0 && !mbar_wait_warp(&bar.o_done[1], (it[1] - 1) & 1, err))) {
+        if ((both && !o_done(made + all - 2)) || !o_done(made + all - 1)) {  // in this order: the products' own
           failed = true;
           break;
         }
@@ -450,18 +462,18 @@ __global__ void __launch_bounds__(THREADS, 1)
             const float sum = (a.x == NEG_INF ? a.y : a.y * f0[e]) + (b.x == NEG_INF ? b.y : b.y * f1[e]);
             out[e] = row_out(p, w, row, row < sg.rows, top, sum, q == 0);
           }
-          const uint32_t o0 = tmem + lanes + 256 + ((uint32_t)(16 * h) << 16);
+          const uint32_t o0 = tmem + lanes + 128 * C::NB + ((uint32_t)(16 * h) << 16);
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
             uint32_t r[16], r1[16];
             tmem_ld_16x32(o0 + c, r);
-            if (n1 > 0) tmem_ld_16x32(o0 + 128 + c, r1);
+            if (both) tmem_ld_16x32(o0 + D + c, r1);
             tmem_wait_ld();
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
               const int e = (k >> 1) & 1;
               float x = __uint_as_float(r[k]) * f0[e];
-              if (n1 > 0) x = fmaf(__uint_as_float(r1[k]), f1[e], x);
+              if (both) x = fmaf(__uint_as_float(r1[k]), f1[e], x);
               r[k] = __float_as_uint(x);
             }
             put_columns<D>(p, w, out, c, q, r);
@@ -489,7 +501,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const bool copies = box << box_bits < KT;
       for (bool more_work = any_work; !failed && more_work; more_work = walk.next(p, block)) {
         const PagedWalk& w = walk.now();
-        const Segment sg(p, w);
+        const Segment sg(p, w, C::NB);
         if (!mbar_wait_warp(&bar.q_empty, (seg & 1) ^ 1, err)) break;
         if (lane == 0) {
           const int streams = sg.lag == 1 ? 2 : 1;
@@ -506,8 +518,8 @@ __global__ void __launch_bounds__(THREADS, 1)
           bool is_v;
           const int key = (w.k0 + sg.tile(i, is_v)) * KT + (box << box_bits);
           const int page = copies && key < total ? page_of(table, p.P, key >> p.s_bits, err) : p.P;
-          const int st = nt % SLOTS;
-          if (!mbar_wait_warp(&bar.empty[st], ((nt / SLOTS) & 1) ^ 1, err)) {
+          const int st = nt % C::SLOTS;
+          if (!mbar_wait_warp(&bar.empty[st], ((nt / C::SLOTS) & 1) ^ 1, err)) {
             failed = true;
             break;
           }
@@ -522,8 +534,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       // copies still in flight land before shared memory goes away (bounded; at once unless a wait failed)
       if (lane == 0) {
         if (seg > 0) mbar_wait(&bar.q_full, (seg - 1) & 1, err, 100000000ull);
-        for (uint32_t u = nt > SLOTS ? nt - SLOTS : 0; u < nt; ++u)
-          mbar_wait(&bar.full[u % SLOTS], (u / SLOTS) & 1, err, 100000000ull);
+        for (uint32_t u = nt > C::SLOTS ? nt - C::SLOTS : 0; u < nt; ++u)
+          mbar_wait(&bar.full[u % C::SLOTS], (u / C::SLOTS) & 1, err, 100000000ull);
       }
       __syncwarp();
     } else if (warp == ISSUER) {
@@ -532,14 +544,16 @@ __global__ void __launch_bounds__(THREADS, 1)
       constexpr uint32_t id_pv = idesc_bf16_f32(128, D) | (1u << 16);  // V: d contiguous, N-major
       Walk walk;
       walk.start(first, &sh.walks[9]);
-      uint32_t nt = 0, seg = 0, it[2] = {0, 0};
+      uint32_t nt = 0, seg = 0, made = 0;  // tiles, segments, products so far
       bool failed = false;
-      // tile n is here (v_valid: a V tile's keys in use)
-      auto tile_here = [&](uint32_t n, int v_valid) {
-        if (!mbar_wait_warp(&bar.full[n % SLOTS], (n / SLOTS) & 1, err)) return false;
+      // the next tile is here (v_valid: a V tile's keys in use); its slot
+      auto tile_here = [&](uint32_t& slot, int v_valid) {
+        slot = nt % C::SLOTS;
+        if (!mbar_wait_warp(&bar.full[slot], (nt / C::SLOTS) & 1, err)) return false;
+        ++nt;
         if (v_valid < KT) {
           // values past the sequence's end are multiplied by weights of 0: they have to be finite
-          uint8_t* t = sT + (n % SLOTS) * C::TILE;
+          uint8_t* t = sT + slot * C::TILE;
           for (int c = 0; c < DH; ++c)
             for (int i = max(0, v_valid) * 8 + lane; i < KT * 8; i += 32)
               *reinterpret_cast<uint4*>(t + c * (KT * 128) + i * 16) = make_uint4(0, 0, 0, 0);
@@ -554,84 +568,57 @@ __global__ void __launch_bounds__(THREADS, 1)
       const uint32_t k_hi = (uint32_t)(k_desc >> 32), q_lo = (uint32_t)smem_desc_sw128(smem_u32(sQ), 16, 1024);
       const uint32_t k_lo = (uint32_t)k_desc, v_lo = (uint32_t)smem_desc_sw128(smem_u32(sT), KT * 128, 1024);
       auto desc = [&](uint32_t lo) { return pack_u32x2(lo, k_hi); };  // (8-row groups of 1024 bytes in all of them)
-      auto qk = [&](int h, int qs, uint32_t n) {  // S of stream h = Q (slot qs) K^T
-        const uint32_t a = q_lo + qs * (C::QT_BYTES >> 4), b = k_lo + (n % SLOTS) * (C::TILE >> 4), d = tmem + 128 * h;
+      auto qk = [&](uint32_t buf, int qs, uint32_t slot) {  // S of a buffer = Q (slot qs) K^T
+        const uint32_t a = q_lo + qs * (C::QT_BYTES >> 4), b = k_lo + slot * (C::TILE >> 4), d = tmem + 128 * buf;
 #pragma unroll
         for (int s = 0; s < D / 16; ++s)
           umma_bf16(d, desc(a + (((s >> 2) * (128 * 128) + (s & 3) * 32) >> 4)),
                     desc(b + (((s >> 2) * (KT * 128) + (s & 3) * 32) >> 4)), id_qk, s > 0 ? 1u : 0u);
-        umma_commit(&bar.s_full[h]);
+        umma_commit(&bar.s_full[buf]);
       };
-      auto pv = [&](int h, uint32_t n, bool first) {  // O of stream h (+)= P V
-        const uint32_t b = v_lo + (n % SLOTS) * (C::TILE >> 4), d = tmem + 256 + 128 * h, a = tmem + 128 * h;
+      auto pv = [&](uint32_t buf, int h, uint32_t slot, bool first) {  // O of stream h (+)= P V
+        const uint32_t b = v_lo + slot * (C::TILE >> 4), d = tmem + 128 * C::NB + D * h, a = tmem + 128 * buf;
 #pragma unroll
         for (int s = 0; s < KT / 16; ++s)
           umma_bf16_ts(d, a + 8 * s, desc(b + ((s * 16 * 128) >> 4)), id_pv, s > 0 ? 1u : first ? 0u : 1u);
-        umma_commit(&bar.o_done[h]);
+        umma_commit(&bar.o_done[buf]);
       };
       for (bool more_work = any_work; !failed && more_work; more_work = walk.next(p, block)) {
         const PagedWalk& w = walk.now();
-        const Segment sg(p, w);
+        const Segment sg(p, w, C::NB);
         const int end = w.s.L + w.s.n - w.k0 * KT;  // the sequence's end, from the segment's first key
         if (!mbar_wait_warp(&bar.q_full, seg & 1, err)) break;
         ++seg;
-        const int head = min(sg.lag, sg.nk);
-        for (int j = 0; j < head && !failed; ++j, ++nt) {
-          if (!tile_here(nt, KT)) {
+        const int all = sg.products();
+        const bool by_rows = sg.lag == 1;
+        uint32_t ks = 0, vs = 0;  // slots of the K and V tiles in use
+        auto score = [&](int u) {  // product u's S
+          if ((!by_rows || (u & 1) == 0) && !tile_here(ks, KT)) return false;
+          tc_fence_after();
+          if (elect_one()) {
+            qk((made + u) % C::NB, by_rows ? u & 1 : 0, ks);
+            if (!by_rows || (u & 1)) umma_commit(&bar.empty[ks]);
+            if (u == all - 1) umma_commit(&bar.q_empty);
+          }
+          __syncwarp();
+          return true;
+        };
+        for (int u = 0; u < min(C::NB, all) && !failed; ++u) failed = !score(u);
+        for (int u = 0; u < all && !failed; ++u) {
+          const int h = u & 1, j = by_rows ? u >> 1 : u;
+          if (((!by_rows || h == 0) && !tile_here(vs, end - j * KT)) || !mbar_wait_warp(&bar.p_full[(made + u) % C::NB], ((made + u) / C::NB) & 1, err)) {
             failed = true;
             break;
           }
           tc_fence_after();
           if (elect_one()) {
-            if (sg.lag == 1) {
-              qk(0, 0, nt);
-              qk(1, 1, nt);
-            } else {
-              qk(j, 0, nt);
-            }
-            umma_commit(&bar.empty[nt % SLOTS]);
-            if (j == sg.nk - 1) umma_commit(&bar.q_empty);
+            pv((made + u) % C::NB, h, vs, u < 2);
+            if (!by_rows || h == 1) umma_commit(&bar.empty[vs]);
           }
           __syncwarp();
+          if (u + C::NB < all) failed = !score(u + C::NB);
         }
-        for (int j = 0; j < sg.nk && !failed; ++j) {
-          const uint32_t nv = nt++;
-          const bool more = j + sg.lag < sg.nk;
-          const uint32_t nn = more ? nt++ : 0;
-          if (!tile_here(nv, end - j * KT)) {
-            failed = true;
-            break;
-          }
-          const int h0 = sg.lag == 1 ? 0 : j & 1, h1 = sg.lag == 1 ? 1 : h0;
-          for (int h = h0; h <= h1; ++h) {
-            if (!mbar_wait_warp(&bar.p_full[h], it[h] & 1, err)) {
-              failed = true;
-              break;
-            }
-            ++it[h];
-            tc_fence_after();
-            if (elect_one()) {
-              pv(h, nv, j < sg.lag);
-              if (h == h1) umma_commit(&bar.empty[nv % SLOTS]);
-            }
-            __syncwarp();
-            if (more) {
-              if (h == h0 && !tile_here(nn, KT)) {
-                failed = true;
-                break;
-              }
-              tc_fence_after();
-              if (elect_one()) {
-                qk(h, sg.lag == 1 ? h : 0, nn);
-                if (h == h1) {
-                  umma_commit(&bar.empty[nn % SLOTS]);
-                  if (j + sg.lag == sg.nk - 1) umma_commit(&bar.q_empty);
-                }
-              }
-              __syncwarp();
-            }
-          }
-        }
+        made += all;
       }
       if (elect_one()) {  // every MMA issued has completed before the tensor memory is released (bounded)
         umma_commit(&bar.drain);
@@ -656,7 +643,7 @@ cudaError_t launch_t(const PagedParams& p, cudaStream_t s) {
       !encode_page_map(&mapK, p.K, D, 1 << p.s_bits, p.H_kv, p.P, box) ||
       !encode_page_map(&mapV, p.V, D, 1 << p.s_bits, p.H_kv, p.P, box))
     return cudaErrorInvalidValue;
-  constexpr size_t smem = C::TILES + sizeof(Shared);
+  constexpr size_t smem = C::TILES + sizeof(Shared<D>);
   static_assert(smem <= 227 * 1024, "a block's shared memory");
   const cudaError_t e = allow_shared<paged_tc_kernel<D>>(smem);
   if (e != cudaSuccess) return e;

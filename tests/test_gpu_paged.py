@@ -114,6 +114,26 @@ def test_attn_many_sequences():
     no_error()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new", [5, 30, 40])
+def test_attn_waits_for_memory(d, new):
+    """Many keys for few rows: the softmax runs ahead of the tiles.  Checked by attending in two halves of the heads."""
+    B, H_kv, G, S = 48, 4, 8, 16
+    c = Paged([1500 + 37 * b for b in range(B)], [new] * B, H_kv, d, S, seed=new)
+    q = c.rand(c.R, H_kv * G, d, scale=1.5)
+    o, lse = pisa.pisa_paged_attn(q, c.K, c.V, c.table, c.len, row_start=c.rows)
+    no_error()
+    for h in range(H_kv):
+        heads = slice(h * G, (h + 1) * G)
+        o1, lse1 = pisa.pisa_paged_attn(q[:, heads].contiguous(), c.K[:, h:h + 1].contiguous(), c.V[:, h:h + 1].contiguous(),
+                                        c.table, c.len, row_start=c.rows)
+        # twice attend64's bounds, with sum w |v| <= max |v| < 6 and |q| . |k| <= |q| |k| < 3 sqrt(d) 2 sqrt(d)
+        e = (d + 8) * R.F * 6 * math.sqrt(d)
+        assert (o[:, heads].float() - o1.float()).abs().max() <= 2 * ((R.U + 4 * e + 2.0 ** -16) * 6 + R.U * 6)
+        assert (lse[:, heads] - lse1).abs().max() <= 2 * (2 * e + 2.0 ** -18 + 2.0 ** -22 * 16)
+    no_error()
+
+
 def test_attn_strided_rows_and_scale():
     c = Paged([100, 40], [3, 70], 2, 128, 32)
     fused = c.rand(c.R, 12, 128)
