@@ -4,10 +4,12 @@
 //   S = Q K^T (fp32 in tensor memory), P = 2^(S scale log2 e - m) as bf16 back into tensor memory over S,
 //   O += P V in tensor memory, l = sum of the unrounded P
 //
-// m is a row's reference, not its running maximum: it is raised, and O multiplied by 2^(old - new), only when the
-// maximum has grown by more than 2^8 past it (P stays below 2^8, and the division by l at the end is exact
-// whatever m is).  With the usual logits that happens in a job's first steps alone.  P is rounded to bf16, 2^-9 of
-// each weight, the size of the output's own rounding.
+// m is a row's reference, not its running maximum: a segment's first step sets it to the step's maximum, and later ones
+// take it as it is.  Only where a lane's sum of a step's weights (32 keys of a row) passes 2^8 are the maxima found, the
+// reference raised to them, O multiplied by 2^(old - new) and the step's weights made again: P and the sums stay far
+// from the end of their ranges, and the division by l at the end is exact whatever m is.  With the usual logits that
+// hardly happens, so most steps look for no maximum at all (with one a step: 4096 tokens after 28672 of 32 / 8 heads
+// 1550 us).  P is rounded to bf16, 2^-9 of each weight, the size of the output's own rounding.
 //
 // Two streams keep the tensor pipe busy while the softmax of the other one runs, a warpgroup for each.  With more than
 // 128 rows a stream is a half of the rows, and both use the same tiles; with fewer, both streams have all rows, one
@@ -32,7 +34,7 @@ namespace pisa {
 namespace {
 
 constexpr int ROWS = PAGED_TC_ROWS, KT = PAGED_KT;
-constexpr float MAX_GROWTH = 8.f;  // log2 units the maximum may pass a row's reference
+constexpr float MOST = 256.f;  // a lane's sum of a row's weights in a step above which the references are raised
 
 constexpr int THREADS = 384, PRODUCER = 8, ISSUER = 9;  // warps
 // Registers a thread of the softmax and of the other warpgroup, of 384 x 168 at launch: the softmax holds 128 logits.
@@ -275,6 +277,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       // v's buffer, of product v - NB, is known to be done: S of v was issued behind it.)
       auto o_done = [&](uint32_t v) { return mbar_wait_warp(&bar.o_done[v % C::NB], (v / C::NB) & 1, err); };
       bool begun = false;  // O holds sums of this segment
+      bool blank = true;   // a row of the warp has no reference yet
       bool gone = look(sg.lag == 1 ? 0 : h);
       for (int j = sg.lag == 1 ? 0 : h; j < sg.nk; j += sg.lag, u += 2) {
         const uint32_t buf = u % C::NB, s_tmem = tmem + lanes + 128 * buf;
@@ -313,33 +316,71 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                   for (int c = 0; c < 4; ++c) s[i][4 * g + c] = __float_as_uint(NEG_INF);
           }
-          bool moved = false;
-          float top[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t* x = &s[i >> 1][2 * (i & 1)];
-            float a = NEG_INF, b = NEG_INF;
-#pragma unroll
-            for (int g = 0; g < 16; g += 2) {
-              a = fmaxf(fmaxf(a, __uint_as_float(x[4 * g])), __uint_as_float(x[4 * g + 1]));
-              b = fmaxf(fmaxf(b, __uint_as_float(x[4 * g + 4])), __uint_as_float(x[4 * g + 5]));
-            }
-            a = fmaxf(a, b);
-            a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
-            a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
-            top[i] = a * p.sl2;
-            moved = moved || top[i] > m[i] + MAX_GROWTH;
-          }
-          if (__any_sync(0xffffffffu, moved)) {
-            // the references follow the maxima; O (of the steps before) with them
-            float f[4];
+          // P against the references, and its sums
+          unsigned long long sum[4];
+          auto weights = [&] {
+            unsigned long long ref[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const float to = fmaxf(m[i], top[i]);
+              const float x = m[i] == NEG_INF ? 0.f : -m[i];
+              ref[i] = pack_f32x2(x, x);
+              sum[i] = 0ull;
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c)  // 64 keys
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                uint32_t pk[16];
+#pragma unroll
+                for (int g = 0; g < 8; ++g)
+#pragma unroll
+                  for (int e = 0; e < 2; ++e) {  // row r + 16 i + 8 e
+                    const uint32_t* x = &s[i][32 * c + 4 * g + 2 * e];
+                    float a, b;
+                    unpack_f32x2(fma_f32x2(pack_u32x2(x[0], x[1]), sl2, ref[2 * i + e]), a, b);
+                    a = fast_exp2(a);
+                    b = fast_exp2(b);
+                    sum[2 * i + e] = add_f32x2(sum[2 * i + e], pack_f32x2(a, b));
+                    pk[2 * g + e] = pack_bf16x2(a, b);
+                  }
+                tmem_st_16x32(s_tmem + ((uint32_t)(16 * i) << 16) + 32 * c, pk);
+              }
+          };
+          bool again = blank;
+          if (!again) {
+            weights();
+            bool far = false;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float a, b;
+              unpack_f32x2(sum[i], a, b);
+              far = far || a + b > MOST;
+            }
+            again = __any_sync(0xffffffffu, far);
+          }
+          if (again) {
+            // the references follow the maxima, O (of the steps before) with them
+            float f[4];
+            bool none_seen = false;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t* x = &s[i >> 1][2 * (i & 1)];
+              float a = NEG_INF, b = NEG_INF;
+#pragma unroll
+              for (int g = 0; g < 16; g += 2) {
+                a = fmaxf(fmaxf(a, __uint_as_float(x[4 * g])), __uint_as_float(x[4 * g + 1]));
+                b = fmaxf(fmaxf(b, __uint_as_float(x[4 * g + 4])), __uint_as_float(x[4 * g + 5]));
+              }
+              a = fmaxf(a, b);
+              a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
+              a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
+              const float to = fmaxf(m[i], a * p.sl2);
               f[i] = to == NEG_INF ? 1.f : fast_exp2(m[i] - to);
               m[i] = to;
+              none_seen = none_seen || to == NEG_INF;
               l2[i] = mul_f32x2(l2[i], pack_f32x2(f[i], f[i]));
             }
+            blank = __any_sync(0xffffffffu, none_seen);
             if (begun) {
               if (!o_done(u - 2)) {
                 failed = true;
@@ -359,32 +400,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                 tmem_st_16x16(at, r);
               }
             }
-          }
-          unsigned long long ref[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float x = m[i] == NEG_INF ? 0.f : -m[i];
-            ref[i] = pack_f32x2(x, x);
+            weights();
           }
 #pragma unroll
-          for (int c = 0; c < 2; ++c)  // 64 keys
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              uint32_t pk[16];
-#pragma unroll
-              for (int g = 0; g < 8; ++g)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {  // row r + 16 i + 8 e
-                  const uint32_t* x = &s[i][32 * c + 4 * g + 2 * e];
-                  float a, b;
-                  unpack_f32x2(fma_f32x2(pack_u32x2(x[0], x[1]), sl2, ref[2 * i + e]), a, b);
-                  a = fast_exp2(a);
-                  b = fast_exp2(b);
-                  l2[2 * i + e] = add_f32x2(l2[2 * i + e], pack_f32x2(a, b));
-                  pk[2 * g + e] = pack_bf16x2(a, b);
-                }
-              tmem_st_16x32(s_tmem + ((uint32_t)(16 * i) << 16) + 32 * c, pk);
-            }
+          for (int i = 0; i < 4; ++i) l2[i] = add_f32x2(l2[i], sum[i]);
           tmem_wait_st();
         }
         tc_fence_before();
@@ -544,23 +563,16 @@ __global__ void __launch_bounds__(THREADS, 1)
       constexpr uint32_t id_pv = idesc_bf16_f32(128, D) | (1u << 16);  // V: d contiguous, N-major
       Walk walk;
       walk.start(first, &sh.walks[9]);
+      // A product's tiles are waited for first and its P last, so that nothing is waited for between its MMAs.  (One lane
+      // that does everything is slower, 1667 us for 4096 tokens after 28672 of 32 / 8 heads: issuing wants a
+      // converged warp.)
       uint32_t nt = 0, seg = 0, made = 0;  // tiles, segments, products so far
       bool failed = false;
-      // the next tile is here (v_valid: a V tile's keys in use); its slot
-      auto tile_here = [&](uint32_t& slot, int v_valid) {
+      auto tile_here = [&](uint32_t& slot) {  // the next tile is here; its slot
         slot = nt % C::SLOTS;
-        if (!mbar_wait_warp(&bar.full[slot], (nt / C::SLOTS) & 1, err)) return false;
+        const bool ok = mbar_wait_warp(&bar.full[slot], (nt / C::SLOTS) & 1, err);
         ++nt;
-        if (v_valid < KT) {
-          // values past the sequence's end are multiplied by weights of 0: they have to be finite
-          uint8_t* t = sT + slot * C::TILE;
-          for (int c = 0; c < DH; ++c)
-            for (int i = max(0, v_valid) * 8 + lane; i < KT * 8; i += 32)
-              *reinterpret_cast<uint4*>(t + c * (KT * 128) + i * 16) = make_uint4(0, 0, 0, 0);
-          fence_proxy_async();
-          __syncwarp();
-        }
-        return true;
+        return ok;
       };
       // descriptors of the first tile and Q slot: the others differ in the address field alone (16-byte units of the
       // low word)
@@ -587,36 +599,48 @@ __global__ void __launch_bounds__(THREADS, 1)
         const PagedWalk& w = walk.now();
         const Segment sg(p, w, C::NB);
         const int end = w.s.L + w.s.n - w.k0 * KT;  // the sequence's end, from the segment's first key
-        if (!mbar_wait_warp(&bar.q_full, seg & 1, err)) break;
-        ++seg;
         const int all = sg.products();
         const bool by_rows = sg.lag == 1;
         uint32_t ks = 0, vs = 0;  // slots of the K and V tiles in use
-        auto score = [&](int u) {  // product u's S
-          if ((!by_rows || (u & 1) == 0) && !tile_here(ks, KT)) return false;
-          tc_fence_after();
-          if (elect_one()) {
-            qk((made + u) % C::NB, by_rows ? u & 1 : 0, ks);
-            if (!by_rows || (u & 1)) umma_commit(&bar.empty[ks]);
-            if (u == all - 1) umma_commit(&bar.q_empty);
-          }
-          __syncwarp();
-          return true;
+        auto k_here = [&](int u) { return (by_rows && (u & 1)) || tile_here(ks); };  // product u's K tile
+        auto score = [&](int u) {                                                    // its S (elected lane)
+          qk((made + u) % C::NB, by_rows ? u & 1 : 0, ks);
+          if (!by_rows || (u & 1)) umma_commit(&bar.empty[ks]);
+          if (u == all - 1) umma_commit(&bar.q_empty);
         };
-        for (int u = 0; u < min(C::NB, all) && !failed; ++u) failed = !score(u);
+        if (!mbar_wait_warp(&bar.q_full, seg & 1, err)) break;
+        ++seg;
+        for (int u = 0; u < min(C::NB, all) && !failed; ++u) {
+          failed = !k_here(u);
+          tc_fence_after();
+          if (!failed && elect_one()) score(u);
+          __syncwarp();
+        }
         for (int u = 0; u < all && !failed; ++u) {
-          const int h = u & 1, j = by_rows ? u >> 1 : u;
-          if (((!by_rows || h == 0) && !tile_here(vs, end - j * KT)) || !mbar_wait_warp(&bar.p_full[(made + u) % C::NB], ((made + u) / C::NB) & 1, err)) {
-            failed = true;
-            break;
+          const uint32_t g = made + u;
+          if (!by_rows || (u & 1) == 0) {
+            failed = !tile_here(vs);
+            const int v_valid = end - (by_rows ? u >> 1 : u) * KT;
+            if (v_valid < KT && !failed) {
+              // values past the sequence's end are multiplied by weights of 0: they have to be finite
+              uint8_t* t = sT + vs * C::TILE;
+              for (int c = 0; c < DH; ++c)
+                for (int i = max(0, v_valid) * 8 + lane; i < KT * 8; i += 32)
+                  *reinterpret_cast<uint4*>(t + c * (KT * 128) + i * 16) = make_uint4(0, 0, 0, 0);
+              fence_proxy_async();
+              __syncwarp();
+            }
           }
+          const bool more = u + C::NB < all;
+          failed = failed || (more && !k_here(u + C::NB)) || !mbar_wait_warp(&bar.p_full[g % C::NB], (g / C::NB) & 1, err);
+          if (failed) break;
           tc_fence_after();
           if (elect_one()) {
-            pv((made + u) % C::NB, h, vs, u < 2);
-            if (!by_rows || h == 1) umma_commit(&bar.empty[vs]);
+            pv(g % C::NB, u & 1, vs, u < 2);
+            if (!by_rows || (u & 1)) umma_commit(&bar.empty[vs]);
+            if (more) score(u + C::NB);
           }
           __syncwarp();
-          if (u + C::NB < all) failed = !score(u + C::NB);
         }
         made += all;
       }
