@@ -105,6 +105,15 @@ __device__ __forceinline__ void set_regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
 
+// The slots of a ring in turn, with the parity of their phase.
+template <uint32_t N>
+struct Ring {
+  uint32_t slot = 0, phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == N) slot = 0, phase ^= 1;
+  }
+};
+
 // A segment's streams: by rows (`lag` 1: both use every tile) or by steps (`lag` 2: stream = step mod 2).  Its products
 // are numbered in the order in which they are made, streams in turn: product u is of stream u mod 2 and step u / 2 (by
 // rows) or u (by steps), and S of u lies in buffer (products before the segment + u) mod NB.  S of u + NB is issued right
@@ -563,17 +572,13 @@ __global__ void __launch_bounds__(THREADS, 1)
       constexpr uint32_t id_pv = idesc_bf16_f32(128, D) | (1u << 16);  // V: d contiguous, N-major
       Walk walk;
       walk.start(first, &sh.walks[9]);
-      // A product's tiles are waited for first and its P last, so that nothing is waited for between its MMAs.  (One lane
-      // that does everything is slower, 1667 us for 4096 tokens after 28672 of 32 / 8 heads: issuing wants a
-      // converged warp.)
-      uint32_t nt = 0, seg = 0, made = 0;  // tiles, segments, products so far
+      // A product's tiles and its P are asked for together, so that little time passes between two products' MMAs: the
+      // tensor pipe's queue is short.  (One wait after the other, 150 clocks each though nothing was missing: 1490 us for
+      // 4096 tokens after 28672 of 32 / 8 heads.  One lane that does everything, 1667 us: issuing wants a converged warp.
+      // Two warps in turn, 1720 us: their MMAs mix, and a stream gets its next S later.)
+      uint32_t seg = 0, made = 0;  // segments, products so far
+      Ring<C::SLOTS> tiles;        // the next tile
       bool failed = false;
-      auto tile_here = [&](uint32_t& slot) {  // the next tile is here; its slot
-        slot = nt % C::SLOTS;
-        const bool ok = mbar_wait_warp(&bar.full[slot], (nt / C::SLOTS) & 1, err);
-        ++nt;
-        return ok;
-      };
       // descriptors of the first tile and Q slot: the others differ in the address field alone (16-byte units of the
       // low word)
       const uint64_t k_desc = smem_desc_sw128(smem_u32(sT), 16, 1024);
@@ -602,8 +607,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int all = sg.products();
         const bool by_rows = sg.lag == 1;
         uint32_t ks = 0, vs = 0;  // slots of the K and V tiles in use
-        auto k_here = [&](int u) { return (by_rows && (u & 1)) || tile_here(ks); };  // product u's K tile
-        auto score = [&](int u) {                                                    // its S (elected lane)
+        auto score = [&](int u) {  // S of product u (elected lane)
           qk((made + u) % C::NB, by_rows ? u & 1 : 0, ks);
           if (!by_rows || (u & 1)) umma_commit(&bar.empty[ks]);
           if (u == all - 1) umma_commit(&bar.q_empty);
@@ -611,17 +615,43 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!mbar_wait_warp(&bar.q_full, seg & 1, err)) break;
         ++seg;
         for (int u = 0; u < min(C::NB, all) && !failed; ++u) {
-          failed = !k_here(u);
+          if (!by_rows || (u & 1) == 0) {
+            failed = !mbar_wait_warp(&bar.full[tiles.slot], tiles.phase, err);
+            ks = tiles.slot;
+            tiles.next();
+          }
           tc_fence_after();
           if (!failed && elect_one()) score(u);
           __syncwarp();
         }
         for (int u = 0; u < all && !failed; ++u) {
           const uint32_t g = made + u;
-          if (!by_rows || (u & 1) == 0) {
-            failed = !tile_here(vs);
+          const bool new_v = !by_rows || (u & 1) == 0, more = u + C::NB < all;
+          const bool new_k = more && (!by_rows || ((u + C::NB) & 1) == 0);
+          // what the product needs: its V, the K of the S behind it, its P (where a tile is there already: P's barrier again)
+          uint64_t* const p_bar = &bar.p_full[g % C::NB];
+          const uint32_t p_phase = (g / C::NB) & 1;
+          uint64_t *v_bar = p_bar, *k_bar = p_bar;
+          uint32_t v_phase = p_phase, k_phase = p_phase;
+          if (new_v) {
+            v_bar = &bar.full[tiles.slot];
+            v_phase = tiles.phase;
+            vs = tiles.slot;
+            tiles.next();
+          }
+          if (new_k) {
+            k_bar = &bar.full[tiles.slot];
+            k_phase = tiles.phase;
+            ks = tiles.slot;
+            tiles.next();
+          }
+          const bool v = mbar_try_wait(v_bar, v_phase), k = mbar_try_wait(k_bar, k_phase), pp = mbar_try_wait(p_bar, p_phase);
+          if (!__all_sync(0xffffffffu, v && k && pp))
+            failed = !mbar_wait_warp(v_bar, v_phase, err) || !mbar_wait_warp(k_bar, k_phase, err) || !mbar_wait_warp(p_bar, p_phase, err);
+          if (failed) break;
+          if (new_v) {
             const int v_valid = end - (by_rows ? u >> 1 : u) * KT;
-            if (v_valid < KT && !failed) {
+            if (v_valid < KT) {
               // values past the sequence's end are multiplied by weights of 0: they have to be finite
               uint8_t* t = sT + vs * C::TILE;
               for (int c = 0; c < DH; ++c)
@@ -631,9 +661,6 @@ __global__ void __launch_bounds__(THREADS, 1)
               __syncwarp();
             }
           }
-          const bool more = u + C::NB < all;
-          failed = failed || (more && !k_here(u + C::NB)) || !mbar_wait_warp(&bar.p_full[g % C::NB], (g / C::NB) & 1, err);
-          if (failed) break;
           tc_fence_after();
           if (elect_one()) {
             pv(g % C::NB, u & 1, vs, u < 2);
