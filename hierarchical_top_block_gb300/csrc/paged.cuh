@@ -36,11 +36,13 @@ struct PagedParams {
   float* lse;                // nullable
   float* part_o;             // [2 blocks][ROWS][d] output sums relative to the row maximum
   float2* part_ml;           // [2 blocks][ROWS] row maximum (log2 units) and sum
-  long long* base;           // [B + 2] first position of each sequence, the line's length, `extra`
+  long long* base;           // [2 B + 3] first position of each sequence, the line's length, `extra`, first job of each
+                             // sequence, their number
   long long q_stride;        // elements between rows of q
   int B, R, H_q, H_kv, GQ, P, M;
   int s_bits, gq_bits, row_bits;  // S, G_Q and ROWS are 2 to these
   int causal, accumulate;
+  int by_job;                // the joining kernel's blockIdx.x is a job; else a block in which one begins
   int blocks, stop;          // thread blocks the line is cut for; steps that a second job in a block costs
   float sl2;
   uint32_t* err;
@@ -200,10 +202,11 @@ struct PagedLine {
     if (record && lane == 0) {
       p.base[p.B] = cut.S;
       p.base[p.B + 1] = extra;
+      p.base[2 * p.B + 2] = jobs;
     }
     if (at >= end && !record) return;
     // the sequence that holds position `at`
-    long long before = 0;
+    long long before = 0, jobs_before = 0;
     bool found = false;
     for (int i0 = 0; i0 < p.B && !(found && !record); i0 += 32) {
       const int i = i0 + lane;
@@ -214,7 +217,20 @@ struct PagedLine {
         const long long y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
       }
-      if (record && i < p.B) p.base[i] = before + x - mine_all;
+      if (record) {
+        const int mine_jobs = i < p.B ? p.H_kv * Jobs(p, seq(i)).tiles : 0;
+        long long y = mine_jobs;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long z = __shfl_up_sync(0xffffffffu, y, o);
+          if (lane >= o) y += z;
+        }
+        if (i < p.B) {
+          p.base[i] = before + x - mine_all;
+          p.base[p.B + 2 + i] = jobs_before + y - mine_jobs;
+        }
+        jobs_before += __shfl_sync(0xffffffffu, y, 31);
+      }
       const unsigned past = __ballot_sync(0xffffffffu, before + x > at);
       if (past && !found) {
         const int l = __ffs(past) - 1;
@@ -269,16 +285,19 @@ struct PagedLine {
     }
   }
 
-  // For the kernel that joins: moves to the job that begins in block c0 and goes on behind it, if there is one.  Its
-  // parts: slot0 of block c0, then the first slots of blocks c0 + 1 .. c1.
-  __device__ __forceinline__ bool split_job(const PagedParams& p, int c0, int& c1, int& slot0) {
+  // For the kernel that joins: moves to job `index`, or to the job that begins in block `index` and goes on behind it.
+  // False if there is none, or a block had all of it.  Its parts: slot0 of block c0, then the first slots of blocks c0 + 1
+  // .. c1.
+  __device__ __forceinline__ bool split_job(const PagedParams& p, int index, int& c0, int& c1, int& slot0) {
     const PagedCut cut = paged_cut(p, p.base[p.B], (int)p.base[p.B + 1]);
-    if (c0 >= cut.blocks || cut.S == 0) return false;
-    const long long last = cut.start(c0 + 1) - 1;  // the job that holds the block's last position
-    int lo = 0, hi = p.B - 1;                      // the last sequence that begins at or before it
+    if (cut.S == 0 || index >= (p.by_job ? p.base[2 * p.B + 2] : cut.blocks)) return false;
+    // the last sequence whose first job, or first position, is at or before it
+    const long long* first = p.by_job ? p.base + p.B + 2 : p.base;
+    const long long want = p.by_job ? index : cut.start(index + 1) - 1;
+    int lo = 0, hi = p.B - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (p.base[mid] <= last)
+      if (first[mid] <= want)
         lo = mid;
       else
         hi = mid - 1;
@@ -288,13 +307,18 @@ struct PagedLine {
     s = paged_seq(p, lo, bad);
     const Jobs j(p, s);
     if (j.tiles == 0) return false;
-    long long off = last - p.base[lo];
+    long long off = want - first[lo];
     const long long span = j.span(cut.extra);
-    head = (int)whole_quotient(off, span);
-    off -= head * span;
-    tile = j.tile_at(off, cut.extra);
-    const long long s0 = last - off + j.before(tile) + (long long)tile * cut.extra, s1 = s0 + cut.extra;  // its first position and step
-    if (cut.block_of(s1) != c0) return false;
+    if (p.by_job) {
+      head = (int)whole_quotient(off, j.tiles);
+      tile = (int)(off - (long long)head * j.tiles);
+    } else {
+      head = (int)whole_quotient(off, span);
+      tile = j.tile_at(off - head * span, cut.extra);
+    }
+    const long long s0 = p.base[lo] + head * span + j.before(tile) + (long long)tile * cut.extra, s1 = s0 + cut.extra;
+    c0 = cut.block_of(s1);  // (s0: its first position, s1: its first step)
+    if (!p.by_job && c0 != index) return false;
     // (in range as long as nobody changes the lengths under the call)
     c1 = min(cut.block_of(s1 + j.steps(tile) - 1), p.blocks - 1);
     slot0 = 2 * c0 + (cut.start(c0) >= s0 ? 0 : 1);  // 1: the block had a job before

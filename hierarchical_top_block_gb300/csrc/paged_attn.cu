@@ -159,34 +159,39 @@ __global__ void __launch_bounds__(THREADS, FewCfg<D, KEYS, NH>::PER_SM)
   }
 }
 
-// Joins the parts of the jobs that span blocks.  blockIdx.x: the block in which such a job begins; its rows are
-// taken by WARPS warps each, which take the parts in turn, BATCH of them in flight, and meet in shared memory.
-template <int D, int WARPS>
-__global__ void __launch_bounds__(THREADS, 8) paged_join_kernel(PagedParams p) {
-  constexpr int V = D / 32, BATCH = 5, PER = THREADS / 32 / WARPS;  // rows a block at a time
-  __shared__ float so[PER][WARPS][D];
-  __shared__ float2 sml[PER][WARPS];
-  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % WARPS, sub = (threadIdx.x >> 5) / WARPS;
-  const int c0 = blockIdx.x;
+// Joins the parts of the jobs that span blocks: blockIdx.x finds a job, blockIdx.y takes its share of the job's rows.  A row
+// is joined by one warp where there are few parts, by four or all sixteen where there are more: they take the parts in
+// turn, BATCH of them in flight, and meet in shared memory.  (Two or four warps a row, a row at a time, and a block for
+// two rows: 30 us behind 880 jobs of 256 rows, d = 64.)
+constexpr int JOIN_WARPS = 16;
+template <int D>
+__global__ void __launch_bounds__(32 * JOIN_WARPS, 3) paged_join_kernel(PagedParams p) {
+  constexpr int V = D / 32, BATCH = 4;
+  __shared__ float so[JOIN_WARPS][D];
+  __shared__ float2 sml[JOIN_WARPS];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_wait();
   PagedWalk w;
-  int c1, slot0;
-  if (!w.split_job(p, c0, c1, slot0)) return;
-  const int rows = w.rows(p);
-  for (int row0 = blockIdx.y * PER; row0 < rows; row0 += gridDim.y * PER) {
-    const int row = min(row0 + sub, rows - 1);
+  int c0, c1, slot0;
+  if (!w.split_job(p, blockIdx.x, c0, c1, slot0)) return;
+  const int parts = c1 - c0 + 1, bits = parts <= 4 ? 0 : parts <= 32 ? 2 : 4, W = 1 << bits;  // warps a row
+  const int turn = warp & (W - 1), rows = w.rows(p);
+  for (int row0 = blockIdx.y << (4 - bits); row0 < rows; row0 += (int)gridDim.y << (4 - bits)) {
+    const int row = row0 + (warp >> bits);
+    const bool live = row < rows;
     float m = NEG_INF, l = 0.f, acc[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = 0.f;
-    for (int c = c0 + warp; c <= c1; c += WARPS * BATCH) {
+    for (int c = c0 + turn; live && c <= c1; c += W * BATCH) {
       float2 ml[BATCH];
       float x[BATCH][V];
 #pragma unroll
       for (int u = 0; u < BATCH; ++u) {
-        const int cc = c + u * WARPS;
-        const bool in = cc <= c1;
-        const size_t at = ((size_t)(cc == c0 || !in ? slot0 : 2 * cc) << p.row_bits) + row;
-        ml[u] = in ? p.part_ml[at] : make_float2(NEG_INF, 0.f);
+        const int cc = c + u * W;
+        ml[u] = make_float2(NEG_INF, 0.f);
+        if (cc > c1) continue;
+        const size_t at = ((size_t)(cc == c0 ? slot0 : 2 * cc) << p.row_bits) + row;
+        ml[u] = p.part_ml[at];
         const float* src = p.part_o + at * D + lane * V;
         if constexpr (V == 4)
           *reinterpret_cast<float4*>(x[u]) = *reinterpret_cast<const float4*>(src);
@@ -213,40 +218,41 @@ __global__ void __launch_bounds__(THREADS, 8) paged_join_kernel(PagedParams p) {
         for (int i = 0; i < V; ++i) acc[i] += x[u][i] * f;
       }
     }
+    if (W > 1) {  // (the same for the whole block)
 #pragma unroll
-    for (int i = 0; i < V; ++i) so[sub][warp][lane * V + i] = acc[i];
-    if (lane == 0) sml[sub][warp] = make_float2(m, l);
-    __syncthreads();
-    if (warp == 0 && row0 + sub < rows) {
-      m = NEG_INF;
+      for (int i = 0; i < V; ++i) so[warp][lane * V + i] = acc[i];
+      if (lane == 0) sml[warp] = make_float2(m, l);
+      __syncthreads();
+      if (turn == 0) {
+        m = NEG_INF;
+        for (int u = 0; u < W; ++u) m = fmaxf(m, sml[warp + u].x);
+        l = 0.f;
 #pragma unroll
-      for (int u = 0; u < WARPS; ++u) m = fmaxf(m, sml[sub][u].x);
-      l = 0.f;
+        for (int i = 0; i < V; ++i) acc[i] = 0.f;
+        for (int u = 0; u < W; ++u) {
+          const float2 ml = sml[warp + u];
+          const float f = ml.x == NEG_INF ? 0.f : fast_exp2(ml.x - m);
+          l += ml.x == NEG_INF ? ml.y : ml.y * f;
+          if (f != 0.f)
 #pragma unroll
-      for (int i = 0; i < V; ++i) acc[i] = 0.f;
-#pragma unroll
-      for (int u = 0; u < WARPS; ++u) {
-        const float2 ml = sml[sub][u];
-        const float f = ml.x == NEG_INF ? 0.f : fast_exp2(ml.x - m);
-        l += ml.x == NEG_INF ? ml.y : ml.y * f;
-        if (f != 0.f)
-#pragma unroll
-          for (int i = 0; i < V; ++i) acc[i] += so[sub][u][lane * V + i] * f;
+            for (int i = 0; i < V; ++i) acc[i] += so[warp + u][lane * V + i] * f;
+        }
       }
-      float lse;
-      const float f = finish_row(m, l, lse);
-      const size_t at = w.row_at(p, row);
-      uint32_t y[V / 2];
-#pragma unroll
-      for (int i = 0; i < V / 2; ++i) y[i] = f == 0.f ? 0u : pack_bf16x2(acc[2 * i] * f, acc[2 * i + 1] * f);
-      uint16_t* dst = p.o + at * D + lane * V;
-      if constexpr (V == 4)
-        *reinterpret_cast<uint2*>(dst) = make_uint2(y[0], y[1]);
-      else
-        *reinterpret_cast<uint32_t*>(dst) = y[0];
-      if (p.lse && lane == 0) p.lse[at] = lse;
+      __syncthreads();
     }
-    __syncthreads();
+    if (!live || turn != 0) continue;
+    float lse;
+    const float f = finish_row(m, l, lse);
+    const size_t at = w.row_at(p, row);
+    uint32_t y[V / 2];
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) y[i] = f == 0.f ? 0u : pack_bf16x2(acc[2 * i] * f, acc[2 * i + 1] * f);
+    uint16_t* dst = p.o + at * D + lane * V;
+    if constexpr (V == 4)
+      *reinterpret_cast<uint2*>(dst) = make_uint2(y[0], y[1]);
+    else
+      *reinterpret_cast<uint32_t*>(dst) = y[0];
+    if (p.lse && lane == 0) p.lse[at] = lse;
   }
 }
 
@@ -298,7 +304,7 @@ int bits_of(int x) {  // of a power of two
 size_t paged_workspace_bytes(const Problem& p, const Pages& pg) {
   const Plan plan = paged_plan(p, pg);
   const size_t parts = (size_t)2 * plan.blocks * plan.rows;
-  return up256(parts * p.d * 4) + up256(parts * 8) + up256((size_t)(p.B + 2) * 8);
+  return up256(parts * p.d * 4) + up256(parts * 8) + up256((size_t)(2 * p.B + 3) * 8);
 }
 
 cudaError_t launch_paged_attn(const uint16_t* q, long long q_stride, const uint16_t* Kp, const uint16_t* Vp,
@@ -346,11 +352,15 @@ cudaError_t launch_paged_attn(const uint16_t* q, long long q_stride, const uint1
   else
     e = pg.s_bits > 4 ? launch_few_rows<64, 32>(p, s) : launch_few_rows<64, 16>(p, s);
   if (e != cudaSuccess) return e;
-  const int warps = plan.rows <= 16 ? 4 : 2, per = 4 / warps;  // a row; rows a block
-  const dim3 grid((unsigned)p.blocks, (unsigned)std::min(plan.rows / per, std::max(1, num_sms * 16 / p.blocks)));
-  auto join = pr.d == 128 ? (warps == 4 ? paged_join_kernel<128, 4> : paged_join_kernel<128, 2>)
-                          : (warps == 4 ? paged_join_kernel<64, 4> : paged_join_kernel<64, 2>);
-  return launch_pdl(join, grid, dim3(THREADS), 0, s, p);
+  // The joining kernel's blocks: one a job where there are fewer of them than blocks, which then have many parts each and
+  // get several blocks for their rows.
+  const long long rows = (long long)p.R * p.GQ, jobs = p.H_kv * (rows / plan.rows + std::min<long long>(p.B, rows));
+  p.by_job = jobs <= p.blocks;
+  const int x = p.by_job ? (int)jobs : p.blocks;
+  const int most = plan.tc ? plan.rows / 16 : plan.rows;
+  const int y = std::min(most, std::max(plan.tc ? 4 : 1, num_sms * 4 / std::max(x, 1)));
+  return launch_pdl(pr.d == 128 ? paged_join_kernel<128> : paged_join_kernel<64>, dim3((unsigned)x, (unsigned)y),
+                    dim3(32 * JOIN_WARPS), 0, s, p);
 }
 
 }  // namespace pisa

@@ -360,10 +360,10 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
 __global__ void __launch_bounds__(KEYS) paged_weights_join_kernel(PagedParams p) {
   pdl_wait();
   KeyWalk w;
-  int c1, slot0;
-  if (!w.split_job(p, blockIdx.x, c1, slot0)) return;
+  int c0, c1, slot0;
+  if (!w.split_job(p, blockIdx.x, c0, c1, slot0)) return;
   float sum = p.part_o[(size_t)slot0 * KEYS + threadIdx.x];
-  for (int c = blockIdx.x + 1; c <= c1; ++c) sum += p.part_o[(size_t)2 * c * KEYS + threadIdx.x];
+  for (int c = c0 + 1; c <= c1; ++c) sum += p.part_o[(size_t)2 * c * KEYS + threadIdx.x];
   put_weight(p, w, w.tile * KEYS + threadIdx.x, sum);
 }
 
@@ -389,7 +389,7 @@ cudaError_t launch_t(const PagedParams& p, cudaStream_t s) {
 }  // namespace
 
 size_t paged_weights_workspace_bytes(const Problem& p) {
-  return up256((size_t)2 * MAX_SMS * KEYS * 4) + up256((size_t)(p.B + 2) * 8);
+  return up256((size_t)2 * MAX_SMS * KEYS * 4) + up256((size_t)(2 * p.B + 3) * 8);
 }
 
 cudaError_t launch_paged_weights(const uint16_t* q, long long q_stride, const float* lse, const uint16_t* Kp, float* w,
