@@ -15,12 +15,11 @@
 // 128 rows a stream is a half of the rows, and both use the same tiles; with fewer, both streams have all rows, one
 // the even steps and one the odd ones, each with its own m, l and O, joined when a job's segment ends.
 //
-// A step's keys come in copies of min(S, 128) tokens of a page, issued by as many lanes of the producing warp, each
-// with the page it looked up while it waited for the slot.  Copies for pages that are not there, or that begin behind
+// A step's keys come in copies of min(S, 128) tokens of a page, issued by as many lanes of the producing warps.  Copies for pages that are not there, or that begin behind
 // the sequence's last key, are given a page number past the pool and read as zeros.  Logits are masked by row only
 // in steps that pass the last key which the warp's first row sees, and in steps with such a page.
 //
-// Roles: two softmax warpgroups; a producer warp (TMA); a warp that issues the MMAs.  TMEM: NB buffers of 128 columns
+// Roles: two softmax warpgroups; two producer warps (TMA); a warp that issues the MMAs.  TMEM: NB buffers of 128 columns
 // for S (the first 64 of one hold P afterwards), then O of both streams.  With d = 64 there is room for a third buffer,
 // so that a stream finds its next S made when it has handed over its P.  The MMAs of one thread run in order, so the next
 // S of a buffer is issued right behind the O += P V that reads P from it.  Every wait is bounded.
@@ -36,7 +35,7 @@ namespace {
 constexpr int ROWS = PAGED_TC_ROWS, KT = PAGED_KT;
 constexpr float MOST = 256.f;  // a lane's sum of a row's weights in a step above which the references are raised
 
-constexpr int THREADS = 384, PRODUCER = 8, ISSUER = 9;  // warps
+constexpr int THREADS = 384, PRODUCER = 8, ISSUER = 9, PRODUCER2 = 10;  // warps
 // Registers a thread of the softmax and of the other warpgroup, of 384 x 168 at launch: the softmax holds 128 logits.
 constexpr int REGS_SOFTMAX = 208, REGS_ISSUE = 88;
 static_assert(2 * REGS_SOFTMAX + REGS_ISSUE <= 3 * 168, "registers of the block");
@@ -69,8 +68,8 @@ struct Counts {
 template <int D>
 struct Shared {
   Bars<D> bar;
-  float2 ml[2][128];      // the streams' maxima and sums, when they meet
-  PagedWalk walks[10];    // each warp's walk: registers are wanted elsewhere
+  float2 ml[2][64];       // a stream's maxima and sums of the rows that the other one writes, when they meet
+  PagedWalk walks[11];    // each warp's walk: registers are wanted elsewhere
   Counts counts[8];
   uint32_t tmem;
 };
@@ -127,23 +126,7 @@ struct Segment {
     lag = rows > ROWS / 2 ? 1 : 2;
     head = min(lag == 1 ? (buffers + 1) / 2 : buffers, nk);
   }
-  __device__ __forceinline__ int tiles() const { return 2 * nk; }
   __device__ __forceinline__ int products() const { return lag == 1 ? 2 * nk : nk; }
-  // Tile i of the order: returns its step, and whether it is a V.
-  __device__ __forceinline__ int tile(int i, bool& is_v) const {
-    const int both = 2 * (nk - head);
-    if (i < head) {
-      is_v = false;
-      return i;
-    }
-    i -= head;
-    if (i < both) {
-      is_v = (i & 1) == 0;
-      return is_v ? i >> 1 : head + (i >> 1);
-    }
-    is_v = true;
-    return nk - head + (i - both);
-  }
 };
 
 // Where a finished query row goes: the output (the whole job was this segment) or a part's slot.  The output sums are
@@ -207,8 +190,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint32_t* err = p.err;
   const int box_bits = min(p.s_bits, 7);  // a copy's keys, 2 to this
 
-  // The producer sets up the barriers and starts to fetch at once; the others meet when they and the tensor memory are
-  // there.
+  // The first producer sets up the barriers and starts to fetch at once; the others meet when they and the tensor memory
+  // are there.
   if (warp == PRODUCER) {
     if (lane == 0) {
       prefetch_map(&mapQ);
@@ -267,10 +250,10 @@ __global__ void __launch_bounds__(THREADS, 1)
       const bool any = warp_row < sg.rows;
       const int total = w.s.L + w.s.n, least = w.seen(p, warp_row);
       const int32_t* table = p.table + (size_t)w.b * p.M;
-      // whether the copy that this lane stands for has no page, of step j
+      // the page of the copy that this lane stands for, of step j (looked at a step later: the load is not waited for)
       auto look = [&](int j) {
         const int key = (w.k0 + j) * KT + (lane << box_bits);
-        return (lane << box_bits) < KT && j < sg.nk && key < total ? (unsigned)__ldg(table + (key >> p.s_bits)) >= (unsigned)p.P : false;
+        return (lane << box_bits) < KT && j < sg.nk && key < total ? __ldg(table + (key >> p.s_bits)) : 0;
       };
       float m[4];                // references, log2 units
       unsigned long long l2[4];  // a lane's share of the sum, even and odd columns
@@ -287,12 +270,12 @@ __global__ void __launch_bounds__(THREADS, 1)
       auto o_done = [&](uint32_t v) { return mbar_wait_warp(&bar.o_done[v % C::NB], (v / C::NB) & 1, err); };
       bool begun = false;  // O holds sums of this segment
       bool blank = true;   // a row of the warp has no reference yet
-      bool gone = look(sg.lag == 1 ? 0 : h);
+      int page = look(sg.lag == 1 ? 0 : h);
       for (int j = sg.lag == 1 ? 0 : h; j < sg.nk; j += sg.lag, u += 2) {
         const uint32_t buf = u % C::NB, s_tmem = tmem + lanes + 128 * buf;
         const int key0 = (w.k0 + j) * KT;
-        const unsigned none = __ballot_sync(0xffffffffu, gone);
-        gone = look(j + sg.lag);
+        const unsigned none = __ballot_sync(0xffffffffu, (unsigned)page >= (unsigned)p.P);  // copies that have none
+        page = look(j + sg.lag);
         if (!mbar_wait_warp(&bar.s_full[buf], (u / C::NB) & 1, err)) {
           failed = true;
           break;
@@ -462,9 +445,10 @@ __global__ void __launch_bounds__(THREADS, 1)
       } else {
         // both streams have parts of every row: joined here, rows below 16 of 32 by one warpgroup, the others by the
         // other one
+        float2* other = &sh.ml[h][(warp & 3) * 16 + (lane >> 2)];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (q == 0) sh.ml[h][row0 + 8 * i] = make_float2(m[i], l[i]);
+        for (int e = 0; e < 2; ++e)
+          if (q == 0) other[8 * e] = h == 0 ? make_float2(m[2 + e], l[2 + e]) : make_float2(m[e], l[e]);
         __syncwarp();
         if ((both && !o_done(made + all - 2)) || !o_done(made + all - 1)) {  // in this order: the products' own
           failed = true;
@@ -482,7 +466,9 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int row = row0 + 16 * h + 8 * e;
-            const float2 a = sh.ml[0][row], b = sh.ml[1][row];
+            const float2 mine = h == 0 ? make_float2(m[e], l[e]) : make_float2(m[2 + e], l[2 + e]);
+            const float2 its = sh.ml[1 - h][(warp & 3) * 16 + (lane >> 2) + 8 * e];
+            const float2 a = h == 0 ? mine : its, b = h == 0 ? its : mine;
             const float top = fmaxf(a.x, b.x);
             f0[e] = a.x == NEG_INF ? 0.f : fast_exp2(a.x - top);
             f1[e] = b.x == NEG_INF ? 0.f : fast_exp2(b.x - top);
@@ -519,49 +505,74 @@ __global__ void __launch_bounds__(THREADS, 1)
   } else {
     // The producing and issuing warps are two of one warpgroup: all of it changes its registers by one instruction.
     set_regs_down<REGS_ISSUE>();
-    if (warp == PRODUCER) {
-      // ------------------------------ producer ------------------------------
+    if (warp == PRODUCER || warp == PRODUCER2) {
+      // ------------------------------ producers ------------------------------
+      // A copy takes its warp 80 clocks, and a tile of pages of 16 tokens 8 or 16 copies: each warp issues every other.
+      const int which = warp == PRODUCER ? 0 : 1;
       Walk walk;
-      walk.start(first, &sh.walks[8]);
-      uint32_t nt = 0, seg = 0;  // tiles and segments so far
+      walk.start(first, &sh.walks[which == 0 ? 8 : 10]);
+      uint32_t seg = 0, nt = 0;  // segments and tiles so far
+      Ring<C::SLOTS> ring;
       bool failed = false;
-      const int piece = lane & (DH - 1), box = lane / DH;  // this lane's copy of a tile
-      const bool copies = box << box_bits < KT;
+      const int copy = 2 * lane + which, piece = copy & (DH - 1), box = copy / DH;  // this lane's copy of a tile
+      const int in_tile = box << box_bits;
+      const bool copies = in_tile < KT;
+      uint8_t* const dst = sT + piece * (KT * 128) + in_tile * 128;
+      const int in_page = (1 << p.s_bits) - 1;
       for (bool more_work = any_work; !failed && more_work; more_work = walk.next(p, block)) {
         const PagedWalk& w = walk.now();
         const Segment sg(p, w, C::NB);
-        if (!mbar_wait_warp(&bar.q_empty, (seg & 1) ^ 1, err)) break;
-        if (lane == 0) {
-          const int streams = sg.lag == 1 ? 2 : 1;
-          mbar_arrive_expect_tx(&bar.q_full, streams * C::QT_BYTES);
-          for (int h = 0; h < streams; ++h)
-            for (int c = 0; c < DH; ++c)
-              tma_load_4d(sQ + h * C::QT_BYTES + c * (128 * 128), &mapQ, &bar.q_full, 64 * c, 0, w.head,
-                          w.s.first + ((w.tile * ROWS + h * 128) >> p.gq_bits));
+        if (which == 0) {
+          if (!mbar_wait_warp(&bar.q_empty, (seg & 1) ^ 1, err)) break;
+          if (lane == 0) {
+            const int streams = sg.lag == 1 ? 2 : 1;
+            mbar_arrive_expect_tx(&bar.q_full, streams * C::QT_BYTES);
+            for (int h = 0; h < streams; ++h)
+              for (int c = 0; c < DH; ++c)
+                tma_load_4d(sQ + h * C::QT_BYTES + c * (128 * 128), &mapQ, &bar.q_full, 64 * c, 0, w.head,
+                            w.s.first + ((w.tile * ROWS + h * 128) >> p.gq_bits));
+          }
         }
         ++seg;
-        const int total = w.s.L + w.s.n, head = w.head;
+        const int total = w.s.L + w.s.n, head = w.head, nk = sg.nk, key0 = w.k0 * KT + in_tile, lead = sg.head;
         const int32_t* table = p.table + (size_t)w.b * p.M;
-        for (int i = 0; i < sg.tiles(); ++i, ++nt) {
-          bool is_v;
-          const int key = (w.k0 + sg.tile(i, is_v)) * KT + (box << box_bits);
-          const int page = copies && key < total ? page_of(table, p.P, key >> p.s_bits, err) : p.P;
-          const int st = nt % C::SLOTS;
-          if (!mbar_wait_warp(&bar.empty[st], ((nt / C::SLOTS) & 1) ^ 1, err)) {
+        // the page of this lane's copy of step j (read ahead, so that nobody waits for it)
+        auto entry_of = [&](int j) {
+          const int key = key0 + j * KT;
+          return copies && j < nk && key < total ? __ldg(table + (key >> p.s_bits)) : -1;
+        };
+        int k_next[2] = {entry_of(0), entry_of(1)}, v_next[2] = {entry_of(0), entry_of(1)};
+        int jk = 0, jv = 0;  // the next steps
+        for (int i = 0; i < 2 * nk; ++i) {
+          const bool is_v = jk == nk || (i >= lead && ((i - lead) & 1) == 0);
+          const int j = is_v ? jv++ : jk++, key = key0 + j * KT, later = entry_of(j + 2);
+          int entry;
+          if (is_v) {
+            entry = v_next[0];
+            v_next[0] = v_next[1];
+            v_next[1] = later;
+          } else {
+            entry = k_next[0];
+            k_next[0] = k_next[1];
+            k_next[1] = later;
+          }
+          if (!mbar_wait_warp(&bar.empty[ring.slot], ring.phase ^ 1, err)) {
             failed = true;
             break;
           }
-          if (lane == 0) mbar_arrive_expect_tx(&bar.full[st], C::TILE);
-          __syncwarp();
+          if (lane == 0 && which == 0) mbar_arrive_expect_tx(&bar.full[ring.slot], C::TILE);
           if (copies)
-            tma_load_4d(sT + st * C::TILE + piece * (KT * 128) + ((box << box_bits) * 128), is_v ? &mapV : &mapK,
-                        &bar.full[st], 64 * piece, key & ((1 << p.s_bits) - 1), head, page);
+            tma_load_4d(dst + ring.slot * C::TILE, is_v ? &mapV : &mapK, &bar.full[ring.slot], 64 * piece, key & in_page, head,
+                        (unsigned)entry < (unsigned)p.P ? entry : p.P);
+          if (entry >= p.P) report_error(err, ERR_BAD_INDEX);
           __syncwarp();
+          ring.next();
+          ++nt;
         }
       }
       // copies still in flight land before shared memory goes away (bounded; at once unless a wait failed)
       if (lane == 0) {
-        if (seg > 0) mbar_wait(&bar.q_full, (seg - 1) & 1, err, 100000000ull);
+        if (seg > 0 && which == 0) mbar_wait(&bar.q_full, (seg - 1) & 1, err, 100000000ull);
         for (uint32_t u = nt > C::SLOTS ? nt - C::SLOTS : 0; u < nt; ++u)
           mbar_wait(&bar.full[u % C::SLOTS], (u / C::SLOTS) & 1, err, 100000000ull);
       }
