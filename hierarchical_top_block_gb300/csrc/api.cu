@@ -1095,7 +1095,7 @@ pisa_status pisa_paged_evict(uint16_t* Kp, uint16_t* Vp, float* w, const int32_t
   if ((rc = device_state(&st)) != PISA_OK) return rc;
   PhaseTimer tm(static_cast<cudaStream_t>(stream));
   const cudaError_t e = launch_paged_evict(Kp, Vp, w, page_table, seq_len, new_table, new_len, kept, keep, sinks, recent,
-                                           new_max_pages, p, pg, st->err, static_cast<cudaStream_t>(stream));
+                                           new_max_pages, p, pg, st->num_sms, st->err, static_cast<cudaStream_t>(stream));
   tm.mark(PH_PAGED_EVICT);
   return cuda_status(e);
 }

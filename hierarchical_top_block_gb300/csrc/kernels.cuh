@@ -132,7 +132,7 @@ cudaError_t launch_paged_weights(const uint16_t* q, long long q_stride, const fl
 size_t paged_evict_workspace_bytes(const Problem& p, int keep);
 cudaError_t launch_paged_evict(uint16_t* Kp, uint16_t* Vp, float* w, const int32_t* table, const int32_t* seq_len,
                                const int32_t* new_table, int32_t* new_len, int32_t* kept, int keep, int sinks, int recent,
-                               int new_max_pages, const Problem& p, const Pages& pg, uint32_t* err, cudaStream_t s);
+                               int new_max_pages, const Problem& p, const Pages& pg, int num_sms, uint32_t* err, cudaStream_t s);
 
 // One CTA whose bounded waits run out after limit_ns (checks the timeout path).
 cudaError_t launch_wait_check(uint64_t limit_ns, uint32_t* err, cudaStream_t s);

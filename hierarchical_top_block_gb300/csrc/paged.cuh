@@ -355,6 +355,15 @@ __device__ __forceinline__ int page_of(const int32_t* table, int P, int entry, u
 constexpr int PAGED_TC_ROWS = 256;
 cudaError_t launch_paged_tc(const PagedParams& p, int d, cudaStream_t s);
 
+// The slots of a ring in turn, with the parity of their phase.
+template <uint32_t N>
+struct Ring {
+  uint32_t slot = 0, phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == N) slot = 0, phase ^= 1;
+  }
+};
+
 // A finished row: the factor of its output sums, and its log-sum-exp.
 __device__ __forceinline__ float finish_row(float m, float l, float& lse) {
   lse = l == 0.f ? NEG_INF : (m + log2f(l)) * LN2;

@@ -92,7 +92,8 @@ __global__ void __launch_bounds__(WRITE_THREADS) paged_write_kernel(WriteParams 
 
 // ---- eviction: the choice ----------------------------------------------------------------
 constexpr int PICK_THREADS = 512, PICK_WARPS = PICK_THREADS / 32;
-constexpr int PICK_CACHED = 12288;  // weights a block keeps in shared memory; further ones are read again
+constexpr uint32_t MAX_CLUSTER = 8;
+constexpr int PICK_CACHED = 12288;  // weights a block keeps in shared memory at most (a multiple of 4); further ones are read again
 
 struct EvictParams {
   uint16_t* K;
@@ -103,7 +104,7 @@ struct EvictParams {
   const int32_t* new_table;
   int32_t* new_len;
   int32_t* kept;  // [B][H][keep]
-  int B, H, P, M, M_new, s_bits, keep, sinks, recent;
+  int B, H, P, M, M_new, s_bits, keep, sinks, recent, cached;
   uint32_t* err;
 };
 
@@ -138,8 +139,9 @@ __device__ __forceinline__ uint32_t weight_order(float w) {
 
 __global__ void __launch_bounds__(PICK_THREADS) paged_pick_kernel(EvictParams p) {
   pdl_trigger();
-  extern __shared__ uint32_t cached[];  // [PICK_CACHED]
+  extern __shared__ __align__(16) uint32_t cached[];  // [p.cached]
   __shared__ uint32_t hist[2][256];     // of passes in turn
+  __shared__ uint32_t part[8][256];     // the first pass's, a lane's mod 8: weights have few exponents
   __shared__ uint32_t warp_sum[2][PICK_WARPS];
   __shared__ uint32_t totals[2];        // this block's keys above the limit, and at it
   __shared__ uint32_t found[2];         // digit, and keys above it
@@ -153,24 +155,58 @@ __global__ void __launch_bounds__(PICK_THREADS) paged_pick_kernel(EvictParams p)
       for (int i = threadIdx.x; i < p.keep; i += PICK_THREADS) p.kept[(size_t)bh * p.keep + i] = -1;
     return;
   }
-  // this block's keys: a whole number of 32 for each warp, so that the warps' shares follow one another
-  const int share = (int)((((long long)n + blocks - 1) / blocks + PICK_THREADS - 1) / PICK_THREADS * PICK_THREADS);
+  // this block's keys, four a lane at a time (they lie in one page); a whole number of 128 for each warp, so that the
+  // warps' shares follow one another
+  constexpr int STEP = 128 * PICK_WARPS;
+  const int share = (int)((((long long)n + blocks - 1) / blocks + STEP - 1) / STEP * STEP);
   const int c0 = min((long long)n, (long long)rank * share), c1 = min((long long)n, (long long)(rank + 1) * share);
   const int32_t* table = p.table + (size_t)b * p.M;
-  auto fetch = [&](int c) -> uint32_t {
-    const int page = page_of(table, p.P, c >> p.s_bits, p.err);
-    if (page == p.P) return 0;
-    if (c < p.sinks || c >= n - p.recent) return 0xffffffffu;
-    return weight_order(__ldg(p.w + ((((size_t)page * p.H + h)) << p.s_bits) + (c & ((1 << p.s_bits) - 1))));
+  auto weights_at = [&](int page, int c) {
+    return __ldg(reinterpret_cast<const float4*>(p.w + ((((size_t)page * p.H + h)) << p.s_bits) + (c & ((1 << p.s_bits) - 1))));
   };
-  auto order = [&](int i) { return i < PICK_CACHED ? cached[i] : fetch(c0 + i); };
-  for (int i = threadIdx.x; i < 256; i += PICK_THREADS) hist[0][i] = 0;
+  auto order_of = [&](int page, int c, float w) -> uint32_t {
+    return page == p.P || c >= n ? 0 : c < p.sinks || c >= n - p.recent ? 0xffffffffu : weight_order(w);
+  };
+  auto orders_of = [&](int page, int c, float4 w) {
+    return make_uint4(order_of(page, c, w.x), order_of(page, c + 1, w.y), order_of(page, c + 2, w.z), order_of(page, c + 3, w.w));
+  };
+  auto order = [&](int i) {  // of keys c0 + i .. + 3
+    if (i < p.cached) return *reinterpret_cast<const uint4*>(cached + i);
+    const int page = page_of(table, p.P, (c0 + i) >> p.s_bits, p.err);
+    return orders_of(page, c0 + i, page == p.P ? make_float4(0.f, 0.f, 0.f, 0.f) : weights_at(page, c0 + i));
+  };
+  for (int i = threadIdx.x; i < 8 * 256; i += PICK_THREADS) part[0][i] = 0;
   __syncthreads();
   const int mine = c1 - c0;
-  for (int i = threadIdx.x; i < mine; i += PICK_THREADS) {
-    const uint32_t x = fetch(c0 + i);
-    if (i < PICK_CACHED) cached[i] = x;
-    if (x) atomicAdd(&hist[0][x >> 24], 1u);
+  constexpr int BATCH = 4;  // groups of four keys a thread has under way
+  for (int i0 = 4 * threadIdx.x; i0 < mine; i0 += 4 * BATCH * PICK_THREADS) {
+    int page[BATCH];
+    float4 w[BATCH];
+#pragma unroll
+    for (int u = 0; u < BATCH; ++u) {
+      const int i = i0 + 4 * u * PICK_THREADS;
+      page[u] = i < mine ? page_of(table, p.P, (c0 + i) >> p.s_bits, p.err) : p.P;
+    }
+#pragma unroll
+    for (int u = 0; u < BATCH; ++u)
+      w[u] = page[u] == p.P ? make_float4(0.f, 0.f, 0.f, 0.f) : weights_at(page[u], c0 + i0 + 4 * u * PICK_THREADS);
+#pragma unroll
+    for (int u = 0; u < BATCH; ++u) {
+      const int i = i0 + 4 * u * PICK_THREADS;
+      const uint4 x = orders_of(page[u], c0 + i, w[u]);
+      if (i < mine && i < p.cached) *reinterpret_cast<uint4*>(cached + i) = x;
+      if (x.x) atomicAdd(&part[lane & 7][x.x >> 24], 1u);
+      if (x.y) atomicAdd(&part[lane & 7][x.y >> 24], 1u);
+      if (x.z) atomicAdd(&part[lane & 7][x.z >> 24], 1u);
+      if (x.w) atomicAdd(&part[lane & 7][x.w >> 24], 1u);
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 256; i += PICK_THREADS) {
+    uint32_t t = 0;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) t += part[u][i];
+    hist[0][i] = t;
   }
   // the limit: the want-th largest, 8 bits a pass
   uint32_t limit = 0, want = p.keep;
@@ -180,15 +216,27 @@ __global__ void __launch_bounds__(PICK_THREADS) paged_pick_kernel(EvictParams p)
     uint32_t* now = hist[pass & 1];
     uint32_t* next = hist[(pass & 1) ^ 1];
     if (pass > 0) {
-      for (int i = threadIdx.x; i < mine; i += PICK_THREADS) {
-        const uint32_t x = order(i);
+      auto count = [&](uint32_t x) {
         if (x && x >> (shift + 8) == limit >> (shift + 8)) atomicAdd(&now[(x >> shift) & 255], 1u);
+      };
+#pragma unroll 4
+      for (int i = 4 * threadIdx.x; i < mine; i += 4 * PICK_THREADS) {
+        const uint4 x = order(i);
+        count(x.x);
+        count(x.y);
+        count(x.z);
+        count(x.w);
       }
     }
     cluster_sync();
     uint32_t count = 0;
-    if (threadIdx.x < 256)
-      for (uint32_t k = 0; k < blocks; ++k) count += peer_word(&now[255 - threadIdx.x], k);
+    if (threadIdx.x < 256) {
+      uint32_t its[MAX_CLUSTER];
+#pragma unroll
+      for (uint32_t k = 0; k < MAX_CLUSTER; ++k) its[k] = k < blocks ? peer_word(&now[255 - threadIdx.x], k) : 0;
+#pragma unroll
+      for (uint32_t k = 0; k < MAX_CLUSTER; ++k) count += its[k];
+    }
     // `next` was last read before the barrier
     for (int i = threadIdx.x; i < 256; i += PICK_THREADS) next[i] = 0;
     // sums from the largest digit down
@@ -220,11 +268,18 @@ __global__ void __launch_bounds__(PICK_THREADS) paged_pick_kernel(EvictParams p)
   if (all) limit = 0, want = 0;  // every key is above it
   // keys above the limit, and at it, of which the first `want` stay: this block's, and those of the blocks before
   const int per = share / PICK_WARPS, w0 = min(mine, warp * per), w1 = min(mine, (warp + 1) * per);
+  // (keys above it in the low half of a word, at it in the high one)
+  auto kinds = [&](const uint4& x) {
+    auto kind = [&](uint32_t v) { return v > limit ? 1u : v == limit && v != 0 ? 0x10000u : 0u; };
+    return make_uint4(kind(x.x), kind(x.y), kind(x.z), kind(x.w));
+  };
   uint32_t gt = 0, eq = 0;
-  for (int i = w0 + lane; i < w1; i += 32) {
-    const uint32_t x = order(i);
-    gt += x > limit;
-    eq += x == limit && x != 0;
+#pragma unroll 4
+  for (int i = w0 + 4 * lane; i < w1; i += 128) {
+    const uint4 k = kinds(order(i));
+    const uint32_t both = k.x + k.y + k.z + k.w;
+    gt += both & 0xffffu;
+    eq += both >> 16;
   }
   gt = __reduce_add_sync(0xffffffffu, gt);
   eq = __reduce_add_sync(0xffffffffu, eq);
@@ -240,25 +295,46 @@ __global__ void __launch_bounds__(PICK_THREADS) paged_pick_kernel(EvictParams p)
   }
   cluster_sync();
   uint32_t before[2] = {0, 0}, every[2] = {0, 0};
-  for (uint32_t k = 0; k < blocks; ++k)
+  uint32_t its[MAX_CLUSTER][2];
+#pragma unroll
+  for (uint32_t k = 0; k < MAX_CLUSTER; ++k)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) its[k][e] = k < blocks ? peer_word(&totals[e], k) : 0;
+#pragma unroll
+  for (uint32_t k = 0; k < MAX_CLUSTER; ++k)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const uint32_t t = peer_word(&totals[e], k);
-      every[e] += t;
-      if (k < rank) before[e] += t;
+      every[e] += its[k][e];
+      if (k < rank) before[e] += its[k][e];
     }
   for (int k = 0; k < warp; ++k) before[0] += warp_sum[0][k], before[1] += warp_sum[1][k];
   int32_t* kept = p.kept + (size_t)bh * p.keep;
-  for (int i0 = w0; i0 < w1; i0 += 32) {
-    const int i = i0 + lane;
-    const uint32_t x = i < w1 ? order(i) : 0;
-    const bool is_gt = x > limit, is_eq = x == limit && x != 0;
-    const unsigned gts = __ballot_sync(0xffffffffu, is_gt), eqs = __ballot_sync(0xffffffffu, is_eq), below = (1u << lane) - 1;
-    const uint32_t g = before[0] + __popc(gts & below), q = before[1] + __popc(eqs & below);
-    const uint32_t to = g + min(q, want);
-    if ((is_gt || (is_eq && q < want)) && to < (uint32_t)p.keep) kept[to] = c0 + i;
-    before[0] += __popc(gts);
-    before[1] += __popc(eqs);
+#pragma unroll 2
+  for (int i0 = w0; i0 < w1; i0 += 128) {
+    const int i = i0 + 4 * lane;
+    const uint4 k = i < w1 ? kinds(order(i)) : make_uint4(0, 0, 0, 0);
+    const uint32_t mine4 = k.x + k.y + k.z + k.w;
+    uint32_t sum = mine4;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += y;
+    }
+    uint32_t g = before[0] + ((sum - mine4) & 0xffffu), q = before[1] + ((sum - mine4) >> 16);
+    auto put = [&](uint32_t kind, int c) {
+      if (kind == 0) return;
+      const uint32_t to = g + min(q, want);
+      if ((kind == 1 || q < want) && to < (uint32_t)p.keep) kept[to] = c;
+      g += kind & 1;
+      q += kind >> 16;
+    };
+    put(k.x, c0 + i);
+    put(k.y, c0 + i + 1);
+    put(k.z, c0 + i + 2);
+    put(k.w, c0 + i + 3);
+    sum = __shfl_sync(0xffffffffu, sum, 31);
+    before[0] += sum & 0xffffu;
+    before[1] += sum >> 16;
   }
   const uint32_t stay = every[0] + min(every[1], want);
   for (uint32_t i = stay + rank * PICK_THREADS + threadIdx.x; i < (uint32_t)p.keep; i += blocks * PICK_THREADS) kept[i] = -1;
@@ -347,17 +423,21 @@ size_t paged_evict_workspace_bytes(const Problem& pr, int keep) { return up256((
 
 cudaError_t launch_paged_evict(uint16_t* Kp, uint16_t* Vp, float* w, const int32_t* table, const int32_t* seq_len,
                                const int32_t* new_table, int32_t* new_len, int32_t* kept, int keep, int sinks, int recent,
-                               int new_max_pages, const Problem& pr, const Pages& pg, uint32_t* err, cudaStream_t s) {
+                               int new_max_pages, const Problem& pr, const Pages& pg, int num_sms, uint32_t* err, cudaStream_t s) {
   EvictParams p{Kp, Vp, w,    table, seq_len,       new_table,  new_len, kept,  pr.B,
-                pr.H_kv,  pg.P, pg.M,  new_max_pages, pg.s_bits, keep,    sinks, recent, err};
-  constexpr size_t smem = PICK_CACHED * 4;
-  cudaError_t e = allow_shared<paged_pick_kernel>(smem);
+                pr.H_kv,  pg.P, pg.M,  new_max_pages, pg.s_bits, keep,    sinks, recent, 0,   err};
+  cudaError_t e = allow_shared<paged_pick_kernel>(PICK_CACHED * 4);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  const unsigned blocks = ((long long)pg.M << pg.s_bits) > 4096 ? 8 : 1;  // a head
+  // blocks a head: as many as find room at once (two a SM), where there are keys for them
+  unsigned blocks = MAX_CLUSTER;
+  while (blocks > 1 && ((long long)pr.B * pr.H_kv * blocks > 2ll * num_sms || ((long long)pg.M << pg.s_bits) <= 1024ll * blocks)) blocks /= 2;
   cfg.gridDim = dim3((unsigned)pr.B * pr.H_kv * blocks);
   cfg.blockDim = dim3(PICK_THREADS);
-  cfg.dynamicSmemBytes = smem;
+  // no more shared memory than the longest sequence wants
+  const long long share = ((((long long)pg.M << pg.s_bits) + blocks - 1) / blocks + 2047) / 2048 * 2048;
+  p.cached = (int)std::min<long long>(PICK_CACHED, share);
+  cfg.dynamicSmemBytes = (size_t)p.cached * 4;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;

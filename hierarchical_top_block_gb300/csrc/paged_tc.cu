@@ -104,15 +104,6 @@ __device__ __forceinline__ void set_regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
 
-// The slots of a ring in turn, with the parity of their phase.
-template <uint32_t N>
-struct Ring {
-  uint32_t slot = 0, phase = 0;
-  __device__ __forceinline__ void next() {
-    if (++slot == N) slot = 0, phase ^= 1;
-  }
-};
-
 // A segment's streams: by rows (`lag` 1: both use every tile) or by steps (`lag` 2: stream = step mod 2).  Its products
 // are numbered in the order in which they are made, streams in turn: product u is of stream u mod 2 and step u / 2 (by
 // rows) or u (by steps), and S of u lies in buffer (products before the segment + u) mod NB.  S of u + NB is issued right
