@@ -261,6 +261,7 @@ struct PagedLine {
           if (++b >= p.B) return false;  // (unless somebody changes the lengths under the call)
           bool bad;
           s = paged_seq(p, b, bad);
+          job_end = -1;  // (of another sequence)
           continue;
         }
         head = (int)whole_quotient(off, span);

@@ -91,6 +91,34 @@ def attend(c, q, causal=True, scale=None, gone=()):
     return o, lse, bo, bl
 
 
+def attend_many(c, q):
+    """attend's o, lse and bounds of causal rows, whole sequences at a time."""
+    H_q, d = q.shape[1:]
+    G, scale = H_q // c.H_kv, 1 / math.sqrt(d)
+    o = torch.full(q.shape, math.nan, dtype=torch.float64, device=DEV)
+    lse = torch.full(q.shape[:2], math.nan, dtype=torch.float64, device=DEV)
+    bo, bl = o.clone(), lse.clone()
+    for b in range(c.B):
+        n, T = c.lens[b] + c.new[b], c.new[b]
+        if T == 0:
+            continue
+        rows = slice(c.first[b], c.first[b] + T)
+        k, v = (c.get(x, b, n).double().transpose(0, 1) for x in (c.K, c.V))  # [H, n, d]
+        x = q[rows].double().reshape(T, c.H_kv, G, d).permute(1, 2, 0, 3)     # [H, G, T, d]
+        z = scale * torch.einsum("hgtd,hcd->hgtc", x, k)
+        see = torch.arange(n, device=DEV) <= c.lens[b] + torch.arange(T, device=DEV)[:, None]
+        e = (d + 8) * R.F * scale * torch.einsum("hgtd,hcd->hgtc", x.abs(), k.abs()).masked_fill(~see, 0).amax(-1)
+        z = z.masked_fill(~see, -math.inf)
+        l = torch.logsumexp(z, -1)
+        w = torch.exp(z - l[..., None])
+        y, va = torch.einsum("hgtc,hcd->hgtd", w, v), torch.einsum("hgtc,hcd->hgtd", w, v.abs())
+        flat = lambda t: t.permute(2, 0, 1, *range(3, t.dim())).reshape(T, H_q, *t.shape[3:])  # noqa: E731
+        o[rows], lse[rows] = flat(y), flat(l)
+        bo[rows] = flat((R.U + 4 * e[..., None] + 2.0 ** -16) * va + R.U * y.abs())
+        bl[rows] = flat(2 * e + 2.0 ** -18 + 2.0 ** -22 * l.abs())
+    return o, lse, bo, bl
+
+
 def weights(c, q, lse, causal=True, scale=None, gone=()):
     """What the rows give to each key, and the bound: [P, H_kv, S], NaN where a key belongs to nobody (or is gone)."""
     H_q, d = q.shape[1:]

@@ -114,6 +114,31 @@ def test_attn_many_sequences():
     no_error()
 
 
+@pytest.mark.parametrize("d,G,H_kv,S,lens,new", [
+    # tensor cores: 300 and more jobs over the SMs, sequences longer and shorter than the one before, several a block
+    (64, 1, 16, 128, [0, 0, 0, 0], [1500, 600, 1100, 200]),
+    (128, 2, 8, 16, [0, 900, 130, 0, 77, 1], [300, 40, 513, 900, 128, 700]),
+    (64, 4, 8, 32, [(97 * i) % 500 for i in range(40)], [1 + (61 * i) % 150 for i in range(40)]),
+    # few rows: thousands of jobs
+    (64, 4, 8, 16, [(211 * i) % 700 for i in range(150)], [1 + i % 2 for i in range(150)]),
+    (128, 16, 8, 64, [(433 * i) % 1500 for i in range(90)], [1] * 90)])
+def test_many_jobs(d, G, H_kv, S, lens, new):
+    """More jobs than blocks: every one of a block's jobs is found, with the next sequence's after a longer one's."""
+    c = Paged(lens, new, H_kv, d, S, seed=H_kv + S)
+    q = c.rand(c.R, H_kv * G, d, scale=1.5)
+    o, lse = pisa.pisa_paged_attn(q, c.K, c.V, c.table, c.len, row_start=c.rows)
+    wo, wl, bo, bl = H.attend_many(c, q)
+    R.close(o, wo, bo, "o")
+    R.close(lse, wl, bl, "lse")
+    w = c.w.clone()
+    pisa.pisa_paged_weights(q, lse, c.K, w, c.table, c.len, row_start=c.rows, accumulate=False)
+    want, bound = H.weights(c, q, lse)
+    live = ~want.isnan()
+    assert (w[~live] == -7).all()
+    R.close(w[live], want[live], bound[live], "w")
+    no_error()
+
+
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("new", [5, 30, 40])
 def test_attn_waits_for_memory(d, new):
@@ -217,6 +242,37 @@ def test_attn_nan_shows():
     q = c.rand(1, 4, 64)
     o, lse = pisa.pisa_paged_attn(q, c.K, c.V, c.table, c.len)
     assert o.isnan().all() and lse.isnan().all()
+
+
+@pytest.mark.parametrize("T,G", [(1, 4), (70, 4)])
+def test_far_pages(T, G):
+    """Pages behind 2^31 elements of the pool: offsets of keys, values and weights in 64 bits."""
+    H_kv, d, S, n = 8, 128, 64, 700
+    P = (1 << 31) // (H_kv * S * d) + 2 * (n // S + 1) + 8
+    K = torch.empty((P, H_kv, S, d), dtype=torch.bfloat16, device=DEV)
+    V, w = torch.empty_like(K), torch.zeros((P, H_kv, S), device=DEV)
+    m = -(-n // S)
+    c = Paged([n - T], [T], H_kv, d, S, seed=3)
+    table = torch.arange(P - m, P, device=DEV, dtype=torch.int32).flip(0)[None].contiguous()
+    g = lambda x: c.get(x, 0, n)  # noqa: E731
+    pisa.pisa_paged_write(g(c.K), g(c.V), K, V, table, i32(0), w=w)
+    q = c.rand(T, H_kv * G, d, scale=1.5)
+    o, lse = pisa.pisa_paged_attn(q, K, V, table, c.len)
+    wo, wl, bo, bl = H.attend(c, q)
+    R.close(o, wo, bo, "o")
+    R.close(lse, wl, bl, "lse")
+    pisa.pisa_paged_weights(q, lse, K, w, table, c.len)
+    want, bound = H.weights(c, q, lse)
+    at = torch.arange(n, device=DEV)
+    got = w[table[0, at // S].long(), :, at % S]
+    R.close(got, g(want), g(bound), "w")
+    new = torch.arange(3, device=DEV, dtype=torch.int32)[None] + (P - m - 3)
+    new_len, kept = pisa.pisa_paged_evict(K, V, w, table, i32(n), new, 150)
+    j = torch.arange(150, device=DEV)
+    for h in range(H_kv):
+        assert torch.equal(K[new[0, j // S].long(), h, j % S], g(c.K)[kept[0, h].long(), h])
+    assert new_len.tolist() == [150]
+    no_error()
 
 
 # ---- weights -----------------------------------------------------------------------------------
