@@ -160,14 +160,13 @@ struct CacheTile {
   struct State {
     float n[NH][2];
     unsigned long long l[NH];
-    unsigned long long lr[NH];  // the same of the rounded weights (where asked for)
     float o[DT][NH][4];
   };
   __device__ static __forceinline__ void clear(State& s) {
 #pragma unroll
     for (int h = 0; h < NH; ++h) {
       s.n[h][0] = s.n[h][1] = NEG_INF;
-      s.l[h] = s.lr[h] = pack_f32x2(0.f, 0.f);
+      s.l[h] = pack_f32x2(0.f, 0.f);
     }
 #pragma unroll
     for (int t = 0; t < DT; ++t)
@@ -182,8 +181,9 @@ struct CacheTile {
   }
 
   // Adds the first `n` keys of the granule at `g` in shared memory.  LIMITS: row 8 h + 2 q + e sees the first
-  // lim[h][e] of them alone.  ROUNDED: the rounded weights are summed too, in st.lr.
-  template <bool LIMITS = false, bool ROUNDED = false>
+  // lim[h][e] of them alone.  EXACT (bf16): what rounding leaves of a weight is a second bf16 operand, so that 2^-17 of it
+  // is lost, not 2^-9.
+  template <bool LIMITS = false, bool EXACT = false>
   __device__ static __forceinline__ void add(State& st, const uint8_t* g, const Scales& sc, const Query& qr, int n, int r,
                                              int q, const int (*lim)[2] = nullptr) {
     float s[MT][NH][4];  // keys of groups 2 i (elements 0, 1: rows 2 q, 2 q + 1) and 2 i + 1 (2, 3)
@@ -266,7 +266,6 @@ struct CacheTile {
           st.n[h][e] = to;
         }
         st.l[h] = pack_f32x2(l[0], l[1]);
-        if constexpr (ROUNDED) st.lr[h] = mul_f32x2(st.lr[h], pack_f32x2(f[0], f[1]));
 #pragma unroll
         for (int t = 0; t < DT; ++t) {
           st.o[t][h][0] *= f[0];
@@ -277,6 +276,7 @@ struct CacheTile {
       }
     }
     uint32_t pt[MT][NH][2];  // P^T: rows 8 h + r, keys 2 q, 2 q + 1 of groups 2 i and 2 i + 1
+    uint32_t rest[EXACT ? MT : 1][EXACT ? NH : 1][2];
 #pragma unroll
     for (int h = 0; h < NH; ++h) {
       // a row that has seen no key (or only logits of -inf) has n = -inf: its weights are 0
@@ -295,8 +295,8 @@ struct CacheTile {
           pt[i >> 1][h][i & 1] = transpose8(pack_f16x2(a, b));
         } else {
           const uint32_t ab16 = pack_bf16x2(a, b);
-          if constexpr (ROUNDED) st.lr[h] = add_f32x2(st.lr[h], pack_f32x2(bf16_lo(ab16), bf16_hi(ab16)));
           pt[i >> 1][h][i & 1] = transpose8(ab16);
+          if constexpr (EXACT) rest[i >> 1][h][i & 1] = transpose8(pack_bf16x2(a - bf16_lo(ab16), b - bf16_hi(ab16)));
         }
       }
     }
@@ -345,7 +345,10 @@ struct CacheTile {
           const uint32_t a0 = __byte_perm(v[0][w], v[1][w], 0x5410), a1 = __byte_perm(v[0][w], v[1][w], 0x7632);
           const uint32_t a2 = __byte_perm(v[2][w], v[3][w], 0x5410), a3 = __byte_perm(v[2][w], v[3][w], 0x7632);
 #pragma unroll
-          for (int h = 0; h < NH; ++h) product_bf16(st.o[w][h], a0, a1, a2, a3, pt[i][h][0], pt[i][h][1]);
+          for (int h = 0; h < NH; ++h) {
+            product_bf16(st.o[w][h], a0, a1, a2, a3, pt[i][h][0], pt[i][h][1]);
+            if constexpr (EXACT) product_bf16(st.o[w][h], a0, a1, a2, a3, rest[i][h][0], rest[i][h][1]);
+          }
         }
       }
     }
@@ -370,29 +373,16 @@ struct WarpRing {
 
 // Joins the states of a block's four warps into shared memory.  po [4][ROWS][D] and sn, sl [4][16] are
 // scratch; afterwards ml holds each row's reference and sum and po its output sums (`rows` rows are in
-// use).  All 128 threads.  ROUNDED (sr [5][16] is scratch): the output sums are multiplied by the sum of the weights over
-// that of the rounded ones, so that divided by the sum they are a mean of the values, by weights that are off but add
-// up to 1: a row that one key dominates gets its value.
-template <typename Tile, int D, bool ROUNDED = false>
+// use).  All 128 threads.
+template <typename Tile, int D>
 __device__ __forceinline__ void join_warps(typename Tile::State& st, float* po, float (*sn)[16], float (*sl)[16],
-                                           float2* ml, int rows, float (*sr)[16] = nullptr) {
+                                           float2* ml, int rows) {
   constexpr int ROWS = Tile::ROWS, NH = ROWS / 8;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, q = lane & 3;
 #pragma unroll
   for (int h = 0; h < NH; ++h) {
     float l[2];
     unpack_f32x2(st.l[h], l[0], l[1]);
-    if constexpr (ROUNDED) {
-      float x[2];
-      unpack_f32x2(st.lr[h], x[0], x[1]);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        x[e] += __shfl_xor_sync(0xffffffffu, x[e], 4);
-        x[e] += __shfl_xor_sync(0xffffffffu, x[e], 8);
-        x[e] += __shfl_xor_sync(0xffffffffu, x[e], 16);
-        if (r == 0) sr[warp][8 * h + 2 * q + e] = x[e];
-      }
-    }
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       l[e] += __shfl_xor_sync(0xffffffffu, l[e], 4);
@@ -419,12 +409,6 @@ __device__ __forceinline__ void join_warps(typename Tile::State& st, float* po, 
         l += a == NEG_INF ? b : times_exp2(b, a - n);
       }
       if (warp == 0 && r == 0 && row < rows) ml[row] = make_float2(n, l);
-      if constexpr (ROUNDED) {
-        float lr = 0.f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) lr += sn[k][row] == NEG_INF ? 0.f : times_exp2(sr[k][row], sn[k][row] - n);
-        if (warp == 0 && r == 0) sr[4][row] = lr > 0.f ? l / lr : 1.f;
-      }
       const float f = st.n[h][e] == NEG_INF ? 0.f : fast_exp2(st.n[h][e] - n);
       if (row < rows) {
         float* dst = po + ((size_t)warp * ROWS + row) * D;
@@ -436,10 +420,8 @@ __device__ __forceinline__ void join_warps(typename Tile::State& st, float* po, 
       }
     }
   __syncthreads();
-  for (int i = threadIdx.x; i < rows * D; i += 128) {
-    const float sum = (po[i] + po[i + ROWS * D]) + (po[i + 2 * ROWS * D] + po[i + 3 * ROWS * D]);
-    po[i] = ROUNDED ? sum * sr[4][i / D] : sum;
-  }
+  for (int i = threadIdx.x; i < rows * D; i += 128)
+    po[i] = (po[i] + po[i + ROWS * D]) + (po[i + 2 * ROWS * D] + po[i + 3 * ROWS * D]);
   __syncthreads();
 }
 

@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(THREADS, FewCfg<D, KEYS, NH>::PER_SM)
   extern __shared__ __align__(1024) uint8_t smem[];
   float* po = reinterpret_cast<float*>(smem);  // [4][ROWS][D]
   __shared__ uint64_t full[4][C::SLOTS];
-  __shared__ float sn[4][16], sl[4][16], sr[5][16];
+  __shared__ float sn[4][16], sl[4][16];
   __shared__ float2 ml[ROWS];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, q = lane & 3;
   uint8_t* ring = smem + warp * C::SLOTS * Tile::BYTES;
@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(THREADS, FewCfg<D, KEYS, NH>::PER_SM)
     }
     if (failed)  // copies still in flight land before their memory is used again (bounded)
       for (; s < got; ++s) wait(s, 100000000ull);
-    join_warps<Tile, D, true>(st, po, sn, sl, ml, rows, sr);
+    join_warps<Tile, D>(st, po, sn, sl, ml, rows);
     if (w.slot < 0) {
       for (int i = threadIdx.x; i < rows * D / 2; i += THREADS) {
         const int row = 2 * i / D, c = 2 * i - row * D;
