@@ -23,6 +23,13 @@ namespace pisa {
 
 constexpr int PAGED_KT = 128;  // keys a step
 
+// A job that spans blocks, written by the one where it begins: its parts are slot0, then the first slots of the blocks behind
+// it up to c1 (c1 < 0: there is no such job).
+struct __align__(16) PagedSplit {
+  int b, first, n, L;  // sequence; its first row, rows and keys before them
+  int head, tile, c1, slot0;
+};
+
 struct PagedParams {
   const uint16_t* q;
   const uint16_t* K;
@@ -36,13 +43,11 @@ struct PagedParams {
   float* lse;                // nullable
   float* part_o;             // [2 blocks][ROWS][d] output sums relative to the row maximum
   float2* part_ml;           // [2 blocks][ROWS] row maximum (log2 units) and sum
-  long long* base;           // [2 B + 3] first position of each sequence, the line's length, `extra`, first job of each
-                             // sequence, their number
+  PagedSplit* split;         // [blocks] the job that a block leaves unfinished, where it has its beginning
   long long q_stride;        // elements between rows of q
   int B, R, H_q, H_kv, GQ, P, M;
   int s_bits, gq_bits, row_bits;  // S, G_Q and ROWS are 2 to these
   int causal, accumulate;
-  int by_job;                // the joining kernel's blockIdx.x is a job; else a block in which one begins
   int blocks, stop;          // thread blocks the line is cut for; steps that a second job in a block costs
   float sl2;
   uint32_t* err;
@@ -155,6 +160,7 @@ struct PagedLine {
   long long at, end;  // next position and end of the range
   long long gbase;    // first position of the current sequence
   long long job_end;  // the position behind the current job
+  long long length;   // the line's
   int b;              // current sequence
   short extra;        // empty steps before a job's own
   bool begun;         // a segment of the range is behind
@@ -163,8 +169,8 @@ struct PagedLine {
   int head, tile, k0, k1;  // KV head, tile, steps [k0, k1) of the job
   int slot;                // -1: the whole job; else the part's slot (2 block + 0 or 1)
 
-  // Warp-wide.  `record`: this warp writes the sequences' first positions and reports bad inputs.
-  __device__ __forceinline__ void init(const PagedParams& p, int block, bool record) {
+  // Warp-wide.  `report`: this warp reports bad inputs.
+  __device__ __forceinline__ void init(const PagedParams& p, int block, bool report) {
     const int lane = threadIdx.x & 31;
     begun = false;
     b = 0;
@@ -191,7 +197,7 @@ struct PagedLine {
       S += __shfl_xor_sync(0xffffffffu, S, o);
       jobs += __shfl_xor_sync(0xffffffffu, jobs, o);
     }
-    if (record && any_bad) report_error(p.err, ERR_BAD_INDEX);
+    if (report && any_bad) report_error(p.err, ERR_BAD_INDEX);
     const PagedCut cut = paged_cut_of(p, S, jobs);
     extra = (short)cut.extra;
     at = end = 0;
@@ -199,16 +205,12 @@ struct PagedLine {
       at = cut.start(block);
       end = cut.start(block + 1);
     }
-    if (record && lane == 0) {
-      p.base[p.B] = cut.S;
-      p.base[p.B + 1] = extra;
-      p.base[2 * p.B + 2] = jobs;
-    }
-    if (at >= end && !record) return;
+    length = cut.S;
+    if (at >= end) return;
     // the sequence that holds position `at`
-    long long before = 0, jobs_before = 0;
+    long long before = 0;
     bool found = false;
-    for (int i0 = 0; i0 < p.B && !(found && !record); i0 += 32) {
+    for (int i0 = 0; i0 < p.B && !found; i0 += 32) {
       const int i = i0 + lane;
       const long long mine_all = i < p.B ? p.H_kv * Jobs(p, seq(i)).span(extra) : 0;
       long long x = mine_all;
@@ -216,20 +218,6 @@ struct PagedLine {
       for (int o = 1; o < 32; o <<= 1) {
         const long long y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
-      }
-      if (record) {
-        const int mine_jobs = i < p.B ? p.H_kv * Jobs(p, seq(i)).tiles : 0;
-        long long y = mine_jobs;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const long long z = __shfl_up_sync(0xffffffffu, y, o);
-          if (lane >= o) y += z;
-        }
-        if (i < p.B) {
-          p.base[i] = before + x - mine_all;
-          p.base[p.B + 2 + i] = jobs_before + y - mine_jobs;
-        }
-        jobs_before += __shfl_sync(0xffffffffu, y, 31);
       }
       const unsigned past = __ballot_sync(0xffffffffu, before + x > at);
       if (past && !found) {
@@ -286,44 +274,23 @@ struct PagedLine {
     }
   }
 
-  // For the kernel that joins: moves to job `index`, or to the job that begins in block `index` and goes on behind it.
-  // False if there is none, or a block had all of it.  Its parts: slot0 of block c0, then the first slots of blocks c0 + 1
-  // .. c1.
-  __device__ __forceinline__ bool split_job(const PagedParams& p, int index, int& c0, int& c1, int& slot0) {
-    const PagedCut cut = paged_cut(p, p.base[p.B], (int)p.base[p.B + 1]);
-    if (cut.S == 0 || index >= (p.by_job ? p.base[2 * p.B + 2] : cut.blocks)) return false;
-    // the last sequence whose first job, or first position, is at or before it
-    const long long* first = p.by_job ? p.base + p.B + 2 : p.base;
-    const long long want = p.by_job ? index : cut.start(index + 1) - 1;
-    int lo = 0, hi = p.B - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (first[mid] <= want)
-        lo = mid;
-      else
-        hi = mid - 1;
-    }
-    bool bad;
-    b = lo;
-    s = paged_seq(p, lo, bad);
-    const Jobs j(p, s);
-    if (j.tiles == 0) return false;
-    long long off = want - first[lo];
-    const long long span = j.span(cut.extra);
-    if (p.by_job) {
-      head = (int)whole_quotient(off, j.tiles);
-      tile = (int)(off - (long long)head * j.tiles);
-    } else {
-      head = (int)whole_quotient(off, span);
-      tile = j.tile_at(off - head * span, cut.extra);
-    }
-    const long long s0 = p.base[lo] + head * span + j.before(tile) + (long long)tile * cut.extra, s1 = s0 + cut.extra;
-    c0 = cut.block_of(s1);  // (s0: its first position, s1: its first step)
-    if (!p.by_job && c0 != index) return false;
-    // (in range as long as nobody changes the lengths under the call)
-    c1 = min(cut.block_of(s1 + j.steps(tile) - 1), p.blocks - 1);
-    slot0 = 2 * c0 + (cut.start(c0) >= s0 ? 0 : 1);  // 1: the block had a job before
-    return c1 > c0;
+  // Behind the last segment: the job that goes on in the next blocks, if it begins in this one.
+  __device__ __forceinline__ PagedSplit split(const PagedParams& p, int block) const {
+    PagedSplit x = {b, s.first, s.n, s.L, head, tile, -1, slot};
+    if (begun && slot >= 0 && k0 == 0)
+      x.c1 = PagedCut{length, (int)max(min(length, (long long)p.blocks), 1ll), extra}.block_of(job_end - 1);
+    if (x.c1 <= block) x.c1 = -1;
+    return x;
+  }
+  // For the kernel that joins.
+  __device__ __forceinline__ bool take(const PagedSplit& x) {
+    b = x.b;
+    s.first = x.first;
+    s.n = x.n;
+    s.L = x.L;
+    head = x.head;
+    tile = x.tile;
+    return x.c1 >= 0;
   }
 };
 

@@ -157,26 +157,26 @@ __global__ void __launch_bounds__(THREADS, FewCfg<D, KEYS, NH>::PER_SM)
     fence_proxy_async();  // the next copies go where po was
     __syncthreads();
   }
+  if (threadIdx.x == 0) p.split[blockIdx.x] = w.split(p, blockIdx.x);
 }
 
-// Joins the parts of the jobs that span blocks: blockIdx.x finds a job, blockIdx.y takes its share of the job's rows.  A row
-// is joined by one warp where there are few parts, by four or all sixteen where there are more: they take the parts in
-// turn, BATCH of them in flight, and meet in shared memory.  (Two or four warps a row, a row at a time, and a block for
-// two rows: 30 us behind 880 jobs of 256 rows, d = 64.)
-constexpr int JOIN_WARPS = 16;
-template <int D>
-__global__ void __launch_bounds__(32 * JOIN_WARPS, 3) paged_join_kernel(PagedParams p) {
-  constexpr int V = D / 32, BATCH = 4;
-  __shared__ float so[JOIN_WARPS][D];
-  __shared__ float2 sml[JOIN_WARPS];
+// Joins the parts of the jobs that span blocks: blockIdx.x is the block where the job begins, blockIdx.y takes its share of
+// the job's rows.  A row is joined by one warp where there are few parts, by more where there are more: they take the parts
+// in turn, BATCH of them in flight, and meet in shared memory.
+template <int D, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS) paged_join_kernel(PagedParams p) {
+  constexpr int V = D / 32, BATCH = 4, WARP_BITS = WARPS == 16 ? 4 : 2;
+  __shared__ float so[WARPS][D];
+  __shared__ float2 sml[WARPS];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_wait();
+  const PagedSplit x = p.split[blockIdx.x];
   PagedWalk w;
-  int c0, c1, slot0;
-  if (!w.split_job(p, blockIdx.x, c0, c1, slot0)) return;
-  const int parts = c1 - c0 + 1, bits = parts <= 4 ? 0 : parts <= 32 ? 2 : 4, W = 1 << bits;  // warps a row
+  if (!w.take(x)) return;
+  const int c0 = blockIdx.x, c1 = x.c1, slot0 = x.slot0;
+  const int parts = c1 - c0 + 1, bits = parts <= 4 ? 0 : parts <= 32 ? 2 : WARP_BITS, W = 1 << bits;  // warps a row
   const int turn = warp & (W - 1), rows = w.rows(p);
-  for (int row0 = blockIdx.y << (4 - bits); row0 < rows; row0 += (int)gridDim.y << (4 - bits)) {
+  for (int row0 = blockIdx.y << (WARP_BITS - bits); row0 < rows; row0 += (int)gridDim.y << (WARP_BITS - bits)) {
     const int row = row0 + (warp >> bits);
     const bool live = row < rows;
     float m = NEG_INF, l = 0.f, acc[V];
@@ -304,7 +304,7 @@ int bits_of(int x) {  // of a power of two
 size_t paged_workspace_bytes(const Problem& p, const Pages& pg) {
   const Plan plan = paged_plan(p, pg);
   const size_t parts = (size_t)2 * plan.blocks * plan.rows;
-  return up256(parts * p.d * 4) + up256(parts * 8) + up256((size_t)(2 * p.B + 3) * 8);
+  return up256(parts * p.d * 4) + up256(parts * 8) + up256((size_t)plan.blocks * sizeof(PagedSplit));
 }
 
 cudaError_t launch_paged_attn(const uint16_t* q, long long q_stride, const uint16_t* Kp, const uint16_t* Vp,
@@ -343,7 +343,7 @@ cudaError_t launch_paged_attn(const uint16_t* q, long long q_stride, const uint1
   at += up256(parts * pr.d * 4);
   p.part_ml = reinterpret_cast<float2*>(at);
   at += up256(parts * 8);
-  p.base = reinterpret_cast<long long*>(at);
+  p.split = reinterpret_cast<PagedSplit*>(at);
   cudaError_t e;
   if (plan.tc)
     e = launch_paged_tc(p, pr.d, s);
@@ -352,15 +352,13 @@ cudaError_t launch_paged_attn(const uint16_t* q, long long q_stride, const uint1
   else
     e = pg.s_bits > 4 ? launch_few_rows<64, 32>(p, s) : launch_few_rows<64, 16>(p, s);
   if (e != cudaSuccess) return e;
-  // The joining kernel's blocks: one a job where there are fewer of them than blocks, which then have many parts each and
-  // get several blocks for their rows.
+  // blocks for the rows of a job that spans blocks: many where there are few jobs, which then have many parts
   const long long rows = (long long)p.R * p.GQ, jobs = p.H_kv * (rows / plan.rows + std::min<long long>(p.B, rows));
-  p.by_job = jobs <= p.blocks;
-  const int x = p.by_job ? (int)jobs : p.blocks;
-  const int most = plan.tc ? plan.rows / 16 : plan.rows;
-  const int y = std::min(most, std::max(plan.tc ? 4 : 1, num_sms * 4 / std::max(x, 1)));
-  return launch_pdl(pr.d == 128 ? paged_join_kernel<128> : paged_join_kernel<64>, dim3((unsigned)x, (unsigned)y),
-                    dim3(32 * JOIN_WARPS), 0, s, p);
+  if (plan.tc)
+    return launch_pdl(pr.d == 128 ? paged_join_kernel<128, 16> : paged_join_kernel<64, 16>,
+                      dim3((unsigned)p.blocks, jobs < num_sms ? 16 : 4), dim3(32 * 16), 0, s, p);
+  return launch_pdl(pr.d == 128 ? paged_join_kernel<128, 4> : paged_join_kernel<64, 4>,
+                    dim3((unsigned)p.blocks, (unsigned)(jobs < num_sms ? plan.rows : plan.rows / 4)), dim3(32 * 4), 0, s, p);
 }
 
 }  // namespace pisa

@@ -493,6 +493,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
     }
+    if (warp == 0 && lane == 0) p.split[block] = walk.now().split(p, block);
   } else {
     // The producing and issuing warps are two of one warpgroup: all of it changes its registers by one instruction.
     set_regs_down<REGS_ISSUE>();

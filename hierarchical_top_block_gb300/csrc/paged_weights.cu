@@ -351,6 +351,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
         if (lane == 0) mbar_arrive(&sh.l_full[ls]);
       }
     }
+    if (lane == 0) p.split[blockIdx.x] = w.split(p, blockIdx.x);
   }
   tc_fence_before();
   __syncthreads();
@@ -363,11 +364,11 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
 // Adds the parts of the jobs that span blocks, a key a thread.
 __global__ void __launch_bounds__(KEYS) paged_weights_join_kernel(PagedParams p) {
   pdl_wait();
+  const PagedSplit x = p.split[blockIdx.x];
   KeyWalk w;
-  int c0, c1, slot0;
-  if (!w.split_job(p, blockIdx.x, c0, c1, slot0)) return;
-  float sum = p.part_o[(size_t)slot0 * KEYS + threadIdx.x];
-  for (int c = c0 + 1; c <= c1; ++c) sum += p.part_o[(size_t)2 * c * KEYS + threadIdx.x];
+  if (!w.take(x)) return;
+  float sum = p.part_o[(size_t)x.slot0 * KEYS + threadIdx.x];
+  for (int c = blockIdx.x + 1; c <= x.c1; ++c) sum += p.part_o[(size_t)2 * c * KEYS + threadIdx.x];
   put_weight(p, w, w.tile * KEYS + threadIdx.x, sum);
 }
 
@@ -393,7 +394,7 @@ cudaError_t launch_t(const PagedParams& p, cudaStream_t s) {
 }  // namespace
 
 size_t paged_weights_workspace_bytes(const Problem& p) {
-  return up256((size_t)2 * MAX_SMS * KEYS * 4) + up256((size_t)(2 * p.B + 3) * 8);
+  return up256((size_t)2 * MAX_SMS * KEYS * 4) + up256((size_t)MAX_SMS * sizeof(PagedSplit));
 }
 
 cudaError_t launch_paged_weights(const uint16_t* q, long long q_stride, const float* lse, const uint16_t* Kp, float* w,
@@ -429,7 +430,7 @@ cudaError_t launch_paged_weights(const uint16_t* q, long long q_stride, const fl
   const long long steps = keys * (((long long)pr.N * pr.GQ >> p.row_bits) + pr.B) * pr.H_kv;
   p.blocks = (int)std::min<long long>(MAX_SMS, std::max(1ll, steps));
   p.part_o = static_cast<float*>(ws);
-  p.base = reinterpret_cast<long long*>(static_cast<uint8_t*>(ws) + up256((size_t)2 * MAX_SMS * KEYS * 4));
+  p.split = reinterpret_cast<PagedSplit*>(static_cast<uint8_t*>(ws) + up256((size_t)2 * MAX_SMS * KEYS * 4));
   cudaError_t e;
   if (pr.d == 128)
     e = few ? launch_t<128, 16>(p, s) : launch_t<128, 128>(p, s);
