@@ -49,6 +49,7 @@ struct PagedParams {
   int s_bits, gq_bits, row_bits;  // S, G_Q and ROWS are 2 to these
   int causal, accumulate;
   int blocks, stop;          // thread blocks the line is cut for; steps that a second job in a block costs
+  unsigned long long inverse;  // ceil(2^64 / blocks)
   float sl2;
   uint32_t* err;
 };
@@ -135,23 +136,27 @@ struct PagedJobs {
   __device__ __forceinline__ int tile_at(long long x, int extra) const { return tile_of(*this, x, extra); }
 };
 
-// The cut of S positions over `blocks` blocks: every block in use has one at least, so a job's parts are in
-// consecutive blocks.
+// The cut of S positions over the blocks: every block in use has one at least, so a job's parts are in consecutive
+// blocks.  x / blocks of x < 2^64 / blocks as one product: with m = ceil(2^64 / blocks) = (2^64 + e) / blocks, e < blocks,
+// x m / 2^64 exceeds x / blocks by x e / (blocks 2^64) < 1 / blocks.
 struct PagedCut {
   long long S;
-  int blocks, extra;
-  __device__ __forceinline__ long long start(int block) const { return whole_quotient(S * block, blocks); }
+  int extra;
+  __device__ __forceinline__ int used(const PagedParams& p) const { return (int)max(min(S, (long long)p.blocks), 1ll); }
+  __device__ __forceinline__ long long start(const PagedParams& p, int block) const {
+    if (S <= p.blocks) return block;
+    return p.blocks == 1 ? S * block : (long long)__umul64hi((unsigned long long)S * block, p.inverse);
+  }
   // The block that holds position s: the last one that starts at or before it.
-  __device__ __forceinline__ int block_of(long long s) const { return (int)whole_quotient((s + 1) * blocks - 1, S); }
+  __device__ __forceinline__ int block_of(const PagedParams& p, long long s) const {
+    return S <= p.blocks ? (int)s : (int)whole_quotient((s + 1) * p.blocks - 1, S);
+  }
 };
-__device__ __forceinline__ PagedCut paged_cut(const PagedParams& p, long long S, int extra) {
-  return PagedCut{S, (int)max(min(S, (long long)p.blocks), 1ll), extra};
-}
 __device__ __forceinline__ PagedCut paged_cut_of(const PagedParams& p, long long S, long long jobs) {
-  const PagedCut c = paged_cut(p, S, 0);
-  const long long len = whole_quotient(S, c.blocks), with = S + jobs * p.stop;
+  if (S <= p.blocks || p.blocks == 1) return PagedCut{S, 0};  // a step a block
+  const long long len = (long long)__umul64hi((unsigned long long)S, p.inverse), with = S + jobs * p.stop;
   // with many jobs a block; or where the longest range is no longer with the empty steps than with one stop
-  return jobs > c.blocks || (jobs > 1 && with <= (len + p.stop) * c.blocks) ? paged_cut(p, with, p.stop) : c;
+  return jobs > p.blocks || (jobs > 1 && with <= (len + p.stop) * p.blocks) ? PagedCut{with, p.stop} : PagedCut{S, 0};
 }
 
 // Walks a block's range job by job.  Every thread of a warp holds the same state.
@@ -176,58 +181,56 @@ struct PagedLine {
     b = 0;
     gbase = 0;
     job_end = -1;
-    bool bad = false, any_bad = false;
-    const PagedSeq mine = paged_seq(p, min(lane, p.B - 1), bad);
-    any_bad = bad;
-    auto seq = [&](int i) {  // a lane's own
-      if (i < 32) return mine;
-      bool x;
-      const PagedSeq s = paged_seq(p, i, x);
-      any_bad = any_bad || x;
-      return s;
-    };
-    long long S = 0, jobs = 0;
-    for (int i = lane; i < p.B; i += 32) {
-      const Jobs j(p, seq(i));
-      jobs += (long long)p.H_kv * j.tiles;
-      S += p.H_kv * j.before(j.tiles);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      S += __shfl_xor_sync(0xffffffffu, S, o);
-      jobs += __shfl_xor_sync(0xffffffffu, jobs, o);
-    }
-    if (report && any_bad) report_error(p.err, ERR_BAD_INDEX);
-    const PagedCut cut = paged_cut_of(p, S, jobs);
-    extra = (short)cut.extra;
-    at = end = 0;
-    if (block < cut.blocks) {
-      at = cut.start(block);
-      end = cut.start(block + 1);
-    }
-    length = cut.S;
-    if (at >= end) return;
-    // the sequence that holds position `at`
-    long long before = 0;
-    bool found = false;
-    for (int i0 = 0; i0 < p.B && !found; i0 += 32) {
-      const int i = i0 + lane;
-      const long long mine_all = i < p.B ? p.H_kv * Jobs(p, seq(i)).span(extra) : 0;
-      long long x = mine_all;
+    // sums over the sequences before and with a lane's own: steps and jobs
+    long long S = 0;
+    int jobs = 0;
+    auto sums = [&](int i0, long long& x, int& n) {
+      x = n = 0;
+      bool bad = false;
+      if (i0 + lane < p.B) {
+        const Jobs j(p, paged_seq(p, i0 + lane, bad));
+        x = p.H_kv * j.before(j.tiles);
+        n = p.H_kv * j.tiles;
+      }
+      if (report && bad) report_error(p.err, ERR_BAD_INDEX);
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const long long y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
+        const int k = __shfl_up_sync(0xffffffffu, n, o);
+        if (lane >= o) x += y, n += k;
       }
-      const unsigned past = __ballot_sync(0xffffffffu, before + x > at);
-      if (past && !found) {
+    };
+    long long x;
+    int n;
+    for (int i0 = 0; i0 < p.B; i0 += 32) {
+      sums(i0, x, n);
+      S += __shfl_sync(0xffffffffu, x, 31);
+      jobs += __shfl_sync(0xffffffffu, n, 31);
+    }
+    const PagedCut cut = paged_cut_of(p, S, jobs);
+    extra = (short)cut.extra;
+    length = cut.S;
+    at = end = 0;
+    if (block >= cut.used(p)) return;
+    at = cut.start(p, block);
+    end = cut.start(p, block + 1);
+    if (at >= end) return;
+    // the sequence that holds position `at`
+    long long before = 0;
+    for (int i0 = 0; i0 < p.B; i0 += 32) {
+      if (p.B > 32) sums(i0, x, n);  // (else they are there)
+      const long long upto = before + x + (long long)n * extra;
+      const unsigned past = __ballot_sync(0xffffffffu, upto > at);
+      if (past) {
         const int l = __ffs(past) - 1;
         b = i0 + l;
-        gbase = before + __shfl_sync(0xffffffffu, x - mine_all, l);
-        found = true;
+        const long long begin = __shfl_sync(0xffffffffu, upto, max(l - 1, 0));
+        gbase = l > 0 ? begin : before;
+        break;
       }
-      before += __shfl_sync(0xffffffffu, x, 31);
+      before = __shfl_sync(0xffffffffu, upto, 31);
     }
+    bool bad;
     s = paged_seq(p, b, bad);
   }
 
@@ -278,7 +281,7 @@ struct PagedLine {
   __device__ __forceinline__ PagedSplit split(const PagedParams& p, int block) const {
     PagedSplit x = {b, s.first, s.n, s.L, head, tile, -1, slot};
     if (begun && slot >= 0 && k0 == 0)
-      x.c1 = PagedCut{length, (int)max(min(length, (long long)p.blocks), 1ll), extra}.block_of(job_end - 1);
+      x.c1 = PagedCut{length, extra}.block_of(p, job_end - 1);
     if (x.c1 <= block) x.c1 = -1;
     return x;
   }

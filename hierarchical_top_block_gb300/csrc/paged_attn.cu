@@ -336,6 +336,7 @@ cudaError_t launch_paged_attn(const uint16_t* q, long long q_stride, const uint1
   p.gq_bits = bits_of(pr.GQ);
   p.row_bits = bits_of(plan.rows);
   p.blocks = plan.blocks;
+  p.inverse = ~0ull / p.blocks + 1;
   p.stop = plan.stop;
   const size_t parts = (size_t)2 * p.blocks * plan.rows;
   uint8_t* at = static_cast<uint8_t*>(ws);

@@ -332,14 +332,20 @@ __global__ void __launch_bounds__(THREADS, 1)
           bool again = blank;
           if (!again) {
             weights();
-            bool far = false;
+            uint32_t far = 0;  // bits of the rows
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               float a, b;
               unpack_f32x2(sum[i], a, b);
-              far = far || a + b > MOST;
+              far |= a + b > MOST ? 1u << i : 0u;
             }
             again = __any_sync(0xffffffffu, far);
+            if (again) {  // (what lies in the rows behind the tile's last asks for nothing)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (row0 + 8 * i >= sg.rows) far &= ~(1u << i);
+              again = __any_sync(0xffffffffu, far);
+            }
           }
           if (again) {
             // the references follow the maxima, O (of the steps before) with them
@@ -360,7 +366,7 @@ __global__ void __launch_bounds__(THREADS, 1)
               const float to = fmaxf(m[i], a * p.sl2);
               f[i] = to == NEG_INF ? 1.f : fast_exp2(m[i] - to);
               m[i] = to;
-              none_seen = none_seen || to == NEG_INF;
+              none_seen = none_seen || (row0 + 8 * i < sg.rows && to == NEG_INF);
               l2[i] = mul_f32x2(l2[i], pack_f32x2(f[i], f[i]));
             }
             blank = __any_sync(0xffffffffu, none_seen);

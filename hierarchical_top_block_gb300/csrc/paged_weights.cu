@@ -429,6 +429,7 @@ cudaError_t launch_paged_weights(const uint16_t* q, long long q_stride, const fl
   const long long keys = (((long long)pg.M << pg.s_bits) + KEYS - 1) / KEYS;  // tiles a sequence may have
   const long long steps = keys * (((long long)pr.N * pr.GQ >> p.row_bits) + pr.B) * pr.H_kv;
   p.blocks = (int)std::min<long long>(MAX_SMS, std::max(1ll, steps));
+  p.inverse = ~0ull / p.blocks + 1;
   p.part_o = static_cast<float*>(ws);
   p.split = reinterpret_cast<PagedSplit*>(static_cast<uint8_t*>(ws) + up256((size_t)2 * MAX_SMS * KEYS * 4));
   cudaError_t e;
