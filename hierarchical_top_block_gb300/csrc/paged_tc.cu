@@ -43,17 +43,17 @@ static_assert(2 * REGS_SOFTMAX + REGS_ISSUE <= 3 * 168, "registers of the block"
 template <int D>
 struct Cfg {
   static constexpr int NB = D == 64 ? 3 : 2;         // buffers of S
-  static constexpr int SLOTS = D == 64 ? 9 : 5;      // K and V tiles
+  static constexpr int K_SLOTS = D == 64 ? 5 : 3, V_SLOTS = D == 64 ? 4 : 2;  // tiles
   static constexpr uint32_t QT_BYTES = 128 * D * 2;  // 128 query rows
   static constexpr uint32_t TILE = KT * D * 2;       // a K or V tile
-  static constexpr size_t TILES = 2 * QT_BYTES + SLOTS * TILE;
+  static constexpr size_t TILES = 2 * QT_BYTES + (K_SLOTS + V_SLOTS) * TILE;
   static_assert(NB * 128 + 2 * D <= 512, "tensor memory");
 };
 
 template <int D>
 struct Bars {
   uint64_t q_full, q_empty;             // Q copied; no longer read
-  uint64_t full[Cfg<D>::SLOTS], empty[Cfg<D>::SLOTS];  // K and V tiles
+  uint64_t k_full[Cfg<D>::K_SLOTS], k_empty[Cfg<D>::K_SLOTS], v_full[Cfg<D>::V_SLOTS], v_empty[Cfg<D>::V_SLOTS];
   uint64_t s_full[Cfg<D>::NB], p_full[Cfg<D>::NB], o_done[Cfg<D>::NB];  // of a buffer of S: made, P in it, O += P V made
   uint64_t x_full, x_done;              // the streams' meeting at the end of a segment
   uint64_t drain;
@@ -107,15 +107,13 @@ __device__ __forceinline__ void set_regs_down() {
 // A segment's streams: by rows (`lag` 1: both use every tile) or by steps (`lag` 2: stream = step mod 2).  Its products
 // are numbered in the order in which they are made, streams in turn: product u is of stream u mod 2 and step u / 2 (by
 // rows) or u (by steps), and S of u lies in buffer (products before the segment + u) mod NB.  S of u + NB is issued right
-// behind the O += P V of u, which reads P from the same buffer.  So the tiles are wanted in this order: K of the first
-// `head` steps, then V j and K j + head.
+// behind the O += P V of u, which reads P from the same buffer.
 struct Segment {
-  int rows, nk, lag, head;
-  __device__ __forceinline__ Segment(const PagedParams& p, const PagedWalk& w, int buffers) {
+  int rows, nk, lag;
+  __device__ __forceinline__ Segment(const PagedParams& p, const PagedWalk& w) {
     rows = w.rows(p);
     nk = w.k1 - w.k0;
     lag = rows > ROWS / 2 ? 1 : 2;
-    head = min(lag == 1 ? (buffers + 1) / 2 : buffers, nk);
   }
   __device__ __forceinline__ int products() const { return lag == 1 ? 2 * nk : nk; }
 };
@@ -190,9 +188,13 @@ __global__ void __launch_bounds__(THREADS, 1)
       prefetch_map(&mapV);
       mbar_init(&bar.q_full, 1);
       mbar_init(&bar.q_empty, 1);
-      for (int i = 0; i < C::SLOTS; ++i) {
-        mbar_init(&bar.full[i], 1);
-        mbar_init(&bar.empty[i], 1);
+      for (int i = 0; i < C::K_SLOTS; ++i) {
+        mbar_init(&bar.k_full[i], 1);
+        mbar_init(&bar.k_empty[i], 1);
+      }
+      for (int i = 0; i < C::V_SLOTS; ++i) {
+        mbar_init(&bar.v_full[i], 1);
+        mbar_init(&bar.v_empty[i], 1);
       }
       for (int i = 0; i < C::NB; ++i) {
         mbar_init(&bar.s_full[i], 1);
@@ -235,7 +237,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     bool failed = false;
     for (bool more_work = any_work; !failed && more_work; more_work = walk.next(p, block)) {
       const PagedWalk& w = walk.now();
-      const Segment sg(p, w, C::NB);
+      const Segment sg(p, w);
       const int warp_row = (sg.lag == 1 ? 128 * h : 0) + (warp & 3) * 32;  // the warp's first row in the tile
       const int row0 = warp_row + (lane >> 2);                             // the first of the lane's four, 8 apart
       const bool any = warp_row < sg.rows;
@@ -504,23 +506,25 @@ __global__ void __launch_bounds__(THREADS, 1)
     // The producing and issuing warps are two of one warpgroup: all of it changes its registers by one instruction.
     set_regs_down<REGS_ISSUE>();
     if (warp == PRODUCER || warp == PRODUCER2) {
-      // ------------------------------ producers ------------------------------
-      // A copy takes its warp 80 clocks, and a tile of pages of 16 tokens 8 or 16 copies: each warp issues every other.
-      const int which = warp == PRODUCER ? 0 : 1;
+      // ------------------------------ producers: Q and K; V ------------------------------
+      // A warp each: a copy takes its warp 80 clocks, and a tile of pages of 16 tokens 8 or 16 copies.
+      const bool is_v = warp == PRODUCER2;
       Walk walk;
-      walk.start(first, &sh.walks[which == 0 ? 8 : 10]);
+      walk.start(first, &sh.walks[is_v ? 10 : 8]);
       uint32_t seg = 0, nt = 0;  // segments and tiles so far
-      Ring<C::SLOTS> ring;
+      const uint32_t slots = is_v ? C::V_SLOTS : C::K_SLOTS;
+      uint64_t *const full = is_v ? bar.v_full : bar.k_full, *const empty = is_v ? bar.v_empty : bar.k_empty;
+      const CUtensorMap* map = is_v ? &mapV : &mapK;
+      uint32_t slot = 0, phase = 0;
       bool failed = false;
-      const int copy = 2 * lane + which, piece = copy & (DH - 1), box = copy / DH;  // this lane's copy of a tile
-      const int in_tile = box << box_bits;
+      const int piece = lane & (DH - 1), in_tile = lane / DH << box_bits;  // this lane's copy of a tile
       const bool copies = in_tile < KT;
-      uint8_t* const dst = sT + piece * (KT * 128) + in_tile * 128;
+      uint8_t* const dst = sT + (is_v ? C::K_SLOTS * C::TILE : 0) + piece * (KT * 128) + in_tile * 128;
       const int in_page = (1 << p.s_bits) - 1;
       for (bool more_work = any_work; !failed && more_work; more_work = walk.next(p, block)) {
         const PagedWalk& w = walk.now();
-        const Segment sg(p, w, C::NB);
-        if (which == 0) {
+        const Segment sg(p, w);
+        if (!is_v) {
           if (!mbar_wait_warp(&bar.q_empty, (seg & 1) ^ 1, err)) break;
           if (lane == 0) {
             const int streams = sg.lag == 1 ? 2 : 1;
@@ -532,47 +536,36 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
         }
         ++seg;
-        const int total = w.s.L + w.s.n, head = w.head, nk = sg.nk, key0 = w.k0 * KT + in_tile, lead = sg.head;
+        const int total = w.s.L + w.s.n, head = w.head, nk = sg.nk;
+        int key = w.k0 * KT + in_tile;
+        const int end = w.k1 * KT;
         const int32_t* table = p.table + (size_t)w.b * p.M;
-        // the page of this lane's copy of step j (read ahead, so that nobody waits for it)
-        auto entry_of = [&](int j) {
-          const int key = key0 + j * KT;
-          return copies && j < nk && key < total ? __ldg(table + (key >> p.s_bits)) : -1;
-        };
-        int k_next[2] = {entry_of(0), entry_of(1)}, v_next[2] = {entry_of(0), entry_of(1)};
-        int jk = 0, jv = 0;  // the next steps
-        for (int i = 0; i < 2 * nk; ++i) {
-          const bool is_v = jk == nk || (i >= lead && ((i - lead) & 1) == 0);
-          const int j = is_v ? jv++ : jk++, key = key0 + j * KT, later = entry_of(j + 2);
-          int entry;
-          if (is_v) {
-            entry = v_next[0];
-            v_next[0] = v_next[1];
-            v_next[1] = later;
-          } else {
-            entry = k_next[0];
-            k_next[0] = k_next[1];
-            k_next[1] = later;
-          }
-          if (!mbar_wait_warp(&bar.empty[ring.slot], ring.phase ^ 1, err)) {
+        // the page of this lane's copy (read two steps ahead, so that nobody waits for it)
+        auto entry_of = [&](int c) { return copies && c < end && c < total ? __ldg(table + (c >> p.s_bits)) : -1; };
+        int entry = entry_of(key), next = entry_of(key + KT);
+        for (int j = 0; j < nk; ++j, key += KT) {
+          const int later = entry_of(key + 2 * KT);
+          if (!mbar_wait_warp(empty + slot, phase ^ 1, err)) {
             failed = true;
             break;
           }
-          if (lane == 0 && which == 0) mbar_arrive_expect_tx(&bar.full[ring.slot], C::TILE);
+          if (lane == 0) mbar_arrive_expect_tx(full + slot, C::TILE);
+          __syncwarp();
           if (copies)
-            tma_load_4d(dst + ring.slot * C::TILE, is_v ? &mapV : &mapK, &bar.full[ring.slot], 64 * piece, key & in_page, head,
+            tma_load_4d(dst + slot * C::TILE, map, full + slot, 64 * piece, key & in_page, head,
                         (unsigned)entry < (unsigned)p.P ? entry : p.P);
           if (entry >= p.P) report_error(err, ERR_BAD_INDEX);
           __syncwarp();
-          ring.next();
+          entry = next;
+          next = later;
+          if (++slot == slots) slot = 0, phase ^= 1;
           ++nt;
         }
       }
       // copies still in flight land before shared memory goes away (bounded; at once unless a wait failed)
       if (lane == 0) {
-        if (seg > 0 && which == 0) mbar_wait(&bar.q_full, (seg - 1) & 1, err, 100000000ull);
-        for (uint32_t u = nt > C::SLOTS ? nt - C::SLOTS : 0; u < nt; ++u)
-          mbar_wait(&bar.full[u % C::SLOTS], (u / C::SLOTS) & 1, err, 100000000ull);
+        if (seg > 0 && !is_v) mbar_wait(&bar.q_full, (seg - 1) & 1, err, 100000000ull);
+        for (uint32_t u = nt > slots ? nt - slots : 0; u < nt; ++u) mbar_wait(full + u % slots, (u / slots) & 1, err, 100000000ull);
       }
       __syncwarp();
     } else if (warp == ISSUER) {
@@ -586,13 +579,14 @@ __global__ void __launch_bounds__(THREADS, 1)
       // 4096 tokens after 28672 of 32 / 8 heads.  One lane that does everything, 1667 us: issuing wants a converged warp.
       // Two warps in turn, 1720 us: their MMAs mix, and a stream gets its next S later.)
       uint32_t seg = 0, made = 0;  // segments, products so far
-      Ring<C::SLOTS> tiles;        // the next tile
+      Ring<C::K_SLOTS> kr;         // the next tiles
+      Ring<C::V_SLOTS> vr;
       bool failed = false;
       // descriptors of the first tile and Q slot: the others differ in the address field alone (16-byte units of the
       // low word)
       const uint64_t k_desc = smem_desc_sw128(smem_u32(sT), 16, 1024);
       const uint32_t k_hi = (uint32_t)(k_desc >> 32), q_lo = (uint32_t)smem_desc_sw128(smem_u32(sQ), 16, 1024);
-      const uint32_t k_lo = (uint32_t)k_desc, v_lo = (uint32_t)smem_desc_sw128(smem_u32(sT), KT * 128, 1024);
+      const uint32_t k_lo = (uint32_t)k_desc, v_lo = (uint32_t)smem_desc_sw128(smem_u32(sT + C::K_SLOTS * C::TILE), KT * 128, 1024);
       auto desc = [&](uint32_t lo) { return pack_u32x2(lo, k_hi); };  // (8-row groups of 1024 bytes in all of them)
       auto qk = [&](uint32_t buf, int qs, uint32_t slot) {  // S of a buffer = Q (slot qs) K^T
         const uint32_t a = q_lo + qs * (C::QT_BYTES >> 4), b = k_lo + slot * (C::TILE >> 4), d = tmem + 128 * buf;
@@ -611,23 +605,23 @@ __global__ void __launch_bounds__(THREADS, 1)
       };
       for (bool more_work = any_work; !failed && more_work; more_work = walk.next(p, block)) {
         const PagedWalk& w = walk.now();
-        const Segment sg(p, w, C::NB);
+        const Segment sg(p, w);
         const int end = w.s.L + w.s.n - w.k0 * KT;  // the sequence's end, from the segment's first key
         const int all = sg.products();
         const bool by_rows = sg.lag == 1;
         uint32_t ks = 0, vs = 0;  // slots of the K and V tiles in use
         auto score = [&](int u) {  // S of product u (elected lane)
           qk((made + u) % C::NB, by_rows ? u & 1 : 0, ks);
-          if (!by_rows || (u & 1)) umma_commit(&bar.empty[ks]);
+          if (!by_rows || (u & 1)) umma_commit(&bar.k_empty[ks]);
           if (u == all - 1) umma_commit(&bar.q_empty);
         };
         if (!mbar_wait_warp(&bar.q_full, seg & 1, err)) break;
         ++seg;
         for (int u = 0; u < min(C::NB, all) && !failed; ++u) {
           if (!by_rows || (u & 1) == 0) {
-            failed = !mbar_wait_warp(&bar.full[tiles.slot], tiles.phase, err);
-            ks = tiles.slot;
-            tiles.next();
+            failed = !mbar_wait_warp(&bar.k_full[kr.slot], kr.phase, err);
+            ks = kr.slot;
+            kr.next();
           }
           tc_fence_after();
           if (!failed && elect_one()) score(u);
@@ -643,16 +637,16 @@ __global__ void __launch_bounds__(THREADS, 1)
           uint64_t *v_bar = p_bar, *k_bar = p_bar;
           uint32_t v_phase = p_phase, k_phase = p_phase;
           if (new_v) {
-            v_bar = &bar.full[tiles.slot];
-            v_phase = tiles.phase;
-            vs = tiles.slot;
-            tiles.next();
+            v_bar = &bar.v_full[vr.slot];
+            v_phase = vr.phase;
+            vs = vr.slot;
+            vr.next();
           }
           if (new_k) {
-            k_bar = &bar.full[tiles.slot];
-            k_phase = tiles.phase;
-            ks = tiles.slot;
-            tiles.next();
+            k_bar = &bar.k_full[kr.slot];
+            k_phase = kr.phase;
+            ks = kr.slot;
+            kr.next();
           }
           const bool v = mbar_try_wait(v_bar, v_phase), k = mbar_try_wait(k_bar, k_phase), pp = mbar_try_wait(p_bar, p_phase);
           if (!__all_sync(0xffffffffu, v && k && pp))
@@ -662,7 +656,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int v_valid = end - (by_rows ? u >> 1 : u) * KT;
             if (v_valid < KT) {
               // values past the sequence's end are multiplied by weights of 0: they have to be finite
-              uint8_t* t = sT + vs * C::TILE;
+              uint8_t* t = sT + (C::K_SLOTS + vs) * C::TILE;
               for (int c = 0; c < DH; ++c)
                 for (int i = max(0, v_valid) * 8 + lane; i < KT * 8; i += 32)
                   *reinterpret_cast<uint4*>(t + c * (KT * 128) + i * 16) = make_uint4(0, 0, 0, 0);
@@ -673,7 +667,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           tc_fence_after();
           if (elect_one()) {
             pv(g % C::NB, u & 1, vs, u < 2);
-            if (!by_rows || (u & 1)) umma_commit(&bar.empty[vs]);
+            if (!by_rows || (u & 1)) umma_commit(&bar.v_empty[vs]);
             if (more) score(u + C::NB);
           }
           __syncwarp();
