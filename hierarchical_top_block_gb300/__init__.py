@@ -724,7 +724,17 @@ def _page_pool(Kp, Vp, page_table, seq_len, row_start, dev):
     _fits(page_table, "page_table", (B, M), torch.int32, dev)
     _fits(seq_len, "seq_len", (B,), torch.int32, dev)
     _fits(row_start, "row_start", (B + 1,), torch.int32, dev)
-    return B, H_kv, d, pisa_pages(P, S, M)
+    return B, H_kv, d, (P, S, M)
+
+
+@functools.lru_cache(maxsize=256)
+def _paged_sizes(B, R, H_q, H_kv, d, causal, scale, pages):
+    """The shape, parameters and pages of a call, and the bytes of scratch that its attention and its weights want (at
+    least 256; a call that the library refuses it refuses itself)."""
+    shape, params, pages = pisa_shape(B, R, H_q, H_kv, d, 0), pisa_params(64, 2, 1, causal, scale, 0), pisa_pages(*pages)
+    attn = lib().pisa_paged_attn_workspace_bytes(shape, params, pages)
+    weights = lib().pisa_paged_weights_workspace_bytes(shape, params, pages)
+    return shape, params, pages, max(attn, 256), max(weights, 256)
 
 
 def pisa_paged_write(k, v, Kp, Vp, page_table, seq_len, row_start=None, w=None) -> None:
@@ -739,24 +749,13 @@ def pisa_paged_write(k, v, Kp, Vp, page_table, seq_len, row_start=None, w=None) 
     R = k.shape[0]
     k_stride, v_stride = _token_rows(k, "k", R, H_kv, d, dev), _token_rows(v, "v", R, H_kv, d, dev)
     _fits(w, "w", Kp.shape[:3], torch.float32, dev)
+    shape, _, pages, _, _ = _paged_sizes(B, R, H_kv, H_kv, d, 1, 0.0, pages)
     _call(lib().pisa_paged_write, "pisa_paged_write", dev, k.data_ptr(), v.data_ptr(), Kp.data_ptr(), Vp.data_ptr(),
-          _addr(w), page_table.data_ptr(), seq_len.data_ptr(), _addr(row_start), k_stride, v_stride,
-          pisa_shape(B, R, H_kv, H_kv, d, 0), pages)
+          _addr(w), page_table.data_ptr(), seq_len.data_ptr(), _addr(row_start), k_stride, v_stride, shape, pages)
 
 
 def pisa_paged_attn_workspace_bytes(shape: pisa_shape, params: pisa_params, pages: pisa_pages) -> int:
     return int(lib().pisa_paged_attn_workspace_bytes(shape, params, pages))
-
-
-@functools.lru_cache(maxsize=256)
-def _paged_sizes(B, R, H_q, H_kv, d, causal, scale, P, S, M):
-    """The shape, parameters and pages of a call, and the bytes of scratch its attention wants (at least 256)."""
-    shape, params = pisa_shape(B, R, H_q, H_kv, d, 0), pisa_params(64, 2, 1, causal, scale, 0)
-    pages = pisa_pages(P, S, M)
-    need = lib().pisa_paged_attn_workspace_bytes(shape, params, pages)
-    if need == 0 and B > 0 and R > 0:
-        raise PisaError(2, "paged cache: unsupported shape or parameters")
-    return shape, params, pages, max(need, 256)
 
 
 def pisa_paged_attn(q, Kp, Vp, page_table, seq_len, row_start=None, causal: bool = True, scale: float = 0.0, o=None,
@@ -782,8 +781,7 @@ def pisa_paged_attn(q, Kp, Vp, page_table, seq_len, row_start=None, causal: bool
         _fits(lse, "lse", want[:2], torch.float32, dev)
     elif want_lse:
         lse = torch.empty(want[:2], dtype=torch.float32, device=q.device)
-    shape, params, pages, need = _paged_sizes(B, R, H_q, H_kv, d, 1 if causal else 0, float(scale), pages.pages,
-                                              pages.page_size, pages.max_pages)
+    shape, params, pages, need, _ = _paged_sizes(B, R, H_q, H_kv, d, 1 if causal else 0, float(scale), pages)
     if ws is None:
         ws = torch.empty(need, dtype=torch.uint8, device=q.device)
     else:
@@ -813,8 +811,11 @@ def pisa_paged_weights(q, lse, Kp, w, page_table, seq_len, row_start=None, accum
     q_stride = _token_rows(q, "q", R, H_q, d, dev)
     _fits(lse, "lse", (R, H_q), torch.float32, dev)
     _fits(w, "w", Kp.shape[:3], torch.float32, dev)
-    shape, params = pisa_shape(B, R, H_q, H_kv, d, 0), pisa_params(64, 2, 1, 1 if causal else 0, float(scale), 0)
-    ws = _workspace(ws, lib().pisa_paged_weights_workspace_bytes(shape, params, pages), q.device)
+    shape, params, pages, _, need = _paged_sizes(B, R, H_q, H_kv, d, 1 if causal else 0, float(scale), pages)
+    if ws is None:
+        ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+    else:
+        ws = _workspace(ws, need, q.device)
     _call(lib().pisa_paged_weights, "pisa_paged_weights", dev, q.data_ptr(), lse.data_ptr(), Kp.data_ptr(), w.data_ptr(),
           page_table.data_ptr(), seq_len.data_ptr(), _addr(row_start), ws.data_ptr(), ws.numel(), 1 if accumulate else 0,
           q_stride, shape, params, pages)
@@ -843,7 +844,7 @@ def pisa_paged_evict(Kp, Vp, w, page_table, seq_len, new_table, keep: int, sinks
     if kept is None and want_kept:
         kept = torch.empty((B, H_kv, max(keep, 0)), dtype=torch.int32, device=Kp.device)
     _fits(kept, "kept", (B, H_kv, keep), torch.int32, dev)
-    shape = pisa_shape(B, 0, H_kv, H_kv, d, 0)
+    shape, _, pages, _, _ = _paged_sizes(B, 0, H_kv, H_kv, d, 1, 0.0, pages)
     if kept is None:
         ws = _workspace(ws, pisa_paged_evict_workspace_bytes(shape, pages, keep), Kp.device)
     _call(lib().pisa_paged_evict, "pisa_paged_evict", dev, Kp.data_ptr(), Vp.data_ptr(), w.data_ptr(),

@@ -466,7 +466,8 @@ def test_same_every_time_and_in_graphs():
     o, lse = pisa.pisa_paged_attn(q, c.K, c.V, c.table, c.len, row_start=c.rows)
     pisa.pisa_paged_weights(q, lse, c.K, w, c.table, c.len, row_start=c.rows)
     first = [x.clone() for x in (o, lse, w)]
-    shape, params, pages, need = pisa._paged_sizes(4, c.R, 16, 2, 128, 1, 0.0, c.P, 16, c.M)
+    shape, params = pisa.make_shape(4, c.R, 16, 2, 128), pisa.make_params(1)
+    need = pisa.pisa_paged_attn_workspace_bytes(shape, params, pisa.pisa_pages(c.P, 16, c.M))
     ws = torch.empty(need, dtype=torch.uint8, device=DEV)
     kept = torch.empty((4, 2, 150), dtype=torch.int32, device=DEV)
     new_len = i32(0, 0, 0, 0)
