@@ -244,6 +244,65 @@ def test_attn_nan_shows():
     assert o.isnan().all() and lse.isnan().all()
 
 
+@pytest.mark.parametrize("new", [[1, 1, 1], [200, 3, 90]])
+def test_one_page_a_sequence(new):
+    """A cache [B][H_kv][N_cap][d] of the other entry points, as pages; and the same keys in small pages."""
+    lens, S = [2000, 77, 500], 4096
+    c = Paged(lens, new, 2, 128, S, M=1, spare=0)
+    q = c.rand(c.R, 8, 128, scale=1.5)
+    o, lse = pisa.pisa_paged_attn(q, c.K, c.V, c.table, c.len, row_start=c.rows)
+    wo, wl, bo, bl = H.attend_many(c, q)
+    R.close(o, wo, bo, "o")
+    R.close(lse, wl, bl, "lse")
+    w = c.w.clone()
+    pisa.pisa_paged_weights(q, lse, c.K, w, c.table, c.len, row_start=c.rows, accumulate=False)
+    small = Paged(lens, new, 2, 128, 16, seed=5)
+    for b in range(3):
+        n = lens[b] + new[b]
+        small.put(b, c.get(c.K, b, n), c.get(c.V, b, n))
+    o2, lse2 = pisa.pisa_paged_attn(q, small.K, small.V, small.table, c.len, row_start=c.rows)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    w2 = small.w.clone()
+    pisa.pisa_paged_weights(q, lse, small.K, w2, small.table, c.len, row_start=c.rows, accumulate=False)
+    for b in range(3):
+        assert torch.equal(c.get(w, b, lens[b] + new[b]), small.get(w2, b, lens[b] + new[b]))
+    no_error()
+
+
+def test_a_thousand_sequences():
+    lens, new = [(7 * i) % 40 for i in range(1100)], [1 if i % 5 else 0 for i in range(1100)]
+    c = Paged(lens, new, 2, 64, 16, seed=1)
+    q = c.rand(c.R, 4, 64, scale=1.5)
+    o, lse = pisa.pisa_paged_attn(q, c.K, c.V, c.table, c.len, row_start=c.rows)
+    wo, wl, bo, bl = H.attend_many(c, q)
+    R.close(o, wo, bo, "o")
+    R.close(lse, wl, bl, "lse")
+    w = c.w.clone()
+    pisa.pisa_paged_weights(q, lse, c.K, w, c.table, c.len, row_start=c.rows, accumulate=False)
+    want, bound = H.weights(c, q, lse)
+    live = ~want.isnan()
+    R.close(w[live], want[live], bound[live], "w")
+    no_error()
+
+
+def test_two_streams():
+    """Calls of two sets of sequences at once, on streams other than the current one, each with its own scratch."""
+    cases = [Paged([3000, 5], [300, 1], 4, 128, 16, seed=1), Paged([100 * i for i in range(30)], [1] * 30, 4, 128, 64, seed=2)]
+    qs = [c.rand(c.R, 16, 128, scale=1.5) for c in cases]
+    want = [pisa.pisa_paged_attn(q, c.K, c.V, c.table, c.len, row_start=c.rows) for c, q in zip(cases, qs)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [[], []]
+    for _ in range(20):
+        for i, (c, q) in enumerate(zip(cases, qs)):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(pisa.pisa_paged_attn(q, c.K, c.V, c.table, c.len, row_start=c.rows))
+    torch.cuda.synchronize()
+    for g, (o, lse) in zip(got, want):
+        assert all(torch.equal(x, o) and torch.equal(y, lse) for x, y in g)
+    no_error()
+
+
 @pytest.mark.parametrize("T,G", [(1, 4), (70, 4)])
 def test_far_pages(T, G):
     """Pages behind 2^31 elements of the pool: offsets of keys, values and weights in 64 bits."""
