@@ -983,7 +983,7 @@ pisa_status pisa_paged_write(const uint16_t* k, const uint16_t* v, uint16_t* Kp,
   if ((rc = device_state(&st)) != PISA_OK) return rc;
   PhaseTimer tm(static_cast<cudaStream_t>(stream));
   const cudaError_t e = launch_paged_write(k, v, k_stride, v_stride, Kp, Vp, w, page_table, seq_len, row_start, p, pg,
-                                           st->num_sms, st->err, static_cast<cudaStream_t>(stream));
+                                           st->err, static_cast<cudaStream_t>(stream));
   tm.mark(PH_PAGED_WRITE);
   return cuda_status(e);
 }

@@ -115,8 +115,7 @@ struct Pages {
 // p.N new tokens' rows into their pages; w (nullable): the weights beside the pages, cleared there.
 cudaError_t launch_paged_write(const uint16_t* k, const uint16_t* v, long long k_stride, long long v_stride, uint16_t* Kp,
                                uint16_t* Vp, float* w, const int32_t* table, const int32_t* seq_len,
-                               const int32_t* row_start, const Problem& p, const Pages& pg, int num_sms, uint32_t* err,
-                               cudaStream_t s);
+                               const int32_t* row_start, const Problem& p, const Pages& pg, uint32_t* err, cudaStream_t s);
 // Attention of p.N new tokens of p.B sequences over their pages.
 size_t paged_workspace_bytes(const Problem& p, const Pages& pg);
 cudaError_t launch_paged_attn(const uint16_t* q, long long q_stride, const uint16_t* Kp, const uint16_t* Vp,

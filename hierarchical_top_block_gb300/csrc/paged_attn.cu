@@ -33,11 +33,14 @@ namespace {
 constexpr int THREADS = 128;
 constexpr int few_blocks(int rows) { return rows > 8 ? 2 : 4; }  // a SM
 
-// Tiles of 8 NH rows.  A block's four warps take the granules of a segment in turn, each with a ring of its own that
+// Tiles of 8 NH rows (few tiles of 8 are as fast as of 16 with many sequences, and 14.4 : 15.7 us with one of 8000 keys).  A
+// block's four warps take the granules of a segment in turn, each with a ring of its own that
 // it fills by TMA.  A granule lies in one page (KEYS <= S).
 template <int D, int KEYS, int NH>
 struct FewCfg {
-  static constexpr int SLOTS = (D == 64 && KEYS == 32) || (NH == 2 && D == 128) ? 2 : KEYS * D == 1024 ? 2 : 1;
+  // Granules a warp has under way: 16 KB a warp with 16 rows, 8 KB with 8, where four blocks a SM have to find room (two of
+  // 8 KB leave it to three: 64 sequences of 8192 keys, 32 / 8 heads, d = 64: 178 us).
+  static constexpr int SLOTS = NH * 2048 / (KEYS * D);
   static constexpr int PER_SM = few_blocks(8 * NH);
   using Tile = CacheTile<D, 16, KEYS, NH>;
   static constexpr uint32_t RING = 4 * SLOTS * Tile::BYTES, OUT = 4 * 8 * NH * D * 4;
@@ -258,6 +261,10 @@ __global__ void __launch_bounds__(32 * WARPS) paged_join_kernel(PagedParams p) {
 
 constexpr int MAX_SMS = 152;  // this GPU's: the scratch does not depend on the device at hand
 
+// Which kernel, by the query rows a sequence has on average (their own numbers are on the device; any kernel takes any).
+// 32 sequences of 8192 keys, 8 KV heads, few-row against tensor-core kernel: d = 64, 8 rows 97 : 95 us, 16 rows 92 : 97, 24
+// rows 166 : 96; d = 128, 8 rows 170 : 168, 16 rows 170 : 171, 24 rows 319 : 172 (the few-row kernel then reads the keys
+// twice).
 struct Plan {
   bool tc;
   int rows, blocks, stop;

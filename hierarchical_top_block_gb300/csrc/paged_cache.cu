@@ -46,10 +46,12 @@ __device__ __forceinline__ int sequence_of(const int32_t* row_start, int B, int 
   return lo < B ? lo : -1;
 }
 
-template <int D, int RPT>
+// A thread has one 16-byte piece of K and of V: four rows' pieces were slower (64000 rows x 8 heads, d = 128: 86 us and 80
+// with one; 64 x 8 rows 6.3 and 4.2).
+template <int D>
 __global__ void __launch_bounds__(WRITE_THREADS) paged_write_kernel(WriteParams p) {
-  constexpr int LANES = D / 8, RPB = WRITE_THREADS / LANES;  // lanes a row, rows a block and step
-  const int part = threadIdx.x % LANES, sub = threadIdx.x / LANES;
+  constexpr int LANES = D / 8, RPB = WRITE_THREADS / LANES;  // lanes a row, rows a block
+  const int part = threadIdx.x % LANES;
   const int cap = p.M << p.s_bits;
   if (blockIdx.x == 0)  // sequences without rows are looked at too
     for (int b = threadIdx.x; b < p.B; b += WRITE_THREADS) {
@@ -57,37 +59,26 @@ __global__ void __launch_bounds__(WRITE_THREADS) paged_write_kernel(WriteParams 
       paged_seq(p.row_start, p.seq_len, p.B, p.R, cap, b, bad);
       if (bad) report_error(p.err, ERR_BAD_INDEX);
     }
-  const long long first = (long long)blockIdx.x * RPB * RPT + sub, all = (long long)p.R * p.H;
-  uint4 x[RPT][2];
-  long long at[RPT];
-#pragma unroll
-  for (int i = 0; i < RPT; ++i) {
-    const long long u = first + (long long)i * RPB;  // row * H + head
-    at[i] = -1;
-    if (u >= all) continue;
-    const int row = (int)whole_quotient(u, p.H), head = (int)(u - (long long)row * p.H);
-#pragma unroll
-    for (int kv = 0; kv < 2; ++kv) x[i][kv] = ldg16(p.x[kv] + row * p.stride[kv] + head * D + part * 8);
-    const int b = sequence_of(p.row_start, p.B, p.R, row);
-    if (b < 0) continue;
-    bool bad;
-    const PagedSeq s = paged_seq(p.row_start, p.seq_len, p.B, p.R, cap, b, bad);
-    const int t = row - s.first;
-    if (t < 0 || t >= s.n) continue;
-    const int c = s.L + t, page = __ldg(p.table + (size_t)b * p.M + (c >> p.s_bits));
-    if ((unsigned)page >= (unsigned)p.P) {
-      report_error(p.err, ERR_BAD_INDEX);
-      continue;
-    }
-    at[i] = (((long long)page * p.H + head) << p.s_bits) + (c & ((1 << p.s_bits) - 1));
+  const long long u = (long long)blockIdx.x * RPB + threadIdx.x / LANES;  // row * H + head
+  if (u >= (long long)p.R * p.H) return;
+  const int row = (int)whole_quotient(u, p.H), head = (int)(u - (long long)row * p.H);
+  const uint4 k = ldg16(p.x[0] + row * p.stride[0] + head * D + part * 8);
+  const uint4 v = ldg16(p.x[1] + row * p.stride[1] + head * D + part * 8);
+  const int b = sequence_of(p.row_start, p.B, p.R, row);
+  if (b < 0) return;
+  bool bad;
+  const PagedSeq s = paged_seq(p.row_start, p.seq_len, p.B, p.R, cap, b, bad);
+  const int t = row - s.first;
+  if (t < 0 || t >= s.n) return;
+  const int c = s.L + t, page = __ldg(p.table + (size_t)b * p.M + (c >> p.s_bits));
+  if ((unsigned)page >= (unsigned)p.P) {
+    report_error(p.err, ERR_BAD_INDEX);
+    return;
   }
-#pragma unroll
-  for (int i = 0; i < RPT; ++i) {
-    if (at[i] < 0) continue;
-#pragma unroll
-    for (int kv = 0; kv < 2; ++kv) *reinterpret_cast<uint4*>(p.y[kv] + at[i] * D + part * 8) = x[i][kv];
-    if (p.w && part == 0) p.w[at[i]] = 0.f;
-  }
+  const long long at = (((long long)page * p.H + head) << p.s_bits) + (c & ((1 << p.s_bits) - 1));
+  *reinterpret_cast<uint4*>(p.y[0] + at * D + part * 8) = k;
+  *reinterpret_cast<uint4*>(p.y[1] + at * D + part * 8) = v;
+  if (p.w && part == 0) p.w[at] = 0.f;
 }
 
 // ---- eviction: the choice ----------------------------------------------------------------
@@ -401,21 +392,16 @@ size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 cudaError_t launch_paged_write(const uint16_t* k, const uint16_t* v, long long k_stride, long long v_stride, uint16_t* Kp,
                                uint16_t* Vp, float* w, const int32_t* table, const int32_t* seq_len,
-                               const int32_t* row_start, const Problem& pr, const Pages& pg, int num_sms, uint32_t* err,
-                               cudaStream_t s) {
+                               const int32_t* row_start, const Problem& pr, const Pages& pg, uint32_t* err, cudaStream_t s) {
   WriteParams p{{k, v}, {Kp, Vp}, w, table, seq_len, row_start, {k_stride, v_stride},
                 pr.B,   pr.N,     pr.H_kv, pg.P, pg.M, pg.s_bits, err};
   const long long rows = (long long)pr.N * pr.H_kv;
   const int rpb = WRITE_THREADS * 8 / pr.d;
-  const int rpt = rows >= 32ll * num_sms * rpb ? 4 : 1;
-  const unsigned grid = (unsigned)((rows + (long long)rpb * rpt - 1) / ((long long)rpb * rpt));
-  if (pr.d == 128) {
-    if (rpt == 4) paged_write_kernel<128, 4><<<grid, WRITE_THREADS, 0, s>>>(p);
-    else paged_write_kernel<128, 1><<<grid, WRITE_THREADS, 0, s>>>(p);
-  } else {
-    if (rpt == 4) paged_write_kernel<64, 4><<<grid, WRITE_THREADS, 0, s>>>(p);
-    else paged_write_kernel<64, 1><<<grid, WRITE_THREADS, 0, s>>>(p);
-  }
+  const unsigned grid = (unsigned)((rows + rpb - 1) / rpb);
+  if (pr.d == 128)
+    paged_write_kernel<128><<<grid, WRITE_THREADS, 0, s>>>(p);
+  else
+    paged_write_kernel<64><<<grid, WRITE_THREADS, 0, s>>>(p);
   return cudaGetLastError();
 }
 
@@ -429,7 +415,8 @@ cudaError_t launch_paged_evict(uint16_t* Kp, uint16_t* Vp, float* w, const int32
   cudaError_t e = allow_shared<paged_pick_kernel>(PICK_CACHED * 4);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  // blocks a head: as many as find room at once (two a SM), where there are keys for them
+  // blocks a head: as many as find room at once (two a SM), where there are keys for them (with 1, 2, 4, 8: 8 heads of 32768
+  // keys 62, 33, 19, 16 us, 64 heads 64, 35, 25, 37, 240 heads of 8000 keys 26, 34, 50, 91)
   unsigned blocks = MAX_CLUSTER;
   while (blocks > 1 && ((long long)pr.B * pr.H_kv * blocks > 2ll * num_sms || ((long long)pg.M << pg.s_bits) <= 1024ll * blocks)) blocks /= 2;
   cfg.gridDim = dim3((unsigned)pr.B * pr.H_kv * blocks);
@@ -446,11 +433,13 @@ cudaError_t launch_paged_evict(uint16_t* Kp, uint16_t* Vp, float* w, const int32
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if ((e = cudaLaunchKernelEx(&cfg, paged_pick_kernel, p)) != cudaSuccess) return e;
-  constexpr int RPT = 4;
-  const int rpb = MOVE_THREADS * 8 / pr.d * RPT;
-  const dim3 grid((unsigned)((keep + rpb - 1) / rpb), (unsigned)(pr.B * pr.H_kv));
-  return launch_pdl(pr.d == 128 ? paged_move_kernel<128, RPT> : paged_move_kernel<64, RPT>, grid, dim3(MOVE_THREADS), 0, s,
-                    p);
+  // two rows a thread where they fill the SMs, one where latency counts (64 x 8192 rows 106.7 us and 109.9 with one, 107.2 with
+  // four; 8 x 250 rows 13.4 and 12.4, 14.4 with four)
+  const int one = MOVE_THREADS * 8 / pr.d, rpt = (long long)pr.B * pr.H_kv * keep >= 32ll * num_sms * one ? 2 : 1;
+  const dim3 grid((unsigned)((keep + one * rpt - 1) / (one * rpt)), (unsigned)(pr.B * pr.H_kv));
+  auto move = pr.d == 128 ? (rpt == 2 ? paged_move_kernel<128, 2> : paged_move_kernel<128, 1>)
+                          : (rpt == 2 ? paged_move_kernel<64, 2> : paged_move_kernel<64, 1>);
+  return launch_pdl(move, grid, dim3(MOVE_THREADS), 0, s, p);
 }
 
 }  // namespace pisa
