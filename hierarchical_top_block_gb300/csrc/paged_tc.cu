@@ -244,9 +244,11 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int total = w.s.L + w.s.n, least = w.seen(p, warp_row);
       const int32_t* table = p.table + (size_t)w.b * p.M;
       // the page of the copy that this lane stands for, of step j (looked at a step later: the load is not waited for)
+      const int first_key = w.k0 * KT, nk = sg.nk, lag = sg.lag;
+      const int look_end = (lane << box_bits) < KT ? min(total, w.k1 * KT) : 0;
       auto look = [&](int j) {
-        const int key = (w.k0 + j) * KT + (lane << box_bits);
-        return (lane << box_bits) < KT && j < sg.nk && key < total ? __ldg(table + (key >> p.s_bits)) : 0;
+        const int key = first_key + j * KT + (lane << box_bits);
+        return key < look_end ? __ldg(table + (key >> p.s_bits)) : 0;
       };
       float m[4];                // references, log2 units
       unsigned long long l2[4];  // a lane's share of the sum, even and odd columns
@@ -263,12 +265,12 @@ __global__ void __launch_bounds__(THREADS, 1)
       auto o_done = [&](uint32_t v) { return mbar_wait_warp(&bar.o_done[v % C::NB], (v / C::NB) & 1, err); };
       bool begun = false;  // O holds sums of this segment
       bool blank = true;   // a row of the warp has no reference yet
-      int page = look(sg.lag == 1 ? 0 : h);
-      for (int j = sg.lag == 1 ? 0 : h; j < sg.nk; j += sg.lag, u += 2) {
+      int page = look(lag == 1 ? 0 : h);
+      for (int j = lag == 1 ? 0 : h; j < nk; j += lag, u += 2) {
         const uint32_t buf = u % C::NB, s_tmem = tmem + lanes + 128 * buf;
-        const int key0 = (w.k0 + j) * KT;
+        const int key0 = first_key + j * KT;
         const unsigned none = __ballot_sync(0xffffffffu, (unsigned)page >= (unsigned)p.P);  // copies that have none
-        page = look(j + sg.lag);
+        page = look(j + lag);
         if (!mbar_wait_warp(&bar.s_full[buf], (u / C::NB) & 1, err)) {
           failed = true;
           break;

@@ -178,8 +178,9 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
         const int m0 = (t0 + t - w.k0) * NQ, hi = (w.s.n << p.gq_bits) - m0;  // rows in use: those before hi
         const int lo = p.causal ? ((c - w.s.L) << p.gq_bits) - m0 : 0;        // that see the key: from lo on
         const uint32_t st = nt & 1, ls = nt % L_SLOTS;
-        if (!mbar_wait_warp(&sh.l_full[ls], (nt / L_SLOTS) & 1, err) ||
-            !mbar_wait_warp(&sh.s_full[st][half], (nt >> 1) & 1, err)) {
+        const bool l_here = mbar_try_wait(&sh.l_full[ls], (nt / L_SLOTS) & 1), s_here = mbar_try_wait(&sh.s_full[st][half], (nt >> 1) & 1);
+        if (!__all_sync(0xffffffffu, l_here && s_here) && (!mbar_wait_warp(&sh.l_full[ls], (nt / L_SLOTS) & 1, err) ||
+                                                           !mbar_wait_warp(&sh.s_full[st][half], (nt >> 1) & 1, err))) {
           failed = true;
           break;
         }
