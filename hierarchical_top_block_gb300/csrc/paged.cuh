@@ -10,7 +10,8 @@
 // is finished there; of one that spans blocks each stores its part (row maxima, sums and output sums), and a
 // second kernel joins them.  A block has at most two such parts: the first job of its range and the last.  On
 // the line every job begins with `extra` empty steps, as long as a block stops for it (rows written, others
-// fetched): 880 jobs of 2 to 47 steps over 152 blocks, d = 64, take 234 us without them.  The cut depends on the sizes alone, so results are the same in every run.
+// fetched): 880 jobs of 2 to 47 steps over 152 blocks, d = 64, took 191 us with them and 234 without.  The cut depends on
+// the sizes alone, so results are the same in every run.
 //
 // With the causal mask the jobs of a head have different numbers of steps; their sums have a closed form:
 // a tile of TT tokens (a power of two) ends at token (i + 1) TT, so it takes floor((L + 127 + (i + 1) TT) / 128)
@@ -182,26 +183,24 @@ struct PagedLine {
     gbase = 0;
     job_end = -1;
     // sums over the sequences before and with a lane's own: steps and jobs
-    long long S = 0;
-    int jobs = 0;
-    auto sums = [&](int i0, long long& x, int& n) {
+    long long S = 0, jobs = 0;
+    auto sums = [&](int i0, long long& x, long long& n) {
       x = n = 0;
       bool bad = false;
       if (i0 + lane < p.B) {
         const Jobs j(p, paged_seq(p, i0 + lane, bad));
         x = p.H_kv * j.before(j.tiles);
-        n = p.H_kv * j.tiles;
+        n = (long long)p.H_kv * j.tiles;
       }
       if (report && bad) report_error(p.err, ERR_BAD_INDEX);
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const long long y = __shfl_up_sync(0xffffffffu, x, o);
-        const int k = __shfl_up_sync(0xffffffffu, n, o);
+        const long long k = __shfl_up_sync(0xffffffffu, n, o);
         if (lane >= o) x += y, n += k;
       }
     };
-    long long x;
-    int n;
+    long long x, n;
     for (int i0 = 0; i0 < p.B; i0 += 32) {
       sums(i0, x, n);
       S += __shfl_sync(0xffffffffu, x, 31);
@@ -219,7 +218,7 @@ struct PagedLine {
     long long before = 0;
     for (int i0 = 0; i0 < p.B; i0 += 32) {
       if (p.B > 32) sums(i0, x, n);  // (else they are there)
-      const long long upto = before + x + (long long)n * extra;
+      const long long upto = before + x + n * extra;
       const unsigned past = __ballot_sync(0xffffffffu, upto > at);
       if (past) {
         const int l = __ffs(past) - 1;
