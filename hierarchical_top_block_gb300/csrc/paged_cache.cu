@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(PICK_THREADS) paged_pick_kernel(EvictParams p)
   __shared__ uint32_t part[8][256];     // the first pass's, a lane's mod 8: weights have few exponents
   __shared__ uint32_t warp_sum[2][PICK_WARPS];
   __shared__ uint32_t totals[2];        // this block's keys above the limit, and at it
-  __shared__ uint32_t found[2];         // digit, and keys above it
+  __shared__ uint32_t found[3];         // digit, keys above it, keys that have it
   const uint32_t rank = cluster_rank(), blocks = cluster_size();
   const int bh = blockIdx.x / blocks, b = bh / p.H, h = bh - b * p.H;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -245,6 +245,7 @@ __global__ void __launch_bounds__(PICK_THREADS) paged_pick_kernel(EvictParams p)
       if (sum >= want && sum - count < want) {
         found[0] = 255 - threadIdx.x;
         found[1] = sum - count;
+        found[2] = count;
       }
     }
     __syncthreads();
@@ -254,6 +255,11 @@ __global__ void __launch_bounds__(PICK_THREADS) paged_pick_kernel(EvictParams p)
     }
     limit |= found[0] << shift;
     want -= found[1];
+    if (found[2] == want) {  // all keys of these digits stay: the further ones need not be looked at
+      limit -= limit > 0;
+      want = 0;
+      break;
+    }
     __syncthreads();
   }
   if (all) limit = 0, want = 0;  // every key is above it
