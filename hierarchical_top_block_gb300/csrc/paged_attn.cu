@@ -360,11 +360,14 @@ cudaError_t launch_paged_attn(const uint16_t* q, long long q_stride, const uint1
   else
     e = pg.s_bits > 4 ? launch_few_rows<64, 32>(p, s) : launch_few_rows<64, 16>(p, s);
   if (e != cudaSuccess) return e;
-  // blocks for the rows of a job that spans blocks: many where there are few jobs, which then have many parts
+  // Blocks for the rows of a job that spans blocks.  Tiles of 256: eight (1024 tokens after 15360 of 32 / 8 heads 190.7 us,
+  // with 4 and 16 190.8 and 192.8; 64 rows over 32768 keys 40.7, 43.4, 40.6; drafted tokens 43.4, 43.0, 45.0).  Few rows: one a
+  // row where there are few jobs, which then have many parts (16 heads over 32768 keys, one KV head, with 4, 8 and 16:
+  // 41, 28, 22 us), else one for four (64 sequences of 4000 keys 165.7, 166.3, 168.9).
   const long long rows = (long long)p.R * p.GQ, jobs = p.H_kv * (rows / plan.rows + std::min<long long>(p.B, rows));
   if (plan.tc)
     return launch_pdl(pr.d == 128 ? paged_join_kernel<128, 16> : paged_join_kernel<64, 16>,
-                      dim3((unsigned)p.blocks, jobs < num_sms ? 16 : 4), dim3(32 * 16), 0, s, p);
+                      dim3((unsigned)p.blocks, 8), dim3(32 * 16), 0, s, p);
   return launch_pdl(pr.d == 128 ? paged_join_kernel<128, 4> : paged_join_kernel<64, 4>,
                     dim3((unsigned)p.blocks, (unsigned)(jobs < num_sms ? plan.rows : plan.rows / 4)), dim3(32 * 4), 0, s, p);
 }
