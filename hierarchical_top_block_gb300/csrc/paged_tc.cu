@@ -393,6 +393,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 tmem_st_16x16(at, r);
               }
             }
+            tmem_wait_st();  // the weights made before lie in the same columns, and two stores may land in any order
             weights();
           }
 #pragma unroll
