@@ -53,6 +53,18 @@ __device__ __forceinline__ void product_bf16(float (&c)[4], uint32_t a0, uint32_
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// a b + c of bf16 pairs.
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+// A bf16 pair with 0 for infinities and NaN.
+__device__ __forceinline__ uint32_t finite_bf16x2(uint32_t x) {
+  if ((x & 0x7f80u) == 0x7f80u) x &= 0xffff0000u;
+  if ((x & 0x7f800000u) == 0x7f800000u) x &= 0xffffu;
+  return x;
+}
 // An 8 x 8 matrix of 16-bit elements, row r in lanes 4 r .. 4 r + 3, transposed.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t r;
@@ -328,9 +340,9 @@ struct CacheTile {
           }
         }
       }
+      if constexpr (BITS == 8) {
 #pragma unroll
-      for (int w = 0; w < VW; ++w) {
-        if constexpr (BITS == 8) {  // four columns: bytes of two keys interleaved, then widened
+        for (int w = 0; w < VW; ++w) {  // four columns: bytes of two keys interleaved, then widened
           const uint32_t x0 = v[0][w] ^ 0x80808080u, x1 = v[1][w] ^ 0x80808080u;
           const uint32_t x2 = v[2][w] ^ 0x80808080u, x3 = v[3][w] ^ 0x80808080u;
 #pragma unroll
@@ -341,14 +353,35 @@ struct CacheTile {
 #pragma unroll
             for (int h = 0; h < NH; ++h) product_f16(st.o[2 * w + e][h], a0, a1, a2, a3, pt[i][h][0], pt[i][h][1]);
           }
-        } else {
+        }
+      } else {
+#pragma unroll
+        for (int w = 0; w < VW; ++w) {
           const uint32_t a0 = __byte_perm(v[0][w], v[1][w], 0x5410), a1 = __byte_perm(v[0][w], v[1][w], 0x7632);
           const uint32_t a2 = __byte_perm(v[2][w], v[3][w], 0x5410), a3 = __byte_perm(v[2][w], v[3][w], 0x7632);
+          v[0][w] = a0, v[1][w] = a1, v[2][w] = a2, v[3][w] = a3;
 #pragma unroll
-          for (int h = 0; h < NH; ++h) {
-            product_bf16(st.o[w][h], a0, a1, a2, a3, pt[i][h][0], pt[i][h][1]);
-            if constexpr (EXACT) product_bf16(st.o[w][h], a0, a1, a2, a3, rest[i][h][0], rest[i][h][1]);
+          for (int h = 0; h < NH; ++h) product_bf16(st.o[w][h], a0, a1, a2, a3, pt[i][h][0], pt[i][h][1]);
+        }
+        if constexpr (EXACT) {
+          // What is left of a weight may be 0 or negative, and its product with an infinite value no number: such values
+          // count by the first operand alone.
+          uint32_t odd[2] = {0, 0};  // 0 times every value: 0, or NaN where one is infinite or NaN
+#pragma unroll
+          for (int w = 0; w < VW; ++w)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) odd[u & 1] = fma_bf16x2(v[u][w], 0, odd[u & 1]);
+          if (__any_sync(0xffffffffu, (odd[0] | odd[1]) != 0)) {
+#pragma unroll
+            for (int w = 0; w < VW; ++w)
+#pragma unroll
+              for (int u = 0; u < 4; ++u) v[u][w] = finite_bf16x2(v[u][w]);
           }
+#pragma unroll
+          for (int w = 0; w < VW; ++w)
+#pragma unroll
+            for (int h = 0; h < NH; ++h)
+              product_bf16(st.o[w][h], v[0][w], v[1][w], v[2][w], v[3][w], rest[i][h][0], rest[i][h][1]);
         }
       }
     }

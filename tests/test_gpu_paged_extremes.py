@@ -47,3 +47,28 @@ def test_references_rise(d, S, G, new, levels):
         R.close(o, wo, bo, "o")
         R.close(lse, wl, bl, "lse")
     no_error()
+
+
+@pytest.mark.parametrize("d,S", [(64, 16), (64, 32), (128, 16), (128, 64)])
+@pytest.mark.parametrize("G,new", [(1, 1), (4, 1), (16, 1), (4, 3), (16, 5), (4, 40), (4, 90)])
+@pytest.mark.parametrize("long", [False, True])
+def test_infinite_values(d, S, G, new, long):
+    """Values of +-infinity and NaN among the keys that every row sees: the output has them, whichever kernel runs (few rows,
+    streams by steps, by rows), and its other columns are as always."""
+    n = 5000 if long else 150
+    c = Paged([n, 40, n // 2], [new] * 3, 2, d, S, seed=G + new)
+    for b in range(3):
+        k, v = c.get(c.K, b, c.lens[b]), c.get(c.V, b, c.lens[b])
+        last = c.lens[b] - 1
+        v[0, 0, 0] = v[last, 0, 1] = v[17, 0, d - 1] = math.inf
+        v[5, 0, 2] = v[6, 0, 2] = -math.inf
+        v[8, 0, 3], v[last, 0, 3] = math.inf, -math.inf  # their sum is no number
+        v[9, 1, 9] = math.nan
+        c.put(b, k, v)
+    q = c.rand(c.R, 2 * G, d)
+    o, lse = pisa.pisa_paged_attn(q, c.K, c.V, c.table, c.len, row_start=c.rows, causal=False)
+    wo, wl, bo, bl = H.attend(c, q, causal=False)
+    assert wo.isposinf().any() and wo.isneginf().any() and wo.isnan().any()
+    R.close(o, wo, bo.nan_to_num(0), "o")
+    R.close(lse, wl, bl, "lse")
+    no_error()
