@@ -4,10 +4,11 @@
 //   S = Q K^T (fp32 in tensor memory), P = 2^(S scale log2 e - m) as bf16 back into tensor memory over S,
 //   O += P V in tensor memory, l = sum of the unrounded P
 //
-// m is a row's reference, not its running maximum: a segment's first step sets it to the step's maximum, and later ones
-// take it as it is.  Only where a lane's sum of a step's weights (32 keys of a row) passes 2^8 are the maxima found, the
-// reference raised to them, O multiplied by 2^(old - new) and the step's weights made again: P and the sums stay far
-// from the end of their ranges, and the division by l at the end is exact whatever m is.  With the usual logits that
+// m is a row's reference, not its running maximum: a segment's first step sets it to 8 above the step's maximum, and
+// later ones take it as it is.  Only where a lane's sum of a step's weights (32 keys of a row) passes 1 are the maxima found,
+// the reference raised to 8 above them, O multiplied by 2^(old - new) and the step's weights made again.  So no weight is above
+// 1 (a value at the end of bf16's range gives a finite product), a row's largest is 2^-8 at least, and the division by l at
+// the end is exact whatever m is.  With the usual logits that
 // hardly happens, so most steps look for no maximum at all (with one a step: 4096 tokens after 28672 of 32 / 8 heads
 // 1550 us).  P is rounded to bf16, 2^-9 of each weight, the size of the output's own rounding.
 //
@@ -33,7 +34,8 @@ namespace pisa {
 namespace {
 
 constexpr int ROWS = PAGED_TC_ROWS, KT = PAGED_KT;
-constexpr float MOST = 256.f;  // a lane's sum of a row's weights in a step above which the references are raised
+constexpr float MOST = 1.f;  // a lane's sum of a row's weights in a step above which the references are raised
+constexpr float ROOM = 8.f;  // how far above the maxima (log2 units)
 
 constexpr int THREADS = 384, PRODUCER = 8, ISSUER = 9, PRODUCER2 = 10;  // warps
 // Registers a thread of the softmax and of the other warpgroup, of 384 x 168 at launch: the softmax holds 128 logits.
@@ -367,7 +369,7 @@ __global__ void __launch_bounds__(THREADS, 1)
               a = fmaxf(a, b);
               a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
               a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
-              const float to = fmaxf(m[i], a * p.sl2);
+              const float to = fmaxf(m[i], a * p.sl2 + ROOM);
               f[i] = to == NEG_INF ? 1.f : fast_exp2(m[i] - to);
               m[i] = to;
               none_seen = none_seen || (row0 + 8 * i < sg.rows && to == NEG_INF);

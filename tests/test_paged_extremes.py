@@ -72,3 +72,28 @@ def test_infinite_values(d, S, G, new, long):
     R.close(o, wo, bo.nan_to_num(0), "o")
     R.close(lse, wl, bl, "lse")
     no_error()
+
+
+@pytest.mark.parametrize("d,S", [(64, 16), (64, 32), (128, 64)])
+@pytest.mark.parametrize("G,new", [(4, 20), (4, 90)])
+def test_large_values(d, S, G, new):
+    """Values of 5e37 at keys whose logits rise by half from one to the next.  The largest weight is 1 and the sums of weights of
+    them are at most 1 / (1 - e^-0.5) < 2.6, so with weights of at most 1 no sum is above 1.3e38 and the output is finite; with
+    weights relative to a reference 2^3 and more below the largest logit it is not."""
+    B, H_kv, n = 6, 4, 5000
+    c = Paged([n - 31 * b for b in range(B)], [new] * B, H_kv, d, S, seed=G + new)
+    along = torch.full((d,), d ** -0.5, device=DEV)
+    for b in range(B):
+        k, v = c.get(c.K, b, c.lens[b]).clone(), c.get(c.V, b, c.lens[b]).clone()
+        for i in range(11):
+            at = 400 * i + 333
+            k[at] = ((1 + 0.25 * i) * math.sqrt(d) * along).to(torch.bfloat16)  # logit 2 + i / 2 for q of 2 along it
+            v[at] = torch.where(torch.arange(d, device=DEV) % 2 == 0, 5e37, -5e37).to(torch.bfloat16)
+        c.put(b, k, v)
+    q = (0.3 * c.rand(c.R, H_kv * G, d).float() + 2 * along).to(torch.bfloat16)
+    o, lse = pisa.pisa_paged_attn(q, c.K, c.V, c.table, c.len, row_start=c.rows)
+    wo, wl, bo, bl = H.attend_many(c, q)
+    assert wo.abs().max() > 1e36
+    R.close(o, wo, bo, "o")
+    R.close(lse, wl, bl, "lse")
+    no_error()
