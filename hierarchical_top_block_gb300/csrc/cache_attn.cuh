@@ -194,7 +194,8 @@ struct CacheTile {
 
   // Adds the first `n` keys of the granule at `g` in shared memory.  LIMITS: row 8 h + 2 q + e sees the first
   // lim[h][e] of them alone.  EXACT (bf16): what rounding leaves of a weight is a second bf16 operand, so that 2^-17 of it
-  // is lost, not 2^-9.
+  // is lost, not 2^-8; and n is raised to 2^8 above the largest z when that passes it, so that no weight is above 1 and large values
+  // give finite products.
   template <bool LIMITS = false, bool EXACT = false>
   __device__ static __forceinline__ void add(State& st, const uint8_t* g, const Scales& sc, const Query& qr, int n, int r,
                                              int q, const int (*lim)[2] = nullptr) {
@@ -262,7 +263,8 @@ struct CacheTile {
       }
       top[h][0] = column_max(x0);
       top[h][1] = column_max(x1);
-      moved = moved || top[h][0] > st.n[h][0] + 8.f || top[h][1] > st.n[h][1] + 8.f;
+      const float past = EXACT ? 0.f : 8.f;
+      moved = moved || top[h][0] > st.n[h][0] + past || top[h][1] > st.n[h][1] + past;
     }
     if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
@@ -271,7 +273,7 @@ struct CacheTile {
         unpack_f32x2(st.l[h], l[0], l[1]);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float to = fmaxf(st.n[h][e], top[h][e]), by = to == NEG_INF ? 0.f : st.n[h][e] - to;
+          const float to = fmaxf(st.n[h][e], top[h][e] + (EXACT ? 8.f : 0.f)), by = to == NEG_INF ? 0.f : st.n[h][e] - to;
           f[e] = fast_exp2(by);  // 0 before the first keys
           // (n covers the values' scales too: where those rise by far, l is large and may keep what f does not)
           l[e] = times_exp2(l[e], by);

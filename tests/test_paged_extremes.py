@@ -75,7 +75,7 @@ def test_infinite_values(d, S, G, new, long):
 
 
 @pytest.mark.parametrize("d,S", [(64, 16), (64, 32), (128, 64)])
-@pytest.mark.parametrize("G,new", [(4, 20), (4, 90)])
+@pytest.mark.parametrize("G,new", [(4, 1), (16, 1), (4, 3), (4, 20), (4, 90)])
 def test_large_values(d, S, G, new):
     """Values of 5e37 at keys whose logits rise by half from one to the next.  The largest weight is 1 and the sums of weights of
     them are at most 1 / (1 - e^-0.5) < 2.6, so with weights of at most 1 no sum is above 1.3e38 and the output is finite; with
