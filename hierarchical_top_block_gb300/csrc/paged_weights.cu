@@ -89,8 +89,9 @@ __device__ __forceinline__ void put_weight(const PagedParams& p, const KeyWalk& 
 __device__ __forceinline__ void load_columns(uint32_t at, uint32_t (&x)[32]) { tmem_ld32(at, x); }
 __device__ __forceinline__ void load_columns(uint32_t at, uint32_t (&x)[16]) { tmem_ld16(at, x); }
 
-// Adds COLS columns of x (from column c on of the tile) with the rows' terms at `neg`; MASK: columns lo .. hi - 1 alone.
-template <int COLS, bool MASK>
+// Adds COLS columns of x (from column c on of the tile) with the rows' terms at `neg`.  MASK 1: columns lo .. hi - 1 alone; 2:
+// of them those whose row saw something, whatever the product made of it.
+template <int COLS, int MASK>
 __device__ __forceinline__ void add_columns(const uint32_t (&x)[COLS], const float* neg, unsigned long long sl2, int lo, int hi,
                                             unsigned long long (&sum)[2]) {
 #pragma unroll
@@ -99,11 +100,11 @@ __device__ __forceinline__ void add_columns(const uint32_t (&x)[COLS], const flo
     float a, b, e, f;
     unpack_f32x2(fma_f32x2(pack_u32x2(x[c], x[c + 1]), sl2, pack_f32x2(l.x, l.y)), a, b);
     unpack_f32x2(fma_f32x2(pack_u32x2(x[c + 2], x[c + 3]), sl2, pack_f32x2(l.z, l.w)), e, f);
-    if constexpr (MASK) {
-      if (c < lo || c >= hi) a = NEG_INF;
-      if (c + 1 < lo || c + 1 >= hi) b = NEG_INF;
-      if (c + 2 < lo || c + 2 >= hi) e = NEG_INF;
-      if (c + 3 < lo || c + 3 >= hi) f = NEG_INF;
+    if constexpr (MASK > 0) {
+      if (c < lo || c >= hi || (MASK == 2 && l.x == NEG_INF)) a = NEG_INF;
+      if (c + 1 < lo || c + 1 >= hi || (MASK == 2 && l.y == NEG_INF)) b = NEG_INF;
+      if (c + 2 < lo || c + 2 >= hi || (MASK == 2 && l.z == NEG_INF)) e = NEG_INF;
+      if (c + 3 < lo || c + 3 >= hi || (MASK == 2 && l.w == NEG_INF)) f = NEG_INF;
     }
     sum[0] = add_f32x2(sum[0], pack_f32x2(fast_exp2(a), fast_exp2(b)));
     sum[1] = add_f32x2(sum[1], pack_f32x2(fast_exp2(e), fast_exp2(f)));
@@ -195,9 +196,27 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
           load_columns(at + cc, x);
           tmem_wait_ld();
           if (!mask)
-            add_columns<COLS, false>(x, sh.neg[ls] + cc, sl2, 0, 0, sum);
+            add_columns<COLS, 0>(x, sh.neg[ls] + cc, sl2, 0, 0, sum);
           else if (cc < hi)
-            add_columns<COLS, true>(x, sh.neg[ls] + cc, sl2, lo - cc, hi - cc, sum);
+            add_columns<COLS, 1>(x, sh.neg[ls] + cc, sl2, lo - cc, hi - cc, sum);
+        }
+        auto summed = [&] {
+          float a, b, e, f;
+          unpack_f32x2(sum[0], a, b);
+          unpack_f32x2(sum[1], e, f);
+          return (a + b) + (e + f);
+        };
+        float y = summed();
+        if (__any_sync(0xffffffffu, y != y)) {  // perhaps of a row that saw nothing (looked for here alone: 1% of a tile)
+          sum[0] = sum[1] = 0ull;
+#pragma unroll 1
+          for (int cc = 0; cc < min(NQ, hi); cc += 16) {
+            uint32_t x[16];
+            load_columns(at + cc, x);
+            tmem_wait_ld();
+            add_columns<16, 2>(x, sh.neg[ls] + cc, sl2, lo - cc, hi - cc, sum);
+          }
+          y = summed();
         }
         tc_fence_before();
         __syncwarp();
@@ -205,10 +224,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
           mbar_arrive(&sh.s_empty[st][half]);
           mbar_arrive(&sh.l_empty[ls]);
         }
-        float a, b, e, f;
-        unpack_f32x2(sum[0], a, b);
-        unpack_f32x2(sum[1], e, f);
-        total += (a + b) + (e + f);
+        total += y;
       }
       if (failed) break;
       if constexpr (C::EPILOGUE == 16) {  // the two stages' sums meet

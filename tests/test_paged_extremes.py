@@ -97,3 +97,34 @@ def test_large_values(d, S, G, new):
     R.close(o, wo, bo, "o")
     R.close(lse, wl, bl, "lse")
     no_error()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G,new", [(4, [1, 1, 1]), (4, [3, 1, 4]), (16, [1, 1, 1]), (4, [70, 1, 40]), (16, [20, 17, 8]), (1, [300, 257, 130])])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_weights_of_rows_that_saw_nothing(d, G, new, accumulate):
+    """Rows with lse = -inf give nothing, whatever lies in q there; the others' weights are as always."""
+    H_kv = 2
+    c = Paged([700, 40, 129], new, H_kv, d, 16, seed=d + G)
+    q = c.rand(c.R, H_kv * G, d, scale=1.5)
+    _, lse = pisa.pisa_paged_attn(q, c.K, c.V, c.table, c.len, row_start=c.rows)
+    off = torch.rand((c.R, H_kv * G), generator=c.g, device=DEV) < 0.3
+    off[c.R - 1, 0], off[0, -1] = True, True
+    lse[off] = -math.inf
+    w = c.w.clone()
+    want, bound = H.weights(c, q, lse)
+    bad = torch.tensor([math.nan, math.inf, -math.inf, 1e38], device=DEV)[torch.arange(int(off.sum()), device=DEV) % 4]
+    q[off] = bad[:, None].to(torch.bfloat16)
+    pisa.pisa_paged_weights(q, lse, c.K, w, c.table, c.len, row_start=c.rows, accumulate=accumulate)
+    live = ~want.isnan()
+    assert (w[~live] == -7).all()
+    if accumulate:  # one more sum
+        want, bound = want - 7, bound + 2.0 ** -24 * (want + 7)
+    R.close(w[live], want[live], bound[live], "w")
+    # no row of a sequence saw anything: no key gets anything
+    lse.fill_(-math.inf)
+    q.fill_(math.nan)
+    w = c.w.clone()
+    pisa.pisa_paged_weights(q, lse, c.K, w, c.table, c.len, row_start=c.rows, accumulate=accumulate)
+    assert (w[~live] == -7).all() and (w[live] == (-7 if accumulate else 0)).all()
+    no_error()
