@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
           mbar_arrive_expect_tx(&sh.q_full[qs], C::Q_BYTES);
           for (int i = 0; i < DH; ++i)
             tma_load_4d(sQ + qs * C::Q_BYTES + i * (NQ * 128), &mapQ, &sh.q_full[qs], 64 * i, 0, w.head,
-                        w.s.first + ((t0 + t) << (p.row_bits - p.gq_bits)));
+                        w.s.first + ((t0 + t) << (p.row_bits - p.gq_bits)) + (p.R == 0 ? 1 : 0));
         }
         __syncwarp();
       }
@@ -398,7 +398,7 @@ cudaError_t launch_t(const PagedParams& p, cudaStream_t s) {
   using C = Cfg<D, NQ>;
   CUtensorMap mapK, mapQ = {};
   if (!encode_page_map(&mapK, p.K, D, 1 << p.s_bits, p.H_kv, p.P, 1 << std::min(p.s_bits, 7))) return cudaErrorInvalidValue;
-  // (without rows nothing of q is read but zeros: any address does)
+  // (without rows the map is over one token, behind which the copies begin: nothing is read, any address does)
   if (!encode_token_map(&mapQ, p.R > 0 ? p.q : p.K, D, p.GQ, p.H_kv, std::max(p.R, 1), p.q_stride, NQ)) return cudaErrorInvalidValue;
   constexpr size_t smem = C::TILES + sizeof(Shared);
   static_assert(smem <= 227 * 1024, "a block's shared memory");

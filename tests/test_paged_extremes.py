@@ -128,3 +128,17 @@ def test_weights_of_rows_that_saw_nothing(d, G, new, accumulate):
     pisa.pisa_paged_weights(q, lse, c.K, w, c.table, c.len, row_start=c.rows, accumulate=accumulate)
     assert (w[~live] == -7).all() and (w[live] == (-7 if accumulate else 0)).all()
     no_error()
+
+
+@pytest.mark.parametrize("G", [1, 16])
+def test_weights_without_rows_in_the_smallest_pool(G):
+    """One page of 16 keys, no token at all: a call that puts weights in place clears them, and reads neither q nor, in its
+    stead, a row of the pool (which holds NaN behind the sequence's end)."""
+    c = Paged([7], [0], 1, 64, 16, M=1, spare=0)
+    q, lse = torch.empty(0, G, 64, dtype=torch.bfloat16, device=DEV), torch.empty(0, G, device=DEV)
+    for rows in (None, c.rows):
+        c.w.fill_(-7)
+        pisa.pisa_paged_weights(q, lse, c.K, c.w, c.table, c.len, row_start=rows, accumulate=False)
+        got = c.w.flatten().tolist()
+        assert got == [0.0] * 7 + [-7.0] * 9
+    no_error()
