@@ -10,7 +10,7 @@
 // 1 (a value at the end of bf16's range gives a finite product), a row's largest is 2^-8 at least, and the division by l at
 // the end is exact whatever m is.  With the usual logits that
 // hardly happens, so most steps look for no maximum at all (with one a step: 4096 tokens after 28672 of 32 / 8 heads
-// 1550 us).  P is rounded to bf16, 2^-9 of each weight, the size of the output's own rounding.
+// 1550 us).  P is rounded to bf16, half a step (2^-8) of each weight, as the output is.
 //
 // Two streams keep the tensor pipe busy while the softmax of the other one runs, a warpgroup for each.  With more than
 // 128 rows a stream is a half of the rows, and both use the same tiles; with fewer, both streams have all rows, one

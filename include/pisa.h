@@ -392,9 +392,10 @@ PISA_API pisa_status pisa_paged_write(const uint16_t* k, const uint16_t* v, uint
  *   q, o [R][H_q][d] bf16 (o's rows follow one another);  lse [R][H_q] fp32, nullable.
  *   ws   device scratch, 256-B aligned, ws_bytes >= pisa_paged_attn_workspace_bytes(); not to be used by other work
  *        until the call has run (two captured graphs that may run at once need one each).
- * A row that sees no key gives o = 0 and lse = -inf.  With many query rows a sequence (tensor cores: more than 16 tokens x G_Q
- * on average) weights are rounded to bf16, 2^-9 of each, with few they keep 2^-17; logits and sums are fp32.  Keys behind a sequence's last may hold anything; a value that is infinite or NaN shows in the rows that
- * see its key, and may show in others of its sequence.  params.scale and causal are used. */
+ * A row that sees no key gives o = 0 and lse = -inf.  Which kernel runs depends on the batch's query rows a sequence, N G_Q / B on
+ * average: with more than 16 (tensor cores) weights are rounded to bf16, 2^-8 of each at most, with fewer 2^-17 of each is
+ * lost; logits and sums are fp32.  Keys behind a sequence's last may hold anything; a value that is infinite or NaN shows in the
+ * rows that see its key, and may show in others of its sequence.  params.scale and causal are used. */
 PISA_API size_t pisa_paged_attn_workspace_bytes(pisa_shape shape, pisa_params params, pisa_pages pages);
 PISA_API pisa_status pisa_paged_attn(const uint16_t* q, const uint16_t* Kp, const uint16_t* Vp, const int32_t* page_table,
                                      const int32_t* seq_len, const int32_t* row_start, uint16_t* o, float* lse, void* ws,
