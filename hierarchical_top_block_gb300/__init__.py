@@ -763,7 +763,8 @@ def pisa_paged_attn(q, Kp, Vp, page_table, seq_len, row_start=None, causal: bool
     """Attention of the new tokens q [R, H_q, d] over the pages of their sequences (see pisa_paged_write, which has put
     their own rows there): token t of sequence b sees its keys 0 .. seq_len[b] + t, or with causal = False all
     seq_len[b] + n_b.  Returns o [R, H_q, d] and lse [R, H_q]; rows of no sequence are left as they are (an o or
-    lse allocated here holds nothing in particular there)."""
+    lse allocated here holds nothing in particular there).  The kernel is chosen by the mean of the sequences' rows: many
+    single tokens and a long chunk are faster in two calls."""
     dev = _cuda(q, "q")
     if q.dim() != 3:
         raise ValueError("q must be [R, H_q, d]")
@@ -800,7 +801,8 @@ def pisa_paged_weights(q, lse, Kp, w, page_table, seq_len, row_start=None, accum
                        scale: float = 0.0, ws=None) -> None:
     """Add to w [pages, H_kv, page_size] fp32 (accumulate = False: put there) the attention weight that every key of
     the sequences got from the new tokens q [R, H_q, d], summed over them and the query heads of its KV head.  lse
-    [R, H_q]: pisa_paged_attn's of the same tokens, with the same causal and scale."""
+    [R, H_q]: pisa_paged_attn's of the same tokens, with the same causal and scale.  No page may be of two of the
+    sequences (sums would be lost)."""
     dev = _cuda(q, "q")
     if q.dim() != 3:
         raise ValueError("q must be [R, H_q, d]")

@@ -264,7 +264,9 @@ constexpr int MAX_SMS = 152;  // this GPU's: the scratch does not depend on the 
 // Which kernel, by the query rows a sequence has on average (their own numbers are on the device; any kernel takes any).
 // 32 sequences of 8192 keys, 8 KV heads, few-row against tensor-core kernel: d = 64, 8 rows 97 : 95 us, 16 rows 92 : 97, 24
 // rows 166 : 96; d = 128, 8 rows 170 : 168, 16 rows 170 : 171, 24 rows 319 : 172 (the few-row kernel then reads the keys
-// twice).
+// twice).  A mean says little of a mixed batch: with four heads a group, 128 tokens of as many sequences of 4000 keys and one
+// chunk of 256 after 30000 take 1104 : 489 us (alone 315 and, on tensor cores, 115); 255 of 1000 keys and a prompt of 700
+// 227 : 290 (170 and 27).
 struct Plan {
   bool tc;
   int rows, blocks, stop;

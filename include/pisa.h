@@ -371,8 +371,13 @@ PISA_API pisa_status pisa_prefix_attn(const uint16_t* q, const void* Kp, const v
  * A sequence whose seq_len is negative or whose keys do not fit in M S is left as it is, decreasing row bounds are
  * brought into range, and both are flagged (PISA_ERR_BAD_INDEX).  A table entry that names no page: keys there are seen
  * by no row; from P on it is flagged as well (a negative one may stand for a page that is gone).  No argument may
- * overlap another unless this says so, and no page may be written for two sequences (it would hold rows of
- * either).  Results are the same in every run. */
+ * overlap another unless this says so.  Pages may be shared for reading (by the attention, and as those that an eviction
+ * reads), but none may be written for two sequences or at two places of one, which nothing detects: the write and the eviction would
+ * leave rows of either, and the weights, which go to every page of a sequence, would lose sums.  Else results are the
+ * same in every run.
+ * The attention and the weights choose their kernel by N G_Q / B, the query rows a sequence on average (the
+ * numbers themselves are on the device).  A batch of many sequences of one token and a long chunk may be slower by
+ * far than two calls, one for each kind. */
 typedef struct {
   int pages;      /* P, pages in the pool */
   int page_size;  /* S, tokens a page */
